@@ -388,6 +388,151 @@ vc_status vc_snapkv_importance(const vc_shape* shape, const vc_importance_req* r
 size_t vc_importance_workspace_size(const vc_shape* shape, int32_t window, int32_t max_ctx);
 
 /* ------------------------------------------------------------------------------------------ */
+/* Caches that grow, are shared and shrink while requests decode.
+ *
+ * vc_compress_kv rebuilds KV_comp from a KV_full that stays whole. The calls below serve a cache
+ * that is all there is of a request, or the draft's own working copy: vc_rope_append rotates the
+ * new tokens' queries and keys to their positions and writes the cache rows, vc_prefix_attn and
+ * vc_scored_attn attend to it, vc_evict_kv shrinks it in place to a budget ("Architecture
+ * support": token drop is one of the compressor families; eviction by accumulated attention weight
+ * is the form of it that follows a growing cache).
+ *
+ * Rows 0..n-1 of every KV head are valid, in any order of positions: attention without a mask does
+ * not depend on the order, and vc_evict_kv fills the rows it frees from the back. The caller moves
+ * n: up by n_rows after vc_rope_append, to min(n, keep) after vc_evict_kv. Rows n..cap-1 are never
+ * read, whatever they hold. */
+typedef struct vc_live_kv {
+  void* k;           /* bf16 [Hkv][cap][d] */
+  void* v;           /* bf16 [Hkv][cap][d] */
+  float* score;      /* fp32 [Hkv][cap]: attention weight each row has gathered; NULL where not kept */
+  int32_t* pos;      /* int32 [Hkv][cap]: token position each row holds; NULL where not kept */
+  int32_t n;         /* rows held per head, 0 <= n <= cap */
+  int32_t cap;       /* rows per head, >= 1 */
+} vc_live_kv;
+
+/* ------------------------------------------------------------------------------------------ */
+/* vc_rope_init — the rotary table of vc_rope_append. Pair j of rot_dim / 2 turns by
+ * theta_j = base^(-2 j / rot_dim) radians a position, scaled for contexts longer than the trained one:
+ *   VC_ROPE_NONE    theta_j
+ *   VC_ROPE_LINEAR  theta_j / factor (positions squeezed)
+ *   VC_ROPE_NTK     base replaced by base * factor^(rot_dim / (rot_dim - 2)); rot_dim > 2
+ *   VC_ROPE_BANDS   with r = orig_ctx * theta_j / 2 pi turns over the original context and
+ *                   m = clamp((r - low) / (high - low), 0, 1): m theta_j + (1 - m) theta_j / factor
+ *                   (fast pairs stay, slow ones are squeezed, those between are mixed)
+ * amp multiplies every rotated channel (attention temperature of some scalings; 1 = none).
+ * layout: VC_ROPE_HALF pairs channels (j, j + rot_dim / 2), VC_ROPE_INTERLEAVED (2 j, 2 j + 1).
+ * Channels rot_dim..d-1 pass through. The caller may change or fill in freq itself.
+ * Errors: VC_ERR_INVALID (null, unknown kind or layout, base or factor not finite and positive, amp
+ * not finite; BANDS: orig_ctx < 1, low < 0 or high <= low); VC_ERR_UNSUPPORTED (rot_dim not a
+ * multiple of 16 in 16..2 * VC_ROPE_MAX_PAIRS). Host only. */
+#define VC_ROPE_MAX_PAIRS 64
+#define VC_ROPE_NONE 0
+#define VC_ROPE_LINEAR 1
+#define VC_ROPE_NTK 2
+#define VC_ROPE_BANDS 3
+#define VC_ROPE_HALF 0
+#define VC_ROPE_INTERLEAVED 1
+
+typedef struct vc_rope_config {
+  int32_t kind, layout, rot_dim, orig_ctx;
+  double base, factor, low, high, amp;
+} vc_rope_config;
+
+typedef struct vc_rope {
+  int32_t rot_dim, layout;
+  double amp;
+  double freq[VC_ROPE_MAX_PAIRS]; /* radians a position, rot_dim / 2 of them */
+} vc_rope;
+
+vc_status vc_rope_init(const vc_rope_config* config, vc_rope* out);
+
+/* vc_rope_append — the new tokens of B requests: q and k rotated to the tokens' positions, k and v
+ * written to cache rows n .. n+n_rows-1 of every KV head, with the position (where pos is kept) and
+ * score 0 (where score is kept). The cache's n is the caller's to move.
+ * q, k and v may be slices of one fused projection: token t's heads start at q + t * q_stride
+ * elements (a multiple of 8; 0 = packed heads, Hq * d or Hkv * d). Positions are pos[t], or
+ * pos0 + t with pos == NULL; any int32, taken in 64 bits (angles of far positions keep their
+ * accuracy: cos and sin are within 2^-21 for every |position * theta| < 2^30).
+ * q_out may be q itself when q is packed; otherwise outputs do not overlap inputs. q may be NULL
+ * (with q_out) for keys alone. Requests with n_rows == 0 are skipped; pos0 + n_rows must stay
+ * within int32. rot_dim <= d. Rotation in fp32, rounded once to bf16. */
+typedef struct vc_rope_req {
+  const void* q;       /* bf16, token t's [Hq][d] at q + t * q_stride */
+  const void* k;       /* bf16, token t's [Hkv][d] at k + t * k_stride */
+  const void* v;       /* bf16, token t's [Hkv][d] at v + t * v_stride */
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t* pos;  /* device int32 [n_rows], or NULL */
+  int32_t pos0;
+  int32_t n_rows;
+  void* q_out;         /* bf16 [n_rows][Hq][d] */
+  vc_live_kv kv;       /* rows n .. n+n_rows-1 are written (n + n_rows <= cap) */
+} vc_rope_req;
+
+vc_status vc_rope_append(const vc_shape* shape, const vc_rope* rope, const vc_rope_req* req, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
+/* vc_prefix_attn — attention of B requests that share a prefix (a system prompt, a document), whose
+ * K and V are read once for the whole batch instead of once per request.
+ *
+ * Query row i of request b (0 <= i < n_rows) attends to every prefix row and to the rows
+ * t <= n - n_rows + i of its own cache: its n_rows tokens are the cache's last rows (appended by
+ * vc_rope_append, n moved), and row i sees those up to its own. n_rows = 1 is a decode step; more
+ * are drafts to verify or a prompt chunk. Scale 1/sqrt(d), GQA as in the other calls. A row that
+ * sees no key gets zeros. K or V rows that a query row may not see do not reach it, whatever they
+ * hold. Requests with n_rows == 0 are skipped; an own cache may be empty (n == 0).
+ * prefix: ctx >= 0 rows (ctx == 0 or a NULL prefix: none); own caches' score and pos are not read.
+ * bf16 products accumulated in fp32 on the tensor cores, softmax in fp32, weights rounded to bf16 for
+ * the product with V, output rounded to bf16.
+ * ws: vc_prefix_workspace_size(shape, max_rows) bytes for calls of up to max_rows rows a request; no
+ * initialisation. Calls that overlap on the GPU must not share a workspace.
+ * Errors before anything is launched: VC_ERR_INVALID, VC_ERR_WORKSPACE. */
+typedef struct vc_live_req {
+  const void* q;     /* bf16 [n_rows][Hq][d] */
+  void* o;           /* bf16 [n_rows][Hq][d] */
+  int32_t n_rows;    /* >= 0 */
+  vc_live_kv kv;
+} vc_live_req;
+
+vc_status vc_prefix_attn(const vc_shape* shape, const vc_kv_full* prefix, const vc_live_req* req, void* ws,
+                         size_t ws_bytes, int32_t* dev_status, cudaStream_t stream);
+size_t vc_prefix_workspace_size(const vc_shape* shape, int32_t max_rows);
+
+/* vc_scored_attn — the same attention over the own caches alone, which also adds to score[h][t] the
+ * softmax weight that cached row t got from this call's rows: the sum over the request's n_rows rows
+ * and the Hq/Hkv query heads of KV head h, in fp32 from fp32 scores (fixed order: the same call gives
+ * the same bits). n_rows * Hq/Hkv <= VC_SCORED_MAX_ROWS (VC_ERR_UNSUPPORTED beyond: split a longer
+ * chunk over calls, each after its own vc_rope_append); every kv needs score.
+ * ws: vc_scored_workspace_size(shape, max_rows, max_n) bytes for calls of up to max_rows rows a
+ * request over caches of up to max_n rows; no initialisation. */
+#define VC_SCORED_MAX_ROWS 256
+
+vc_status vc_scored_attn(const vc_shape* shape, const vc_live_req* req, void* ws, size_t ws_bytes,
+                         int32_t* dev_status, cudaStream_t stream);
+size_t vc_scored_workspace_size(const vc_shape* shape, int32_t max_rows, int32_t max_n);
+
+/* ------------------------------------------------------------------------------------------ */
+/* vc_evict_kv — shrink caches in place to the rows of largest score.
+ *
+ * Of each KV head's n rows, min(n, keep) are kept, each head by its own scores: first those that are
+ * guarded (pos < sink or pos >= recent_from), then by score, largest first (-0 == +0, NaN below
+ * -infinity); equal ranks, guarded rows among themselves included, keep the lower row. Kept rows
+ * below keep stay where they are; those behind move into the freed rows, in ascending order both, with
+ * K, V, score and position. Rows keep..n-1 are left as they were; the caller sets n to min(n, keep).
+ * Every kv needs score and pos. keep >= 1. Requests with n <= keep are left alone.
+ * ws: vc_evict_workspace_size(shape, max_n) bytes for caches of up to max_n rows; no initialisation.
+ * dev_status receives VC_DEV_INTERNAL if a plan does not add up (nothing is moved for that head). */
+typedef struct vc_evict_req {
+  vc_live_kv kv;
+  int32_t keep;
+  int32_t sink;         /* rows with pos < sink are guarded (0: none) */
+  int32_t recent_from;  /* rows with pos >= recent_from are guarded (INT32_MAX: only that position) */
+} vc_evict_req;
+
+vc_status vc_evict_kv(const vc_shape* shape, const vc_evict_req* req, void* ws, size_t ws_bytes,
+                      int32_t* dev_status, cudaStream_t stream);
+size_t vc_evict_workspace_size(const vc_shape* shape, int32_t max_n);
+
+/* ------------------------------------------------------------------------------------------ */
 /* vc_plan_stagger — choose the two alternating groups of cross-resource staggering ("Cross-resource
  * staggering (P1)": while some requests draft, bound by HBM bandwidth, the KV_full of others moves
  * over the host link and is verified; the pages fix no rule for choosing who does which).

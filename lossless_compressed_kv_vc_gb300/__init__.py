@@ -2,8 +2,9 @@
 
 Argument marshalling only: every step runs in the library's CUDA kernels. The names follow the
 C ABI in include/vc.h (vc_comp_bytes, vc_compress_kv, vc_draft_attn(_noalloc), vc_verify_attn(_heads), vc_accept,
-vc_append_kv, vc_stage_full_kv, vc_snapkv_importance, vc_plan_stagger(_local), vc_stagger_period and the
-workspace-size / status-string calls). Tensors are torch tensors on the GPU; their data pointers
+vc_append_kv, vc_stage_full_kv, vc_snapkv_importance, vc_rope_init, vc_rope_append, vc_prefix_attn,
+vc_scored_attn, vc_evict_kv, vc_plan_stagger(_local), vc_stagger_period and the workspace-size /
+status-string calls). Tensors are torch tensors on the GPU; their data pointers
 and the current (or given) CUDA stream are passed through.
 
 Importing this package loads libvc.so and raises ImportError when it has not been built
@@ -33,6 +34,10 @@ VC_POOL_MAX, VC_POOL_AVG = 0, 1
 VC_DRAFT_MAX_KV_HEADS = 256
 VC_DRAFT_COUNTER_BYTES = VC_DRAFT_MAX_KV_HEADS * VC_MAX_BATCH * 4
 VC_DRAFT_NOALLOC_SCRATCH_BYTES = 32 << 20
+VC_ROPE_MAX_PAIRS = 64
+VC_ROPE_NONE, VC_ROPE_LINEAR, VC_ROPE_NTK, VC_ROPE_BANDS = range(4)
+VC_ROPE_HALF, VC_ROPE_INTERLEAVED = 0, 1
+VC_SCORED_MAX_ROWS = 256
 
 _p = C.c_void_p
 _i32 = C.c_int32
@@ -80,6 +85,33 @@ class vc_verify_req(C.Structure):
                 ("n_rows", _i32), ("o", _p)]
 
 
+class vc_live_kv(C.Structure):
+    _fields_ = [("k", _p), ("v", _p), ("score", _p), ("pos", _p), ("n", _i32), ("cap", _i32)]
+
+
+class vc_rope_config(C.Structure):
+    _fields_ = [("kind", _i32), ("layout", _i32), ("rot_dim", _i32), ("orig_ctx", _i32), ("base", C.c_double),
+                ("factor", C.c_double), ("low", C.c_double), ("high", C.c_double), ("amp", C.c_double)]
+
+
+class vc_rope(C.Structure):
+    _fields_ = [("rot_dim", _i32), ("layout", _i32), ("amp", C.c_double), ("freq", C.c_double * VC_ROPE_MAX_PAIRS)]
+
+
+class vc_rope_req(C.Structure):
+    _fields_ = [("q", _p), ("k", _p), ("v", _p), ("q_stride", C.c_int64), ("k_stride", C.c_int64),
+                ("v_stride", C.c_int64), ("pos", _p), ("pos0", _i32), ("n_rows", _i32), ("q_out", _p),
+                ("kv", vc_live_kv)]
+
+
+class vc_live_req(C.Structure):
+    _fields_ = [("q", _p), ("o", _p), ("n_rows", _i32), ("kv", vc_live_kv)]
+
+
+class vc_evict_req(C.Structure):
+    _fields_ = [("kv", vc_live_kv), ("keep", _i32), ("sink", _i32), ("recent_from", _i32)]
+
+
 _lib.vc_compress_kv.argtypes = [C.POINTER(vc_shape), C.POINTER(vc_kv_full), C.POINTER(_p), C.POINTER(_i32),
                                 _i32, C.POINTER(vc_kv_comp), _p, _p]
 _lib.vc_draft_attn.argtypes = [C.POINTER(vc_shape), C.POINTER(vc_draft_req), _p, C.c_size_t, _p, _p]
@@ -101,6 +133,18 @@ _lib.vc_plan_stagger.argtypes = [C.POINTER(vc_stagger_cost), _i32, C.POINTER(_i3
 _lib.vc_stagger_period.argtypes = [C.POINTER(vc_stagger_cost), _i32, C.POINTER(_i32), C.POINTER(C.c_int64)]
 _lib.vc_plan_stagger_local.argtypes = [C.POINTER(vc_stagger_cost), _i32, C.POINTER(_i32), C.POINTER(C.c_int64)]
 _lib.vc_comp_bytes.argtypes = [C.POINTER(vc_shape), _i32, _i32, _i32, _i32, _i32, _i32, _i32, C.POINTER(vc_comp_sizes)]
+_lib.vc_rope_init.argtypes = [C.POINTER(vc_rope_config), C.POINTER(vc_rope)]
+_lib.vc_rope_append.argtypes = [C.POINTER(vc_shape), C.POINTER(vc_rope), C.POINTER(vc_rope_req), _p]
+_lib.vc_prefix_attn.argtypes = [C.POINTER(vc_shape), C.POINTER(vc_kv_full), C.POINTER(vc_live_req), _p, C.c_size_t,
+                                _p, _p]
+_lib.vc_prefix_workspace_size.argtypes = [C.POINTER(vc_shape), _i32]
+_lib.vc_prefix_workspace_size.restype = C.c_size_t
+_lib.vc_scored_attn.argtypes = [C.POINTER(vc_shape), C.POINTER(vc_live_req), _p, C.c_size_t, _p, _p]
+_lib.vc_scored_workspace_size.argtypes = [C.POINTER(vc_shape), _i32, _i32]
+_lib.vc_scored_workspace_size.restype = C.c_size_t
+_lib.vc_evict_kv.argtypes = [C.POINTER(vc_shape), C.POINTER(vc_evict_req), _p, C.c_size_t, _p, _p]
+_lib.vc_evict_workspace_size.argtypes = [C.POINTER(vc_shape), _i32]
+_lib.vc_evict_workspace_size.restype = C.c_size_t
 _lib.vc_workspace_size.argtypes = [_i32, C.POINTER(vc_shape), _i32]
 _lib.vc_workspace_size.restype = C.c_size_t
 _lib.vc_status_string.argtypes = [_i32]
@@ -108,13 +152,15 @@ _lib.vc_status_string.restype = C.c_char_p
 _lib.vc_version.restype = _i32
 for _f in ("vc_compress_kv", "vc_draft_attn", "vc_draft_attn_noalloc", "vc_verify_attn", "vc_verify_attn_heads",
            "vc_accept", "vc_stage_full_kv", "vc_append_kv", "vc_plan_stagger", "vc_stagger_period",
-           "vc_plan_stagger_local", "vc_snapkv_importance", "vc_comp_bytes"):
+           "vc_plan_stagger_local", "vc_snapkv_importance", "vc_comp_bytes", "vc_rope_init", "vc_rope_append",
+           "vc_prefix_attn", "vc_scored_attn", "vc_evict_kv"):
     getattr(_lib, _f).restype = _i32
 
 EXPORTS = ["vc_compress_kv", "vc_draft_attn", "vc_draft_attn_noalloc", "vc_verify_attn", "vc_verify_attn_heads",
            "vc_accept", "vc_stage_full_kv", "vc_append_kv", "vc_plan_stagger", "vc_stagger_period",
            "vc_plan_stagger_local", "vc_snapkv_importance", "vc_importance_workspace_size", "vc_workspace_size", "vc_status_string",
-           "vc_version", "vc_comp_bytes"]
+           "vc_version", "vc_comp_bytes", "vc_rope_init", "vc_rope_append", "vc_prefix_attn", "vc_prefix_workspace_size",
+           "vc_scored_attn", "vc_scored_workspace_size", "vc_evict_kv", "vc_evict_workspace_size"]
 
 
 class VCError(RuntimeError):
@@ -247,6 +293,65 @@ def vc_snapkv_importance(shape: vc_shape, req, window: int, pool_kernel: int = 7
     st = _lib.vc_snapkv_importance(C.byref(shape), req, window, pool_kernel, pool_kind, _ptr(ws), wsb,
                                    _ptr(dev_status), _stream(stream))
     return _check(st, "vc_snapkv_importance", raise_on_error)
+
+
+def live_kv(k, v, n: int, score=None, pos=None) -> vc_live_kv:
+    """Descriptor of one request's cache: k, v bf16 [Hkv][cap][d], score fp32 and pos int32 [Hkv][cap]
+    (None where not kept), all contiguous; n rows a head are valid."""
+    for t in (k, v, score, pos):
+        if t is not None and not t.is_contiguous():
+            raise ValueError("a live cache's tensors are contiguous")
+    return vc_live_kv(_ptr(k), _ptr(v), _ptr(score), _ptr(pos), n, k.shape[1])
+
+
+def vc_rope_init(kind: int, rot_dim: int, layout: int = VC_ROPE_HALF, base: float = 10000.0, factor: float = 1.0,
+                 orig_ctx: int = 0, low: float = 1.0, high: float = 4.0, amp: float = 1.0) -> vc_rope:
+    """The rotary table of vc_rope_append. Raises VCError on bad arguments."""
+    out = vc_rope()
+    cfg = vc_rope_config(kind, layout, rot_dim, orig_ctx, base, factor, low, high, amp)
+    _check(_lib.vc_rope_init(C.byref(cfg), C.byref(out)), "vc_rope_init", True)
+    return out
+
+
+def vc_rope_append(shape: vc_shape, rope: vc_rope, req, stream=None, raise_on_error=True) -> int:
+    """req: vc_rope_req array [B]; the caches' n stay the caller's to move."""
+    st = _lib.vc_rope_append(C.byref(shape), C.byref(rope) if rope is not None else None, req, _stream(stream))
+    return _check(st, "vc_rope_append", raise_on_error)
+
+
+def vc_prefix_workspace_size(shape: vc_shape, max_rows: int) -> int:
+    return _lib.vc_prefix_workspace_size(C.byref(shape), max_rows)
+
+
+def vc_prefix_attn(shape: vc_shape, prefix, req, ws=None, dev_status=None, stream=None, raise_on_error=True) -> int:
+    """prefix: one vc_kv_full, or None; req: vc_live_req array [B]."""
+    wsb = ws.numel() * ws.element_size() if ws is not None else 0
+    st = _lib.vc_prefix_attn(C.byref(shape), C.byref(prefix) if prefix is not None else None, req, _ptr(ws), wsb,
+                             _ptr(dev_status), _stream(stream))
+    return _check(st, "vc_prefix_attn", raise_on_error)
+
+
+def vc_scored_workspace_size(shape: vc_shape, max_rows: int, max_n: int) -> int:
+    return _lib.vc_scored_workspace_size(C.byref(shape), max_rows, max_n)
+
+
+def vc_scored_attn(shape: vc_shape, req, ws=None, dev_status=None, stream=None, raise_on_error=True) -> int:
+    """req: vc_live_req array [B], every cache with scores."""
+    wsb = ws.numel() * ws.element_size() if ws is not None else 0
+    st = _lib.vc_scored_attn(C.byref(shape), req, _ptr(ws), wsb, _ptr(dev_status), _stream(stream))
+    return _check(st, "vc_scored_attn", raise_on_error)
+
+
+def vc_evict_workspace_size(shape: vc_shape, max_n: int) -> int:
+    return _lib.vc_evict_workspace_size(C.byref(shape), max_n)
+
+
+def vc_evict_kv(shape: vc_shape, req, ws=None, dev_status=None, stream=None, raise_on_error=True) -> int:
+    """req: vc_evict_req array [B], every cache with scores and positions; the caller then sets each
+    cache's n to min(n, keep)."""
+    wsb = ws.numel() * ws.element_size() if ws is not None else 0
+    st = _lib.vc_evict_kv(C.byref(shape), req, _ptr(ws), wsb, _ptr(dev_status), _stream(stream))
+    return _check(st, "vc_evict_kv", raise_on_error)
 
 
 def _costs(costs):

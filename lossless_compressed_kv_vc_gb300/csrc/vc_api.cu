@@ -87,6 +87,11 @@ static void set_last_op(cudaStream_t s, int op) {
   g_last_op[s] = op;
 }
 
+namespace vc {
+// An operation that writes caches or queries outside this file: a draft step after it waits for it.
+void note_cache_writer(cudaStream_t s) { set_last_op(s, kOpCompress); }
+}  // namespace vc
+
 extern "C" {
 
 int32_t vc_version(void) { return 100; }

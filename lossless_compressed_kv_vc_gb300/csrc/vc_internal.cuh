@@ -418,4 +418,70 @@ struct AppendParams {
 };
 cudaError_t launch_append(const AppendParams& p, int max_ext_rows, cudaStream_t s);
 
+// ---- caches that grow, are shared and shrink (live_api.cu and the kernels behind it) ----------
+// Marks `s` as having a cache or query writer in flight (vc_api.cu): a draft step launched after it
+// starts reading only when it has finished.
+void note_cache_writer(cudaStream_t s);
+
+struct RopeReqDev {
+  const bf16 *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;  // elements between tokens
+  const int32_t* pos;
+  bf16* q_out;
+  bf16 *kc, *vc;  // cache rows of head 0 from row n on
+  float* score;
+  int32_t* cpos;
+  int64_t cap;
+  int32_t pos0;
+  int32_t tok_begin;  // first token of the request in the call's token sequence
+};
+struct RopeParams {
+  RopeReqDev req[VC_MAX_BATCH];
+  double turns[VC_ROPE_MAX_PAIRS];  // turns a position: theta / 2 pi
+  int32_t B, Hq, Hkv, rot, inter, n_tok;
+  float amp;
+};
+cudaError_t launch_rope(const RopeParams& p, int d, cudaStream_t s);
+
+struct EvictReqDev {
+  bf16 *k, *v;
+  float* score;
+  int32_t* pos;
+  int32_t* plan;  // [Hkv][plan_stride]: number of moves, 4 ints on room destinations, then room sources
+  int64_t cap;
+  int32_t n, keep, sink, recent_from;
+  int32_t room;   // min(keep, n - keep): moves a head can need
+  int64_t plan_stride;
+};
+struct EvictParams {
+  EvictReqDev req[VC_MAX_BATCH];
+  int32_t B, Hkv;
+  int32_t* dev_status;
+};
+cudaError_t launch_evict(const EvictParams& p, int d, cudaStream_t s);
+
+// Attention of new rows over live caches and an optional shared prefix.
+struct LiveReqDev {
+  const bf16* q;
+  bf16* o;
+  const bf16 *k, *v;
+  float* score;   // scored attention only
+  int64_t cap;
+  int32_t n, n_rows;
+  int32_t tok_begin;  // first query token of the request in the call's token sequence
+};
+struct LiveArgs {
+  LiveReqDev req[VC_MAX_BATCH];
+  int32_t B, Hq, Hkv, d, n_tok;
+  const bf16 *pk, *pv;  // prefix rows [Hkv][pcap][d]
+  int64_t pcap;
+  int32_t pn;
+  void* ws;
+  size_t ws_bytes;
+  int32_t* dev_status;
+};
+size_t live_workspace_size(const vc_shape* s, int32_t max_rows, int32_t max_n, bool scored);
+// VC_ERR_WORKSPACE in *st: the workspace is too small (nothing launched)
+cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_status* st);
+
 }  // namespace vc

@@ -16,6 +16,8 @@ import torch
 from . import (vc_shape, vc_kv_full, vc_kv_comp, vc_draft_req, vc_verify_req, vc_append_req, vc_importance_req,
                vc_snapkv_importance, vc_importance_workspace_size, VC_POOL_MAX, vc_compress_kv, vc_comp_bytes,
                vc_draft_attn, vc_verify_attn, vc_verify_attn_heads, vc_verify_launches, vc_accept, vc_append_kv, vc_workspace_size,
+               vc_rope, vc_rope_req, vc_live_req, vc_evict_req, live_kv, vc_rope_append, vc_prefix_attn,
+               vc_prefix_workspace_size, vc_scored_attn, vc_scored_workspace_size, vc_evict_kv, vc_evict_workspace_size,
                VC_TOKEN_DROP, VC_QUANT, VC_CALL_DRAFT, VC_CALL_VERIFY)
 
 
@@ -710,3 +712,125 @@ def move_full_kv_to_host(groups: List[Batch]):
         slots.append(ss)
     torch.cuda.synchronize()
     return host_kv, slots
+
+
+class LiveBatch:
+    """Requests that decode from caches of their own, which grow with every step.
+
+    Each step rotates the new tokens' queries and keys to their positions and appends keys and values
+    (vc_rope_append), then attends: with a `prefix` (k, v bf16 [Hkv][cap][d] and its rows), shared by
+    all requests and read once for them (vc_prefix_attn); without one, gathering every cached row's
+    attention weight (vc_scored_attn), and a cache that has outgrown `budget` rows by more than
+    `slack` is cut back to its rows of largest weight (vc_evict_kv), the first `sink` tokens and the
+    newest `recent` ones always among them. budget 0 keeps everything.
+
+    k, v: bf16 [B][Hkv][cap][d]; n[b]: rows request b holds; next_pos[b]: its next token's position
+    (a prefix takes the first ones). All of a step's calls run on `stream` (the current one by
+    default); like a Batch's, each stream first waits for the construction.
+    """
+
+    def __init__(self, Hq: int, Hkv: int, d: int, B: int, cap: int, rope: vc_rope, max_rows: int = 1, prefix=None,
+                 budget: int = 0, slack: int = 0, sink: int = 4, recent: int = 0, device="cuda"):
+        if budget > 0 and prefix is not None:
+            raise ValueError("a batch over a shared prefix keeps its own caches whole: budget needs prefix=None")
+        if budget > 0 and (cap < budget + slack + max_rows or min(slack, sink, recent) < 0):
+            raise ValueError("cap must hold budget + slack + max_rows rows; slack, sink and recent are not negative")
+        self.Hq, self.Hkv, self.d, self.B, self.cap, self.rope, self.max_rows = Hq, Hkv, d, B, cap, rope, max_rows
+        self.prefix, self.budget, self.slack, self.sink, self.recent = prefix, budget, slack, sink, recent
+        self.device = torch.device(device)
+        self.shape = vc_shape(B, Hq, Hkv, d)
+        new = lambda shape, dt: torch.zeros(shape, dtype=dt, device=self.device)
+        self.k, self.v = (new((B, Hkv, cap, d), torch.bfloat16) for _ in range(2))
+        self.score = new((B, Hkv, cap), torch.float32) if prefix is None else None
+        self.pos = new((B, Hkv, cap), torch.int32) if prefix is None else None
+        self.q_rot = new((B, max_rows, Hq, d), torch.bfloat16)
+        self.dev_status = new(1, torch.int32)
+        self.n = [0] * B
+        self.next_pos = [prefix[2] if prefix is not None else 0] * B
+        if prefix is not None:
+            pk, pv, ctx = prefix
+            self._prefix = vc_kv_full(pk.data_ptr(), pv.data_ptr(), ctx, pk.shape[1])
+            size = vc_prefix_workspace_size(self.shape, max_rows)
+        else:
+            size = vc_scored_workspace_size(self.shape, max_rows, cap)
+            size = size and max(size, vc_evict_workspace_size(self.shape, cap))
+        if size == 0:
+            raise ValueError(f"no workspace for Hq {Hq}, Hkv {Hkv}, d {d}, B {B}, max_rows {max_rows}")
+        self.ws = torch.empty(size, dtype=torch.uint8, device=self.device)
+        self._rope_req, self._live_req = (vc_rope_req * B)(), (vc_live_req * B)()
+        self._built = torch.cuda.Event()
+        with torch.cuda.device(self.device):
+            self._built.record()
+        self._ordered = set()
+
+    def _order(self, stream):
+        """A stream given for the first time (the current one for None) waits for the construction. A
+        capturing stream may not wait for work outside its graph; torch.cuda.graph has synchronised the
+        device by then."""
+        if torch.cuda.is_current_stream_capturing():
+            return
+        Batch._order(self, torch.cuda.current_stream(self.device) if stream is None else stream)
+
+    def _kv(self, b: int):
+        return live_kv(self.k[b], self.v[b], self.n[b], None if self.score is None else self.score[b],
+                       None if self.pos is None else self.pos[b])
+
+    def append(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rows: List[int], stream=None):
+        """The next rows[b] tokens of every request: q bf16 [B][R][Hq][d], k and v bf16 [B][R][Hkv][d],
+        R >= max(rows), any stride between tokens (slices of a fused projection). Rotated queries land in
+        q_rot; caches, n and next_pos move on."""
+        if len(rows) != self.B or any(r < 0 or r > min(self.max_rows, q.shape[1]) for r in rows):
+            raise ValueError("rows: one count per request, 0 .. min(max_rows, the tokens given)")
+        for t, heads in ((q, self.Hq), (k, self.Hkv), (v, self.Hkv)):
+            if t.dtype != torch.bfloat16 or tuple(t.shape) != (self.B, q.shape[1], heads, self.d) or \
+                    t.stride(3) != 1 or t.stride(2) != self.d:
+                raise ValueError("q, k and v are bf16 [B][R][heads][d] with each token's heads contiguous")
+        for b in range(self.B):
+            e = self._rope_req[b]
+            e.q, e.k, e.v = q[b].data_ptr(), k[b].data_ptr(), v[b].data_ptr()
+            e.q_stride, e.k_stride, e.v_stride = q.stride(1), k.stride(1), v.stride(1)
+            e.pos, e.pos0, e.n_rows, e.q_out, e.kv = None, self.next_pos[b], rows[b], self.q_rot[b].data_ptr(), self._kv(b)
+        with torch.cuda.device(self.device):
+            self._order(stream)
+            vc_rope_append(self.shape, self.rope, self._rope_req, stream)
+        for b in range(self.B):
+            self.n[b] += rows[b]
+            self.next_pos[b] += rows[b]
+
+    def attend(self, o: torch.Tensor, rows: List[int], stream=None):
+        """Attention of the rows just appended, into o bf16 [B][R][Hq][d], R >= max(rows)."""
+        if o.dtype != torch.bfloat16 or o.shape[0] != self.B or o.shape[1] < max(rows) or \
+                tuple(o.shape[2:]) != (self.Hq, self.d) or not o[0].is_contiguous():
+            raise ValueError("o is bf16 [B][R][Hq][d], R >= max(rows), each request's rows contiguous")
+        for b in range(self.B):
+            e = self._live_req[b]
+            e.q, e.o, e.n_rows, e.kv = self.q_rot[b].data_ptr(), o[b].data_ptr(), rows[b], self._kv(b)
+        with torch.cuda.device(self.device):
+            self._order(stream)
+            if self.prefix is not None:
+                vc_prefix_attn(self.shape, self._prefix, self._live_req, self.ws, self.dev_status, stream)
+            else:
+                vc_scored_attn(self.shape, self._live_req, self.ws, self.dev_status, stream)
+
+    def evict(self, stream=None):
+        """Cut caches that hold more than budget + slack rows back to budget."""
+        over = [b for b in range(self.B) if self.budget > 0 and self.n[b] > self.budget + self.slack]
+        if not over:
+            return
+        arr = (vc_evict_req * len(over))()
+        for i, b in enumerate(over):
+            arr[i].kv, arr[i].keep, arr[i].sink = self._kv(b), self.budget, self.sink
+            arr[i].recent_from = self.next_pos[b] - self.recent
+        with torch.cuda.device(self.device):
+            self._order(stream)
+            vc_evict_kv(vc_shape(len(over), self.Hq, self.Hkv, self.d), arr, self.ws, self.dev_status, stream)
+        for b in over:
+            self.n[b] = self.budget
+
+    def step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, rows: Optional[List[int]] = None,
+             stream=None):
+        """append, attend and evict for the next rows (one token per request by default)."""
+        rows = [1] * self.B if rows is None else rows
+        self.append(q, k, v, rows, stream)
+        self.attend(o, rows, stream)
+        self.evict(stream)
