@@ -1,129 +1,796 @@
-// Attention of new rows over live caches and an optional shared prefix; with the scores of eviction.
+// Attention of new rows over live caches and an optional shared prefix, on tcgen05 tensor cores; with
+// the weights that eviction ranks by.
 //
 // Row i of a request's n_rows rows sees every prefix row and own rows t <= n - n_rows + i:
 //   s_t = q . k_t / sqrt(d),  o = sum_t 2^(s_t - lse) v_t  (log2 domain),  score[t] += sum_rows 2^(s_t - lse).
-// One CTA takes one (token, query head): its warps stride over the keys with a running maximum and sum
-// each and meet in shared memory; a second kernel takes the scores' sums, a warp per key.
-#include "vc_internal.cuh"
+//
+// Work decomposition. A group is a key sequence with the query rows that read it: the prefix with the
+// rows of all requests, or one request's own cache with its rows. The rows of one KV head (tokens x
+// G = Hq / Hkv heads) are cut into units of up to 256, the keys into tiles of 128; all units' tiles form
+// one sequence that is cut into equal ranges, one per CTA (one CTA per SM: 8 softmax warps, 2 MMA issuers,
+// 1 loader). A CTA's part of a unit (a piece) leaves (o, lse) partials; a second kernel merges a row's
+// partials over both its groups. So the prefix is read once for up to 256 rows, whatever requests they
+// come from, and a request's own rows cost what they are.
+//
+// Within a CTA two chains run side by side, each an issuer thread and a warpgroup of softmax threads (a
+// thread per query row): S = Q K^T into TMEM, softmax in registers, P (bf16) over S in TMEM, O += P V with P
+// read from TMEM. The chains meet only in the ring of K and V tiles, so one's softmax runs while the
+// tensor cores work for the other. A unit of more than 128 rows gives each chain 128 rows and every tile
+// (a tile serves 256 rows); one of up to 128 rows gives both chains the same rows and every other tile,
+// and each leaves its own partial.
+#include "tc05.cuh"
 
+#include <cudaTypedefs.h>
 #include <math.h>
+#include <string.h>
 
 namespace vc {
 
-constexpr int kLiveWarps = 8;
+constexpr int LM = 128;         // query rows of a chain
+constexpr int LN = 128;         // keys per tile
+constexpr int LU = 2 * LM;      // query rows of a unit
+constexpr int LTHREADS = 352;   // warps 0-3, 4-7 softmax of chains 0 and 1; 8, 9 their MMA issue; 10 TMA
+constexpr int SCORE_KEYS = 1024;  // keys of a score block
+
+struct LiveGroup {
+  int32_t n;          // keys
+  int32_t rows;       // query rows of one KV head
+  int32_t tok_begin;  // first query token (of the call)
+  int32_t causal;     // 1: row of token i sees keys <= n - n_rows + i; 0: every row sees every key
+  int32_t n_rows;     // query tokens
+  int32_t units;      // ceil(rows / LU)
+  int32_t tiles;      // ceil(n / LN)
+  int32_t tile_begin; // first tile of the group in the call's sequence: [Hkv][units][tiles]
+  int32_t unit_begin; // first unit among the units of its kind (prefix or own)
+  int32_t chunk_begin;  // scored: first score block [Hkv][ceil(n / SCORE_KEYS)]
+  float* score;
+  int64_t cap;        // row stride of score
+  float* s;           // scored: scores in the log2 domain [Hkv][rows][tiles * LN]
+};
+
+struct LiveParams {
+  CUtensorMap tm[VC_MAX_BATCH + 1][2];  // K, V of each group
+  LiveGroup grp[VC_MAX_BATCH + 1];      // the prefix first where there is one
+  const bf16* q[VC_MAX_BATCH];
+  bf16* o[VC_MAX_BATCH];
+  int32_t tok_begin[VC_MAX_BATCH];
+  int32_t own_of[VC_MAX_BATCH];         // group of the request's own cache, -1: empty
+  int32_t B, Hq, Hkv, G, n_tok;
+  int32_t n_grp, has_prefix, n_cta, total;  // total: tiles
+  int32_t merge_blocks, score_blocks;
+  int32_t slot_rows[2];                 // partial rows of a slot: prefix, own
+  float* ws_o[2];                       // [slots][slot_rows][d] of prefix and own units; slot = CTA + unit
+  float* ws_lse[2];                     // [slots][slot_rows], log2 domain, -inf: saw nothing
+  float scale_log2;
+  int32_t* dev_status;
+};
 
 template <int D>
-__device__ __forceinline__ float row_dot(const float (&q)[D / 32], const bf16* k, int lane) {
-  float s = 0.f;
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) s = fmaf(q[e], __bfloat162float(k[e * 32 + lane]), s);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-  return s;
+struct LCfg {
+  static constexpr int KB = D / 64;            // 64-channel (128-byte) blocks
+  static constexpr int T_BYTES = KB * LN * 128;  // a K, V or Q tile
+  static constexpr int NST = D == 128 ? 5 : 10;  // K and V tiles in flight or in use
+  static constexpr int OFF_T = 2 * T_BYTES;    // behind a Q tile per chain
+  static constexpr int OFF_BAR = OFF_T + NST * T_BYTES;
+  static constexpr int SMEM = OFF_BAR + 320;
+  static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
+  static_assert((2 * NST + 12) * 8 + 20 <= 320, "barriers fit");
+  static constexpr int OCOL = 2 * LN;          // TMEM: S (and P) of chain w at w LN, O at OCOL + w D
+  static constexpr uint32_t TCOLS = 512;
+  static_assert(OCOL + 2 * D <= (int)TCOLS, "TMEM");
+};
+
+// A CTA's part of a unit: tiles [j0, j1) of it.
+struct LPiece {
+  int g, hk, u, j0, j1;  // group, KV head, unit of the head, tiles
+  int rows;              // the unit's query rows
+  bool split;            // both chains hold the same rows and take every other tile
+};
+
+__device__ __forceinline__ LPiece live_piece(const LiveParams& p, int pos, int end) {
+  LPiece q;
+  q.g = 0;
+#pragma unroll 1
+  for (int i = 1; i < p.n_grp; ++i)
+    if (p.grp[i].tile_begin <= pos) q.g = i;
+  const LiveGroup& R = p.grp[q.g];
+  const int rel = pos - R.tile_begin, ul = rel / R.tiles;
+  q.hk = ul / R.units;
+  q.u = ul - q.hk * R.units;
+  q.j0 = rel - ul * R.tiles;
+  q.j1 = min(R.tiles, q.j0 + end - pos);
+  q.rows = min(LU, R.rows - q.u * LU);
+  q.split = q.rows <= LM;
+  return q;
 }
 
-__device__ __forceinline__ int live_req_of(const LiveArgs& p, int tok) {
+__device__ __forceinline__ int live_req_of(const LiveParams& p, int tok) {
   int b = 0;
 #pragma unroll 1
   for (int i = 1; i < p.B; ++i)
-    if (p.req[i].tok_begin <= tok) b = i;
+    if (p.tok_begin[i] <= tok) b = i;
   return b;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kLiveWarps * 32) live_rows_kernel(const __grid_constant__ LiveArgs p, float scale, float* lse) {
-  constexpr int E = D / 32;
-  pdl_wait();
-  pdl_launch_dependents();
-  const int tok = blockIdx.x, hq = blockIdx.y, hk = hq / (p.Hq / p.Hkv);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const LiveReqDev& r = p.req[live_req_of(p, tok)];
-  const int i = tok - r.tok_begin;
-  float q[E], acc[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(r.q[((size_t)i * p.Hq + hq) * D + e * 32 + lane]) * scale;
-    acc[e] = 0.f;
+// Bounded mbarrier wait that also gives up when another role of the CTA has aborted.
+__device__ __forceinline__ bool lwait(uint64_t* bar, uint32_t parity, int32_t* st, volatile int* abort) {
+  for (uint32_t it = 0; it < kSpinLimit; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 31u) == 31u && *abort) return false;
   }
-  auto over = [&](const bf16* k, const bf16* v, int n) {
-    for (int t = warp; t < n; t += kLiveWarps) {
-      const float s = row_dot<D>(q, k + (size_t)t * D, lane);
-      const float mn = fmaxf(m, s);
-      const float f = m == -INFINITY ? 0.f : exp2f(m - mn), w = mn == -INFINITY ? 0.f : exp2f(s - mn);
-      m = mn;
-      l = l * f + w;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + w * __bfloat162float(v[(size_t)t * D + e * 32 + lane]);
+  set_status(st, VC_DEV_TIMEOUT);
+  *abort = 1;
+  return false;
+}
+
+__device__ __forceinline__ bool nonfinite_bf16x2(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+template <int D, bool SCORED>
+__global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_constant__ LiveParams p) {
+  using C = LCfg<D>;
+  constexpr int NST = C::NST;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (smem_u32(smem) & 1023u) {  // the swizzled layouts need 1024-byte aligned tiles
+    pdl_wait();
+    if (tid == 0) set_status(p.dev_status, VC_DEV_INTERNAL);
+    return;
+  }
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [NST] tile landed
+  uint64_t* empty = full + NST;   // [NST] both chains' MMAs are done with it
+  uint64_t* sfull = empty + NST;  // [2] S of the chain's tile in TMEM
+  uint64_t* pfull = sfull + 2;    // [2] its P in TMEM (4 warps)
+  uint64_t* ofull = pfull + 2;    // [2] its P V done
+  uint64_t* qfull = ofull + 2;    // [2] the piece's Q tile in shared memory (4 warps)
+  uint64_t* vbar = qfull + 2;     // [2] the chain's warps have looked through a V tile (4 warps)
+  uint64_t* xbar = vbar + 2;      // [2] drain of the chain's MMAs
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(xbar + 2);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
+  volatile uint32_t* s_odd = tslot + 2;  // [2] 1 + the chain's last tile whose P V the softmax warps took
+  volatile uint32_t* s_issued = tslot + 4;  // loads issued so far
+
+  if (warp == 10) tc05::alloc(tslot, C::TCOLS);
+  if (tid == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 2);
     }
-  };
-  if (p.pn > 0) over(p.pk + (size_t)hk * p.pcap * D, p.pv + (size_t)hk * p.pcap * D, p.pn);
-  over(r.k + (size_t)hk * r.cap * D, r.v + (size_t)hk * r.cap * D, r.n - r.n_rows + i + 1);
-  __shared__ float sm[kLiveWarps], sl[kLiveWarps], so[kLiveWarps][D];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&sfull[w], 1);
+      mbar_init(&pfull[w], 4);
+      mbar_init(&ofull[w], 1);
+      mbar_init(&qfull[w], 4);
+      mbar_init(&vbar[w], 4);
+      mbar_init(&xbar[w], 1);
+      s_odd[w] = 0;
+    }
+    fence_mbar_init();
+    *s_abort = 0;
+    *s_issued = 0;
   }
-#pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][e * 32 + lane] = acc[e];
+  tc05::fence_before();
   __syncthreads();
-  float M = -INFINITY, L = 0.f;
-  for (int w = 0; w < kLiveWarps; ++w) M = fmaxf(M, sm[w]);
-  for (int w = 0; w < kLiveWarps; ++w)
-    if (sl[w] != 0.f) L += sl[w] * exp2f(sm[w] - M);
-  for (int c = threadIdx.x; c < D; c += kLiveWarps * 32) {
-    float o = 0.f;
-    for (int w = 0; w < kLiveWarps; ++w)
-      if (sl[w] != 0.f) o += so[w][c] * exp2f(sm[w] - M);
-    r.o[((size_t)i * p.Hq + hq) * D + c] = __float2bfloat16(L != 0.f ? o / L : 0.f);
-  }
-  if (lse && threadIdx.x == 0) lse[(size_t)tok * p.Hq + hq] = L != 0.f ? M + log2f(L) : INFINITY;
-}
-
-template <int D>
-__global__ void __launch_bounds__(256) live_score_kernel(const __grid_constant__ LiveArgs p, float scale, const float* lse) {
-  constexpr int E = D / 32;
+  tc05::fence_after();
   pdl_wait();
   pdl_launch_dependents();
-  const int hk = blockIdx.y, G = p.Hq / p.Hkv, lane = threadIdx.x & 31;
-  const LiveReqDev& r = p.req[blockIdx.z];
-  for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < r.n && r.n_rows > 0; t += gridDim.x * 8) {
-    const bf16* k = r.k + ((size_t)hk * r.cap + t) * D;
-    float w = 0.f;
-    for (int i = max(0, t - (r.n - r.n_rows)); i < r.n_rows; ++i)
-      for (int g = 0; g < G; ++g) {
-        const size_t row = (size_t)i * p.Hq + hk * G + g;
-        float q[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) q[e] = __bfloat162float(r.q[row * D + e * 32 + lane]) * scale;
-        w += exp2f(row_dot<D>(q, k, lane) - lse[(size_t)r.tok_begin * p.Hq + row]);
+  const uint32_t tmem = *tslot;
+  const int beg = (int)((int64_t)blockIdx.x * p.total / p.n_cta);
+  const int end = (int)((int64_t)(blockIdx.x + 1) * p.total / p.n_cta);
+
+  // Load `it` has landed. A chain that skips the other's tiles does not see every phase of a stage's
+  // barrier, so its parity alone could be that of two phases before: once the load is issued, the
+  // stage's phase before it is over, and its own cannot pass until this chain releases the stage.
+  auto landed = [&](uint32_t it) -> bool {
+    for (uint32_t i = 0; *s_issued <= it; ++i) {
+      if (i >= kSpinLimit || ((i & 31u) == 31u && *s_abort)) {
+        if (!*s_abort) set_status(p.dev_status, VC_DEV_TIMEOUT);
+        *s_abort = 1;
+        return false;
       }
-    if (lane == 0) r.score[(size_t)hk * r.cap + t] += w;
+    }
+    return lwait(&full[it % NST], (it / NST) & 1, p.dev_status, s_abort);
+  };
+
+  if (warp == 10) {
+    // ---- TMA: tiles in order, K then V of each ---------------------------------------------------
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int pos = beg; pos < end && ok;) {
+        const LPiece q = live_piece(p, pos, end);
+        for (int j = q.j0; j < q.j1 && ok; ++j)
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t st = it % NST;
+            if (it >= (uint32_t)NST && !lwait(&empty[st], (it / NST - 1) & 1, p.dev_status, s_abort)) {
+              ok = false;
+              break;
+            }
+            uint8_t* dst = smem + C::OFF_T + st * C::T_BYTES;
+            mbar_arrive_expect_tx(&full[st], C::T_BYTES);
+#pragma unroll
+            for (int kb = 0; kb < C::KB; ++kb)
+              tc05::tma_load_3d(dst + kb * (LN * 128), &p.tm[q.g][kv], kb * 64, j * LN, q.hk, &full[st]);
+            __threadfence_block();
+            *s_issued = ++it;
+          }
+        pos += q.j1 - q.j0;
+      }
+      if (*s_abort)  // drain (bounded): a ring's worth of loads may still be landing
+        for (uint32_t i = it > (uint32_t)NST ? it - NST : 0; i < it; ++i)
+          mbar_wait_bounded(&full[i % NST], (i / NST) & 1, p.dev_status);
+    }
+  } else if (warp >= 8) {
+    // ---- MMA issue of chain w: S of a tile once the tile before is done, then its P V -------------
+    if (lane == 0) {
+      const int w = warp - 8;
+      constexpr uint32_t IDESC_S = tc05::idesc_bf16(LM, LN, false);
+      constexpr uint32_t IDESC_O = tc05::idesc_bf16(LM, D, true);
+      const uint32_t aQ = smem_u32(smem) + w * C::T_BYTES, aT = smem_u32(smem + C::OFF_T);
+      const uint32_t tS = tmem + w * LN, tO = tmem + C::OCOL + w * D;
+      uint32_t g = 0, t = 0, u = 0;  // tiles of the CTA, tiles and pieces of the chain
+      bool ok = true;
+      for (int pos = beg; pos < end && ok;) {
+        const LPiece q = live_piece(p, pos, end);
+        const int nt = q.j1 - q.j0, first = q.split ? w : 0, step = q.split ? 2 : 1;
+        pos += nt;
+        if (first < nt) {
+          ok = lwait(&qfull[w], u & 1, p.dev_status, s_abort);
+          ++u;
+          for (int jj = first; jj < nt && ok; jj += step, ++t) {
+            const uint32_t ik = 2 * (g + jj), iv = ik + 1, sk = ik % NST, sv = iv % NST;
+            // P of the tile before has been read, where S goes
+            if (t > 0 && !lwait(&ofull[w], (t - 1) & 1, p.dev_status, s_abort)) ok = false;
+            if (!ok || !landed(ik)) {
+              ok = false;
+              break;
+            }
+            tc05::fence_after();
+            const uint32_t kaddr = aT + sk * C::T_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * (LN * 128) + (kk & 3) * 32;
+              tc05::mma_bf16(tS, tc05::sdesc_sw128(aQ + off, 16, 1024), tc05::sdesc_sw128(kaddr + off, 16, 1024),
+                             IDESC_S, kk > 0);
+            }
+            tc05::commit(&sfull[w]);
+            tc05::commit(&empty[sk]);
+            if (q.split) tc05::commit(&empty[sk]);  // the other chain leaves this tile alone
+            if (!landed(iv) || !lwait(&pfull[w], t & 1, p.dev_status, s_abort)) {
+              ok = false;
+              break;
+            }
+            tc05::fence_after();
+            if (s_odd[w] != t + 1) {
+              const uint32_t vaddr = aT + sv * C::T_BYTES;
+#pragma unroll
+              for (int kk = 0; kk < LN / 16; ++kk)
+                tc05::mma_ts(tO, tS + kk * 8, tc05::sdesc_sw128(vaddr + kk * 2048, LN * 128, 1024), IDESC_O,
+                             (jj > first || kk > 0) ? 1u : 0u);
+            }
+            tc05::commit(&ofull[w]);
+            tc05::commit(&empty[sv]);
+            if (q.split) tc05::commit(&empty[sv]);
+          }
+        }
+        g += nt;
+      }
+      // every MMA issued so far has completed before TMEM is released (bounded, even after an abort)
+      tc05::commit(&xbar[w]);
+      mbar_wait_bounded(&xbar[w], 0, p.dev_status);
+    }
+  } else {
+    // ---- softmax of chain w: thread rt owns TMEM lane rt = row rt of the chain ----------------------
+    const int w = warp >> 2, rt = tid & (LM - 1);
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + w * LN, tO = tmem + lane_off + C::OCOL + w * D;
+    uint8_t* sQ = smem + w * C::T_BYTES;
+    uint32_t g = 0, t = 0, looked = 0;
+    bool ok = true;
+    for (int pos = beg; pos < end && ok;) {
+      const LPiece q = live_piece(p, pos, end);
+      const LiveGroup& R = p.grp[q.g];
+      const int nt = q.j1 - q.j0, first = q.split ? w : 0, step = q.split ? 2 : 1;
+      pos += nt;
+      const int ru = q.split ? rt : w * LM + rt;  // row of the unit, of the head
+      const bool row_ok = ru < q.rows;
+      const int row = q.u * LU + ru, tl = row / p.G;
+      const int kind = p.has_prefix && q.g == 0 ? 0 : 1;
+      const int slot = blockIdx.x + R.unit_begin + q.hk * R.units + q.u;
+      const size_t part = (size_t)slot * p.slot_rows[kind] + (q.split ? w * q.rows : 0) + ru;
+      if (first >= nt) {  // a piece of one tile: nothing for chain 1
+        if (row_ok) p.ws_lse[kind][part] = -INFINITY;
+        g += nt;
+        continue;
+      }
+      {
+        // the chain's Q tile: its MMAs on the last one are complete (that piece's end waited for its last P V)
+        const uint4* src = nullptr;
+        if (row_ok) {
+          const int tok = R.tok_begin + tl, b = live_req_of(p, tok);
+          src = reinterpret_cast<const uint4*>(p.q[b] + ((size_t)(tok - p.tok_begin[b]) * p.Hq + q.hk * p.G + row % p.G) * D);
+        }
+#pragma unroll
+        for (int kb = 0; kb < C::KB; ++kb)
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch) {
+            const uint4 v = row_ok ? __ldg(src + kb * 8 + ch) : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(sQ + kb * (LM * 128) + rt * 128 + ((ch ^ (rt & 7)) << 4)) = v;
+          }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qfull[w]);
+      // last key the row sees, and the first one that some row of the chain does not
+      const int last_key = R.causal ? R.n - R.n_rows + tl : R.n - 1;
+      const int blind = R.causal ? R.n - R.n_rows + (q.u * LU + (q.split ? 0 : w * LM)) / p.G + 1 : R.n;
+      float* s_row = SCORED ? R.s + ((size_t)q.hk * R.rows + row) * ((size_t)R.tiles * LN) : nullptr;
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int jj = first; jj < nt; jj += step, ++t) {
+        const int j = q.j0 + jj;
+        if (!lwait(&sfull[w], t & 1, p.dev_status, s_abort)) {
+          ok = false;
+          break;
+        }
+        tc05::fence_after();
+        float x[LN];
+#pragma unroll
+        for (int cb = 0; cb < LN / 32; ++cb) {
+          uint32_t r[32];
+          tc05::ld32(tS + cb * 32, r);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[cb * 32 + e] = __uint_as_float(r[e]);
+        }
+        tc05::wait_ld();
+        const int last = last_key - j * LN;
+        if (last < LN - 1) {
+#pragma unroll
+          for (int e = 0; e < LN; ++e)
+            if (e > last) x[e] = -INFINITY;
+        }
+        if constexpr (SCORED) {
+          if (row_ok) {
+            float4* d = reinterpret_cast<float4*>(s_row + (size_t)j * LN);
+#pragma unroll
+            for (int e = 0; e < LN / 4; ++e)
+              d[e] = make_float4(x[4 * e] * p.scale_log2, x[4 * e + 1] * p.scale_log2, x[4 * e + 2] * p.scale_log2,
+                                 x[4 * e + 3] * p.scale_log2);
+          }
+        }
+        float mx = -INFINITY, my = -INFINITY, mz = -INFINITY, mw = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < LN; e += 8) {
+          mx = max3f(mx, x[e], x[e + 1]);
+          my = max3f(my, x[e + 2], x[e + 3]);
+          mz = max3f(mz, x[e + 4], x[e + 5]);
+          mw = max3f(mw, x[e + 6], x[e + 7]);
+        }
+        const float m_new = fmaxf(m_run, fmaxf(fmaxf(mx, my), fmaxf(mz, mw)) * p.scale_log2);
+        // O is rescaled only when the running maximum grew by more than 2^8; its last P V is complete (S
+        // was issued after it). TMEM loads and stores are warp-collective: the warp rescales together
+        const bool need = jj > first && m_new > m_run + 8.f;
+        if (jj == first) {
+          m_run = m_new;
+        } else if (__any_sync(0xffffffffu, need)) {
+          float f = 1.f;
+          if (need) {
+            f = ex2_approx(m_run - m_new);
+            l_run *= f;
+            m_run = m_new;
+          }
+#pragma unroll 1
+          for (int cb = 0; cb < D / 32; ++cb) {
+            uint32_t r[32];
+            tc05::ld32(tO + cb * 32, r);
+            tc05::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+            tc05::st32(tO + cb * 32, r);
+          }
+          tc05::wait_st();
+        }
+        // P = 2^(x scale - m), bf16, over S
+        const float mu = m_run == -INFINITY ? 0.f : m_run;
+        const uint64_t sc = f2_pack(p.scale_log2, p.scale_log2), nm = f2_pack(-mu, -mu);
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb) {
+          uint32_t r[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float a0, a1;
+            f2_unpack(f2_fma(f2_pack(x[hb * 64 + 2 * e], x[hb * 64 + 2 * e + 1]), sc, nm), a0, a1);
+            const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+            acc[e & 3] = f2_add(acc[e & 3], f2_pack(p0, p1));
+            r[e] = pack_bf16x2(p0, p1);
+          }
+          tc05::st32(tS + hb * 32, r);
+        }
+        float u0, u1;
+        f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), u0, u1);
+        l_run += u0 + u1;
+        tc05::wait_st();
+        // A tile with keys that some rows see and others do not: a weight of 0 would carry an infinite or
+        // NaN value row to the latter, so if V holds any, the threads add up the seen keys themselves.
+        if (blind < min(R.n, (j + 1) * LN)) {
+          const uint32_t iv = 2 * (g + jj) + 1;
+          if (!landed(iv)) {
+            ok = false;
+            break;
+          }
+          const uint8_t* sV = smem + C::OFF_T + (iv % NST) * C::T_BYTES;
+          bool bad = false;
+#pragma unroll 1
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4*>(sV + (c >> 3) * (LN * 128) + rt * 128 + (((c ^ rt) & 7) << 4));
+            bad |= nonfinite_bf16x2(v.x) || nonfinite_bf16x2(v.y) || nonfinite_bf16x2(v.z) || nonfinite_bf16x2(v.w);
+          }
+          if (bad) s_odd[w] = t + 1;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&vbar[w]);
+          if (!lwait(&vbar[w], looked & 1, p.dev_status, s_abort)) {
+            ok = false;
+            break;
+          }
+          ++looked;
+          if (s_odd[w] == t + 1) {
+#pragma unroll 1
+            for (int cb = 0; cb < D / 32; ++cb) {
+              uint32_t r[32];
+              if (jj > first) {
+                tc05::ld32(tO + cb * 32, r);
+                tc05::wait_ld();
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) r[e] = 0u;
+              }
+#pragma unroll 1
+              for (int k8 = 0; k8 < LN / 16; ++k8) {
+                uint32_t pw[8];
+                tc05::ld8(tS + k8 * 8, pw);
+                tc05::wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const int k = k8 * 16 + e;
+                  const float pk = __uint_as_float(e & 1 ? pw[e >> 1] & 0xffff0000u : pw[e >> 1] << 16);
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) {
+                    const int ch = cb * 4 + c;
+                    const uint4 v = *reinterpret_cast<const uint4*>(sV + (ch >> 3) * (LN * 128) + k * 128 + (((ch ^ k) & 7) << 4));
+                    const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int h = 0; h < 8; ++h) {
+                      const float val = __uint_as_float(h & 1 ? vw[h >> 1] & 0xffff0000u : vw[h >> 1] << 16);
+                      const float a = __uint_as_float(r[c * 8 + h]);
+                      r[c * 8 + h] = __float_as_uint(k <= last ? fmaf(pk, val, a) : a);
+                    }
+                  }
+                }
+              }
+              tc05::st32(tO + cb * 32, r);
+            }
+            tc05::wait_st();
+          }
+        }
+        tc05::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[w]);
+      }
+      if (!ok) break;
+      // the chain's partial of the piece, after its last P V
+      if (!lwait(&ofull[w], (t - 1) & 1, p.dev_status, s_abort)) {
+        ok = false;
+        break;
+      }
+      tc05::fence_after();
+      const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
+#pragma unroll 1
+      for (int cb = 0; cb < D / 32; ++cb) {
+        uint32_t r[32];
+        tc05::ld32(tO + cb * 32, r);  // warp-collective: every lane loads
+        tc05::wait_ld();
+        if (!row_ok) continue;
+        float4* dst = reinterpret_cast<float4*>(p.ws_o[kind] + part * D + cb * 32);
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+          dst[v] = make_float4(__uint_as_float(r[4 * v]) * inv, __uint_as_float(r[4 * v + 1]) * inv,
+                               __uint_as_float(r[4 * v + 2]) * inv, __uint_as_float(r[4 * v + 3]) * inv);
+      }
+      if (row_ok) p.ws_lse[kind][part] = l_run != 0.f ? m_run + log2f(l_run) : -INFINITY;
+      tc05::fence_before();
+      g += nt;
+    }
+  }
+
+  tc05::fence_before();
+  __syncthreads();
+  tc05::fence_after();
+  if (warp == 10) tc05::dealloc(tmem, C::TCOLS);
+}
+
+// Where a row of group g (KV head hk, row r of the head) left its partials: `count` of them, number i
+// at index at(i) of the kind's partial rows.
+struct LParts {
+  int kind, c0, count, stride, sub;  // sub: partials a slot (2 in split units), stride: a slot's rows
+  size_t base;
+  int second;
+  __device__ __forceinline__ size_t at(int i) const {
+    return sub == 2 ? base + (size_t)(i >> 1) * stride + (i & 1) * second : base + (size_t)i * stride;
+  }
+};
+
+__device__ __forceinline__ LParts live_parts(const LiveParams& p, int g, int hk, int r) {
+  const LiveGroup& R = p.grp[g];
+  LParts q;
+  const int u = r / LU, ul = hk * R.units + u, rows = min(LU, R.rows - u * LU);
+  const int64_t U0 = R.tile_begin + (int64_t)ul * R.tiles, U1 = U0 + R.tiles, T = p.total, N = p.n_cta;
+  const int c0 = (int)(((U0 + 1) * N - 1) / T), c1 = (int)((U1 * N - 1) / T);
+  q.kind = p.has_prefix && g == 0 ? 0 : 1;
+  q.c0 = c0;
+  q.sub = rows <= LM ? 2 : 1;
+  q.count = (c1 - c0 + 1) * q.sub;
+  q.stride = p.slot_rows[q.kind];
+  q.base = (size_t)(c0 + R.unit_begin + ul) * q.stride + (r - u * LU);
+  q.second = rows;
+  return q;
+}
+
+// Merge: a warp per (token, query head), o = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M) over the
+// partials of the prefix and of the own cache. Scores: a block per 1024 keys of a (request, KV head)
+// merges the head's rows' lse, then sums 2^(s - lse) over the rows for each key.
+template <int D, bool SCORED>
+__global__ void __launch_bounds__(256) live_finish_kernel(const __grid_constant__ LiveParams p) {
+  constexpr int E = D / 32;  // channels a lane
+  __shared__ float s_lse[VC_SCORED_MAX_ROWS];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((int)blockIdx.x < p.merge_blocks) {
+    const int64_t id = (int64_t)blockIdx.x * 8 + warp;
+    if (id >= (int64_t)p.n_tok * p.Hq) return;
+    const int tok = (int)(id / p.Hq), hq = (int)(id - (int64_t)tok * p.Hq), hk = hq / p.G, gq = hq - hk * p.G;
+    const int b = live_req_of(p, tok), i = tok - p.tok_begin[b], own = p.own_of[b];
+    LParts part[2];
+    int n_part = 0;
+    if (p.has_prefix) part[n_part++] = live_parts(p, 0, hk, tok * p.G + gq);
+    if (own >= 0) part[n_part++] = live_parts(p, own, hk, i * p.G + gq);
+    float M = -INFINITY;
+    for (int a = 0; a < n_part; ++a)
+      for (int k = lane; k < part[a].count; k += 32) M = fmaxf(M, p.ws_lse[part[a].kind][part[a].at(k)]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float L = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int a = 0; a < n_part; ++a)
+#pragma unroll 4
+      for (int k = 0; k < part[a].count; ++k) {
+        const size_t at = part[a].at(k);
+        const float l = p.ws_lse[part[a].kind][at];
+        if (l == -INFINITY) continue;  // saw nothing: its o was never written
+        const float f = M == -INFINITY ? NAN : exp2f(l - M);  // M stays -inf only beside a NaN
+        L += f;
+        const float* src = p.ws_o[part[a].kind] + at * D + lane * E;
+        float v[E];
+        if constexpr (E == 4)
+          *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+        else
+          *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(f, v[e], acc[e]);
+      }
+    const float inv = L != 0.f ? 1.f / L : 0.f;
+    bf16* dst = p.o[b] + ((size_t)i * p.Hq + hq) * D + lane * E;
+    uint32_t o[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) o[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if constexpr (E == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+    else
+      *reinterpret_cast<uint32_t*>(dst) = o[0];
+    return;
+  }
+  if constexpr (SCORED) {
+    const int id = blockIdx.x - p.merge_blocks;
+    int g = 0;
+#pragma unroll 1
+    for (int i = 1; i < p.n_grp; ++i)
+      if (p.grp[i].chunk_begin <= id) g = i;
+    const LiveGroup& R = p.grp[g];
+    const int chunks = (R.n + SCORE_KEYS - 1) / SCORE_KEYS;
+    const int hk = (id - R.chunk_begin) / chunks, k0 = (id - R.chunk_begin - hk * chunks) * SCORE_KEYS;
+    for (int r = threadIdx.x; r < R.rows; r += 256) {
+      const LParts q = live_parts(p, g, hk, r);
+      float M = -INFINITY, L = 0.f;
+      for (int k = 0; k < q.count; ++k) M = fmaxf(M, p.ws_lse[1][q.at(k)]);
+      for (int k = 0; k < q.count; ++k) {
+        const float l = p.ws_lse[1][q.at(k)];
+        if (l != -INFINITY) L += M == -INFINITY ? NAN : exp2f(l - M);
+      }
+      s_lse[r] = L != 0.f ? M + log2f(L) : INFINITY;  // a row that sees nothing has weights 2^-inf
+    }
+    __syncthreads();
+    const size_t stride = (size_t)R.tiles * LN;
+    const float* s = R.s + (size_t)hk * R.rows * stride;
+    float* score = R.score + (size_t)hk * R.cap;
+    float w[SCORE_KEYS / 256];
+#pragma unroll
+    for (int c = 0; c < SCORE_KEYS / 256; ++c) w[c] = 0.f;
+#pragma unroll 4
+    for (int r = 0; r < R.rows; ++r) {
+      const float lse = s_lse[r];
+#pragma unroll
+      for (int c = 0; c < SCORE_KEYS / 256; ++c) {
+        const int k = k0 + c * 256 + threadIdx.x;
+        if (k < R.n) w[c] += ex2_approx(s[r * stride + k] - lse);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < SCORE_KEYS / 256; ++c) {
+      const int k = k0 + c * 256 + threadIdx.x;
+      if (k < R.n) score[k] += w[c];
+    }
   }
 }
 
-size_t live_workspace_size(const vc_shape* s, int32_t max_rows, int32_t max_n, bool scored) {
-  return scored ? (size_t)s->B * max_rows * s->Hq * sizeof(float) + 16 : 16;
+// ------------------------------------------------------------------------------------------------
+// bf16 [Hkv][cap][d] rows 0..rows-1 as a 3-D tensor (d, rows, Hkv); box 64 x 128 x 1, 128-byte swizzle.
+// Rows beyond the last one read as zeros.
+static bool live_map(CUtensorMap* m, const void* base, int d, int rows, int64_t cap, int Hkv) {
+  auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tmap_encoder());
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)Hkv};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)cap * d * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)LN, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
-static cudaError_t launch_live_t(const LiveArgs& a, bool scored, cudaStream_t s) {
-  const float scale = (float)(1.4426950408889634 / sqrt((double)D));
-  float* lse = scored ? static_cast<float*>(a.ws) : nullptr;
-  cudaError_t e = launch_pdl(live_rows_kernel<D>, dim3(a.n_tok, a.Hq), dim3(kLiveWarps * 32), 0, s, a, scale, lse);
-  if (e != cudaSuccess || !scored) return e;
-  int n = 1;
-  for (int b = 0; b < a.B; ++b) n = a.req[b].n > n ? a.req[b].n : n;
-  const int gx = (n + 7) / 8 < 1024 ? (n + 7) / 8 : 1024;
-  return launch_pdl(live_score_kernel<D>, dim3(gx, a.Hkv, a.B), dim3(256), 0, s, a, scale, (const float*)lse);
+static int live_sms() {
+  static int n = 0;
+  if (n == 0) {
+    int dev = 0, v = 0;
+    n = cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess
+            ? v
+            : 152;
+  }
+  return n;
+}
+
+static int64_t units_of(int64_t rows) { return (rows + LU - 1) / LU; }
+static int slot_rows_of(int64_t rows) { return rows <= LM ? (int)(2 * rows) : LU; }
+static size_t pad256(size_t b) { return (b + 255) / 256 * 256; }
+
+// Partials: slots of both kinds (a slot per CTA and unit); scores: every row's, in fp32.
+size_t live_workspace_size(const vc_shape* s, int32_t max_rows, int32_t max_n, bool scored) {
+  const int64_t G = s->Hq / s->Hkv, rows = max_rows * G, ctas = live_sms();
+  const size_t per = (s->d + 1) * sizeof(float);
+  size_t b = pad256((size_t)(ctas + s->B * s->Hkv * units_of(rows)) * slot_rows_of(rows) * per);
+  if (scored)
+    b += pad256((size_t)s->B * s->Hkv * rows * ((max_n + (int64_t)LN - 1) / LN * LN) * sizeof(float));
+  else
+    b += pad256((size_t)(ctas + s->Hkv * units_of(s->B * rows)) * slot_rows_of(s->B * rows) * per);
+  return b + 256;
+}
+
+template <int D, bool SCORED>
+static cudaError_t launch_live_t(const LiveParams& p, cudaStream_t s) {
+  static std::atomic<uint64_t> attr{0};
+  if (p.total > 0) {
+    cudaError_t e = raise_smem_limit(live_attn_kernel<D, SCORED>, LCfg<D>::SMEM, attr);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(live_attn_kernel<D, SCORED>, dim3(p.n_cta), dim3(LTHREADS), LCfg<D>::SMEM, s, p);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(live_finish_kernel<D, SCORED>, dim3(p.merge_blocks + p.score_blocks), dim3(256), 0, s, p);
 }
 
 cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_status* st) {
-  const size_t need = scored ? (size_t)a.n_tok * a.Hq * sizeof(float) : 0;
-  if (need && ((reinterpret_cast<uintptr_t>(a.ws) & 15u) || !a.ws || a.ws_bytes < need)) {
+  const int G = a.Hq / a.Hkv;
+  LiveParams p;  // about 13 KB: the tensor maps travel as kernel parameters
+  memset(&p, 0, sizeof(p));
+  p.B = a.B;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.G = G;
+  p.n_tok = a.n_tok;
+  p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)a.d));
+  p.dev_status = a.dev_status;
+  p.slot_rows[0] = p.slot_rows[1] = 1;
+  int64_t tiles = 0, units[2] = {0, 0}, chunks = 0;
+  size_t s_floats = 0;
+  // adds the group of a key sequence; `b`: the request whose own cache it is, -1: the prefix
+  auto add = [&](int b, int n, int n_rows, int tok_begin) {
+    const int kind = b < 0 ? 0 : 1;
+    LiveGroup& R = p.grp[p.n_grp];
+    R.n = n;
+    R.rows = n_rows * G;
+    R.tok_begin = tok_begin;
+    R.causal = kind;
+    R.n_rows = n_rows;
+    R.units = (int32_t)units_of(R.rows);
+    R.tiles = (n + LN - 1) / LN;
+    R.tile_begin = (int32_t)tiles;
+    R.unit_begin = (int32_t)units[kind];
+    R.chunk_begin = (int32_t)chunks;
+    const int sr = slot_rows_of(R.rows);
+    p.slot_rows[kind] = sr > p.slot_rows[kind] ? sr : p.slot_rows[kind];
+    units[kind] += (int64_t)a.Hkv * R.units;
+    tiles += (int64_t)a.Hkv * R.units * R.tiles;
+    if (scored) {
+      chunks += (int64_t)a.Hkv * ((n + SCORE_KEYS - 1) / SCORE_KEYS);
+      s_floats += (size_t)a.Hkv * R.rows * R.tiles * LN;
+    }
+    ++p.n_grp;
+    // tiles and blocks are counted in 32 bits
+    if (tiles >= INT32_MAX || chunks >= INT32_MAX / 2 || units[kind] >= INT32_MAX / 2) *st = VC_ERR_UNSUPPORTED;
+  };
+  if (a.pn > 0) {
+    p.has_prefix = 1;
+    add(-1, a.pn, a.n_tok, 0);
+  }
+  for (int b = 0; b < a.B && *st == VC_OK; ++b) {
+    const LiveReqDev& r = a.req[b];
+    p.q[b] = r.q;
+    p.o[b] = r.o;
+    p.tok_begin[b] = r.tok_begin;
+    p.own_of[b] = -1;
+    if (r.n_rows == 0 || r.n == 0) continue;
+    p.own_of[b] = p.n_grp;
+    LiveGroup& R = p.grp[p.n_grp];
+    R.score = r.score;
+    R.cap = r.cap;
+    add(b, r.n, r.n_rows, r.tok_begin);
+  }
+  const int64_t merge = ((int64_t)a.n_tok * a.Hq + 7) / 8;
+  if (*st == VC_OK && merge + chunks >= INT32_MAX) *st = VC_ERR_UNSUPPORTED;
+  if (*st != VC_OK) return cudaSuccess;
+  p.total = (int32_t)tiles;
+  p.n_cta = tiles < live_sms() ? (int32_t)tiles : live_sms();
+  p.merge_blocks = (int32_t)merge;
+  p.score_blocks = (int32_t)chunks;
+  uint8_t* at = static_cast<uint8_t*>(a.ws);
+  size_t need = 0;
+  auto take = [&](size_t bytes) {
+    float* f = reinterpret_cast<float*>(at + need);
+    need += pad256(bytes);
+    return f;
+  };
+  if (!a.ws || (reinterpret_cast<uintptr_t>(a.ws) & 15u)) {
     *st = VC_ERR_WORKSPACE;
     return cudaSuccess;
   }
-  return a.d == 128 ? launch_live_t<128>(a, scored, s) : launch_live_t<64>(a, scored, s);
+  for (int kind = 0; kind < 2; ++kind) {
+    const size_t rows = units[kind] ? (size_t)(p.n_cta + units[kind]) * p.slot_rows[kind] : 0;
+    p.ws_o[kind] = take(rows * (a.d + 1) * sizeof(float));
+    p.ws_lse[kind] = p.ws_o[kind] + rows * a.d;
+  }
+  float* scores = take(s_floats * sizeof(float));
+  if (need > a.ws_bytes) {
+    *st = VC_ERR_WORKSPACE;
+    return cudaSuccess;
+  }
+  bool maps = a.pn <= 0 || (live_map(&p.tm[0][0], a.pk, a.d, a.pn, a.pcap, a.Hkv) &&
+                            live_map(&p.tm[0][1], a.pv, a.d, a.pn, a.pcap, a.Hkv));
+  for (int b = 0; b < a.B && maps; ++b) {
+    const LiveReqDev& r = a.req[b];
+    const int g = p.own_of[b];
+    if (g >= 0)
+      maps = live_map(&p.tm[g][0], r.k, a.d, r.n, r.cap, a.Hkv) && live_map(&p.tm[g][1], r.v, a.d, r.n, r.cap, a.Hkv);
+  }
+  if (!maps) {
+    *st = VC_ERR_CUDA;
+    return cudaSuccess;
+  }
+  for (int g = 0; g < p.n_grp && scored; ++g) {
+    p.grp[g].s = scores;
+    scores += (size_t)a.Hkv * p.grp[g].rows * p.grp[g].tiles * LN;
+  }
+  if (a.d == 128) return scored ? launch_live_t<128, true>(p, s) : launch_live_t<128, false>(p, s);
+  return scored ? launch_live_t<64, true>(p, s) : launch_live_t<64, false>(p, s);
 }
 
 }  // namespace vc
