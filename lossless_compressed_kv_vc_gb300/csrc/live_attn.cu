@@ -28,8 +28,9 @@ namespace vc {
 
 constexpr int LM = 128;         // query rows of a chain
 constexpr int LN = 128;         // keys per tile
+constexpr int LS = 64;          // keys per step: S and P of half a tile, double-buffered
 constexpr int LU = 2 * LM;      // query rows of a unit
-constexpr int LTHREADS = 352;   // warps 0-3, 4-7 softmax of chains 0 and 1; 8, 9 their MMA issue; 10 TMA
+constexpr int LTHREADS = 416;   // warps 0-3, 4-7 softmax of chains 0 and 1; 8, 9 issue their S; 10, 11 their P V; 12 TMA
 constexpr int SCORE_KEYS = 1024;  // keys of a score block
 
 struct LiveGroup {
@@ -72,13 +73,16 @@ struct LCfg {
   static constexpr int NST = D == 128 ? 5 : 10;  // K and V tiles in flight or in use
   static constexpr int OFF_T = 2 * T_BYTES;    // behind a Q tile per chain
   static constexpr int OFF_BAR = OFF_T + NST * T_BYTES;
-  static constexpr int SMEM = OFF_BAR + 320;
+  static constexpr int SMEM = OFF_BAR + 384;
   static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
-  static_assert((2 * NST + 12) * 8 + 20 <= 320, "barriers fit");
-  static constexpr int OCOL = 2 * LN;          // TMEM: S (and P) of chain w at w LN, O at OCOL + w D
+  static_assert((2 * NST + 20) * 8 + 20 <= 384, "barriers fit");
+  static constexpr int OCOL = 4 * LS;          // TMEM: S (and P) of chain w at (2 w + step % 2) LS, O at OCOL + w D
   static constexpr uint32_t TCOLS = 512;
   static_assert(OCOL + 2 * D <= (int)TCOLS, "TMEM");
 };
+
+// Steps of tile j of n keys: its second half only where it holds keys.
+__device__ __forceinline__ int live_steps(int n, int j) { return n - j * LN > LS ? 2 : 1; }
 
 // A CTA's part of a unit: tiles [j0, j1) of it.
 struct LPiece {
@@ -140,30 +144,33 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
   }
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [NST] tile landed
   uint64_t* empty = full + NST;   // [NST] both chains' MMAs are done with it
-  uint64_t* sfull = empty + NST;  // [2] S of the chain's tile in TMEM
-  uint64_t* pfull = sfull + 2;    // [2] its P in TMEM (4 warps)
-  uint64_t* ofull = pfull + 2;    // [2] its P V done
-  uint64_t* qfull = ofull + 2;    // [2] the piece's Q tile in shared memory (4 warps)
+  uint64_t* sfull = empty + NST;  // [2][2] S of the chain's step in TMEM buffer step & 1
+  uint64_t* pfull = sfull + 4;    // [2][2] the step's P in the same place (4 warps)
+  uint64_t* ofull = pfull + 4;    // [2][2] its P V done: the buffer may take the S of two steps on
+  uint64_t* qfull = ofull + 4;    // [2] the piece's Q tile in shared memory (4 warps)
   uint64_t* vbar = qfull + 2;     // [2] the chain's warps have looked through a V tile (4 warps)
-  uint64_t* xbar = vbar + 2;      // [2] drain of the chain's MMAs
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(xbar + 2);
+  uint64_t* xbar = vbar + 2;      // [4] drain of an issuer's MMAs
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(xbar + 4);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
-  volatile uint32_t* s_odd = tslot + 2;  // [2] 1 + the chain's last tile whose P V the softmax warps took
+  volatile uint32_t* s_odd = tslot + 2;  // [2] 1 + the chain's last step whose P V the softmax warps took
   volatile uint32_t* s_issued = tslot + 4;  // loads issued so far
 
-  if (warp == 10) tc05::alloc(tslot, C::TCOLS);
+  if (warp == 12) tc05::alloc(tslot, C::TCOLS);
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 2);
     }
     for (int w = 0; w < 2; ++w) {
-      mbar_init(&sfull[w], 1);
-      mbar_init(&pfull[w], 4);
-      mbar_init(&ofull[w], 1);
+      for (int i = 2 * w; i < 2 * w + 2; ++i) {
+        mbar_init(&sfull[i], 1);
+        mbar_init(&pfull[i], 4);
+        mbar_init(&ofull[i], 1);
+      }
       mbar_init(&qfull[w], 4);
       mbar_init(&vbar[w], 4);
       mbar_init(&xbar[w], 1);
+      mbar_init(&xbar[2 + w], 1);
       s_odd[w] = 0;
     }
     fence_mbar_init();
@@ -179,11 +186,15 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
   const int beg = (int)((int64_t)blockIdx.x * p.total / p.n_cta);
   const int end = (int)((int64_t)(blockIdx.x + 1) * p.total / p.n_cta);
 
-  // Load `it` has landed. A chain that skips the other's tiles does not see every phase of a stage's
-  // barrier, so its parity alone could be that of two phases before: once the load is issued, the
-  // stage's phase before it is over, and its own cannot pass until this chain releases the stage.
-  auto landed = [&](uint32_t it) -> bool {
-    for (uint32_t i = 0; *s_issued <= it; ++i) {
+  // Load `it` has landed; `seen` is the caller's count of loads it knows to be issued. A role does not see
+  // every phase of a stage's barrier (the S issuers wait for K tiles only, the P V issuers for V tiles, in
+  // split units each chain for its own), so the parity alone could be that of two phases before: once the
+  // load is issued, the phase before it is over, and its own cannot pass until this role releases the stage.
+  // The chains' barriers are kept per S buffer: step s + 2 cannot complete a phase of one before step s's
+  // has been waited for, while with one barrier for both, steps s and s + 1 could both pass unseen.
+  auto landed = [&](uint32_t it, uint32_t& seen) -> bool {
+    for (uint32_t i = 0; seen <= it; ++i) {
+      seen = *s_issued;
       if (i >= kSpinLimit || ((i & 31u) == 31u && *s_abort)) {
         if (!*s_abort) set_status(p.dev_status, VC_DEV_TIMEOUT);
         *s_abort = 1;
@@ -193,7 +204,7 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
     return lwait(&full[it % NST], (it / NST) & 1, p.dev_status, s_abort);
   };
 
-  if (warp == 10) {
+  if (warp == 12) {
     // ---- TMA: tiles in order, K then V of each ---------------------------------------------------
     if (lane == 0) {
       uint32_t it = 0;
@@ -221,62 +232,92 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
         for (uint32_t i = it > (uint32_t)NST ? it - NST : 0; i < it; ++i)
           mbar_wait_bounded(&full[i % NST], (i / NST) & 1, p.dev_status);
     }
-  } else if (warp >= 8) {
-    // ---- MMA issue of chain w: S of a tile once the tile before is done, then its P V -------------
+  } else if (warp >= 10) {
+    // ---- P V issue of chain w: as soon as a step's P is there ---------------------------------------
     if (lane == 0) {
-      const int w = warp - 8;
-      constexpr uint32_t IDESC_S = tc05::idesc_bf16(LM, LN, false);
+      const int w = warp - 10;
       constexpr uint32_t IDESC_O = tc05::idesc_bf16(LM, D, true);
-      const uint32_t aQ = smem_u32(smem) + w * C::T_BYTES, aT = smem_u32(smem + C::OFF_T);
-      const uint32_t tS = tmem + w * LN, tO = tmem + C::OCOL + w * D;
-      uint32_t g = 0, t = 0, u = 0;  // tiles of the CTA, tiles and pieces of the chain
+      const uint32_t aT = smem_u32(smem + C::OFF_T), tS = tmem + 2 * w * LS, tO = tmem + C::OCOL + w * D;
+      uint32_t g = 0, t = 0, seen = 0;  // tiles of the CTA, steps of the chain
       bool ok = true;
       for (int pos = beg; pos < end && ok;) {
         const LPiece q = live_piece(p, pos, end);
+        const int n = p.grp[q.g].n;
         const int nt = q.j1 - q.j0, first = q.split ? w : 0, step = q.split ? 2 : 1;
         pos += nt;
-        if (first < nt) {
-          ok = lwait(&qfull[w], u & 1, p.dev_status, s_abort);
-          ++u;
-          for (int jj = first; jj < nt && ok; jj += step, ++t) {
-            const uint32_t ik = 2 * (g + jj), iv = ik + 1, sk = ik % NST, sv = iv % NST;
-            // P of the tile before has been read, where S goes
-            if (t > 0 && !lwait(&ofull[w], (t - 1) & 1, p.dev_status, s_abort)) ok = false;
-            if (!ok || !landed(ik)) {
-              ok = false;
-              break;
-            }
-            tc05::fence_after();
-            const uint32_t kaddr = aT + sk * C::T_BYTES;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * (LN * 128) + (kk & 3) * 32;
-              tc05::mma_bf16(tS, tc05::sdesc_sw128(aQ + off, 16, 1024), tc05::sdesc_sw128(kaddr + off, 16, 1024),
-                             IDESC_S, kk > 0);
-            }
-            tc05::commit(&sfull[w]);
-            tc05::commit(&empty[sk]);
-            if (q.split) tc05::commit(&empty[sk]);  // the other chain leaves this tile alone
-            if (!landed(iv) || !lwait(&pfull[w], t & 1, p.dev_status, s_abort)) {
+        bool acc = false;
+        for (int jj = first; jj < nt && ok; jj += step) {
+          const uint32_t iv = 2 * (g + jj) + 1, sv = iv % NST, vaddr = aT + sv * C::T_BYTES;
+          const int hs = live_steps(n, q.j0 + jj);
+          for (int h = 0; h < hs; ++h, ++t) {
+            if ((h == 0 && !landed(iv, seen)) || !lwait(&pfull[2 * w + (t & 1)], (t >> 1) & 1, p.dev_status, s_abort)) {
               ok = false;
               break;
             }
             tc05::fence_after();
             if (s_odd[w] != t + 1) {
-              const uint32_t vaddr = aT + sv * C::T_BYTES;
+              const uint32_t tP = tS + (t & 1) * LS, va = vaddr + h * (LS / 16) * 2048;
 #pragma unroll
-              for (int kk = 0; kk < LN / 16; ++kk)
-                tc05::mma_ts(tO, tS + kk * 8, tc05::sdesc_sw128(vaddr + kk * 2048, LN * 128, 1024), IDESC_O,
-                             (jj > first || kk > 0) ? 1u : 0u);
+              for (int kk = 0; kk < LS / 16; ++kk)
+                tc05::mma_ts(tO, tP + kk * 8, tc05::sdesc_sw128(va + kk * 2048, LN * 128, 1024), IDESC_O,
+                             (acc || kk > 0) ? 1u : 0u);
             }
-            tc05::commit(&ofull[w]);
-            tc05::commit(&empty[sv]);
-            if (q.split) tc05::commit(&empty[sv]);
+            tc05::commit(&ofull[2 * w + (t & 1)]);
+            acc = true;
           }
+          if (!ok) break;
+          tc05::commit(&empty[sv]);
+          if (q.split) tc05::commit(&empty[sv]);  // the other chain leaves this tile alone
         }
         g += nt;
       }
       // every MMA issued so far has completed before TMEM is released (bounded, even after an abort)
+      tc05::commit(&xbar[2 + w]);
+      mbar_wait_bounded(&xbar[2 + w], 0, p.dev_status);
+    }
+  } else if (warp >= 8) {
+    // ---- S issue of chain w: a step ahead of its softmax --------------------------------------------
+    if (lane == 0) {
+      const int w = warp - 8;
+      constexpr uint32_t IDESC_S = tc05::idesc_bf16(LM, LS, false);
+      const uint32_t aQ = smem_u32(smem) + w * C::T_BYTES, aT = smem_u32(smem + C::OFF_T);
+      const uint32_t tS = tmem + 2 * w * LS;
+      uint32_t g = 0, t = 0, u = 0, seen = 0;  // tiles of the CTA, steps and pieces of the chain
+      bool ok = true;
+      for (int pos = beg; pos < end && ok;) {
+        const LPiece q = live_piece(p, pos, end);
+        const int n = p.grp[q.g].n;
+        const int nt = q.j1 - q.j0, first = q.split ? w : 0, step = q.split ? 2 : 1;
+        pos += nt;
+        if (first < nt) {
+          ok = lwait(&qfull[w], u & 1, p.dev_status, s_abort);
+          ++u;
+        }
+        for (int jj = first; jj < nt && ok; jj += step) {
+          const uint32_t ik = 2 * (g + jj), sk = ik % NST, kaddr = aT + sk * C::T_BYTES;
+          const int hs = live_steps(n, q.j0 + jj);
+          for (int h = 0; h < hs; ++h, ++t) {
+            // the P V that read its P from this S buffer is done
+            if ((h == 0 && !landed(ik, seen)) ||
+                (t > 1 && !lwait(&ofull[2 * w + (t & 1)], ((t - 2) >> 1) & 1, p.dev_status, s_abort))) {
+              ok = false;
+              break;
+            }
+            tc05::fence_after();
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * (LN * 128) + (kk & 3) * 32;
+              tc05::mma_bf16(tS + (t & 1) * LS, tc05::sdesc_sw128(aQ + off, 16, 1024),
+                             tc05::sdesc_sw128(kaddr + h * LS * 128 + off, 16, 1024), IDESC_S, kk > 0);
+            }
+            tc05::commit(&sfull[2 * w + (t & 1)]);
+          }
+          if (!ok) break;
+          tc05::commit(&empty[sk]);
+          if (q.split) tc05::commit(&empty[sk]);
+        }
+        g += nt;
+      }
       tc05::commit(&xbar[w]);
       mbar_wait_bounded(&xbar[w], 0, p.dev_status);
     }
@@ -284,9 +325,12 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
     // ---- softmax of chain w: thread rt owns TMEM lane rt = row rt of the chain ----------------------
     const int w = warp >> 2, rt = tid & (LM - 1);
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lane_off + w * LN, tO = tmem + lane_off + C::OCOL + w * D;
+    const uint32_t tS = tmem + lane_off + 2 * w * LS, tO = tmem + lane_off + C::OCOL + w * D;
     uint8_t* sQ = smem + w * C::T_BYTES;
-    uint32_t g = 0, t = 0, looked = 0;
+    uint32_t g = 0, t = 0, looked = 0, seen = 0;
+    // P V of step s done (and with it those before): asked for steps whose S has been read, so the phase
+    // before on that buffer is over
+    auto pv_done = [&](uint32_t s) { return lwait(&ofull[2 * w + (s & 1)], (s >> 1) & 1, p.dev_status, s_abort); };
     bool ok = true;
     for (int pos = beg; pos < end && ok;) {
       const LPiece q = live_piece(p, pos, end);
@@ -327,159 +371,176 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
       const int blind = R.causal ? R.n - R.n_rows + (q.u * LU + (q.split ? 0 : w * LM)) / p.G + 1 : R.n;
       float* s_row = SCORED ? R.s + ((size_t)q.hk * R.rows + row) * ((size_t)R.tiles * LN) : nullptr;
       float m_run = -INFINITY, l_run = 0.f;
-      for (int jj = first; jj < nt; jj += step, ++t) {
-        const int j = q.j0 + jj;
-        if (!lwait(&sfull[w], t & 1, p.dev_status, s_abort)) {
-          ok = false;
-          break;
-        }
-        tc05::fence_after();
-        float x[LN];
-#pragma unroll
-        for (int cb = 0; cb < LN / 32; ++cb) {
-          uint32_t r[32];
-          tc05::ld32(tS + cb * 32, r);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) x[cb * 32 + e] = __uint_as_float(r[e]);
-        }
-        tc05::wait_ld();
-        const int last = last_key - j * LN;
-        if (last < LN - 1) {
-#pragma unroll
-          for (int e = 0; e < LN; ++e)
-            if (e > last) x[e] = -INFINITY;
-        }
-        if constexpr (SCORED) {
-          if (row_ok) {
-            float4* d = reinterpret_cast<float4*>(s_row + (size_t)j * LN);
-#pragma unroll
-            for (int e = 0; e < LN / 4; ++e)
-              d[e] = make_float4(x[4 * e] * p.scale_log2, x[4 * e + 1] * p.scale_log2, x[4 * e + 2] * p.scale_log2,
-                                 x[4 * e + 3] * p.scale_log2);
+      bool fresh = true;  // the piece's first step
+      for (int jj = first; jj < nt && ok; jj += step) {
+        const int j = q.j0 + jj, hs = live_steps(R.n, j);
+        for (int h = 0; h < hs; ++h, ++t, fresh = false) {
+          const int k0 = j * LN + h * LS;  // the step's first key
+          const uint32_t tP = tS + (t & 1) * LS;
+          if (!lwait(&sfull[2 * w + (t & 1)], (t >> 1) & 1, p.dev_status, s_abort)) {
+            ok = false;
+            break;
           }
-        }
-        float mx = -INFINITY, my = -INFINITY, mz = -INFINITY, mw = -INFINITY;
+          tc05::fence_after();
+          float x[LS];
 #pragma unroll
-        for (int e = 0; e < LN; e += 8) {
-          mx = max3f(mx, x[e], x[e + 1]);
-          my = max3f(my, x[e + 2], x[e + 3]);
-          mz = max3f(mz, x[e + 4], x[e + 5]);
-          mw = max3f(mw, x[e + 6], x[e + 7]);
-        }
-        const float m_new = fmaxf(m_run, fmaxf(fmaxf(mx, my), fmaxf(mz, mw)) * p.scale_log2);
-        // O is rescaled only when the running maximum grew by more than 2^8; its last P V is complete (S
-        // was issued after it). TMEM loads and stores are warp-collective: the warp rescales together
-        const bool need = jj > first && m_new > m_run + 8.f;
-        if (jj == first) {
-          m_run = m_new;
-        } else if (__any_sync(0xffffffffu, need)) {
-          float f = 1.f;
-          if (need) {
-            f = ex2_approx(m_run - m_new);
-            l_run *= f;
-            m_run = m_new;
-          }
-#pragma unroll 1
-          for (int cb = 0; cb < D / 32; ++cb) {
+          for (int cb = 0; cb < LS / 32; ++cb) {
             uint32_t r[32];
-            tc05::ld32(tO + cb * 32, r);
-            tc05::wait_ld();
+            tc05::ld32(tP + cb * 32, r);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-            tc05::st32(tO + cb * 32, r);
+            for (int e = 0; e < 32; ++e) x[cb * 32 + e] = __uint_as_float(r[e]);
           }
-          tc05::wait_st();
-        }
-        // P = 2^(x scale - m), bf16, over S
-        const float mu = m_run == -INFINITY ? 0.f : m_run;
-        const uint64_t sc = f2_pack(p.scale_log2, p.scale_log2), nm = f2_pack(-mu, -mu);
-        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+          tc05::wait_ld();
+          const int last = last_key - k0;
+          if (last < LS - 1) {
 #pragma unroll
-        for (int hb = 0; hb < 2; ++hb) {
-          uint32_t r[32];
+            for (int e = 0; e < LS; ++e)
+              if (e > last) x[e] = -INFINITY;
+          }
+          if constexpr (SCORED) {
+            if (row_ok) {
+              float4* d = reinterpret_cast<float4*>(s_row + k0);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float a0, a1;
-            f2_unpack(f2_fma(f2_pack(x[hb * 64 + 2 * e], x[hb * 64 + 2 * e + 1]), sc, nm), a0, a1);
-            const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
-            acc[e & 3] = f2_add(acc[e & 3], f2_pack(p0, p1));
-            r[e] = pack_bf16x2(p0, p1);
+              for (int e = 0; e < LS / 4; ++e)
+                d[e] = make_float4(x[4 * e] * p.scale_log2, x[4 * e + 1] * p.scale_log2, x[4 * e + 2] * p.scale_log2,
+                                   x[4 * e + 3] * p.scale_log2);
+            }
           }
-          tc05::st32(tS + hb * 32, r);
-        }
-        float u0, u1;
-        f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), u0, u1);
-        l_run += u0 + u1;
-        tc05::wait_st();
-        // A tile with keys that some rows see and others do not: a weight of 0 would carry an infinite or
-        // NaN value row to the latter, so if V holds any, the threads add up the seen keys themselves.
-        if (blind < min(R.n, (j + 1) * LN)) {
-          const uint32_t iv = 2 * (g + jj) + 1;
-          if (!landed(iv)) {
-            ok = false;
-            break;
+          float mx = -INFINITY, my = -INFINITY, mz = -INFINITY, mw = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < LS; e += 8) {
+            mx = max3f(mx, x[e], x[e + 1]);
+            my = max3f(my, x[e + 2], x[e + 3]);
+            mz = max3f(mz, x[e + 4], x[e + 5]);
+            mw = max3f(mw, x[e + 6], x[e + 7]);
           }
-          const uint8_t* sV = smem + C::OFF_T + (iv % NST) * C::T_BYTES;
-          bool bad = false;
-#pragma unroll 1
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = *reinterpret_cast<const uint4*>(sV + (c >> 3) * (LN * 128) + rt * 128 + (((c ^ rt) & 7) << 4));
-            bad |= nonfinite_bf16x2(v.x) || nonfinite_bf16x2(v.y) || nonfinite_bf16x2(v.z) || nonfinite_bf16x2(v.w);
-          }
-          if (bad) s_odd[w] = t + 1;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&vbar[w]);
-          if (!lwait(&vbar[w], looked & 1, p.dev_status, s_abort)) {
-            ok = false;
-            break;
-          }
-          ++looked;
-          if (s_odd[w] == t + 1) {
+          const float m_new = fmaxf(m_run, fmaxf(fmaxf(mx, my), fmaxf(mz, mw)) * p.scale_log2);
+          // O is rescaled only when the running maximum grew by more than 2^8, after the P V before. TMEM
+          // loads and stores are warp-collective: the warp rescales together
+          const bool need = !fresh && m_new > m_run + 8.f;
+          if (fresh) {
+            m_run = m_new;
+          } else if (__any_sync(0xffffffffu, need)) {
+            if (!pv_done(t - 1)) {
+              ok = false;
+              break;
+            }
+            tc05::fence_after();
+            float f = 1.f;
+            if (need) {
+              f = ex2_approx(m_run - m_new);
+              l_run *= f;
+              m_run = m_new;
+            }
 #pragma unroll 1
             for (int cb = 0; cb < D / 32; ++cb) {
               uint32_t r[32];
-              if (jj > first) {
-                tc05::ld32(tO + cb * 32, r);
-                tc05::wait_ld();
-              } else {
+              tc05::ld32(tO + cb * 32, r);
+              tc05::wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) r[e] = 0u;
-              }
-#pragma unroll 1
-              for (int k8 = 0; k8 < LN / 16; ++k8) {
-                uint32_t pw[8];
-                tc05::ld8(tS + k8 * 8, pw);
-                tc05::wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const int k = k8 * 16 + e;
-                  const float pk = __uint_as_float(e & 1 ? pw[e >> 1] & 0xffff0000u : pw[e >> 1] << 16);
-#pragma unroll
-                  for (int c = 0; c < 4; ++c) {
-                    const int ch = cb * 4 + c;
-                    const uint4 v = *reinterpret_cast<const uint4*>(sV + (ch >> 3) * (LN * 128) + k * 128 + (((ch ^ k) & 7) << 4));
-                    const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int h = 0; h < 8; ++h) {
-                      const float val = __uint_as_float(h & 1 ? vw[h >> 1] & 0xffff0000u : vw[h >> 1] << 16);
-                      const float a = __uint_as_float(r[c * 8 + h]);
-                      r[c * 8 + h] = __float_as_uint(k <= last ? fmaf(pk, val, a) : a);
-                    }
-                  }
-                }
-              }
+              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
               tc05::st32(tO + cb * 32, r);
             }
             tc05::wait_st();
           }
+          // P = 2^(x scale - m), bf16, over S
+          const float mu = m_run == -INFINITY ? 0.f : m_run;
+          const uint64_t sc = f2_pack(p.scale_log2, p.scale_log2), nm = f2_pack(-mu, -mu);
+          uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+          {
+            uint32_t r[LS / 2];
+#pragma unroll
+            for (int e = 0; e < LS / 2; ++e) {
+              float a0, a1;
+              f2_unpack(f2_fma(f2_pack(x[2 * e], x[2 * e + 1]), sc, nm), a0, a1);
+              const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+              acc[e & 3] = f2_add(acc[e & 3], f2_pack(p0, p1));
+              r[e] = pack_bf16x2(p0, p1);
+            }
+            tc05::st32(tP, r);
+          }
+          float u0, u1;
+          f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), u0, u1);
+          l_run += u0 + u1;
+          tc05::wait_st();
+          // A step with keys that some rows see and others do not: a weight of 0 would carry an infinite or
+          // NaN value row to the latter, so if V holds any, the threads add up the seen keys themselves.
+          if (blind < min(R.n, k0 + LS)) {
+            const uint32_t iv = 2 * (g + jj) + 1;
+            if (!landed(iv, seen)) {
+              ok = false;
+              break;
+            }
+            const uint8_t* sV = smem + C::OFF_T + (iv % NST) * C::T_BYTES;
+            bool bad = false;
+            if (rt < LS) {
+              const int k = h * LS + rt;
+#pragma unroll 1
+              for (int c = 0; c < D / 8; ++c) {
+                const uint4 v = *reinterpret_cast<const uint4*>(sV + (c >> 3) * (LN * 128) + k * 128 + (((c ^ k) & 7) << 4));
+                bad |= nonfinite_bf16x2(v.x) || nonfinite_bf16x2(v.y) || nonfinite_bf16x2(v.z) || nonfinite_bf16x2(v.w);
+              }
+            }
+            if (bad) s_odd[w] = t + 1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&vbar[w]);
+            if (!lwait(&vbar[w], looked & 1, p.dev_status, s_abort)) {
+              ok = false;
+              break;
+            }
+            ++looked;
+            if (s_odd[w] == t + 1) {
+              if (!fresh && !pv_done(t - 1)) {
+                ok = false;
+                break;
+              }
+              tc05::fence_after();
+#pragma unroll 1
+              for (int cb = 0; cb < D / 32; ++cb) {
+                uint32_t r[32];
+                if (!fresh) {
+                  tc05::ld32(tO + cb * 32, r);
+                  tc05::wait_ld();
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) r[e] = 0u;
+                }
+#pragma unroll 1
+                for (int k8 = 0; k8 < LS / 16; ++k8) {
+                  uint32_t pw[8];
+                  tc05::ld8(tP + k8 * 8, pw);
+                  tc05::wait_ld();
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) {
+                    const int k = k8 * 16 + e, kt = h * LS + k;
+                    const float pk = __uint_as_float(e & 1 ? pw[e >> 1] & 0xffff0000u : pw[e >> 1] << 16);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                      const int ch = cb * 4 + c;
+                      const uint4 v = *reinterpret_cast<const uint4*>(sV + (ch >> 3) * (LN * 128) + kt * 128 + (((ch ^ kt) & 7) << 4));
+                      const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                      for (int i = 0; i < 8; ++i) {
+                        const float val = __uint_as_float(i & 1 ? vw[i >> 1] & 0xffff0000u : vw[i >> 1] << 16);
+                        const float a = __uint_as_float(r[c * 8 + i]);
+                        r[c * 8 + i] = __float_as_uint(k <= last ? fmaf(pk, val, a) : a);
+                      }
+                    }
+                  }
+                }
+                tc05::st32(tO + cb * 32, r);
+              }
+              tc05::wait_st();
+            }
+          }
+          tc05::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pfull[2 * w + (t & 1)]);
         }
-        tc05::fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[w]);
       }
       if (!ok) break;
       // the chain's partial of the piece, after its last P V
-      if (!lwait(&ofull[w], (t - 1) & 1, p.dev_status, s_abort)) {
+      if (!pv_done(t - 1)) {
         ok = false;
         break;
       }
@@ -506,7 +567,7 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
   tc05::fence_before();
   __syncthreads();
   tc05::fence_after();
-  if (warp == 10) tc05::dealloc(tmem, C::TCOLS);
+  if (warp == 12) tc05::dealloc(tmem, C::TCOLS);
 }
 
 // Where a row of group g (KV head hk, row r of the head) left its partials: `count` of them, number i
