@@ -6,7 +6,7 @@
 // the keep-th row and how many rows of rank T stay; one ordered pass then numbers the rows: a row below
 // `keep` that goes is hole i - kept(i), a row behind it that stays is move kept(i) - (keep - moves),
 // with kept(i) the kept rows before row i. There are as many holes as moves, and move j goes into hole j.
-// Scores and positions are read once: each thread keeps its rows' ranks in registers.
+// Scores and positions are read once: the ranks are held in shared memory.
 //
 // Move: only the rows behind the budget that stay are read and written (K, V, score, position). A warp
 // takes consecutive moves: their plan, scores and positions lane by lane (neighbours in memory), then
@@ -17,10 +17,10 @@ namespace vc {
 
 constexpr int kEvThreads = 1024;
 constexpr int kEvWarps = kEvThreads / 32;
-constexpr int kEvKeys = 16;  // ranks a thread holds
-constexpr int kEvSlice = kEvThreads * kEvKeys;
-constexpr int kEvCluster = 8;
+constexpr int kEvHeld = 40 * 1024;  // ranks a CTA holds at most (160 KB)
 constexpr int kEvBins = 2048;
+constexpr int kEvCopies = 2;
+constexpr int kEvCoarse = kEvBins / 32;  // sums of 32 consecutive bins
 
 __device__ __forceinline__ uint32_t evict_rank(float s, int pos, int sink, int recent_from) {
   if (pos < sink || pos >= recent_from) return 0xffffffffu;
@@ -49,22 +49,27 @@ __device__ __forceinline__ uint32_t ev_ld_cluster(const void* p, uint32_t rank) 
 }
 
 // CL CTAs (a cluster) per (KV head, request), each with a consecutive slice of the rows, each warp with a
-// consecutive segment of the slice. HELD: a warp's segment is at most 32 kEvKeys rows and its ranks stay
-// in registers; otherwise they are taken from memory again in every pass.
+// consecutive segment of the slice. HELD: the slice's ranks stay in shared memory; otherwise (more than
+// kEvHeld rows a CTA) they are taken from memory again in every pass.
+// The histograms' counters exist kEvCopies times, a lane using one of them, so that lanes with the same
+// digit wait for each other less: scores share few exponents (16384 rows: 18.7 -> 7 thousand clocks).
 template <int CL, bool HELD>
-__global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ uint32_t hist[2][kEvBins];  // this CTA's histogram, double-buffered by pass
-  __shared__ uint32_t s_warp[kEvWarps];
+__global__ void __launch_bounds__(kEvThreads, 2) evict_select_kernel(const __grid_constant__ EvictParams p) {
+  extern __shared__ uint32_t held[];  // [seg * kEvWarps] ranks
+  __shared__ uint32_t count[kEvBins * kEvCopies];
+  __shared__ uint32_t fine[2][kEvBins], coarse[2][kEvCoarse];  // by pass: the cluster may still read the last one's
   __shared__ uint32_t s_prefix, s_rem;
   __shared__ int s_cnt[2][kEvWarps];
   __shared__ int s_cta[2];  // this CTA's rows above T and equal to T
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < kEvBins * kEvCopies; i += kEvThreads) count[i] = 0;
+  if (tid == 0) s_prefix = 0;
   pdl_wait();
   pdl_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = CL > 1 ? ev_cluster_rank() : 0u;
   const int h = blockIdx.x / CL;
   const EvictReqDev& r = p.req[blockIdx.y];
-  const int n = r.n, keep = r.keep;
+  const int n = r.n, keep = r.keep, sink = r.sink, recent_from = r.recent_from, room = r.room;
   const float* score = r.score + (size_t)h * r.cap;
   const int32_t* pos = r.pos + (size_t)h * r.cap;
   int32_t* plan = r.plan + (size_t)h * r.plan_stride;
@@ -72,87 +77,107 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   const int s0 = min((int64_t)n, (int64_t)rank * per), s1 = min((int64_t)n, (int64_t)s0 + per);
   const int seg = ((s1 - s0 + 31) / 32 + kEvWarps - 1) / kEvWarps * 32;  // rows of a warp
   const int w0 = min(s1, s0 + warp * seg), w1 = min(s1, w0 + seg);
-  auto load = [&](int i) { return i < w1 ? evict_rank(__ldg(score + i), __ldg(pos + i), r.sink, r.recent_from) : 0u; };
-  uint32_t key[kEvKeys];
-  if (HELD) {
-#pragma unroll
-    for (int k = 0; k < kEvKeys; ++k) key[k] = load(w0 + 32 * k + lane);
-  }
-  // f(row, rank) for the warp's rows, 32 at a time (the last may be beyond w1)
-  auto each = [&](auto f) {
-    if (HELD) {
-#pragma unroll
-      for (int k = 0; k < kEvKeys; ++k)
-        if (w0 + 32 * k < w1) f(w0 + 32 * k + lane, key[k]);
-    } else {
-      for (int base = w0; base < w1; base += 32) f(base + lane, load(base + lane));
-    }
+  uint32_t* mine = held + warp * seg;
+  auto load = [&](int i) { return i < w1 ? evict_rank(__ldg(score + i), __ldg(pos + i), sink, recent_from) : 0u; };
+  auto rank_of = [&](int i) { return HELD ? mine[i - w0] : load(i); };
+  // one more row of digit dg in lanes with `in`: the lanes of the warp's commonest case, one digit for most
+  // of them (guarded rows, rows without any weight), are added up before they reach the counters
+  auto tally = [&](bool in, uint32_t dg) {
+    const unsigned act = __ballot_sync(0xffffffffu, in);
+    if (!act) return;
+    const int lead = __ffs(act) - 1;
+    const uint32_t lead_dg = __shfl_sync(0xffffffffu, dg, lead);
+    const unsigned same = __ballot_sync(0xffffffffu, in && dg == lead_dg);
+    if (lane == lead)
+      atomicAdd(&count[dg * kEvCopies], (uint32_t)__popc(same));
+    else if (in && !((same >> lane) & 1u))
+      atomicAdd(&count[dg * kEvCopies + lane % kEvCopies], 1u);
   };
-  if (tid == 0) {
-    s_prefix = 0;
-    s_rem = (uint32_t)keep;
-  }
+  if (tid == 0) s_rem = (uint32_t)keep;
+  __syncthreads();
   uint32_t mask = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t digit = pass == 2 ? 1023u : 2047u;
-    uint32_t* hs = hist[pass & 1];  // last read by the cluster before the previous cluster barrier
-    for (int i = tid; i < kEvBins; i += kEvThreads) hs[i] = 0;
-    __syncthreads();
     const uint32_t prefix = s_prefix;
-    each([&](int i, uint32_t u) {
-      // rows of the warp's commonest case, one digit for most lanes (guarded rows, rows without any
-      // weight, one exponent), are added up before they reach the histogram
-      const bool in = i < w1 && (u & mask) == prefix;
-      const uint32_t dg = (u >> shift) & digit;
-      const unsigned act = __ballot_sync(0xffffffffu, in);
-      if (!act) return;
-      const int lead = __ffs(act) - 1;
-      const uint32_t lead_dg = __shfl_sync(0xffffffffu, dg, lead);
-      const unsigned same = __ballot_sync(0xffffffffu, in && dg == lead_dg);
-      if (lane == lead)
-        atomicAdd(&hs[dg], (uint32_t)__popc(same));
-      else if (in && !((same >> lane) & 1u))
-        atomicAdd(&hs[dg], 1u);
-    });
+    if (pass == 0) {
+#pragma unroll 1
+      for (int base = w0; base < w1; base += 32 * 4) {  // loads of four groups of 32 rows in flight
+        uint32_t u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u[k] = load(base + 32 * k + lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = base + 32 * k + lane;
+          if (HELD && i < w1) mine[i - w0] = u[k];
+          tally(i < w1, u[k] >> shift);
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int base = w0; base < w1; base += 32 * 2) {
+        uint32_t u[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) u[k] = base + 32 * k + lane < w1 ? rank_of(base + 32 * k + lane) : 0u;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) tally(base + 32 * k + lane < w1 && (u[k] & mask) == prefix, (u[k] >> shift) & digit);
+      }
+    }
+    __syncthreads();
+    // the copies' sums and those of 32 bins each: only the latter, and then the 32 bins of one of them, are
+    // added up over the cluster (reading all bins of all CTAs kept the cluster's network busy for longer
+    // than everything else)
+    for (int c = warp; c < kEvCoarse; c += kEvWarps) {
+      uint32_t v = 0;
+#pragma unroll
+      for (int k = 0; k < kEvCopies; ++k) {
+        v += count[(32 * c + lane) * kEvCopies + k];
+        count[(32 * c + lane) * kEvCopies + k] = 0;  // for the next pass
+      }
+      fine[pass & 1][32 * c + lane] = v;
+      v = __reduce_add_sync(0xffffffffu, v);
+      if (lane == 0) coarse[pass & 1][c] = v;
+    }
     if (CL > 1)
       ev_cluster_sync();
     else
       __syncthreads();
-    // thread t owns the bins 2t', 2t'+1 from the top: counts of larger digits come from the threads before
-    const int b1 = kEvBins - 1 - 2 * tid, b0 = b1 - 1;
-    uint32_t c1 = 0, c0 = 0;
-    if (CL > 1) {
+    if (warp == 0) {
+      auto total = [&](const uint32_t* word) {
+        if constexpr (CL == 1) return *word;
+        uint32_t v = 0;
 #pragma unroll
-      for (int q = 0; q < CL; ++q) {
-        c1 += ev_ld_cluster(&hs[b1], q);
-        c0 += ev_ld_cluster(&hs[b0], q);
+        for (int q = 0; q < CL; ++q) v += ev_ld_cluster(word, q);
+        return v;
+      };
+      // of a row of counts (lane 0 the largest digit) the lane in which the rem-th row stands, -1: behind
+      // them; rem becomes its number among that lane's
+      auto find = [&](uint32_t cnt, uint32_t& rem) -> int {
+        uint32_t sum = cnt;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const uint32_t o = __shfl_up_sync(0xffffffffu, sum, off);
+          if (lane >= off) sum += o;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, sum >= rem);
+        if (!hit) {
+          rem -= __shfl_sync(0xffffffffu, sum, 31);
+          return -1;
+        }
+        const int at = __ffs(hit) - 1;
+        rem -= __shfl_sync(0xffffffffu, sum - cnt, at);
+        return at;
+      };
+      uint32_t rem = s_rem;
+      const uint32_t hi = total(&coarse[pass & 1][kEvCoarse - 1 - lane]), lo = total(&coarse[pass & 1][31 - lane]);
+      int c = find(hi, rem);
+      c = c >= 0 ? kEvCoarse - 1 - c : 31 - max(0, find(lo, rem));
+      const int at = max(0, find(total(&fine[pass & 1][32 * c + 31 - lane]), rem));
+      if (lane == 0) {
+        s_rem = rem;
+        s_prefix = prefix | ((uint32_t)(32 * c + 31 - at) << shift);
       }
-    } else {
-      c1 = hs[b1];
-      c0 = hs[b0];
-    }
-    uint32_t sum = c1 + c0;  // inclusive prefix over the warp's threads
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t o = __shfl_up_sync(0xffffffffu, sum, off);
-      if (lane >= off) sum += o;
-    }
-    if (lane == 31) s_warp[warp] = sum;
-    const uint32_t rem = s_rem;
-    __syncthreads();
-    uint32_t before = lane < warp ? s_warp[lane] : 0u;  // warps before this one
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
-    const uint32_t cum1 = before + sum - c1 - c0, cum0 = cum1 + c1;  // larger digits than b1, than b0
-    if (cum1 < rem && cum1 + c1 >= rem) {  // exactly one digit satisfies this
-      s_rem = rem - cum1;
-      s_prefix = prefix | ((uint32_t)b1 << shift);
-    }
-    if (cum0 < rem && cum0 + c0 >= rem) {
-      s_rem = rem - cum0;
-      s_prefix = prefix | ((uint32_t)b0 << shift);
     }
     mask |= digit << shift;
     __syncthreads();
@@ -160,28 +185,24 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   const uint32_t T = s_prefix;
   const int need_eq = (int)s_rem;
   int gt = 0, eq = 0;
-  each([&](int i, uint32_t u) {
-    gt += __popc(__ballot_sync(0xffffffffu, i < w1 && u > T));
-    eq += __popc(__ballot_sync(0xffffffffu, i < w1 && u == T));
-  });
+#pragma unroll 4
+  for (int i = w0 + lane; i < w1; i += 32) {
+    const uint32_t u = rank_of(i);
+    gt += u > T;
+    eq += u == T;
+  }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
     s_cnt[0][warp] = gt;
     s_cnt[1][warp] = eq;
   }
   __syncthreads();
   // rows above and equal to T in the warps (and, through the cluster, the CTAs) before this one
-  int gt_run = lane < kEvWarps ? s_cnt[0][lane] : 0, eq_run = lane < kEvWarps ? s_cnt[1][lane] : 0;
-  int gt_all = gt_run, eq_all = eq_run;
-  gt_run = lane < warp ? gt_run : 0;
-  eq_run = lane < warp ? eq_run : 0;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    gt_run += __shfl_xor_sync(0xffffffffu, gt_run, off);
-    eq_run += __shfl_xor_sync(0xffffffffu, eq_run, off);
-    gt_all += __shfl_xor_sync(0xffffffffu, gt_all, off);
-    eq_all += __shfl_xor_sync(0xffffffffu, eq_all, off);
-  }
+  const int gw = s_cnt[0][lane], ew = s_cnt[1][lane];
+  int gt_run = __reduce_add_sync(0xffffffffu, lane < warp ? gw : 0), eq_run = __reduce_add_sync(0xffffffffu, lane < warp ? ew : 0);
   if constexpr (CL > 1) {
+    const int gt_all = __reduce_add_sync(0xffffffffu, gw), eq_all = __reduce_add_sync(0xffffffffu, ew);
     if (tid == 0) {
       s_cta[0] = gt_all;
       s_cta[1] = eq_all;
@@ -193,22 +214,25 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
     }
   }
   const unsigned lt = (1u << lane) - 1u;
-  each([&](int i, uint32_t u) {
+#pragma unroll 2
+  for (int base = w0; base < w1; base += 32) {
+    const int i = base + lane;
+    const uint32_t u = i < w1 ? rank_of(i) : 0u;
     const unsigned mg = __ballot_sync(0xffffffffu, i < w1 && u > T), me = __ballot_sync(0xffffffffu, i < w1 && u == T);
     if (i < w1) {
       const int eq_before = eq_run + __popc(me & lt);
       const int kept = gt_run + __popc(mg & lt) + min(eq_before, need_eq);  // kept rows before row i
       const bool stays = u > T || (u == T && eq_before < need_eq);
       if (i < keep) {
-        if (!stays && i - kept < r.room) plan[4 + i - kept] = i;
+        if (!stays && i - kept < room) plan[4 + i - kept] = i;
         if (i == keep - 1) plan[0] = keep - kept - (stays ? 1 : 0);
-      } else if (stays && keep - 1 - kept < r.room) {
-        plan[4 + r.room + keep - 1 - kept] = i;  // from the last move backwards
+      } else if (stays && keep - 1 - kept < room) {
+        plan[4 + room + keep - 1 - kept] = i;  // from the last move backwards
       }
     }
     gt_run += __popc(mg);
     eq_run += __popc(me);
-  });
+  }
   if (CL > 1) ev_cluster_sync();  // no CTA leaves while another may still read its shared memory
 }
 
@@ -265,10 +289,18 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__
 }
 
 template <int CL, bool HELD>
-static cudaError_t launch_select(const EvictParams& p, cudaStream_t s) {
+static cudaError_t launch_select(const EvictParams& p, int n, cudaStream_t s) {
+  const int per = (n + CL - 1) / CL;  // the largest slice; a warp's part is a multiple of 32 rows
+  const int smem = HELD ? ((per + 31) / 32 + kEvWarps - 1) / kEvWarps * 32 * kEvWarps * 4 : 0;
+  static std::atomic<uint64_t> attr_set{0};
+  if (HELD) {
+    const cudaError_t e = raise_smem_limit(evict_select_kernel<CL, HELD>, kEvHeld * 4, attr_set);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.Hkv * CL, p.B);
   cfg.blockDim = dim3(kEvThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -288,12 +320,19 @@ cudaError_t launch_evict(const EvictParams& p, int d, cudaStream_t s) {
     n = p.req[b].n > n ? p.req[b].n : n;
     room = p.req[b].room > room ? p.req[b].room : room;
   }
-  cudaError_t e = n <= kEvSlice                ? launch_select<1, true>(p, s)
-                  : n <= kEvSlice * kEvCluster ? launch_select<kEvCluster, true>(p, s)
-                                               : launch_select<kEvCluster, false>(p, s);
+  // CTAs per head: as many as one wave holds (two CTAs an SM), with at least 1024 rows each (below that the
+  // passes' fixed part, about 8 us, is all that is left), and enough to hold the ranks
+  const int64_t all = (int64_t)p.Hkv * p.B;
+  int cl = 1;
+  while (cl < 8 && (n > cl * kEvHeld || (all * cl * 2 <= 304 && n >= cl * 2 * 1024))) cl *= 2;
+  cudaError_t e = n > 8 * kEvHeld ? launch_select<8, false>(p, n, s)
+                  : cl == 8       ? launch_select<8, true>(p, n, s)
+                  : cl == 4       ? launch_select<4, true>(p, n, s)
+                  : cl == 2       ? launch_select<2, true>(p, n, s)
+                                  : launch_select<1, true>(p, n, s);
   if (e != cudaSuccess) return e;
   // enough warps to fill the GPU before each takes more moves at a time, up to a lane each
-  const int64_t heads = (int64_t)p.Hkv * p.B, warps = 152 * 64;
+  const int64_t heads = all, warps = 152 * 64;
   int64_t per = (room * heads + warps - 1) / warps;
   per = per < 4 ? 4 : per > 32 ? 32 : per;
   const int64_t want = (room + 8 * per - 1) / (8 * per), wave = (warps / 8 + heads - 1) / heads;

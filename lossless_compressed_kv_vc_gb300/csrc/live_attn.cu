@@ -406,21 +406,36 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
                                    x[4 * e + 3] * p.scale_log2);
             }
           }
-          float mx = -INFINITY, my = -INFINITY, mz = -INFINITY, mw = -INFINITY;
+          // P = 2^(x scale - m), bf16, over S, with the running maximum as it is: the row's new one is found
+          // alongside, and only when it is larger by more than 2^8 (or this is the piece's first step) is m
+          // moved, O rescaled after the P V before, and P computed again. TMEM loads and stores are
+          // warp-collective: the warp does it together.
+          uint32_t r[LS / 2];
+          float u0, u1, mx = -INFINITY, my = -INFINITY, mz = -INFINITY, mw = -INFINITY;
+#pragma unroll 1
+          for (int again = 0; again < 2; ++again) {
+            const float mu = m_run == -INFINITY ? 0.f : m_run;
+            const uint64_t sc = f2_pack(p.scale_log2, p.scale_log2), nm = f2_pack(-mu, -mu);
+            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-          for (int e = 0; e < LS; e += 8) {
-            mx = max3f(mx, x[e], x[e + 1]);
-            my = max3f(my, x[e + 2], x[e + 3]);
-            mz = max3f(mz, x[e + 4], x[e + 5]);
-            mw = max3f(mw, x[e + 6], x[e + 7]);
-          }
-          const float m_new = fmaxf(m_run, fmaxf(fmaxf(mx, my), fmaxf(mz, mw)) * p.scale_log2);
-          // O is rescaled only when the running maximum grew by more than 2^8, after the P V before. TMEM
-          // loads and stores are warp-collective: the warp rescales together
-          const bool need = !fresh && m_new > m_run + 8.f;
-          if (fresh) {
-            m_run = m_new;
-          } else if (__any_sync(0xffffffffu, need)) {
+            for (int e = 0; e < LS / 2; ++e) {
+              float a0, a1;
+              f2_unpack(f2_fma(f2_pack(x[2 * e], x[2 * e + 1]), sc, nm), a0, a1);
+              const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+              acc[e & 3] = f2_add(acc[e & 3], f2_pack(p0, p1));
+              r[e] = pack_bf16x2(p0, p1);
+              float& m = (e & 3) == 0 ? mx : (e & 3) == 1 ? my : (e & 3) == 2 ? mz : mw;
+              m = max3f(m, x[2 * e], x[2 * e + 1]);
+            }
+            f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), u0, u1);
+            if (again) break;
+            const float m_new = fmaxf(m_run, fmaxf(fmaxf(mx, my), fmaxf(mz, mw)) * p.scale_log2);
+            const bool need = m_new > m_run + 8.f;  // from -infinity, any finite score
+            if (!__any_sync(0xffffffffu, need)) break;
+            if (fresh) {
+              m_run = m_new;
+              continue;
+            }
             if (!pv_done(t - 1)) {
               ok = false;
               break;
@@ -434,33 +449,16 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
             }
 #pragma unroll 1
             for (int cb = 0; cb < D / 32; ++cb) {
-              uint32_t r[32];
-              tc05::ld32(tO + cb * 32, r);
+              uint32_t o[32];
+              tc05::ld32(tO + cb * 32, o);
               tc05::wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-              tc05::st32(tO + cb * 32, r);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tc05::st32(tO + cb * 32, o);
             }
-            tc05::wait_st();
           }
-          // P = 2^(x scale - m), bf16, over S
-          const float mu = m_run == -INFINITY ? 0.f : m_run;
-          const uint64_t sc = f2_pack(p.scale_log2, p.scale_log2), nm = f2_pack(-mu, -mu);
-          uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-          {
-            uint32_t r[LS / 2];
-#pragma unroll
-            for (int e = 0; e < LS / 2; ++e) {
-              float a0, a1;
-              f2_unpack(f2_fma(f2_pack(x[2 * e], x[2 * e + 1]), sc, nm), a0, a1);
-              const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
-              acc[e & 3] = f2_add(acc[e & 3], f2_pack(p0, p1));
-              r[e] = pack_bf16x2(p0, p1);
-            }
-            tc05::st32(tP, r);
-          }
-          float u0, u1;
-          f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), u0, u1);
+          if (!ok) break;
+          tc05::st32(tP, r);
           l_run += u0 + u1;
           tc05::wait_st();
           // A step with keys that some rows see and others do not: a weight of 0 would carry an infinite or
@@ -570,86 +568,106 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
   if (warp == 12) tc05::dealloc(tmem, C::TCOLS);
 }
 
-// Where a row of group g (KV head hk, row r of the head) left its partials: `count` of them, number i
-// at index at(i) of the kind's partial rows.
+// Where a row of a group (KV head hk, row r of the head) left its partials: `count` of them, number i at
+// index at(i) of the kind's partial rows. A split unit has two a slot.
 struct LParts {
-  int kind, c0, count, stride, sub;  // sub: partials a slot (2 in split units), stride: a slot's rows
   size_t base;
-  int second;
+  int count, stride, second;  // stride: a slot's rows; second: rows to the slot's second partial, 0: none
   __device__ __forceinline__ size_t at(int i) const {
-    return sub == 2 ? base + (size_t)(i >> 1) * stride + (i & 1) * second : base + (size_t)i * stride;
+    return second ? base + (size_t)(i >> 1) * stride + (i & 1) * second : base + (size_t)i * stride;
   }
 };
 
-__device__ __forceinline__ LParts live_parts(const LiveParams& p, int g, int hk, int r) {
-  const LiveGroup& R = p.grp[g];
+__device__ __forceinline__ LParts live_parts(const LiveParams& p, const LiveGroup& R, int stride, int hk, int r) {
   LParts q;
   const int u = r / LU, ul = hk * R.units + u, rows = min(LU, R.rows - u * LU);
   const int64_t U0 = R.tile_begin + (int64_t)ul * R.tiles, U1 = U0 + R.tiles, T = p.total, N = p.n_cta;
   const int c0 = (int)(((U0 + 1) * N - 1) / T), c1 = (int)((U1 * N - 1) / T);
-  q.kind = p.has_prefix && g == 0 ? 0 : 1;
-  q.c0 = c0;
-  q.sub = rows <= LM ? 2 : 1;
-  q.count = (c1 - c0 + 1) * q.sub;
-  q.stride = p.slot_rows[q.kind];
-  q.base = (size_t)(c0 + R.unit_begin + ul) * q.stride + (r - u * LU);
-  q.second = rows;
+  q.second = rows <= LM ? rows : 0;
+  q.count = (c1 - c0 + 1) * (q.second ? 2 : 1);
+  q.stride = stride;
+  q.base = (size_t)(c0 + R.unit_begin + ul) * stride + (r - u * LU);
   return q;
 }
 
 // Merge: a warp per (token, query head), o = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M) over the
-// partials of the prefix and of the own cache. Scores: a block per 1024 keys of a (request, KV head)
-// merges the head's rows' lse, then sums 2^(s - lse) over the rows for each key.
+// partials of the prefix and of the own cache: a lane per partial takes the weights, then the warp adds
+// up the partials' channels, eight loads in flight. Scores: a block per 1024 keys of a (request, KV head)
+// merges the head's rows' lse, a warp a row, then sums 2^(s - lse) over the rows for each key.
 template <int D, bool SCORED>
-__global__ void __launch_bounds__(256) live_finish_kernel(const __grid_constant__ LiveParams p) {
+__global__ void __launch_bounds__(256, 4) live_finish_kernel(const __grid_constant__ LiveParams p) {
   constexpr int E = D / 32;  // channels a lane
   __shared__ float s_lse[VC_SCORED_MAX_ROWS];
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto warp_max = [](float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+  };
+  auto warp_sum = [](float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+  };
+  // weight of a partial beside the largest lse M: 0 where it saw nothing; M stays -inf only beside a NaN
+  auto weight = [](float l, float M) { return l == -INFINITY ? 0.f : M == -INFINITY ? NAN : exp2f(l - M); };
   if ((int)blockIdx.x < p.merge_blocks) {
     const int64_t id = (int64_t)blockIdx.x * 8 + warp;
     if (id >= (int64_t)p.n_tok * p.Hq) return;
     const int tok = (int)(id / p.Hq), hq = (int)(id - (int64_t)tok * p.Hq), hk = hq / p.G, gq = hq - hk * p.G;
     const int b = live_req_of(p, tok), i = tok - p.tok_begin[b], own = p.own_of[b];
-    LParts part[2];
-    int n_part = 0;
-    if (p.has_prefix) part[n_part++] = live_parts(p, 0, hk, tok * p.G + gq);
-    if (own >= 0) part[n_part++] = live_parts(p, own, hk, i * p.G + gq);
+    LParts a{0, 0, 0, 0}, o{0, 0, 0, 0};  // of the prefix, of the own cache
+    if (p.has_prefix) a = live_parts(p, p.grp[0], p.slot_rows[0], hk, tok * p.G + gq);
+    if (own >= 0) o = live_parts(p, p.grp[own], p.slot_rows[1], hk, i * p.G + gq);
+    const int total = a.count + o.count;
+    auto lse_of = [&](int k) {
+      return k < a.count ? p.ws_lse[0][a.at(k)] : k < total ? p.ws_lse[1][o.at(k - a.count)] : -INFINITY;
+    };
     float M = -INFINITY;
-    for (int a = 0; a < n_part; ++a)
-      for (int k = lane; k < part[a].count; k += 32) M = fmaxf(M, p.ws_lse[part[a].kind][part[a].at(k)]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    for (int k0 = 0; k0 < total; k0 += 32) M = fmaxf(M, lse_of(k0 + lane));
+    M = warp_max(M);
     float L = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int a = 0; a < n_part; ++a)
-#pragma unroll 4
-      for (int k = 0; k < part[a].count; ++k) {
-        const size_t at = part[a].at(k);
-        const float l = p.ws_lse[part[a].kind][at];
-        if (l == -INFINITY) continue;  // saw nothing: its o was never written
-        const float f = M == -INFINITY ? NAN : exp2f(l - M);  // M stays -inf only beside a NaN
-        L += f;
-        const float* src = p.ws_o[part[a].kind] + at * D + lane * E;
-        float v[E];
-        if constexpr (E == 4)
-          *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
-        else
-          *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+    for (int k0 = 0; k0 < total; k0 += 32) {
+      const float l = lse_of(k0 + lane), f = weight(l, M);
+      const unsigned wrote = __ballot_sync(0xffffffffu, l != -INFINITY);
+      L += f;
+      const int cnt = min(32, total - k0);
+      for (int c0 = 0; c0 < cnt; c0 += 8) {
+        float v[8][E], fc[8];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(f, v[e], acc[e]);
+        for (int c = 0; c < 8; ++c) {
+          fc[c] = __shfl_sync(0xffffffffu, f, c0 + c);  // c0 + c < 32; nothing was written beyond cnt
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[c][e] = 0.f;
+          if ((wrote >> (c0 + c)) & 1u) {  // a partial that saw nothing was not written
+            const int k = k0 + c0 + c;
+            const float* src = (k < a.count ? p.ws_o[0] + a.at(k) * D : p.ws_o[1] + o.at(k - a.count) * D) + lane * E;
+            if constexpr (E == 4)
+              *reinterpret_cast<float4*>(v[c]) = __ldg(reinterpret_cast<const float4*>(src));
+            else
+              *reinterpret_cast<float2*>(v[c]) = __ldg(reinterpret_cast<const float2*>(src));
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(fc[c], v[c][e], acc[e]);
       }
+    }
+    L = warp_sum(L);
     const float inv = L != 0.f ? 1.f / L : 0.f;
     bf16* dst = p.o[b] + ((size_t)i * p.Hq + hq) * D + lane * E;
-    uint32_t o[E / 2];
+    uint32_t out[E / 2];
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) o[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    for (int e = 0; e < E / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
     if constexpr (E == 4)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+      *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
     else
-      *reinterpret_cast<uint32_t*>(dst) = o[0];
+      *reinterpret_cast<uint32_t*>(dst) = out[0];
     return;
   }
   if constexpr (SCORED) {
@@ -661,37 +679,48 @@ __global__ void __launch_bounds__(256) live_finish_kernel(const __grid_constant_
     const LiveGroup& R = p.grp[g];
     const int chunks = (R.n + SCORE_KEYS - 1) / SCORE_KEYS;
     const int hk = (id - R.chunk_begin) / chunks, k0 = (id - R.chunk_begin - hk * chunks) * SCORE_KEYS;
-    for (int r = threadIdx.x; r < R.rows; r += 256) {
-      const LParts q = live_parts(p, g, hk, r);
+    constexpr int KT = SCORE_KEYS / 256;  // a thread's keys, 256 apart
+    const size_t stride = (size_t)R.tiles * LN;
+    const float* s = R.s + (size_t)hk * R.rows * stride + k0 + threadIdx.x;
+    float* score = R.score + (size_t)hk * R.cap + k0 + threadIdx.x;
+    const int left = R.n - k0 - (int)threadIdx.x;
+    float w[KT], v[8][KT];
+    auto load8 = [&](int r0) {
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+#pragma unroll
+        for (int c = 0; c < KT; ++c) v[r][c] = r0 + r < R.rows && c * 256 < left ? __ldg(s + (r0 + r) * stride + c * 256) : 0.f;
+    };
+    load8(0);  // in flight while the rows' lse are merged
+#pragma unroll
+    for (int c = 0; c < KT; ++c) w[c] = c * 256 < left ? score[c * 256] : 0.f;
+    for (int r = warp; r < R.rows; r += 8) {
+      const LParts q = live_parts(p, R, p.slot_rows[1], hk, r);
       float M = -INFINITY, L = 0.f;
-      for (int k = 0; k < q.count; ++k) M = fmaxf(M, p.ws_lse[1][q.at(k)]);
-      for (int k = 0; k < q.count; ++k) {
-        const float l = p.ws_lse[1][q.at(k)];
-        if (l != -INFINITY) L += M == -INFINITY ? NAN : exp2f(l - M);
-      }
-      s_lse[r] = L != 0.f ? M + log2f(L) : INFINITY;  // a row that sees nothing has weights 2^-inf
+      for (int k = lane; k < q.count; k += 32) M = fmaxf(M, p.ws_lse[1][q.at(k)]);
+      M = warp_max(M);
+      for (int k = lane; k < q.count; k += 32) L += weight(p.ws_lse[1][q.at(k)], M);
+      L = warp_sum(L);
+      if (lane == 0) s_lse[r] = L != 0.f ? M + log2f(L) : INFINITY;  // a row that sees nothing has weights 2^-inf
     }
     __syncthreads();
-    const size_t stride = (size_t)R.tiles * LN;
-    const float* s = R.s + (size_t)hk * R.rows * stride;
-    float* score = R.score + (size_t)hk * R.cap;
-    float w[SCORE_KEYS / 256];
+    float sum[KT];
 #pragma unroll
-    for (int c = 0; c < SCORE_KEYS / 256; ++c) w[c] = 0.f;
-#pragma unroll 4
-    for (int r = 0; r < R.rows; ++r) {
-      const float lse = s_lse[r];
+    for (int c = 0; c < KT; ++c) sum[c] = 0.f;
+#pragma unroll 1
+    for (int r0 = 0; r0 < R.rows; r0 += 8) {
+      if (r0) load8(r0);
 #pragma unroll
-      for (int c = 0; c < SCORE_KEYS / 256; ++c) {
-        const int k = k0 + c * 256 + threadIdx.x;
-        if (k < R.n) w[c] += ex2_approx(s[r * stride + k] - lse);
-      }
+      for (int r = 0; r < 8; ++r)
+        if (r0 + r < R.rows) {
+          const float lse = s_lse[r0 + r];
+#pragma unroll
+          for (int c = 0; c < KT; ++c) sum[c] += ex2_approx(v[r][c] - lse);
+        }
     }
 #pragma unroll
-    for (int c = 0; c < SCORE_KEYS / 256; ++c) {
-      const int k = k0 + c * 256 + threadIdx.x;
-      if (k < R.n) score[k] += w[c];
-    }
+    for (int c = 0; c < KT; ++c)
+      if (c * 256 < left) score[c * 256] = w[c] + sum[c];
   }
 }
 

@@ -380,6 +380,18 @@ def test_evict_batch_and_long(vc):
     _evict_case(vc, 2, 128, [70001, 200, 40000], [20000, 300, 39999], sink=4, recent=500)
 
 
+@pytest.mark.parametrize("kind", ["random", "ties"])
+@pytest.mark.parametrize("n", [2047, 2048, 2100, 4095, 4096, 8191, 8192, 9000, 40960, 81920, 81921])
+def test_evict_at_the_edges_of_the_cluster_sizes(vc, n, kind):
+    _evict_case(vc, 1, 64, [n, 1500], [n - n // 3, 700], sink=3, recent=100, kind=kind, seed=n)
+
+
+def test_evict_more_rows_than_the_ranks_held(vc):
+    """Beyond 8 x 40960 rows the select kernel takes the ranks from memory again in every pass."""
+    _evict_case(vc, 1, 64, [327681, 1000], [200000, 999], sink=4, recent=700)
+    _evict_case(vc, 1, 64, [400000], [399990], kind="ties")
+
+
 # ---- together ----------------------------------------------------------------------------------------
 def _table(vc, d):
     return vc.vc_rope_init(vc.VC_ROPE_BANDS, d, vc.VC_ROPE_HALF, 500000.0, **ROPE["bands"])
