@@ -30,7 +30,12 @@ constexpr int LM = 128;         // query rows of a chain
 constexpr int LN = 128;         // keys per tile
 constexpr int LS = 64;          // keys per step: S and P of half a tile, double-buffered
 constexpr int LU = 2 * LM;      // query rows of a unit
-constexpr int LTHREADS = 416;   // warps 0-3, 4-7 softmax of chains 0 and 1; 8, 9 issue their S; 10, 11 their P V; 12 TMA
+// warps 0-3, 4-7 softmax of chains 0 and 1; 8, 9 issue their S; 10, 11 their P V; 12 TMA; 13-15 idle (they
+// make a warpgroup with it: registers are handed over by warpgroup)
+constexpr int LTHREADS = 512;
+// Registers a thread: launched with 128 (65536 / 512), then 168 in the softmax warpgroups and 80 in the others
+constexpr int LREG_SOFTMAX = 168, LREG_ISSUE = 80;
+static_assert(256 * (LREG_SOFTMAX + LREG_ISSUE) <= 65536, "no more than the block was launched with");
 constexpr int SCORE_KEYS = 1024;  // keys of a score block
 
 struct LiveGroup {
@@ -204,124 +209,128 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
     return lwait(&full[it % NST], (it / NST) & 1, p.dev_status, s_abort);
   };
 
-  if (warp == 12) {
-    // ---- TMA: tiles in order, K then V of each ---------------------------------------------------
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
-      for (int pos = beg; pos < end && ok;) {
-        const LPiece q = live_piece(p, pos, end);
-        for (int j = q.j0; j < q.j1 && ok; ++j)
-          for (int kv = 0; kv < 2; ++kv) {
-            const uint32_t st = it % NST;
-            if (it >= (uint32_t)NST && !lwait(&empty[st], (it / NST - 1) & 1, p.dev_status, s_abort)) {
-              ok = false;
-              break;
-            }
-            uint8_t* dst = smem + C::OFF_T + st * C::T_BYTES;
-            mbar_arrive_expect_tx(&full[st], C::T_BYTES);
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LREG_ISSUE));
+    if (warp == 12) {
+      // ---- TMA: tiles in order, K then V of each ---------------------------------------------------
+      if (lane == 0) {
+        uint32_t it = 0;
+        bool ok = true;
+        for (int pos = beg; pos < end && ok;) {
+          const LPiece q = live_piece(p, pos, end);
+          for (int j = q.j0; j < q.j1 && ok; ++j)
+            for (int kv = 0; kv < 2; ++kv) {
+              const uint32_t st = it % NST;
+              if (it >= (uint32_t)NST && !lwait(&empty[st], (it / NST - 1) & 1, p.dev_status, s_abort)) {
+                ok = false;
+                break;
+              }
+              uint8_t* dst = smem + C::OFF_T + st * C::T_BYTES;
+              mbar_arrive_expect_tx(&full[st], C::T_BYTES);
 #pragma unroll
-            for (int kb = 0; kb < C::KB; ++kb)
-              tc05::tma_load_3d(dst + kb * (LN * 128), &p.tm[q.g][kv], kb * 64, j * LN, q.hk, &full[st]);
-            __threadfence_block();
-            *s_issued = ++it;
-          }
-        pos += q.j1 - q.j0;
-      }
-      if (*s_abort)  // drain (bounded): a ring's worth of loads may still be landing
-        for (uint32_t i = it > (uint32_t)NST ? it - NST : 0; i < it; ++i)
-          mbar_wait_bounded(&full[i % NST], (i / NST) & 1, p.dev_status);
-    }
-  } else if (warp >= 10) {
-    // ---- P V issue of chain w: as soon as a step's P is there ---------------------------------------
-    if (lane == 0) {
-      const int w = warp - 10;
-      constexpr uint32_t IDESC_O = tc05::idesc_bf16(LM, D, true);
-      const uint32_t aT = smem_u32(smem + C::OFF_T), tS = tmem + 2 * w * LS, tO = tmem + C::OCOL + w * D;
-      uint32_t g = 0, t = 0, seen = 0;  // tiles of the CTA, steps of the chain
-      bool ok = true;
-      for (int pos = beg; pos < end && ok;) {
-        const LPiece q = live_piece(p, pos, end);
-        const int n = p.grp[q.g].n;
-        const int nt = q.j1 - q.j0, first = q.split ? w : 0, step = q.split ? 2 : 1;
-        pos += nt;
-        bool acc = false;
-        for (int jj = first; jj < nt && ok; jj += step) {
-          const uint32_t iv = 2 * (g + jj) + 1, sv = iv % NST, vaddr = aT + sv * C::T_BYTES;
-          const int hs = live_steps(n, q.j0 + jj);
-          for (int h = 0; h < hs; ++h, ++t) {
-            if ((h == 0 && !landed(iv, seen)) || !lwait(&pfull[2 * w + (t & 1)], (t >> 1) & 1, p.dev_status, s_abort)) {
-              ok = false;
-              break;
+              for (int kb = 0; kb < C::KB; ++kb)
+                tc05::tma_load_3d(dst + kb * (LN * 128), &p.tm[q.g][kv], kb * 64, j * LN, q.hk, &full[st]);
+              __threadfence_block();
+              *s_issued = ++it;
             }
-            tc05::fence_after();
-            if (s_odd[w] != t + 1) {
-              const uint32_t tP = tS + (t & 1) * LS, va = vaddr + h * (LS / 16) * 2048;
+          pos += q.j1 - q.j0;
+        }
+        if (*s_abort)  // drain (bounded): a ring's worth of loads may still be landing
+          for (uint32_t i = it > (uint32_t)NST ? it - NST : 0; i < it; ++i)
+            mbar_wait_bounded(&full[i % NST], (i / NST) & 1, p.dev_status);
+      }
+    } else if (warp == 10 || warp == 11) {
+      // ---- P V issue of chain w: as soon as a step's P is there ---------------------------------------
+      if (lane == 0) {
+        const int w = warp - 10;
+        constexpr uint32_t IDESC_O = tc05::idesc_bf16(LM, D, true);
+        const uint32_t aT = smem_u32(smem + C::OFF_T), tS = tmem + 2 * w * LS, tO = tmem + C::OCOL + w * D;
+        uint32_t g = 0, t = 0, seen = 0;  // tiles of the CTA, steps of the chain
+        bool ok = true;
+        for (int pos = beg; pos < end && ok;) {
+          const LPiece q = live_piece(p, pos, end);
+          const int n = p.grp[q.g].n;
+          const int nt = q.j1 - q.j0, first = q.split ? w : 0, step = q.split ? 2 : 1;
+          pos += nt;
+          bool acc = false;
+          for (int jj = first; jj < nt && ok; jj += step) {
+            const uint32_t iv = 2 * (g + jj) + 1, sv = iv % NST, vaddr = aT + sv * C::T_BYTES;
+            const int hs = live_steps(n, q.j0 + jj);
+            for (int h = 0; h < hs; ++h, ++t) {
+              if ((h == 0 && !landed(iv, seen)) || !lwait(&pfull[2 * w + (t & 1)], (t >> 1) & 1, p.dev_status, s_abort)) {
+                ok = false;
+                break;
+              }
+              tc05::fence_after();
+              if (s_odd[w] != t + 1) {
+                const uint32_t tP = tS + (t & 1) * LS, va = vaddr + h * (LS / 16) * 2048;
 #pragma unroll
-              for (int kk = 0; kk < LS / 16; ++kk)
-                tc05::mma_ts(tO, tP + kk * 8, tc05::sdesc_sw128(va + kk * 2048, LN * 128, 1024), IDESC_O,
-                             (acc || kk > 0) ? 1u : 0u);
+                for (int kk = 0; kk < LS / 16; ++kk)
+                  tc05::mma_ts(tO, tP + kk * 8, tc05::sdesc_sw128(va + kk * 2048, LN * 128, 1024), IDESC_O,
+                               (acc || kk > 0) ? 1u : 0u);
+              }
+              tc05::commit(&ofull[2 * w + (t & 1)]);
+              acc = true;
             }
-            tc05::commit(&ofull[2 * w + (t & 1)]);
-            acc = true;
+            if (!ok) break;
+            tc05::commit(&empty[sv]);
+            if (q.split) tc05::commit(&empty[sv]);  // the other chain leaves this tile alone
           }
-          if (!ok) break;
-          tc05::commit(&empty[sv]);
-          if (q.split) tc05::commit(&empty[sv]);  // the other chain leaves this tile alone
+          g += nt;
         }
-        g += nt;
+        // every MMA issued so far has completed before TMEM is released (bounded, even after an abort)
+        tc05::commit(&xbar[2 + w]);
+        mbar_wait_bounded(&xbar[2 + w], 0, p.dev_status);
       }
-      // every MMA issued so far has completed before TMEM is released (bounded, even after an abort)
-      tc05::commit(&xbar[2 + w]);
-      mbar_wait_bounded(&xbar[2 + w], 0, p.dev_status);
-    }
-  } else if (warp >= 8) {
-    // ---- S issue of chain w: a step ahead of its softmax --------------------------------------------
-    if (lane == 0) {
-      const int w = warp - 8;
-      constexpr uint32_t IDESC_S = tc05::idesc_bf16(LM, LS, false);
-      const uint32_t aQ = smem_u32(smem) + w * C::T_BYTES, aT = smem_u32(smem + C::OFF_T);
-      const uint32_t tS = tmem + 2 * w * LS;
-      uint32_t g = 0, t = 0, u = 0, seen = 0;  // tiles of the CTA, steps and pieces of the chain
-      bool ok = true;
-      for (int pos = beg; pos < end && ok;) {
-        const LPiece q = live_piece(p, pos, end);
-        const int n = p.grp[q.g].n;
-        const int nt = q.j1 - q.j0, first = q.split ? w : 0, step = q.split ? 2 : 1;
-        pos += nt;
-        if (first < nt) {
-          ok = lwait(&qfull[w], u & 1, p.dev_status, s_abort);
-          ++u;
-        }
-        for (int jj = first; jj < nt && ok; jj += step) {
-          const uint32_t ik = 2 * (g + jj), sk = ik % NST, kaddr = aT + sk * C::T_BYTES;
-          const int hs = live_steps(n, q.j0 + jj);
-          for (int h = 0; h < hs; ++h, ++t) {
-            // the P V that read its P from this S buffer is done
-            if ((h == 0 && !landed(ik, seen)) ||
-                (t > 1 && !lwait(&ofull[2 * w + (t & 1)], ((t - 2) >> 1) & 1, p.dev_status, s_abort))) {
-              ok = false;
-              break;
-            }
-            tc05::fence_after();
+    } else if (warp < 10) {
+      // ---- S issue of chain w: a step ahead of its softmax --------------------------------------------
+      if (lane == 0) {
+        const int w = warp - 8;
+        constexpr uint32_t IDESC_S = tc05::idesc_bf16(LM, LS, false);
+        const uint32_t aQ = smem_u32(smem) + w * C::T_BYTES, aT = smem_u32(smem + C::OFF_T);
+        const uint32_t tS = tmem + 2 * w * LS;
+        uint32_t g = 0, t = 0, u = 0, seen = 0;  // tiles of the CTA, steps and pieces of the chain
+        bool ok = true;
+        for (int pos = beg; pos < end && ok;) {
+          const LPiece q = live_piece(p, pos, end);
+          const int n = p.grp[q.g].n;
+          const int nt = q.j1 - q.j0, first = q.split ? w : 0, step = q.split ? 2 : 1;
+          pos += nt;
+          if (first < nt) {
+            ok = lwait(&qfull[w], u & 1, p.dev_status, s_abort);
+            ++u;
+          }
+          for (int jj = first; jj < nt && ok; jj += step) {
+            const uint32_t ik = 2 * (g + jj), sk = ik % NST, kaddr = aT + sk * C::T_BYTES;
+            const int hs = live_steps(n, q.j0 + jj);
+            for (int h = 0; h < hs; ++h, ++t) {
+              // the P V that read its P from this S buffer is done
+              if ((h == 0 && !landed(ik, seen)) ||
+                  (t > 1 && !lwait(&ofull[2 * w + (t & 1)], ((t - 2) >> 1) & 1, p.dev_status, s_abort))) {
+                ok = false;
+                break;
+              }
+              tc05::fence_after();
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * (LN * 128) + (kk & 3) * 32;
-              tc05::mma_bf16(tS + (t & 1) * LS, tc05::sdesc_sw128(aQ + off, 16, 1024),
-                             tc05::sdesc_sw128(kaddr + h * LS * 128 + off, 16, 1024), IDESC_S, kk > 0);
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * (LN * 128) + (kk & 3) * 32;
+                tc05::mma_bf16(tS + (t & 1) * LS, tc05::sdesc_sw128(aQ + off, 16, 1024),
+                               tc05::sdesc_sw128(kaddr + h * LS * 128 + off, 16, 1024), IDESC_S, kk > 0);
+              }
+              tc05::commit(&sfull[2 * w + (t & 1)]);
             }
-            tc05::commit(&sfull[2 * w + (t & 1)]);
+            if (!ok) break;
+            tc05::commit(&empty[sk]);
+            if (q.split) tc05::commit(&empty[sk]);
           }
-          if (!ok) break;
-          tc05::commit(&empty[sk]);
-          if (q.split) tc05::commit(&empty[sk]);
+          g += nt;
         }
-        g += nt;
+        tc05::commit(&xbar[w]);
+        mbar_wait_bounded(&xbar[w], 0, p.dev_status);
       }
-      tc05::commit(&xbar[w]);
-      mbar_wait_bounded(&xbar[w], 0, p.dev_status);
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LREG_SOFTMAX));
     // ---- softmax of chain w: thread rt owns TMEM lane rt = row rt of the chain ----------------------
     const int w = warp >> 2, rt = tid & (LM - 1);
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
