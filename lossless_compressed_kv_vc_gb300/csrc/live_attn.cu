@@ -6,18 +6,21 @@
 //
 // Work decomposition. A group is a key sequence with the query rows that read it: the prefix with the
 // rows of all requests, or one request's own cache with its rows. The rows of one KV head (tokens x
-// G = Hq / Hkv heads) are cut into units of up to 256, the keys into tiles of 128; all units' tiles form
-// one sequence that is cut into equal ranges, one per CTA (one CTA per SM: 8 softmax warps, 2 MMA issuers,
-// 1 loader). A CTA's part of a unit (a piece) leaves (o, lse) partials; a second kernel merges a row's
-// partials over both its groups. So the prefix is read once for up to 256 rows, whatever requests they
-// come from, and a request's own rows cost what they are.
+// G = Hq / Hkv heads) are cut into units of up to 256, the keys into tiles of 128. The prefix's tiles, [unit]
+// [head][tile], and the own caches', [request][unit][head][tile], form a sequence each; CTAs (one per SM: 8
+// softmax warps, 4 MMA issuers, 1 loader) are shared out between the two by cost, and each takes an equal
+// range of its sequence. A CTA's part of a unit of a head (a piece) leaves (o, lse) partials; a second kernel
+// merges a row's partials over both its groups. So the prefix is read once for up to 256 rows, whatever
+// requests they come from, and a request's own rows cost what they are. With several units of prefix rows the
+// CTAs are dealt out so that every unit's ranges are cut at the same tiles: they read a tile at about the same
+// time, and it comes from DRAM once.
 //
 // Within a CTA two chains run side by side, each an issuer thread and a warpgroup of softmax threads (a
 // thread per query row): S = Q K^T into TMEM, softmax in registers, P (bf16) over S in TMEM, O += P V with P
 // read from TMEM. The chains meet only in the ring of K and V tiles, so one's softmax runs while the
 // tensor cores work for the other. A unit of more than 128 rows gives each chain 128 rows and every tile
-// (a tile serves 256 rows); one of up to 128 rows gives both chains the same rows and every other tile,
-// and each leaves its own partial.
+// (a tile serves 256 rows and costs 2); one of up to 128 rows gives both chains the same rows and a half of
+// every tile (which costs 1), and each leaves its own partial. So both chains walk through every tile.
 #include "tc05.cuh"
 
 #include <cudaTypedefs.h>
@@ -36,7 +39,8 @@ constexpr int LTHREADS = 512;
 // Registers a thread: launched with 128 (65536 / 512), then 168 in the softmax warpgroups and 80 in the others
 constexpr int LREG_SOFTMAX = 168, LREG_ISSUE = 80;
 static_assert(256 * (LREG_SOFTMAX + LREG_ISSUE) <= 65536, "no more than the block was launched with");
-constexpr int SCORE_KEYS = 1024;  // keys of a score block
+constexpr int SCORE_KEYS = 1024;  // keys of a score block: four a thread
+static_assert(SCORE_KEYS == 4 * 256 && LN % 4 == 0, "whole vectors of scores");
 
 struct LiveGroup {
   int32_t n;          // keys
@@ -44,32 +48,58 @@ struct LiveGroup {
   int32_t tok_begin;  // first query token (of the call)
   int32_t causal;     // 1: row of token i sees keys <= n - n_rows + i; 0: every row sees every key
   int32_t n_rows;     // query tokens
-  int32_t units;      // ceil(rows / LU)
+  int32_t units;      // ceil(rows / LU) of a head; all but the last have LU rows
   int32_t tiles;      // ceil(n / LN)
-  int32_t tile_begin; // first tile of the group in the call's sequence: [Hkv][units][tiles]
-  int32_t unit_begin; // first unit among the units of its kind (prefix or own)
-  int32_t chunk_begin;  // scored: first score block [Hkv][ceil(n / SCORE_KEYS)]
+  int32_t unit_begin; // first (unit, head) among those of its kind (prefix or own)
   float* score;
   int64_t cap;        // row stride of score
   float* s;           // scored: scores in the log2 domain [Hkv][rows][tiles * LN]
 };
 
+// K and V of each group: read by the attention kernel alone.
+struct LiveMaps {
+  CUtensorMap tm[VC_MAX_BATCH + 1][2];
+};
+
 struct LiveParams {
-  CUtensorMap tm[VC_MAX_BATCH + 1][2];  // K, V of each group
-  LiveGroup grp[VC_MAX_BATCH + 1];      // the prefix first where there is one
+  // what is searched lies together: a scan over the groups' own fields took the constant cache 8 us to
+  // bring in at 33 groups
+  int32_t cost_begin[VC_MAX_BATCH + 2];   // first cost of each group in its kind's sequence [units][Hkv][tiles]
+  int32_t chunk_begin[VC_MAX_BATCH + 2];  // scored: first score block of each group, [Hkv][ceil(n / SCORE_KEYS)]
+  int32_t tok_begin[VC_MAX_BATCH + 1];    // first query token of each request
+  int32_t own_of[VC_MAX_BATCH];           // group of the request's own cache, -1: empty
+  LiveGroup grp[VC_MAX_BATCH + 1];        // the prefix first where there is one
   const bf16* q[VC_MAX_BATCH];
   bf16* o[VC_MAX_BATCH];
-  int32_t tok_begin[VC_MAX_BATCH];
-  int32_t own_of[VC_MAX_BATCH];         // group of the request's own cache, -1: empty
   int32_t B, Hq, Hkv, G, n_tok;
-  int32_t n_grp, has_prefix, n_cta, total;  // total: tiles
+  int32_t n_grp, has_prefix;
+  // by kind: its CTAs, the cost of each one's range and how many (the first) have one more
+  int32_t n_cta[2], cta_cost[2], cta_more[2];
   int32_t merge_blocks, score_blocks;
   int32_t slot_rows[2];                 // partial rows of a slot: prefix, own
-  float* ws_o[2];                       // [slots][slot_rows][d] of prefix and own units; slot = CTA + unit
+  float* ws_o[2];                       // [slots][slot_rows][d]; slot = CTA of the kind + (unit, head)
   float* ws_lse[2];                     // [slots][slot_rows], log2 domain, -inf: saw nothing
   float scale_log2;
   int32_t* dev_status;
 };
+
+// The last i in [0, n) with begin[i] <= x.
+__device__ __forceinline__ int last_begin(const int32_t* begin, int n, int x) {
+  int lo = 0;
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1)
+    if (lo + s < n && begin[lo + s] <= x) lo += s;
+  return lo;
+}
+
+// CTA c of a kind has the costs from cta_begin(c) on; x lies in those of cta_of(x).
+__device__ __forceinline__ int cta_begin(const LiveParams& p, int kind, int c) {
+  return c * p.cta_cost[kind] + min(c, p.cta_more[kind]);
+}
+__device__ __forceinline__ int cta_of(const LiveParams& p, int kind, int x) {
+  const int each = p.cta_cost[kind], more = p.cta_more[kind], e = more * (each + 1);
+  return x < e ? x / (each + 1) : more + (x - e) / each;
+}
 
 template <int D>
 struct LCfg {
@@ -89,36 +119,77 @@ struct LCfg {
 // Steps of tile j of n keys: its second half only where it holds keys.
 __device__ __forceinline__ int live_steps(int n, int j) { return n - j * LN > LS ? 2 : 1; }
 
-// A CTA's part of a unit: tiles [j0, j1) of it.
+// A CTA's part of a unit of a head: tiles [j0, j1). Every role of the CTA walks through the same pieces.
 struct LPiece {
-  int g, hk, u, j0, j1;  // group, KV head, unit of the head, tiles
-  int rows;              // the unit's query rows
-  bool split;            // both chains hold the same rows and take every other tile
+  int g, hk, u, j0, j1;  // group, KV head, unit of its rows, tiles
+  int rows, tiles;       // the unit's query rows, the group's tiles
+  int at, end;           // cost at which the head's tiles start, end of the CTA's range
+  bool split;            // both chains hold the same rows, chain w takes half w of every tile
+
+  __device__ __forceinline__ bool valid() const { return at < end; }
+  __device__ __forceinline__ int cost() const { return split ? 1 : 2; }
+  // chain w's steps of tile j of a group of n keys are its halves [h0, h1)
+  __device__ __forceinline__ int h0(int w) const { return split ? w : 0; }
+  __device__ __forceinline__ int h1(int w, int n, int j) const { return min(live_steps(n, j), split ? w + 1 : 2); }
+  // it has none in the whole piece: chain 1 of a split unit's last, short tile
+  __device__ __forceinline__ bool idle(int w, int n) const { return split && w == 1 && j1 - j0 == 1 && live_steps(n, j0) == 1; }
+  __device__ __forceinline__ void fit(const LiveParams& p) {
+    const LiveGroup& R = p.grp[g];
+    rows = min(LU, R.rows - u * LU);
+    tiles = R.tiles;
+    split = rows <= LM;
+  }
+  __device__ __forceinline__ void cut() { j1 = min(tiles, (end - at + cost() - 1) / cost()); }
+  __device__ __forceinline__ void next(const LiveParams& p) {
+    at += cost() * tiles;
+    if (!valid()) return;
+    if (++hk == p.Hkv) {
+      hk = 0;
+      if (++u == p.grp[g].units) {
+        u = 0;
+        ++g;
+      }
+      fit(p);
+    }
+    j0 = 0;
+    cut();
+  }
 };
 
-__device__ __forceinline__ LPiece live_piece(const LiveParams& p, int pos, int end) {
+__device__ __forceinline__ LPiece live_first(const LiveParams& p) {
   LPiece q;
-  q.g = 0;
-#pragma unroll 1
-  for (int i = 1; i < p.n_grp; ++i)
-    if (p.grp[i].tile_begin <= pos) q.g = i;
+  const int kind = (int)blockIdx.x < p.n_cta[0] ? 0 : 1, c = blockIdx.x - (kind ? p.n_cta[0] : 0);
+  const int beg = cta_begin(p, kind, c);
+  q.end = cta_begin(p, kind, c + 1);
+  q.g = kind ? p.has_prefix + last_begin(p.cost_begin + p.has_prefix, p.n_grp - p.has_prefix, beg) : 0;
   const LiveGroup& R = p.grp[q.g];
-  const int rel = pos - R.tile_begin, ul = rel / R.tiles;
-  q.hk = ul / R.units;
-  q.u = ul - q.hk * R.units;
-  q.j0 = rel - ul * R.tiles;
-  q.j1 = min(R.tiles, q.j0 + end - pos);
-  q.rows = min(LU, R.rows - q.u * LU);
-  q.split = q.rows <= LM;
+  int rem = beg - p.cost_begin[q.g];
+  const int unit = 2 * R.tiles * p.Hkv;  // of a unit of more than LM rows
+  q.u = min(rem / unit, R.units - 1);
+  rem -= q.u * unit;
+  q.fit(p);
+  q.hk = rem / (q.cost() * q.tiles);
+  rem -= q.hk * q.cost() * q.tiles;
+  q.at = beg - rem;
+  q.j0 = (rem + q.cost() - 1) / q.cost();
+  q.cut();
+  if (q.j0 >= q.j1) q.next(p);  // the range starts in a head's last tile, which is the CTA's before
   return q;
 }
 
-__device__ __forceinline__ int live_req_of(const LiveParams& p, int tok) {
-  int b = 0;
+__device__ __forceinline__ int live_req_of(const LiveParams& p, int tok) { return last_begin(p.tok_begin, p.B, tok); }
+
+// A launch's parameters are cold in every constant cache: thread t of n reads every n-th 64-byte line of them,
+// so that the searches that follow do not wait for one line after the other (1 us each).
+template <typename T>
+__device__ __forceinline__ void touch_params(const T& p, int t, int n) {
+  const int* w = reinterpret_cast<const int*>(&p);
 #pragma unroll 1
-  for (int i = 1; i < p.B; ++i)
-    if (p.tok_begin[i] <= tok) b = i;
-  return b;
+  for (int i = t; i < (int)(sizeof(T) / 64); i += n) asm volatile("" ::"r"(w[i * 16]));
+}
+
+__device__ __forceinline__ void prefetch_tmap(const void* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
 
 // Bounded mbarrier wait that also gives up when another role of the CTA has aborted.
@@ -132,12 +203,22 @@ __device__ __forceinline__ bool lwait(uint64_t* bar, uint32_t parity, int32_t* s
   return false;
 }
 
+// Arrives where `on`, without a branch.
+__device__ __forceinline__ void mbar_arrive_if(uint64_t* bar, bool on) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"((uint32_t)on)
+      : "memory");
+}
+
 __device__ __forceinline__ bool nonfinite_bf16x2(uint32_t w) {
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
 template <int D, bool SCORED>
-__global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_constant__ LiveParams p) {
+__global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_constant__ LiveParams p, const __grid_constant__ LiveMaps maps) {
   using C = LCfg<D>;
   constexpr int NST = C::NST;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -161,6 +242,7 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
   volatile uint32_t* s_issued = tslot + 4;  // loads issued so far
 
   if (warp == 12) tc05::alloc(tslot, C::TCOLS);
+  if (warp >= 13) touch_params(p, tid - 13 * 32, 96);
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(&full[i], 1);
@@ -185,16 +267,15 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
   tc05::fence_before();
   __syncthreads();
   tc05::fence_after();
+  const uint32_t tmem = *tslot;
+  const int kind = (int)blockIdx.x < p.n_cta[0] ? 0 : 1;
   pdl_wait();
   pdl_launch_dependents();
-  const uint32_t tmem = *tslot;
-  const int beg = (int)((int64_t)blockIdx.x * p.total / p.n_cta);
-  const int end = (int)((int64_t)(blockIdx.x + 1) * p.total / p.n_cta);
 
   // Load `it` has landed; `seen` is the caller's count of loads it knows to be issued. A role does not see
-  // every phase of a stage's barrier (the S issuers wait for K tiles only, the P V issuers for V tiles, in
-  // split units each chain for its own), so the parity alone could be that of two phases before: once the
-  // load is issued, the phase before it is over, and its own cannot pass until this role releases the stage.
+  // every phase of a stage's barrier (the S issuers wait for K tiles only, the P V issuers for V tiles), so the
+  // parity alone could be that of two phases before: once the load is issued, the phase before it is over, and
+  // its own cannot pass until this role releases the stage.
   // The chains' barriers are kept per S buffer: step s + 2 cannot complete a phase of one before step s's
   // has been waited for, while with one barrier for both, steps s and s + 1 could both pass unseen.
   auto landed = [&](uint32_t it, uint32_t& seen) -> bool {
@@ -214,10 +295,15 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
     if (warp == 12) {
       // ---- TMA: tiles in order, K then V of each ---------------------------------------------------
       if (lane == 0) {
+        LPiece q = live_first(p);
+        prefetch_tmap(&maps.tm[q.g][1]);
         uint32_t it = 0;
         bool ok = true;
-        for (int pos = beg; pos < end && ok;) {
-          const LPiece q = live_piece(p, pos, end);
+        for (; q.valid() && ok; q.next(p)) {
+          if (q.end - q.at > q.cost() * q.tiles && q.g + 1 < p.n_grp) {  // the range goes on: maybe to the next group
+            prefetch_tmap(&maps.tm[q.g + 1][0]);
+            prefetch_tmap(&maps.tm[q.g + 1][1]);
+          }
           for (int j = q.j0; j < q.j1 && ok; ++j)
             for (int kv = 0; kv < 2; ++kv) {
               const uint32_t st = it % NST;
@@ -229,11 +315,10 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
               mbar_arrive_expect_tx(&full[st], C::T_BYTES);
 #pragma unroll
               for (int kb = 0; kb < C::KB; ++kb)
-                tc05::tma_load_3d(dst + kb * (LN * 128), &p.tm[q.g][kv], kb * 64, j * LN, q.hk, &full[st]);
+                tc05::tma_load_3d(dst + kb * (LN * 128), &maps.tm[q.g][kv], kb * 64, j * LN, q.hk, &full[st]);
               __threadfence_block();
               *s_issued = ++it;
             }
-          pos += q.j1 - q.j0;
         }
         if (*s_abort)  // drain (bounded): a ring's worth of loads may still be landing
           for (uint32_t i = it > (uint32_t)NST ? it - NST : 0; i < it; ++i)
@@ -245,19 +330,18 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
         const int w = warp - 10;
         constexpr uint32_t IDESC_O = tc05::idesc_bf16(LM, D, true);
         const uint32_t aT = smem_u32(smem + C::OFF_T), tS = tmem + 2 * w * LS, tO = tmem + C::OCOL + w * D;
+        LPiece q = live_first(p);
         uint32_t g = 0, t = 0, seen = 0;  // tiles of the CTA, steps of the chain
         bool ok = true;
-        for (int pos = beg; pos < end && ok;) {
-          const LPiece q = live_piece(p, pos, end);
+        for (; q.valid() && ok; q.next(p)) {
           const int n = p.grp[q.g].n;
-          const int nt = q.j1 - q.j0, first = q.split ? w : 0, step = q.split ? 2 : 1;
-          pos += nt;
           bool acc = false;
-          for (int jj = first; jj < nt && ok; jj += step) {
-            const uint32_t iv = 2 * (g + jj) + 1, sv = iv % NST, vaddr = aT + sv * C::T_BYTES;
-            const int hs = live_steps(n, q.j0 + jj);
-            for (int h = 0; h < hs; ++h, ++t) {
-              if ((h == 0 && !landed(iv, seen)) || !lwait(&pfull[2 * w + (t & 1)], (t >> 1) & 1, p.dev_status, s_abort)) {
+          for (int j = q.j0; j < q.j1 && ok; ++j, ++g) {
+            const uint32_t iv = 2 * g + 1, sv = iv % NST, vaddr = aT + sv * C::T_BYTES;
+            ok = landed(iv, seen);
+            const int h1 = q.h1(w, n, j);
+            for (int h = q.h0(w); h < h1 && ok; ++h, ++t) {
+              if (!lwait(&pfull[2 * w + (t & 1)], (t >> 1) & 1, p.dev_status, s_abort)) {
                 ok = false;
                 break;
               }
@@ -272,11 +356,8 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
               tc05::commit(&ofull[2 * w + (t & 1)]);
               acc = true;
             }
-            if (!ok) break;
-            tc05::commit(&empty[sv]);
-            if (q.split) tc05::commit(&empty[sv]);  // the other chain leaves this tile alone
+            if (ok) tc05::commit(&empty[sv]);
           }
-          g += nt;
         }
         // every MMA issued so far has completed before TMEM is released (bounded, even after an abort)
         tc05::commit(&xbar[2 + w]);
@@ -289,24 +370,22 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
         constexpr uint32_t IDESC_S = tc05::idesc_bf16(LM, LS, false);
         const uint32_t aQ = smem_u32(smem) + w * C::T_BYTES, aT = smem_u32(smem + C::OFF_T);
         const uint32_t tS = tmem + 2 * w * LS;
+        LPiece q = live_first(p);
         uint32_t g = 0, t = 0, u = 0, seen = 0;  // tiles of the CTA, steps and pieces of the chain
         bool ok = true;
-        for (int pos = beg; pos < end && ok;) {
-          const LPiece q = live_piece(p, pos, end);
+        for (; q.valid() && ok; q.next(p)) {
           const int n = p.grp[q.g].n;
-          const int nt = q.j1 - q.j0, first = q.split ? w : 0, step = q.split ? 2 : 1;
-          pos += nt;
-          if (first < nt) {
+          if (!q.idle(w, n)) {
             ok = lwait(&qfull[w], u & 1, p.dev_status, s_abort);
             ++u;
           }
-          for (int jj = first; jj < nt && ok; jj += step) {
-            const uint32_t ik = 2 * (g + jj), sk = ik % NST, kaddr = aT + sk * C::T_BYTES;
-            const int hs = live_steps(n, q.j0 + jj);
-            for (int h = 0; h < hs; ++h, ++t) {
+          for (int j = q.j0; j < q.j1 && ok; ++j, ++g) {
+            const uint32_t ik = 2 * g, sk = ik % NST, kaddr = aT + sk * C::T_BYTES;
+            ok = landed(ik, seen);
+            const int h1 = q.h1(w, n, j);
+            for (int h = q.h0(w); h < h1 && ok; ++h, ++t) {
               // the P V that read its P from this S buffer is done
-              if ((h == 0 && !landed(ik, seen)) ||
-                  (t > 1 && !lwait(&ofull[2 * w + (t & 1)], ((t - 2) >> 1) & 1, p.dev_status, s_abort))) {
+              if (t > 1 && !lwait(&ofull[2 * w + (t & 1)], ((t - 2) >> 1) & 1, p.dev_status, s_abort)) {
                 ok = false;
                 break;
               }
@@ -319,11 +398,8 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
               }
               tc05::commit(&sfull[2 * w + (t & 1)]);
             }
-            if (!ok) break;
-            tc05::commit(&empty[sk]);
-            if (q.split) tc05::commit(&empty[sk]);
+            if (ok) tc05::commit(&empty[sk]);
           }
-          g += nt;
         }
         tc05::commit(&xbar[w]);
         mbar_wait_bounded(&xbar[w], 0, p.dev_status);
@@ -336,54 +412,64 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + 2 * w * LS, tO = tmem + lane_off + C::OCOL + w * D;
     uint8_t* sQ = smem + w * C::T_BYTES;
+    LPiece q = live_first(p);
     uint32_t g = 0, t = 0, looked = 0, seen = 0;
     // P V of step s done (and with it those before): asked for steps whose S has been read, so the phase
     // before on that buffer is over
     auto pv_done = [&](uint32_t s) { return lwait(&ofull[2 * w + (s & 1)], (s >> 1) & 1, p.dev_status, s_abort); };
     bool ok = true;
-    for (int pos = beg; pos < end && ok;) {
-      const LPiece q = live_piece(p, pos, end);
+    auto slot_of = [&](const LiveGroup& R) {
+      return (size_t)(blockIdx.x - (kind ? p.n_cta[0] : 0)) + R.unit_begin + q.u * p.Hkv + q.hk;
+    };
+    // Q of the next piece with steps for this chain, into its Q tile (the chain's S on the last one are all
+    // done: their softmax is); pieces without any leave an empty partial
+    auto fetch = [&]() {
+      for (; q.valid(); g += q.j1 - q.j0, q.next(p)) {
+        const LiveGroup& R = p.grp[q.g];
+        const int ru = q.split ? rt : w * LM + rt, row = q.u * LU + ru;  // row of the unit, of the head
+        const bool row_ok = ru < q.rows;
+        if (q.idle(w, R.n)) {
+          const size_t slot = slot_of(R);
+          if (row_ok) p.ws_lse[kind][slot * p.slot_rows[kind] + w * q.rows + ru] = -INFINITY;
+          continue;
+        }
+        const bf16* src = nullptr;  // this thread's row
+        if (row_ok) {
+          const int tok = R.tok_begin + row / p.G, b = live_req_of(p, tok);
+          src = p.q[b] + ((size_t)(tok - p.tok_begin[b]) * p.Hq + q.hk * p.G + row % p.G) * D;
+        }
+        // the warp's 32 rows, a row's 16-byte pieces in neighbouring lanes (a lane per row would touch 32 lines a load)
+        constexpr int PR = D / 8, RW = 32 / PR;  // pieces of a row, rows a load
+#pragma unroll
+        for (int i = 0; i < 32 / RW; ++i) {
+          const int r = i * RW + lane / PR, c = lane % PR, rr = (warp & 3) * 32 + r;
+          const bf16* from = reinterpret_cast<const bf16*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), r));
+          const uint4 v = from ? __ldg(reinterpret_cast<const uint4*>(from) + c) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(sQ + (c >> 3) * (LM * 128) + rr * 128 + (((c ^ rr) & 7) << 4)) = v;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qfull[w]);
+        return;
+      }
+    };
+    fetch();
+    while (q.valid()) {
       const LiveGroup& R = p.grp[q.g];
-      const int nt = q.j1 - q.j0, first = q.split ? w : 0, step = q.split ? 2 : 1;
-      pos += nt;
-      const int ru = q.split ? rt : w * LM + rt;  // row of the unit, of the head
+      const int ru = q.split ? rt : w * LM + rt;
       const bool row_ok = ru < q.rows;
       const int row = q.u * LU + ru, tl = row / p.G;
-      const int kind = p.has_prefix && q.g == 0 ? 0 : 1;
-      const int slot = blockIdx.x + R.unit_begin + q.hk * R.units + q.u;
-      const size_t part = (size_t)slot * p.slot_rows[kind] + (q.split ? w * q.rows : 0) + ru;
-      if (first >= nt) {  // a piece of one tile: nothing for chain 1
-        if (row_ok) p.ws_lse[kind][part] = -INFINITY;
-        g += nt;
-        continue;
-      }
-      {
-        // the chain's Q tile: its MMAs on the last one are complete (that piece's end waited for its last P V)
-        const uint4* src = nullptr;
-        if (row_ok) {
-          const int tok = R.tok_begin + tl, b = live_req_of(p, tok);
-          src = reinterpret_cast<const uint4*>(p.q[b] + ((size_t)(tok - p.tok_begin[b]) * p.Hq + q.hk * p.G + row % p.G) * D);
-        }
-#pragma unroll
-        for (int kb = 0; kb < C::KB; ++kb)
-#pragma unroll
-          for (int ch = 0; ch < 8; ++ch) {
-            const uint4 v = row_ok ? __ldg(src + kb * 8 + ch) : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(sQ + kb * (LM * 128) + rt * 128 + ((ch ^ (rt & 7)) << 4)) = v;
-          }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&qfull[w]);
+      const size_t part = slot_of(R) * p.slot_rows[kind] + (q.split ? w * q.rows : 0) + ru;
       // last key the row sees, and the first one that some row of the chain does not
-      const int last_key = R.causal ? R.n - R.n_rows + tl : R.n - 1;
-      const int blind = R.causal ? R.n - R.n_rows + (q.u * LU + (q.split ? 0 : w * LM)) / p.G + 1 : R.n;
+      const int n = R.n;
+      const int last_key = R.causal ? n - R.n_rows + tl : n - 1;
+      const int blind = R.causal ? n - R.n_rows + (q.u * LU + (q.split ? 0 : w * LM)) / p.G + 1 : n;
       float* s_row = SCORED ? R.s + ((size_t)q.hk * R.rows + row) * ((size_t)R.tiles * LN) : nullptr;
       float m_run = -INFINITY, l_run = 0.f;
       bool fresh = true;  // the piece's first step
-      for (int jj = first; jj < nt && ok; jj += step) {
-        const int j = q.j0 + jj, hs = live_steps(R.n, j);
-        for (int h = 0; h < hs; ++h, ++t, fresh = false) {
+      for (int j = q.j0; j < q.j1 && ok; ++j, ++g) {
+        const int h1 = q.h1(w, n, j);
+        for (int h = q.h0(w); h < h1; ++h, ++t, fresh = false) {
           const int k0 = j * LN + h * LS;  // the step's first key
           const uint32_t tP = tS + (t & 1) * LS;
           if (!lwait(&sfull[2 * w + (t & 1)], (t >> 1) & 1, p.dev_status, s_abort)) {
@@ -472,8 +558,8 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
           tc05::wait_st();
           // A step with keys that some rows see and others do not: a weight of 0 would carry an infinite or
           // NaN value row to the latter, so if V holds any, the threads add up the seen keys themselves.
-          if (blind < min(R.n, k0 + LS)) {
-            const uint32_t iv = 2 * (g + jj) + 1;
+          if (blind < min(n, k0 + LS)) {
+            const uint32_t iv = 2 * g + 1;
             if (!landed(iv, seen)) {
               ok = false;
               break;
@@ -542,32 +628,47 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
           }
           tc05::fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&pfull[2 * w + (t & 1)]);
+          mbar_arrive_if(&pfull[2 * w + (t & 1)], lane == 0);
         }
       }
       if (!ok) break;
-      // the chain's partial of the piece, after its last P V
+      q.next(p);
+      fetch();
+      // the chain's partial of the piece, after its last P V (the next one's S are under way)
       if (!pv_done(t - 1)) {
         ok = false;
         break;
       }
       tc05::fence_after();
       const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
+      // rows in the order of an MMA's accumulator: four lanes hold 8 neighbouring channels (whole 32-byte
+      // sectors), where a lane per row would write 32 lines at a time
+      float* o_row0 = p.ws_o[kind] + (part - (rt & 31)) * D + 2 * (lane & 3);  // of the warp's first row
+      const unsigned rows_ok = __ballot_sync(0xffffffffu, row_ok);
 #pragma unroll 1
-      for (int cb = 0; cb < D / 32; ++cb) {
-        uint32_t r[32];
-        tc05::ld32(tO + cb * 32, r);  // warp-collective: every lane loads
-        tc05::wait_ld();
-        if (!row_ok) continue;
-        float4* dst = reinterpret_cast<float4*>(p.ws_o[kind] + part * D + cb * 32);
+      for (int hh = 0; hh < 2; ++hh) {
+        if (!((rows_ok >> (16 * hh)) & 0xffffu)) continue;
+        const int r0 = hh * 16 + (lane >> 2), r1 = r0 + 8;
+        const float i0 = __shfl_sync(0xffffffffu, inv, r0), i1 = __shfl_sync(0xffffffffu, inv, r1);
+        const bool ok0 = (rows_ok >> r0) & 1u, ok1 = (rows_ok >> r1) & 1u;
+#pragma unroll 1
+        for (int cb = 0; cb < D / 32; ++cb) {
+          uint32_t r[16];
+          tc05::ld16x256_x4(tO + ((uint32_t)(hh * 16) << 16) + cb * 32, r);  // warp-collective: every lane loads
+          tc05::wait_ld();
 #pragma unroll
-        for (int v = 0; v < 8; ++v)
-          dst[v] = make_float4(__uint_as_float(r[4 * v]) * inv, __uint_as_float(r[4 * v + 1]) * inv,
-                               __uint_as_float(r[4 * v + 2]) * inv, __uint_as_float(r[4 * v + 3]) * inv);
+          for (int k = 0; k < 4; ++k) {
+            if (ok0)
+              *reinterpret_cast<float2*>(o_row0 + (size_t)r0 * D + cb * 32 + 8 * k) =
+                  make_float2(__uint_as_float(r[4 * k]) * i0, __uint_as_float(r[4 * k + 1]) * i0);
+            if (ok1)
+              *reinterpret_cast<float2*>(o_row0 + (size_t)r1 * D + cb * 32 + 8 * k) =
+                  make_float2(__uint_as_float(r[4 * k + 2]) * i1, __uint_as_float(r[4 * k + 3]) * i1);
+          }
+        }
       }
       if (row_ok) p.ws_lse[kind][part] = l_run != 0.f ? m_run + log2f(l_run) : -INFINITY;
       tc05::fence_before();
-      g += nt;
     }
   }
 
@@ -587,28 +688,28 @@ struct LParts {
   }
 };
 
-__device__ __forceinline__ LParts live_parts(const LiveParams& p, const LiveGroup& R, int stride, int hk, int r) {
+__device__ __forceinline__ LParts live_parts(const LiveParams& p, int kind, int g, int hk, int r) {
   LParts q;
-  const int u = r / LU, ul = hk * R.units + u, rows = min(LU, R.rows - u * LU);
-  const int64_t U0 = R.tile_begin + (int64_t)ul * R.tiles, U1 = U0 + R.tiles, T = p.total, N = p.n_cta;
-  const int c0 = (int)(((U0 + 1) * N - 1) / T), c1 = (int)((U1 * N - 1) / T);
+  const LiveGroup& R = p.grp[g];
+  const int u = r / LU, rows = min(LU, R.rows - u * LU), cost = rows <= LM ? 1 : 2;
+  const int at = p.cost_begin[g] + (u * 2 * p.Hkv + hk * cost) * R.tiles;
+  const int c0 = cta_of(p, kind, at), c1 = cta_of(p, kind, at + cost * (R.tiles - 1));  // of its first and last tile
   q.second = rows <= LM ? rows : 0;
   q.count = (c1 - c0 + 1) * (q.second ? 2 : 1);
-  q.stride = stride;
-  q.base = (size_t)(c0 + R.unit_begin + ul) * stride + (r - u * LU);
+  q.stride = p.slot_rows[kind];
+  q.base = (size_t)(c0 + R.unit_begin + u * p.Hkv + hk) * q.stride + (r - u * LU);
   return q;
 }
 
 // Merge: a warp per (token, query head), o = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M) over the
 // partials of the prefix and of the own cache: a lane per partial takes the weights, then the warp adds
-// up the partials' channels, eight loads in flight. Scores: a block per 1024 keys of a (request, KV head)
+// up the partials' channels, four loads in flight. Scores: a block per 1024 keys of a (request, KV head)
 // merges the head's rows' lse, a warp a row, then sums 2^(s - lse) over the rows for each key.
 template <int D, bool SCORED>
-__global__ void __launch_bounds__(256, 4) live_finish_kernel(const __grid_constant__ LiveParams p) {
+__global__ void __launch_bounds__(256, SCORED ? 3 : 4) live_finish_kernel(const __grid_constant__ LiveParams p) {
   constexpr int E = D / 32;  // channels a lane
+  constexpr int PF = 4;      // partials in flight
   __shared__ float s_lse[VC_SCORED_MAX_ROWS];
-  pdl_wait();
-  pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto warp_max = [](float v) {
 #pragma unroll
@@ -624,12 +725,17 @@ __global__ void __launch_bounds__(256, 4) live_finish_kernel(const __grid_consta
   auto weight = [](float l, float M) { return l == -INFINITY ? 0.f : M == -INFINITY ? NAN : exp2f(l - M); };
   if ((int)blockIdx.x < p.merge_blocks) {
     const int64_t id = (int64_t)blockIdx.x * 8 + warp;
-    if (id >= (int64_t)p.n_tok * p.Hq) return;
+    if (id >= (int64_t)p.n_tok * p.Hq) {
+      pdl_wait();
+      return;
+    }
     const int tok = (int)(id / p.Hq), hq = (int)(id - (int64_t)tok * p.Hq), hk = hq / p.G, gq = hq - hk * p.G;
     const int b = live_req_of(p, tok), i = tok - p.tok_begin[b], own = p.own_of[b];
     LParts a{0, 0, 0, 0}, o{0, 0, 0, 0};  // of the prefix, of the own cache
-    if (p.has_prefix) a = live_parts(p, p.grp[0], p.slot_rows[0], hk, tok * p.G + gq);
-    if (own >= 0) o = live_parts(p, p.grp[own], p.slot_rows[1], hk, i * p.G + gq);
+    if (p.has_prefix) a = live_parts(p, 0, 0, hk, tok * p.G + gq);
+    if (own >= 0) o = live_parts(p, 1, own, hk, i * p.G + gq);
+    pdl_wait();  // what needs the parameters alone is done
+    pdl_launch_dependents();
     const int total = a.count + o.count;
     auto lse_of = [&](int k) {
       return k < a.count ? p.ws_lse[0][a.at(k)] : k < total ? p.ws_lse[1][o.at(k - a.count)] : -INFINITY;
@@ -645,10 +751,10 @@ __global__ void __launch_bounds__(256, 4) live_finish_kernel(const __grid_consta
       const unsigned wrote = __ballot_sync(0xffffffffu, l != -INFINITY);
       L += f;
       const int cnt = min(32, total - k0);
-      for (int c0 = 0; c0 < cnt; c0 += 8) {
-        float v[8][E], fc[8];
+      for (int c0 = 0; c0 < cnt; c0 += PF) {
+        float v[PF][E], fc[PF];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < PF; ++c) {
           fc[c] = __shfl_sync(0xffffffffu, f, c0 + c);  // c0 + c < 32; nothing was written beyond cnt
 #pragma unroll
           for (int e = 0; e < E; ++e) v[c][e] = 0.f;
@@ -662,7 +768,7 @@ __global__ void __launch_bounds__(256, 4) live_finish_kernel(const __grid_consta
           }
         }
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
+        for (int c = 0; c < PF; ++c)
 #pragma unroll
           for (int e = 0; e < E; ++e) acc[e] = fmaf(fc[c], v[c][e], acc[e]);
       }
@@ -681,55 +787,56 @@ __global__ void __launch_bounds__(256, 4) live_finish_kernel(const __grid_consta
   }
   if constexpr (SCORED) {
     const int id = blockIdx.x - p.merge_blocks;
-    int g = 0;
-#pragma unroll 1
-    for (int i = 1; i < p.n_grp; ++i)
-      if (p.grp[i].chunk_begin <= id) g = i;
+    const int g = last_begin(p.chunk_begin, p.n_grp, id);
     const LiveGroup& R = p.grp[g];
     const int chunks = (R.n + SCORE_KEYS - 1) / SCORE_KEYS;
-    const int hk = (id - R.chunk_begin) / chunks, k0 = (id - R.chunk_begin - hk * chunks) * SCORE_KEYS;
-    constexpr int KT = SCORE_KEYS / 256;  // a thread's keys, 256 apart
+    const int hk = (id - p.chunk_begin[g]) / chunks, k0 = (id - p.chunk_begin[g] - hk * chunks) * SCORE_KEYS;
     const size_t stride = (size_t)R.tiles * LN;
-    const float* s = R.s + (size_t)hk * R.rows * stride + k0 + threadIdx.x;
-    float* score = R.score + (size_t)hk * R.cap + k0 + threadIdx.x;
-    const int left = R.n - k0 - (int)threadIdx.x;
-    float w[KT], v[8][KT];
+    const int key = k0 + 4 * threadIdx.x, left = R.n - key;  // a thread's four keys; S rows are whole tiles
+    const float* s = R.s + (size_t)hk * R.rows * stride + key;
+    float* score = R.score + (size_t)hk * R.cap + key;
+    const int rows = R.rows;
+    LParts part{0, 0, 0, 0};
+    if (warp < rows) part = live_parts(p, 1, g, hk, warp);
+    pdl_wait();
+    pdl_launch_dependents();
+    float4 v[8];
     auto load8 = [&](int r0) {
 #pragma unroll
       for (int r = 0; r < 8; ++r)
-#pragma unroll
-        for (int c = 0; c < KT; ++c) v[r][c] = r0 + r < R.rows && c * 256 < left ? __ldg(s + (r0 + r) * stride + c * 256) : 0.f;
+        if (r0 + r < rows && left > 0) v[r] = __ldg(reinterpret_cast<const float4*>(s + (r0 + r) * stride));
     };
     load8(0);  // in flight while the rows' lse are merged
+    float w[4];
 #pragma unroll
-    for (int c = 0; c < KT; ++c) w[c] = c * 256 < left ? score[c * 256] : 0.f;
-    for (int r = warp; r < R.rows; r += 8) {
-      const LParts q = live_parts(p, R, p.slot_rows[1], hk, r);
+    for (int c = 0; c < 4; ++c) w[c] = c < left ? score[c] : 0.f;
+    for (int r = warp; r < rows; r += 8) {
+      if (r > warp) part = live_parts(p, 1, g, hk, r);
       float M = -INFINITY, L = 0.f;
-      for (int k = lane; k < q.count; k += 32) M = fmaxf(M, p.ws_lse[1][q.at(k)]);
+      for (int k = lane; k < part.count; k += 32) M = fmaxf(M, p.ws_lse[1][part.at(k)]);
       M = warp_max(M);
-      for (int k = lane; k < q.count; k += 32) L += weight(p.ws_lse[1][q.at(k)], M);
+      for (int k = lane; k < part.count; k += 32) L += weight(p.ws_lse[1][part.at(k)], M);
       L = warp_sum(L);
       if (lane == 0) s_lse[r] = L != 0.f ? M + log2f(L) : INFINITY;  // a row that sees nothing has weights 2^-inf
     }
     __syncthreads();
-    float sum[KT];
-#pragma unroll
-    for (int c = 0; c < KT; ++c) sum[c] = 0.f;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-    for (int r0 = 0; r0 < R.rows; r0 += 8) {
+    for (int r0 = 0; r0 < rows; r0 += 8) {
       if (r0) load8(r0);
 #pragma unroll
       for (int r = 0; r < 8; ++r)
-        if (r0 + r < R.rows) {
+        if (r0 + r < rows) {
           const float lse = s_lse[r0 + r];
-#pragma unroll
-          for (int c = 0; c < KT; ++c) sum[c] += ex2_approx(v[r][c] - lse);
+          sum[0] += ex2_approx(v[r].x - lse);
+          sum[1] += ex2_approx(v[r].y - lse);
+          sum[2] += ex2_approx(v[r].z - lse);
+          sum[3] += ex2_approx(v[r].w - lse);
         }
     }
 #pragma unroll
-    for (int c = 0; c < KT; ++c)
-      if (c * 256 < left) score[c * 256] = w[c] + sum[c];
+    for (int c = 0; c < 4; ++c)
+      if (c < left) score[c] = w[c] + sum[c];
   }
 }
 
@@ -761,6 +868,34 @@ static int live_sms() {
 
 static int64_t units_of(int64_t rows) { return (rows + LU - 1) / LU; }
 static int slot_rows_of(int64_t rows) { return rows <= LM ? (int)(2 * rows) : LU; }
+// CTAs for the prefix's and the own caches' costs: at most one per SM, none with a range below `least`, the
+// cost of the kind's dearest tile (so that none holds less than a tile). With several units of prefix rows their number is a multiple of the units' (a last unit of
+// up to LM rows counting half), where that leaves the longest range within a tenth of the shortest possible.
+static void share_ctas(const int64_t (&cost)[2], const int (&least)[2], int prefix_rows, int32_t (&n)[2]) {
+  int most[2];
+  for (int k = 0; k < 2; ++k) {
+    const int64_t m = cost[k] / least[k];
+    most[k] = cost[k] == 0 ? 0 : m < 1 ? 1 : m < live_sms() ? (int)m : live_sms();
+  }
+  n[0] = most[0];
+  n[1] = most[1];
+  const int units = (int)units_of(prefix_rows), half = prefix_rows - (units - 1) * LU <= LM;
+  const int step = units < 2 ? 1 : 2 * units - half;  // in half units; twice as many CTAs without a half one
+  if (most[0] == 0 || (most[0] + most[1] <= live_sms() && step == 1)) return;
+  const int room = live_sms();
+  int64_t best = -1, best_aligned = -1;
+  int at = 0, at_aligned = 0;
+  for (int c = 1; c <= most[0] && (most[1] == 0 || c < room); ++c) {
+    const int o = most[1] < room - c ? most[1] : room - c;
+    const int64_t p0 = (cost[0] + c - 1) / c, p1 = o > 0 ? (cost[1] + o - 1) / o : 0, longest = p0 > p1 ? p0 : p1;
+    if (best < 0 || longest < best) best = longest, at = c;
+    if ((half ? c : 2 * c) % step == 0 && (best_aligned < 0 || longest < best_aligned)) best_aligned = longest, at_aligned = c;
+  }
+  if (at_aligned && best_aligned * 10 <= best * 11) at = at_aligned;
+  n[0] = at;
+  n[1] = most[1] < room - at ? most[1] : room - at;
+}
+
 static size_t pad256(size_t b) { return (b + 255) / 256 * 256; }
 
 // Partials: slots of both kinds (a slot per CTA and unit); scores: every row's, in fp32.
@@ -776,12 +911,12 @@ size_t live_workspace_size(const vc_shape* s, int32_t max_rows, int32_t max_n, b
 }
 
 template <int D, bool SCORED>
-static cudaError_t launch_live_t(const LiveParams& p, cudaStream_t s) {
+static cudaError_t launch_live_t(const LiveParams& p, const LiveMaps& maps, cudaStream_t s) {
   static std::atomic<uint64_t> attr{0};
-  if (p.total > 0) {
+  if (p.n_cta[0] + p.n_cta[1] > 0) {
     cudaError_t e = raise_smem_limit(live_attn_kernel<D, SCORED>, LCfg<D>::SMEM, attr);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(live_attn_kernel<D, SCORED>, dim3(p.n_cta), dim3(LTHREADS), LCfg<D>::SMEM, s, p);
+    e = launch_pdl(live_attn_kernel<D, SCORED>, dim3(p.n_cta[0] + p.n_cta[1]), dim3(LTHREADS), LCfg<D>::SMEM, s, p, maps);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(live_finish_kernel<D, SCORED>, dim3(p.merge_blocks + p.score_blocks), dim3(256), 0, s, p);
@@ -789,7 +924,8 @@ static cudaError_t launch_live_t(const LiveParams& p, cudaStream_t s) {
 
 cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_status* st) {
   const int G = a.Hq / a.Hkv;
-  LiveParams p;  // about 13 KB: the tensor maps travel as kernel parameters
+  LiveParams p;   // about 4 KB
+  LiveMaps maps;  // about 8 KB: the tensor maps travel as kernel parameters
   memset(&p, 0, sizeof(p));
   p.B = a.B;
   p.Hq = a.Hq;
@@ -799,7 +935,8 @@ cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_
   p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)a.d));
   p.dev_status = a.dev_status;
   p.slot_rows[0] = p.slot_rows[1] = 1;
-  int64_t tiles = 0, units[2] = {0, 0}, chunks = 0;
+  int64_t cost[2] = {0, 0}, units[2] = {0, 0}, chunks = 0;
+  int least[2] = {1, 1};
   size_t s_floats = 0;
   // adds the group of a key sequence; `b`: the request whose own cache it is, -1: the prefix
   auto add = [&](int b, int n, int n_rows, int tok_begin) {
@@ -812,20 +949,22 @@ cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_
     R.n_rows = n_rows;
     R.units = (int32_t)units_of(R.rows);
     R.tiles = (n + LN - 1) / LN;
-    R.tile_begin = (int32_t)tiles;
     R.unit_begin = (int32_t)units[kind];
-    R.chunk_begin = (int32_t)chunks;
+    p.cost_begin[p.n_grp] = (int32_t)cost[kind];
+    p.chunk_begin[p.n_grp] = (int32_t)chunks;
+    if (R.rows > LM) least[kind] = 2;
     const int sr = slot_rows_of(R.rows);
     p.slot_rows[kind] = sr > p.slot_rows[kind] ? sr : p.slot_rows[kind];
     units[kind] += (int64_t)a.Hkv * R.units;
-    tiles += (int64_t)a.Hkv * R.units * R.tiles;
+    // every unit but the last has LU rows
+    cost[kind] += (int64_t)a.Hkv * R.tiles * (2 * R.units - (R.rows - (R.units - 1) * LU <= LM ? 1 : 0));
     if (scored) {
       chunks += (int64_t)a.Hkv * ((n + SCORE_KEYS - 1) / SCORE_KEYS);
       s_floats += (size_t)a.Hkv * R.rows * R.tiles * LN;
     }
     ++p.n_grp;
-    // tiles and blocks are counted in 32 bits
-    if (tiles >= INT32_MAX || chunks >= INT32_MAX / 2 || units[kind] >= INT32_MAX / 2) *st = VC_ERR_UNSUPPORTED;
+    // costs and blocks are counted in 32 bits
+    if (cost[kind] >= INT32_MAX || chunks >= INT32_MAX / 2 || units[kind] >= INT32_MAX / 2) *st = VC_ERR_UNSUPPORTED;
   };
   if (a.pn > 0) {
     p.has_prefix = 1;
@@ -847,8 +986,12 @@ cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_
   const int64_t merge = ((int64_t)a.n_tok * a.Hq + 7) / 8;
   if (*st == VC_OK && merge + chunks >= INT32_MAX) *st = VC_ERR_UNSUPPORTED;
   if (*st != VC_OK) return cudaSuccess;
-  p.total = (int32_t)tiles;
-  p.n_cta = tiles < live_sms() ? (int32_t)tiles : live_sms();
+  share_ctas(cost, least, p.has_prefix ? p.grp[0].rows : 0, p.n_cta);
+  for (int kind = 0; kind < 2; ++kind)
+    if (p.n_cta[kind] > 0) {
+      p.cta_cost[kind] = (int32_t)(cost[kind] / p.n_cta[kind]);
+      p.cta_more[kind] = (int32_t)(cost[kind] % p.n_cta[kind]);
+    }
   p.merge_blocks = (int32_t)merge;
   p.score_blocks = (int32_t)chunks;
   uint8_t* at = static_cast<uint8_t*>(a.ws);
@@ -863,7 +1006,7 @@ cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_
     return cudaSuccess;
   }
   for (int kind = 0; kind < 2; ++kind) {
-    const size_t rows = units[kind] ? (size_t)(p.n_cta + units[kind]) * p.slot_rows[kind] : 0;
+    const size_t rows = units[kind] ? (size_t)(p.n_cta[kind] + units[kind]) * p.slot_rows[kind] : 0;
     p.ws_o[kind] = take(rows * (a.d + 1) * sizeof(float));
     p.ws_lse[kind] = p.ws_o[kind] + rows * a.d;
   }
@@ -872,15 +1015,15 @@ cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_
     *st = VC_ERR_WORKSPACE;
     return cudaSuccess;
   }
-  bool maps = a.pn <= 0 || (live_map(&p.tm[0][0], a.pk, a.d, a.pn, a.pcap, a.Hkv) &&
-                            live_map(&p.tm[0][1], a.pv, a.d, a.pn, a.pcap, a.Hkv));
-  for (int b = 0; b < a.B && maps; ++b) {
+  bool made = a.pn <= 0 || (live_map(&maps.tm[0][0], a.pk, a.d, a.pn, a.pcap, a.Hkv) &&
+                            live_map(&maps.tm[0][1], a.pv, a.d, a.pn, a.pcap, a.Hkv));
+  for (int b = 0; b < a.B && made; ++b) {
     const LiveReqDev& r = a.req[b];
     const int g = p.own_of[b];
     if (g >= 0)
-      maps = live_map(&p.tm[g][0], r.k, a.d, r.n, r.cap, a.Hkv) && live_map(&p.tm[g][1], r.v, a.d, r.n, r.cap, a.Hkv);
+      made = live_map(&maps.tm[g][0], r.k, a.d, r.n, r.cap, a.Hkv) && live_map(&maps.tm[g][1], r.v, a.d, r.n, r.cap, a.Hkv);
   }
-  if (!maps) {
+  if (!made) {
     *st = VC_ERR_CUDA;
     return cudaSuccess;
   }
@@ -888,8 +1031,8 @@ cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_
     p.grp[g].s = scores;
     scores += (size_t)a.Hkv * p.grp[g].rows * p.grp[g].tiles * LN;
   }
-  if (a.d == 128) return scored ? launch_live_t<128, true>(p, s) : launch_live_t<128, false>(p, s);
-  return scored ? launch_live_t<64, true>(p, s) : launch_live_t<64, false>(p, s);
+  if (a.d == 128) return scored ? launch_live_t<128, true>(p, maps, s) : launch_live_t<128, false>(p, maps, s);
+  return scored ? launch_live_t<64, true>(p, maps, s) : launch_live_t<64, false>(p, maps, s);
 }
 
 }  // namespace vc
