@@ -88,10 +88,9 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_select_kernel(const __gri
     const int lead = __ffs(act) - 1;
     const uint32_t lead_dg = __shfl_sync(0xffffffffu, dg, lead);
     const unsigned same = __ballot_sync(0xffffffffu, in && dg == lead_dg);
-    if (lane == lead)
-      atomicAdd(&count[dg * kEvCopies], (uint32_t)__popc(same));
-    else if (in && !((same >> lane) & 1u))
-      atomicAdd(&count[dg * kEvCopies + lane % kEvCopies], 1u);
+    const bool joined = (same >> lane) & 1u;  // one atomic instruction for all
+    if (lane == lead || (in && !joined))
+      atomicAdd(&count[dg * kEvCopies + lane % kEvCopies], joined ? (uint32_t)__popc(same) : 1u);
   };
   if (tid == 0) s_rem = (uint32_t)keep;
   __syncthreads();
@@ -241,7 +240,7 @@ template <int D>
 __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictParams p, int per_warp) {
   constexpr int LANES = D / 4;       // 16-byte pieces of a row of K and of V
   constexpr int RW = 32 / LANES;     // rows a warp copies at a time
-  constexpr int U = 4;               // of those, in flight
+  constexpr int U = 8;               // of those, in flight
   pdl_wait();
   pdl_launch_dependents();
   const int h = blockIdx.y, lane = threadIdx.x & 31;

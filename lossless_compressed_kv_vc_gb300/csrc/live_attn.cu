@@ -101,21 +101,6 @@ __device__ __forceinline__ int cta_of(const LiveParams& p, int kind, int x) {
   return x < e ? x / (each + 1) : more + (x - e) / each;
 }
 
-template <int D>
-struct LCfg {
-  static constexpr int KB = D / 64;            // 64-channel (128-byte) blocks
-  static constexpr int T_BYTES = KB * LN * 128;  // a K, V or Q tile
-  static constexpr int NST = D == 128 ? 5 : 10;  // K and V tiles in flight or in use
-  static constexpr int OFF_T = 2 * T_BYTES;    // behind a Q tile per chain
-  static constexpr int OFF_BAR = OFF_T + NST * T_BYTES;
-  static constexpr int SMEM = OFF_BAR + 384;
-  static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
-  static_assert((2 * NST + 20) * 8 + 20 <= 384, "barriers fit");
-  static constexpr int OCOL = 4 * LS;          // TMEM: S (and P) of chain w at (2 w + step % 2) LS, O at OCOL + w D
-  static constexpr uint32_t TCOLS = 512;
-  static_assert(OCOL + 2 * D <= (int)TCOLS, "TMEM");
-};
-
 // Steps of tile j of n keys: its second half only where it holds keys.
 __device__ __forceinline__ int live_steps(int n, int j) { return n - j * LN > LS ? 2 : 1; }
 
@@ -156,6 +141,21 @@ struct LPiece {
   }
 };
 
+template <int D>
+struct LCfg {
+  static constexpr int KB = D / 64;            // 64-channel (128-byte) blocks
+  static constexpr int T_BYTES = KB * LN * 128;  // a K, V or Q tile
+  static constexpr int NST = D == 128 ? 5 : 10;  // K and V tiles in flight or in use
+  static constexpr int OFF_T = 2 * T_BYTES;    // behind a Q tile per chain
+  static constexpr int OFF_BAR = OFF_T + NST * T_BYTES;
+  static constexpr int SMEM = OFF_BAR + 448;
+  static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
+  static_assert((2 * NST + 20) * 8 + 24 + sizeof(LPiece) <= 448, "barriers fit");
+  static constexpr int OCOL = 4 * LS;          // TMEM: S (and P) of chain w at (2 w + step % 2) LS, O at OCOL + w D
+  static constexpr uint32_t TCOLS = 512;
+  static_assert(OCOL + 2 * D <= (int)TCOLS, "TMEM");
+};
+
 __device__ __forceinline__ LPiece live_first(const LiveParams& p) {
   LPiece q;
   const int kind = (int)blockIdx.x < p.n_cta[0] ? 0 : 1, c = blockIdx.x - (kind ? p.n_cta[0] : 0);
@@ -178,15 +178,6 @@ __device__ __forceinline__ LPiece live_first(const LiveParams& p) {
 }
 
 __device__ __forceinline__ int live_req_of(const LiveParams& p, int tok) { return last_begin(p.tok_begin, p.B, tok); }
-
-// A launch's parameters are cold in every constant cache: thread t of n reads every n-th 64-byte line of them,
-// so that the searches that follow do not wait for one line after the other (1 us each).
-template <typename T>
-__device__ __forceinline__ void touch_params(const T& p, int t, int n) {
-  const int* w = reinterpret_cast<const int*>(&p);
-#pragma unroll 1
-  for (int i = t; i < (int)(sizeof(T) / 64); i += n) asm volatile("" ::"r"(w[i * 16]));
-}
 
 __device__ __forceinline__ void prefetch_tmap(const void* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
@@ -240,9 +231,10 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
   volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
   volatile uint32_t* s_odd = tslot + 2;  // [2] 1 + the chain's last step whose P V the softmax warps took
   volatile uint32_t* s_issued = tslot + 4;  // loads issued so far
+  LPiece* s_first = reinterpret_cast<LPiece*>(tslot + 6);  // the CTA's first piece
 
   if (warp == 12) tc05::alloc(tslot, C::TCOLS);
-  if (warp >= 13) touch_params(p, tid - 13 * 32, 96);
+  if (tid == 13 * 32) *s_first = live_first(p);  // once: its code and parameters are cold in every cache
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(&full[i], 1);
@@ -295,7 +287,7 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
     if (warp == 12) {
       // ---- TMA: tiles in order, K then V of each ---------------------------------------------------
       if (lane == 0) {
-        LPiece q = live_first(p);
+        LPiece q = *s_first;
         prefetch_tmap(&maps.tm[q.g][1]);
         uint32_t it = 0;
         bool ok = true;
@@ -330,7 +322,7 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
         const int w = warp - 10;
         constexpr uint32_t IDESC_O = tc05::idesc_bf16(LM, D, true);
         const uint32_t aT = smem_u32(smem + C::OFF_T), tS = tmem + 2 * w * LS, tO = tmem + C::OCOL + w * D;
-        LPiece q = live_first(p);
+        LPiece q = *s_first;
         uint32_t g = 0, t = 0, seen = 0;  // tiles of the CTA, steps of the chain
         bool ok = true;
         for (; q.valid() && ok; q.next(p)) {
@@ -370,7 +362,7 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
         constexpr uint32_t IDESC_S = tc05::idesc_bf16(LM, LS, false);
         const uint32_t aQ = smem_u32(smem) + w * C::T_BYTES, aT = smem_u32(smem + C::OFF_T);
         const uint32_t tS = tmem + 2 * w * LS;
-        LPiece q = live_first(p);
+        LPiece q = *s_first;
         uint32_t g = 0, t = 0, u = 0, seen = 0;  // tiles of the CTA, steps and pieces of the chain
         bool ok = true;
         for (; q.valid() && ok; q.next(p)) {
@@ -412,7 +404,7 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + 2 * w * LS, tO = tmem + lane_off + C::OCOL + w * D;
     uint8_t* sQ = smem + w * C::T_BYTES;
-    LPiece q = live_first(p);
+    LPiece q = *s_first;
     uint32_t g = 0, t = 0, looked = 0, seen = 0;
     // P V of step s done (and with it those before): asked for steps whose S has been read, so the phase
     // before on that buffer is over
@@ -453,19 +445,59 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
         return;
       }
     };
-    fetch();
-    while (q.valid()) {
+    // the chain's partial of the piece before: written once the next one's S are under way
+    size_t part = 0;
+    float m_run = 0.f, l_run = 0.f;
+    bool row_ok = false, have = false;
+    while (ok) {
+      fetch();
+      if (have) {
+        // after its last P V
+        if (!pv_done(t - 1)) break;
+        tc05::fence_after();
+        const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
+        // rows in the order of an MMA's accumulator: four lanes hold 8 neighbouring channels (whole 32-byte
+        // sectors), where a lane per row would write 32 lines at a time
+        float* o_row0 = p.ws_o[kind] + (part - (rt & 31)) * D + 2 * (lane & 3);  // of the warp's first row
+        const unsigned rows_ok = __ballot_sync(0xffffffffu, row_ok);
+#pragma unroll 1
+        for (int hh = 0; hh < 2; ++hh) {
+          if (!((rows_ok >> (16 * hh)) & 0xffffu)) continue;
+          const int r0 = hh * 16 + (lane >> 2), r1 = r0 + 8;
+          const float i0 = __shfl_sync(0xffffffffu, inv, r0), i1 = __shfl_sync(0xffffffffu, inv, r1);
+          const bool ok0 = (rows_ok >> r0) & 1u, ok1 = (rows_ok >> r1) & 1u;
+#pragma unroll 1
+          for (int cb = 0; cb < D / 32; ++cb) {
+            uint32_t r[16];
+            tc05::ld16x256_x4(tO + ((uint32_t)(hh * 16) << 16) + cb * 32, r);  // warp-collective: every lane loads
+            tc05::wait_ld();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (ok0)
+                *reinterpret_cast<float2*>(o_row0 + (size_t)r0 * D + cb * 32 + 8 * k) =
+                    make_float2(__uint_as_float(r[4 * k]) * i0, __uint_as_float(r[4 * k + 1]) * i0);
+              if (ok1)
+                *reinterpret_cast<float2*>(o_row0 + (size_t)r1 * D + cb * 32 + 8 * k) =
+                    make_float2(__uint_as_float(r[4 * k + 2]) * i1, __uint_as_float(r[4 * k + 3]) * i1);
+            }
+          }
+        }
+        if (row_ok) p.ws_lse[kind][part] = l_run != 0.f ? m_run + log2f(l_run) : -INFINITY;
+        tc05::fence_before();
+      }
+      if (!q.valid()) break;
+      have = true;
       const LiveGroup& R = p.grp[q.g];
       const int ru = q.split ? rt : w * LM + rt;
-      const bool row_ok = ru < q.rows;
+      row_ok = ru < q.rows;
       const int row = q.u * LU + ru, tl = row / p.G;
-      const size_t part = slot_of(R) * p.slot_rows[kind] + (q.split ? w * q.rows : 0) + ru;
+      part = slot_of(R) * p.slot_rows[kind] + (q.split ? w * q.rows : 0) + ru;
       // last key the row sees, and the first one that some row of the chain does not
       const int n = R.n;
       const int last_key = R.causal ? n - R.n_rows + tl : n - 1;
       const int blind = R.causal ? n - R.n_rows + (q.u * LU + (q.split ? 0 : w * LM)) / p.G + 1 : n;
       float* s_row = SCORED ? R.s + ((size_t)q.hk * R.rows + row) * ((size_t)R.tiles * LN) : nullptr;
-      float m_run = -INFINITY, l_run = 0.f;
+      m_run = -INFINITY, l_run = 0.f;
       bool fresh = true;  // the piece's first step
       for (int j = q.j0; j < q.j1 && ok; ++j, ++g) {
         const int h1 = q.h1(w, n, j);
@@ -633,42 +665,6 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
       }
       if (!ok) break;
       q.next(p);
-      fetch();
-      // the chain's partial of the piece, after its last P V (the next one's S are under way)
-      if (!pv_done(t - 1)) {
-        ok = false;
-        break;
-      }
-      tc05::fence_after();
-      const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
-      // rows in the order of an MMA's accumulator: four lanes hold 8 neighbouring channels (whole 32-byte
-      // sectors), where a lane per row would write 32 lines at a time
-      float* o_row0 = p.ws_o[kind] + (part - (rt & 31)) * D + 2 * (lane & 3);  // of the warp's first row
-      const unsigned rows_ok = __ballot_sync(0xffffffffu, row_ok);
-#pragma unroll 1
-      for (int hh = 0; hh < 2; ++hh) {
-        if (!((rows_ok >> (16 * hh)) & 0xffffu)) continue;
-        const int r0 = hh * 16 + (lane >> 2), r1 = r0 + 8;
-        const float i0 = __shfl_sync(0xffffffffu, inv, r0), i1 = __shfl_sync(0xffffffffu, inv, r1);
-        const bool ok0 = (rows_ok >> r0) & 1u, ok1 = (rows_ok >> r1) & 1u;
-#pragma unroll 1
-        for (int cb = 0; cb < D / 32; ++cb) {
-          uint32_t r[16];
-          tc05::ld16x256_x4(tO + ((uint32_t)(hh * 16) << 16) + cb * 32, r);  // warp-collective: every lane loads
-          tc05::wait_ld();
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (ok0)
-              *reinterpret_cast<float2*>(o_row0 + (size_t)r0 * D + cb * 32 + 8 * k) =
-                  make_float2(__uint_as_float(r[4 * k]) * i0, __uint_as_float(r[4 * k + 1]) * i0);
-            if (ok1)
-              *reinterpret_cast<float2*>(o_row0 + (size_t)r1 * D + cb * 32 + 8 * k) =
-                  make_float2(__uint_as_float(r[4 * k + 2]) * i1, __uint_as_float(r[4 * k + 3]) * i1);
-          }
-        }
-      }
-      if (row_ok) p.ws_lse[kind][part] = l_run != 0.f ? m_run + log2f(l_run) : -INFINITY;
-      tc05::fence_before();
     }
   }
 

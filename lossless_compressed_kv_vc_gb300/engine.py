@@ -17,7 +17,7 @@ from . import (vc_shape, vc_kv_full, vc_kv_comp, vc_draft_req, vc_verify_req, vc
                vc_snapkv_importance, vc_importance_workspace_size, VC_POOL_MAX, vc_compress_kv, vc_comp_bytes,
                vc_draft_attn, vc_verify_attn, vc_verify_attn_heads, vc_verify_launches, vc_accept, vc_append_kv, vc_workspace_size,
                vc_rope, vc_rope_req, vc_live_req, vc_evict_req, live_kv, vc_rope_append, vc_prefix_attn,
-               vc_prefix_workspace_size, vc_scored_attn, vc_scored_workspace_size, vc_evict_kv, vc_evict_workspace_size,
+               vc_prefix_workspace_size, _stream, vc_scored_attn, vc_scored_workspace_size, vc_evict_kv, vc_evict_workspace_size,
                VC_TOKEN_DROP, VC_QUANT, VC_CALL_DRAFT, VC_CALL_VERIFY)
 
 
@@ -769,7 +769,7 @@ class LiveBatch:
         device by then."""
         if torch.cuda.is_current_stream_capturing():
             return
-        Batch._order(self, torch.cuda.current_stream(self.device) if stream is None else stream)
+        Batch._order(self, _stream(None) if stream is None else stream)
 
     def _kv(self, b: int):
         return live_kv(self.k[b], self.v[b], self.n[b], None if self.score is None else self.score[b],
