@@ -36,8 +36,8 @@ constexpr int LU = 2 * LM;      // query rows of a unit
 // warps 0-3, 4-7 softmax of chains 0 and 1; 8, 9 issue their S; 10, 11 their P V; 12 TMA; 13-15 idle (they
 // make a warpgroup with it: registers are handed over by warpgroup)
 constexpr int LTHREADS = 512;
-// Registers a thread: launched with 128 (65536 / 512), then 168 in the softmax warpgroups and 80 in the others
-constexpr int LREG_SOFTMAX = 168, LREG_ISSUE = 80;
+// Registers a thread: launched with 128 (65536 / 512), then 144 in the softmax warpgroups and 80 in the others
+constexpr int LREG_SOFTMAX = 144, LREG_ISSUE = 80;
 static_assert(256 * (LREG_SOFTMAX + LREG_ISSUE) <= 65536, "no more than the block was launched with");
 constexpr int SCORE_KEYS = 1024;  // keys of a score block: four a thread
 static_assert(SCORE_KEYS == 4 * 256 && LN % 4 == 0, "whole vectors of scores");
@@ -75,6 +75,7 @@ struct LiveParams {
   int32_t n_grp, has_prefix;
   // by kind: its CTAs, the cost of each one's range and how many (the first) have one more
   int32_t n_cta[2], cta_cost[2], cta_more[2];
+  int32_t keep_ws;                      // tiles read once leave L2 (evict first) to the workspace
   int32_t merge_blocks, score_blocks;
   int32_t slot_rows[2];                 // partial rows of a slot: prefix, own
   float* ws_o[2];                       // [slots][slot_rows][d]; slot = CTA of the kind + (unit, head)
@@ -289,6 +290,7 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
       if (lane == 0) {
         LPiece q = *s_first;
         prefetch_tmap(&maps.tm[q.g][1]);
+        const uint64_t pol = l2_evict_first_policy();
         uint32_t it = 0;
         bool ok = true;
         for (; q.valid() && ok; q.next(p)) {
@@ -296,6 +298,7 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
             prefetch_tmap(&maps.tm[q.g + 1][0]);
             prefetch_tmap(&maps.tm[q.g + 1][1]);
           }
+          const bool once = p.keep_ws && p.grp[q.g].units == 1;  // tiles that one CTA reads once
           for (int j = q.j0; j < q.j1 && ok; ++j)
             for (int kv = 0; kv < 2; ++kv) {
               const uint32_t st = it % NST;
@@ -305,9 +308,15 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
               }
               uint8_t* dst = smem + C::OFF_T + st * C::T_BYTES;
               mbar_arrive_expect_tx(&full[st], C::T_BYTES);
+              if (once) {
 #pragma unroll
-              for (int kb = 0; kb < C::KB; ++kb)
-                tc05::tma_load_3d(dst + kb * (LN * 128), &maps.tm[q.g][kv], kb * 64, j * LN, q.hk, &full[st]);
+                for (int kb = 0; kb < C::KB; ++kb)
+                  tc05::tma_load_3d_hint(dst + kb * (LN * 128), &maps.tm[q.g][kv], kb * 64, j * LN, q.hk, &full[st], pol);
+              } else {
+#pragma unroll
+                for (int kb = 0; kb < C::KB; ++kb)
+                  tc05::tma_load_3d(dst + kb * (LN * 128), &maps.tm[q.g][kv], kb * 64, j * LN, q.hk, &full[st]);
+              }
               __threadfence_block();
               *s_issued = ++it;
             }
@@ -631,14 +640,13 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
                   for (int e = 0; e < 32; ++e) r[e] = 0u;
                 }
 #pragma unroll 1
-                for (int k8 = 0; k8 < LS / 16; ++k8) {
-                  uint32_t pw[8];
-                  tc05::ld8(tP + k8 * 8, pw);
+                for (int kp = 0; kp < LS / 2; ++kp) {  // two keys a column; rare, so kept small
+                  const uint32_t pw = tc05::ld1(tP + kp);
                   tc05::wait_ld();
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) {
-                    const int k = k8 * 16 + e, kt = h * LS + k;
-                    const float pk = __uint_as_float(e & 1 ? pw[e >> 1] & 0xffff0000u : pw[e >> 1] << 16);
+                  for (int e = 0; e < 2; ++e) {
+                    const int k = 2 * kp + e, kt = h * LS + k;
+                    const float pk = __uint_as_float(e ? pw & 0xffff0000u : pw << 16);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                       const int ch = cb * 4 + c;
@@ -1011,6 +1019,9 @@ cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_
     *st = VC_ERR_WORKSPACE;
     return cudaSuccess;
   }
+  // Partials and scores up to half of L2 are found there by the second kernel if the tiles do not push them
+  // out (scored decode, 8 MB of scores: 50.9 us without the hint, 48.9 with it; 134 MB: 371.8 and 377.8)
+  p.keep_ws = need <= (size_t)64 << 20;
   bool made = a.pn <= 0 || (live_map(&maps.tm[0][0], a.pk, a.d, a.pn, a.pcap, a.Hkv) &&
                             live_map(&maps.tm[0][1], a.pv, a.d, a.pn, a.pcap, a.Hkv));
   for (int b = 0; b < a.B && made; ++b) {
