@@ -319,11 +319,12 @@ cudaError_t launch_evict(const EvictParams& p, int d, cudaStream_t s) {
     n = p.req[b].n > n ? p.req[b].n : n;
     room = p.req[b].room > room ? p.req[b].room : room;
   }
-  // CTAs per head: as many as one wave holds (two CTAs an SM), with at least 1024 rows each (below that the
-  // passes' fixed part, about 8 us, is all that is left), and enough to hold the ranks
+  // CTAs per head: enough to hold the ranks; as many as one wave holds (two CTAs an SM) with at least 1024 rows
+  // each (below that the passes' fixed part, about 8 us, is all that is left); and in several waves still with
+  // 4096 rows each, which even out over the SMs
   const int64_t all = (int64_t)p.Hkv * p.B;
   int cl = 1;
-  while (cl < 8 && (n > cl * kEvHeld || (all * cl * 2 <= 304 && n >= cl * 2 * 1024))) cl *= 2;
+  while (cl < 8 && (n > cl * kEvHeld || (all * cl * 2 <= 304 && n >= cl * 2 * 1024) || n >= cl * 2 * 4096)) cl *= 2;
   cudaError_t e = n > 8 * kEvHeld ? launch_select<8, false>(p, n, s)
                   : cl == 8       ? launch_select<8, true>(p, n, s)
                   : cl == 4       ? launch_select<4, true>(p, n, s)

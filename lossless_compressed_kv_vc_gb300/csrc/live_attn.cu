@@ -39,8 +39,8 @@ constexpr int LTHREADS = 512;
 // Registers a thread: launched with 128 (65536 / 512), then 144 in the softmax warpgroups and 80 in the others
 constexpr int LREG_SOFTMAX = 144, LREG_ISSUE = 80;
 static_assert(256 * (LREG_SOFTMAX + LREG_ISSUE) <= 65536, "no more than the block was launched with");
-constexpr int SCORE_KEYS = 1024;  // keys of a score block: four a thread
-static_assert(SCORE_KEYS == 4 * 256 && LN % 4 == 0, "whole vectors of scores");
+constexpr int SCORE_KEYS = 1024;  // keys of a score block: 256 a pass
+static_assert(SCORE_KEYS % 256 == 0 && LN % 4 == 0, "whole vectors of scores");
 
 struct LiveGroup {
   int32_t n;          // keys
@@ -53,7 +53,7 @@ struct LiveGroup {
   int32_t unit_begin; // first (unit, head) among those of its kind (prefix or own)
   float* score;
   int64_t cap;        // row stride of score
-  float* s;           // scored: scores in the log2 domain [Hkv][rows][tiles * LN]
+  float* s;           // scored: q . k of every row and key, [Hkv][tiles * LN / 4][rows][4 keys], -inf where not seen
 };
 
 // K and V of each group: read by the attention kernel alone.
@@ -76,7 +76,8 @@ struct LiveParams {
   // by kind: its CTAs, the cost of each one's range and how many (the first) have one more
   int32_t n_cta[2], cta_cost[2], cta_more[2];
   int32_t keep_ws;                      // tiles read once leave L2 (evict first) to the workspace
-  int32_t merge_blocks, score_blocks;
+  int32_t merge_blocks, merge_warps;    // blocks of the merge, warps a row (1, 2, 4 or 8)
+  int32_t score_blocks;
   int32_t slot_rows[2];                 // partial rows of a slot: prefix, own
   float* ws_o[2];                       // [slots][slot_rows][d]; slot = CTA of the kind + (unit, head)
   float* ws_lse[2];                     // [slots][slot_rows], log2 domain, -inf: saw nothing
@@ -505,7 +506,8 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
       const int n = R.n;
       const int last_key = R.causal ? n - R.n_rows + tl : n - 1;
       const int blind = R.causal ? n - R.n_rows + (q.u * LU + (q.split ? 0 : w * LM)) / p.G + 1 : n;
-      float* s_row = SCORED ? R.s + ((size_t)q.hk * R.rows + row) * ((size_t)R.tiles * LN) : nullptr;
+      const int s_rows = R.rows;
+      float4* s_row = SCORED ? reinterpret_cast<float4*>(R.s) + (size_t)q.hk * R.tiles * (LN / 4) * s_rows + row : nullptr;
       m_run = -INFINITY, l_run = 0.f;
       bool fresh = true;  // the piece's first step
       for (int j = q.j0; j < q.j1 && ok; ++j, ++g) {
@@ -534,12 +536,10 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
               if (e > last) x[e] = -INFINITY;
           }
           if constexpr (SCORED) {
-            if (row_ok) {
-              float4* d = reinterpret_cast<float4*>(s_row + k0);
+            if (row_ok) {  // four keys of neighbouring rows in neighbouring lanes: whole lines
+              float4* d = s_row + (size_t)(k0 / 4) * s_rows;
 #pragma unroll
-              for (int e = 0; e < LS / 4; ++e)
-                d[e] = make_float4(x[4 * e] * p.scale_log2, x[4 * e + 1] * p.scale_log2, x[4 * e + 2] * p.scale_log2,
-                                   x[4 * e + 3] * p.scale_log2);
+              for (int e = 0; e < LS / 4; ++e, d += s_rows) *d = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
             }
           }
           // P = 2^(x scale - m), bf16, over S, with the running maximum as it is: the row's new one is found
@@ -607,13 +607,12 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
             }
             const uint8_t* sV = smem + C::OFF_T + (iv % NST) * C::T_BYTES;
             bool bad = false;
-            if (rt < LS) {
-              const int k = h * LS + rt;
-#pragma unroll 1
-              for (int c = 0; c < D / 8; ++c) {
-                const uint4 v = *reinterpret_cast<const uint4*>(sV + (c >> 3) * (LN * 128) + k * 128 + (((c ^ k) & 7) << 4));
-                bad |= nonfinite_bf16x2(v.x) || nonfinite_bf16x2(v.y) || nonfinite_bf16x2(v.z) || nonfinite_bf16x2(v.w);
-              }
+            const int kv = h * LS + (rt & (LS - 1));  // two threads look through each of the step's rows
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              const int c = (rt / LS) * (D / 16) + i;
+              const uint4 v = *reinterpret_cast<const uint4*>(sV + (c >> 3) * (LN * 128) + kv * 128 + (((c ^ kv) & 7) << 4));
+              bad |= nonfinite_bf16x2(v.x) || nonfinite_bf16x2(v.y) || nonfinite_bf16x2(v.z) || nonfinite_bf16x2(v.w);
             }
             if (bad) s_odd[w] = t + 1;
             __syncwarp();
@@ -705,15 +704,17 @@ __device__ __forceinline__ LParts live_parts(const LiveParams& p, int kind, int 
   return q;
 }
 
-// Merge: a warp per (token, query head), o = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M) over the
+// Merge: one to eight warps per (token, query head), o = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M) over the
 // partials of the prefix and of the own cache: a lane per partial takes the weights, then the warp adds
 // up the partials' channels, four loads in flight. Scores: a block per 1024 keys of a (request, KV head)
-// merges the head's rows' lse, a warp a row, then sums 2^(s - lse) over the rows for each key.
+// merges the head's rows' lse, a warp a row, then sums 2^(s scale - lse) over the rows for each key.
 template <int D, bool SCORED>
 __global__ void __launch_bounds__(256, SCORED ? 3 : 4) live_finish_kernel(const __grid_constant__ LiveParams p) {
   constexpr int E = D / 32;  // channels a lane
   constexpr int PF = 4;      // partials in flight
+  constexpr int SP = SCORE_KEYS / 256;
   __shared__ float s_lse[VC_SCORED_MAX_ROWS];
+  __shared__ float s_acc[8][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto warp_max = [](float v) {
 #pragma unroll
@@ -727,34 +728,37 @@ __global__ void __launch_bounds__(256, SCORED ? 3 : 4) live_finish_kernel(const 
   };
   // weight of a partial beside the largest lse M: 0 where it saw nothing; M stays -inf only beside a NaN
   auto weight = [](float l, float M) { return l == -INFINITY ? 0.f : M == -INFINITY ? NAN : exp2f(l - M); };
-  if ((int)blockIdx.x < p.merge_blocks) {
-    const int64_t id = (int64_t)blockIdx.x * 8 + warp;
-    if (id >= (int64_t)p.n_tok * p.Hq) {
-      pdl_wait();
-      return;
-    }
-    const int tok = (int)(id / p.Hq), hq = (int)(id - (int64_t)tok * p.Hq), hk = hq / p.G, gq = hq - hk * p.G;
-    const int b = live_req_of(p, tok), i = tok - p.tok_begin[b], own = p.own_of[b];
+  if (!SCORED || (int)blockIdx.x >= p.score_blocks) {  // the longer score blocks go first
+    const int wpr = p.merge_warps, part = warp % wpr;  // warps of a row, this one among them
+    const int64_t id = (int64_t)(blockIdx.x - p.score_blocks) * (8 / wpr) + warp / wpr;
+    const bool live = id < (int64_t)p.n_tok * p.Hq;
     LParts a{0, 0, 0, 0}, o{0, 0, 0, 0};  // of the prefix, of the own cache
-    if (p.has_prefix) a = live_parts(p, 0, 0, hk, tok * p.G + gq);
-    if (own >= 0) o = live_parts(p, 1, own, hk, i * p.G + gq);
+    bf16* dst = nullptr;
+    if (live) {
+      const int tok = (int)(id / p.Hq), hq = (int)(id - (int64_t)tok * p.Hq), hk = hq / p.G, gq = hq - hk * p.G;
+      const int b = live_req_of(p, tok), i = tok - p.tok_begin[b], own = p.own_of[b];
+      if (p.has_prefix) a = live_parts(p, 0, 0, hk, tok * p.G + gq);
+      if (own >= 0) o = live_parts(p, 1, own, hk, i * p.G + gq);
+      dst = p.o[b] + ((size_t)i * p.Hq + hq) * D + lane * E;
+    }
     pdl_wait();  // what needs the parameters alone is done
     pdl_launch_dependents();
     const int total = a.count + o.count;
-    auto lse_of = [&](int k) {
-      return k < a.count ? p.ws_lse[0][a.at(k)] : k < total ? p.ws_lse[1][o.at(k - a.count)] : -INFINITY;
+    auto lse_of = [&](int k, int end) {
+      return k >= end ? -INFINITY : k < a.count ? p.ws_lse[0][a.at(k)] : p.ws_lse[1][o.at(k - a.count)];
     };
     float M = -INFINITY;
-    for (int k0 = 0; k0 < total; k0 += 32) M = fmaxf(M, lse_of(k0 + lane));
+    for (int k0 = 0; k0 < total; k0 += 32) M = fmaxf(M, lse_of(k0 + lane, total));
     M = warp_max(M);
     float L = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int k0 = 0; k0 < total; k0 += 32) {
-      const float l = lse_of(k0 + lane), f = weight(l, M);
+    const int beg = total * part / wpr, end = total * (part + 1) / wpr;
+    for (int k0 = beg; k0 < end; k0 += 32) {
+      const float l = lse_of(k0 + lane, end), f = weight(l, M);
       const unsigned wrote = __ballot_sync(0xffffffffu, l != -INFINITY);
       L += f;
-      const int cnt = min(32, total - k0);
+      const int cnt = min(32, end - k0);
       for (int c0 = 0; c0 < cnt; c0 += PF) {
         float v[PF][E], fc[PF];
 #pragma unroll
@@ -778,8 +782,20 @@ __global__ void __launch_bounds__(256, SCORED ? 3 : 4) live_finish_kernel(const 
       }
     }
     L = warp_sum(L);
+    if (wpr > 1) {  // the row's warps meet
+#pragma unroll
+      for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+      if (lane == 0) s_lse[warp] = L;
+      __syncthreads();
+      if (part != 0) return;
+      for (int u = 1; u < wpr; ++u) {
+        L += s_lse[warp + u];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += s_acc[warp + u][lane * E + e];
+      }
+    }
+    if (!live) return;
     const float inv = L != 0.f ? 1.f / L : 0.f;
-    bf16* dst = p.o[b] + ((size_t)i * p.Hq + hq) * D + lane * E;
     uint32_t out[E / 2];
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
@@ -790,30 +806,31 @@ __global__ void __launch_bounds__(256, SCORED ? 3 : 4) live_finish_kernel(const 
     return;
   }
   if constexpr (SCORED) {
-    const int id = blockIdx.x - p.merge_blocks;
+    const int id = blockIdx.x;
     const int g = last_begin(p.chunk_begin, p.n_grp, id);
     const LiveGroup& R = p.grp[g];
     const int chunks = (R.n + SCORE_KEYS - 1) / SCORE_KEYS;
     const int hk = (id - p.chunk_begin[g]) / chunks, k0 = (id - p.chunk_begin[g] - hk * chunks) * SCORE_KEYS;
-    const size_t stride = (size_t)R.tiles * LN;
-    const int key = k0 + 4 * threadIdx.x, left = R.n - key;  // a thread's four keys; S rows are whole tiles
-    const float* s = R.s + (size_t)hk * R.rows * stride + key;
-    float* score = R.score + (size_t)hk * R.cap + key;
-    const int rows = R.rows;
+    const int rows = R.rows, gl = threadIdx.x & 3;  // four lanes share a group of four keys, rows gl, gl + 4, ...
+    const float4* s = reinterpret_cast<const float4*>(R.s) + ((size_t)hk * R.tiles * (LN / 4) + k0 / 4 + threadIdx.x / 4) * rows;
+    float* score = R.score + (size_t)hk * R.cap + k0 + threadIdx.x;  // its key in a pass of 256
+    const int left = R.n - k0 - (int)threadIdx.x, quads = (R.n - k0 + 3) / 4 - (int)threadIdx.x / 4;
     LParts part{0, 0, 0, 0};
     if (warp < rows) part = live_parts(p, 1, g, hk, warp);
     pdl_wait();
     pdl_launch_dependents();
-    float4 v[8];
-    auto load8 = [&](int r0) {
+    float4 v[SP][2];
+    auto load2 = [&](int r0) {
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (r0 + r < rows && left > 0) v[r] = __ldg(reinterpret_cast<const float4*>(s + (r0 + r) * stride));
+      for (int c = 0; c < SP; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (r0 + 4 * e < rows && 64 * c < quads) v[c][e] = __ldg(s + (size_t)(64 * c) * rows + r0 + 4 * e);
     };
-    load8(0);  // in flight while the rows' lse are merged
-    float w[4];
+    load2(gl);  // in flight while the rows' lse are merged
+    float w[SP];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) w[c] = c < left ? score[c] : 0.f;
+    for (int c = 0; c < SP; ++c) w[c] = 256 * c < left ? score[256 * c] : 0.f;
     for (int r = warp; r < rows; r += 8) {
       if (r > warp) part = live_parts(p, 1, g, hk, r);
       float M = -INFINITY, L = 0.f;
@@ -824,23 +841,37 @@ __global__ void __launch_bounds__(256, SCORED ? 3 : 4) live_finish_kernel(const 
       if (lane == 0) s_lse[r] = L != 0.f ? M + log2f(L) : INFINITY;  // a row that sees nothing has weights 2^-inf
     }
     __syncthreads();
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-    for (int r0 = 0; r0 < rows; r0 += 8) {
-      if (r0) load8(r0);
+    float4 sum[SP];
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (r0 + r < rows) {
-          const float lse = s_lse[r0 + r];
-          sum[0] += ex2_approx(v[r].x - lse);
-          sum[1] += ex2_approx(v[r].y - lse);
-          sum[2] += ex2_approx(v[r].z - lse);
-          sum[3] += ex2_approx(v[r].w - lse);
+    for (int c = 0; c < SP; ++c) sum[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int r0 = gl; r0 < rows; r0 += 8) {
+      if (r0 != gl) load2(r0);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (r0 + 4 * e < rows) {
+          const float lse = s_lse[r0 + 4 * e];
+#pragma unroll
+          for (int c = 0; c < SP; ++c) {
+            sum[c].x += ex2_approx(fmaf(v[c][e].x, p.scale_log2, -lse));
+            sum[c].y += ex2_approx(fmaf(v[c][e].y, p.scale_log2, -lse));
+            sum[c].z += ex2_approx(fmaf(v[c][e].z, p.scale_log2, -lse));
+            sum[c].w += ex2_approx(fmaf(v[c][e].w, p.scale_log2, -lse));
+          }
         }
     }
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (c < left) score[c] = w[c] + sum[c];
+    for (int c = 0; c < SP; ++c) {
+#pragma unroll
+      for (int off = 1; off < 4; off <<= 1) {
+        sum[c].x += __shfl_xor_sync(0xffffffffu, sum[c].x, off);
+        sum[c].y += __shfl_xor_sync(0xffffffffu, sum[c].y, off);
+        sum[c].z += __shfl_xor_sync(0xffffffffu, sum[c].z, off);
+        sum[c].w += __shfl_xor_sync(0xffffffffu, sum[c].w, off);
+      }
+      const float mine = gl == 0 ? sum[c].x : gl == 1 ? sum[c].y : gl == 2 ? sum[c].z : sum[c].w;
+      if (256 * c < left) score[256 * c] = w[c] + mine;
+    }
   }
 }
 
@@ -987,8 +1018,8 @@ cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_
     R.cap = r.cap;
     add(b, r.n, r.n_rows, r.tok_begin);
   }
-  const int64_t merge = ((int64_t)a.n_tok * a.Hq + 7) / 8;
-  if (*st == VC_OK && merge + chunks >= INT32_MAX) *st = VC_ERR_UNSUPPORTED;
+  const int64_t out_rows = (int64_t)a.n_tok * a.Hq;
+  if (*st == VC_OK && out_rows + chunks >= INT32_MAX / 2) *st = VC_ERR_UNSUPPORTED;
   if (*st != VC_OK) return cudaSuccess;
   share_ctas(cost, least, p.has_prefix ? p.grp[0].rows : 0, p.n_cta);
   for (int kind = 0; kind < 2; ++kind)
@@ -996,7 +1027,16 @@ cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_
       p.cta_cost[kind] = (int32_t)(cost[kind] / p.n_cta[kind]);
       p.cta_more[kind] = (int32_t)(cost[kind] % p.n_cta[kind]);
     }
-  p.merge_blocks = (int32_t)merge;
+  // Warps a row of the merge: a row's partials, about two a CTA that holds part of its units, by fours (one
+  // round trip each); no more than make a wave of blocks (288 rows with 76 partials: 41 us with a warp a row,
+  // 27 with eight).
+  int64_t parts = 0;
+  for (int kind = 0; kind < 2; ++kind)
+    if (units[kind]) parts += 2 * (1 + p.n_cta[kind] / units[kind]);
+  int wpr = 1;
+  while (wpr < 8 && parts > 4 * wpr && out_rows * wpr * 2 <= (int64_t)live_sms() * 4 * 8) wpr *= 2;
+  p.merge_warps = wpr;
+  p.merge_blocks = (int32_t)((out_rows * wpr + 7) / 8);
   p.score_blocks = (int32_t)chunks;
   uint8_t* at = static_cast<uint8_t*>(a.ws);
   size_t need = 0;
