@@ -14,8 +14,10 @@
  *
  * One attention layer is covered: compress (vc_compress_kv), draft attention (vc_draft_attn),
  * verify attention (vc_verify_attn, vc_verify_attn_heads), greedy accept (vc_accept), full-KV
- * staging (vc_stage_full_kv) and the post-accept cache update (vc_append_kv). Every compute step
- * runs in this library's CUDA kernels.
+ * staging (vc_stage_full_kv) and the post-accept cache update (vc_append_kv); and, for caches that
+ * grow, are shared and shrink while requests decode, rotary append (vc_rope_append), attention over
+ * a shared prefix (vc_prefix_attn), attention that gathers each row's weight (vc_scored_attn) and
+ * eviction by it (vc_evict_kv). Every compute step runs in this library's CUDA kernels.
  *
  * Conventions for every call
  *   - The caller owns every buffer. The library never allocates device or host memory and never
@@ -400,7 +402,8 @@ size_t vc_importance_workspace_size(const vc_shape* shape, int32_t window, int32
  * Rows 0..n-1 of every KV head are valid, in any order of positions: attention without a mask does
  * not depend on the order, and vc_evict_kv fills the rows it frees from the back. The caller moves
  * n: up by n_rows after vc_rope_append, to min(n, keep) after vc_evict_kv. Rows n..cap-1 are never
- * read, whatever they hold. */
+ * read, whatever they hold. The requests of one call that write (vc_rope_append, vc_scored_attn,
+ * vc_evict_kv) have caches of their own; vc_prefix_attn only reads them, so requests may share one. */
 typedef struct vc_live_kv {
   void* k;           /* bf16 [Hkv][cap][d] */
   void* v;           /* bf16 [Hkv][cap][d] */

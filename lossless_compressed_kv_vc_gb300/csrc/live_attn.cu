@@ -998,8 +998,8 @@ cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_
       s_floats += (size_t)a.Hkv * R.rows * R.tiles * LN;
     }
     ++p.n_grp;
-    // costs and blocks are counted in 32 bits
-    if (cost[kind] >= INT32_MAX || chunks >= INT32_MAX / 2 || units[kind] >= INT32_MAX / 2) *st = VC_ERR_UNSUPPORTED;
+    // costs (and twice a unit's) and blocks are counted in 32 bits
+    if (cost[kind] >= INT32_MAX / 2 || chunks >= INT32_MAX / 2 || units[kind] >= INT32_MAX / 2) *st = VC_ERR_UNSUPPORTED;
   };
   if (a.pn > 0) {
     p.has_prefix = 1;

@@ -749,6 +749,10 @@ class LiveBatch:
         self.next_pos = [prefix[2] if prefix is not None else 0] * B
         if prefix is not None:
             pk, pv, ctx = prefix
+            for t in (pk, pv):
+                if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape != pk.shape or t.shape[0] != Hkv or \
+                        t.shape[2] != d or not t.is_contiguous() or not 0 <= ctx <= t.shape[1]:
+                    raise ValueError("a prefix is (k, v, rows): contiguous bf16 [Hkv][cap][d], 0 <= rows <= cap")
             self._prefix = vc_kv_full(pk.data_ptr(), pv.data_ptr(), ctx, pk.shape[1])
             size = vc_prefix_workspace_size(self.shape, max_rows)
         else:
@@ -783,7 +787,7 @@ class LiveBatch:
             raise ValueError("rows: one count per request, 0 .. min(max_rows, the tokens given)")
         for t, heads in ((q, self.Hq), (k, self.Hkv), (v, self.Hkv)):
             if t.dtype != torch.bfloat16 or tuple(t.shape) != (self.B, q.shape[1], heads, self.d) or \
-                    t.stride(3) != 1 or t.stride(2) != self.d:
+                    t.stride(3) != 1 or (heads > 1 and t.stride(2) != self.d):
                 raise ValueError("q, k and v are bf16 [B][R][heads][d] with each token's heads contiguous")
         for b in range(self.B):
             e = self._rope_req[b]
@@ -799,7 +803,9 @@ class LiveBatch:
 
     def attend(self, o: torch.Tensor, rows: List[int], stream=None):
         """Attention of the rows just appended, into o bf16 [B][R][Hq][d], R >= max(rows)."""
-        if o.dtype != torch.bfloat16 or o.shape[0] != self.B or o.shape[1] < max(rows) or \
+        if len(rows) != self.B or any(r < 0 or r > self.max_rows for r in rows):
+            raise ValueError("rows: one count per request, 0 .. max_rows")
+        if o.dtype != torch.bfloat16 or o.dim() != 4 or o.shape[0] != self.B or o.shape[1] < max(rows) or \
                 tuple(o.shape[2:]) != (self.Hq, self.d) or not o[0].is_contiguous():
             raise ValueError("o is bf16 [B][R][Hq][d], R >= max(rows), each request's rows contiguous")
         for b in range(self.B):

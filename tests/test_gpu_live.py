@@ -493,6 +493,13 @@ def test_live_batch_refusals(vc):
             lb.append(q, k, x(2), rows)
     with pytest.raises(ValueError):
         lb.attend(x(8, torch.float32), [1, 1])
+    for rows in ([2, 1], [1], [-1, 1]):                          # more rows than the batch holds queries for
+        with pytest.raises(ValueError):
+            lb.attend(x(8), rows)
+    pk = torch.zeros((2, 20, 64), dtype=torch.bfloat16, device="cuda")
+    for prefix in ((pk, pk[:1], 5), (pk, pk, 21), (pk, pk, -1), (pk.float(), pk.float(), 5), (pk[:, ::2], pk[:, ::2], 5)):
+        with pytest.raises(ValueError):
+            engine.LiveBatch(8, 2, 64, 1, 10, t, prefix=prefix)
     lb.n = [10, 0]
     with pytest.raises(vc.VCError):                               # full: the call is refused, nothing moves on
         lb.append(x(8), x(2), x(2), [1, 1])
@@ -587,3 +594,82 @@ def test_draft_after_rope_reads_the_new_queries(vc):
         for a, r in zip(got, bt.reqs):
             assert torch.equal(a, r.o_draft)
         bt.reset_window()
+
+
+def test_offsets_beyond_32_bits(vc):
+    """Caches whose second head starts beyond 2^31 elements (2^32 bytes): append, both attentions, eviction."""
+    Hq, Hkv, d, n, cap = 4, 2, 128, 300, (1 << 24) + 5
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 20 GB")
+    g = gen(21)
+    k, v = (torch.empty((Hkv, cap, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    score = torch.empty((Hkv, cap), device="cuda")
+    pos = torch.empty((Hkv, cap), dtype=torch.int32, device="cuda")
+    k[:, :n], v[:, :n] = randn(g, Hkv, n, d), randn(g, Hkv, n, d)
+    k[:, n : n + 200], v[:, n : n + 200] = NAN, NAN
+    score[:, :n] = torch.rand((Hkv, n), generator=g, device="cuda")
+    pos[:, :n] = torch.arange(n, device="cuda").int()
+    q, kn, vn = randn(g, 3, Hq, d), randn(g, 3, Hkv, d), randn(g, 3, Hkv, d)
+    q_rot, o = torch.empty_like(q), torch.empty_like(q)
+    table = _table(vc, d)
+    shape = vc.vc_shape(1, Hq, Hkv, d)
+    e = vc.vc_rope_req(q=q.data_ptr(), k=kn.data_ptr(), v=vn.data_ptr(), pos0=n, n_rows=3, q_out=q_rot.data_ptr(),
+                       kv=vc.live_kv(k, v, n, score, pos))
+    vc.vc_rope_append(shape, table, (vc.vc_rope_req * 1)(e))
+    n += 3
+    torch.cuda.synchronize()
+    freqs = O.rope_freqs("bands", d, 500000.0, **ROPE["bands"])
+    ref = O.rope(f64(kn), n - 3 + np.arange(3), freqs, False)
+    assert np.all(np.abs(f64(k[:, n - 3 : n].transpose(0, 1)) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -18)
+    assert torch.equal(v[:, n - 3 : n], vn.transpose(0, 1)) and not score[:, n - 3 : n].any()
+    assert torch.isnan(k[:, n : n + 197]).all()
+    was = score[:, :n].clone()
+    live = (vc.vc_live_req * 1)(vc.vc_live_req(q_rot.data_ptr(), o.data_ptr(), 3, vc.live_kv(k, v, n, score)))
+    ref, w = O.live_attn(f64(q_rot), f64(k[:, :n]), f64(v[:, :n]))
+    ws = torch.empty(max(vc.vc_scored_workspace_size(shape, 3, n), vc.vc_prefix_workspace_size(shape, 3),
+                         vc.vc_evict_workspace_size(shape, n)), dtype=torch.uint8, device="cuda")
+    vc.vc_scored_attn(shape, live, ws)
+    torch.cuda.synchronize()
+    assert_attn_close(o, ref, "scored")
+    # as derived at the top of the file, with at most 16 for sum|q k| / sqrt(d)
+    assert np.all(np.abs(f64(score[:, :n]) - f64(was) - w) <= w * (2 * d * 2.0 ** -23 * 16 + 2.0 ** -20) + 2.0 ** -22)
+    o.zero_()
+    vc.vc_prefix_attn(shape, vc.vc_kv_full(k.data_ptr(), v.data_ptr(), n - 100, cap), live, ws)
+    torch.cuda.synchronize()
+    both, _ = O.live_attn(f64(q_rot), f64(k[:, :n]), f64(v[:, :n]), (f64(k[:, : n - 100]), f64(v[:, : n - 100])))
+    assert_attn_close(o, both, "prefix")
+    old = [t[:, :n].clone() for t in (k, v, score, pos)]
+    vc.vc_evict_kv(shape, (vc.vc_evict_req * 1)(vc.vc_evict_req(vc.live_kv(k, v, n, score, pos), 120, 4, n - 10)), ws)
+    torch.cuda.synchronize()
+    for h in range(Hkv):
+        holes, moves = O.evict(old[2][h].cpu().numpy(), old[3][h].cpu().numpy(), 120, 4, n - 10)
+        for t, was in zip((k, v, score, pos), old):
+            want = was[h].clone()
+            want[holes] = was[h][moves]
+            assert np.array_equal(bits(t[h, :n]), bits(want))
+
+
+def test_prefix_requests_may_share_an_own_cache(vc):
+    """vc_prefix_attn only reads caches: two requests over one, each with its own rows."""
+    g = gen(22)
+    Hq, Hkv, d, n = 8, 2, 64, 90
+    k, v, _, _ = cache(g, Hkv, d, n, n + 4)
+    qs = [randn(g, r, Hq, d) for r in (1, 3)]
+    os_ = [torch.zeros_like(q) for q in qs]
+    shape = vc.vc_shape(2, Hq, Hkv, d)
+    arr = (vc.vc_live_req * 2)(*[vc.vc_live_req(q.data_ptr(), o.data_ptr(), q.shape[0], vc.live_kv(k, v, n)) for q, o in zip(qs, os_)])
+    vc.vc_prefix_attn(shape, None, arr, torch.empty(vc.vc_prefix_workspace_size(shape, 3), dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    for q, o in zip(qs, os_):
+        assert_attn_close(o, O.live_attn(f64(q), f64(k[:, :n]), f64(v[:, :n]))[0])
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(64, 64, 64), (48, 1, 128), (96, 2, 64), (300, 1, 64)])
+def test_prefix_uncommon_head_counts(vc, Hq, Hkv, d):
+    """A query head per KV head, many heads on one, groups that do not divide a tile, more than a unit of them."""
+    _attn_case(vc, Hq, Hkv, d, [70, 200, 5], [3, 1, 5], P=150)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(64, 64, 64), (48, 1, 128), (96, 2, 64), (256, 1, 64)])
+def test_scored_uncommon_head_counts(vc, Hq, Hkv, d):
+    _attn_case(vc, Hq, Hkv, d, [70, 200, 1], [1, 256 // (Hq // Hkv) if Hq // Hkv > 1 else 7, 1], scored=True)
