@@ -663,14 +663,15 @@ __global__ void __launch_bounds__(128, NHB == 1 ? DraftCfg<D, KIND>::CTAS_PER_SM
     }
     q_dst += q_grp * C::QRAW;
   }
-  pdl_launch_dependents();
   // Ordering against the previous kernel in the stream (programmatic dependent launch): queries,
   // kept rows and indices are never written by a draft step, verify or accept, so with p.early the
   // warp streams them at once and waits only before it reads window rows (the previous step
   // appended one), stores this step's row, or writes outputs and partials (the previous step's
-  // merges may still be reading the workspace).
+  // merges may still be reading the workspace). Without it, it waits before the next step, which
+  // may be an early one, is let go.
   bool waited = !p.early;
   if (waited) pdl_wait();
+  pdl_launch_dependents();
   auto ensure_wait = [&]() {
     if (!waited) {
       pdl_wait();

@@ -201,9 +201,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc05::fence_after();
   const uint32_t tmem = *tslot;
-  pdl_launch_dependents();
   bool waited = !p.early;
   if (waited) pdl_wait();
+  pdl_launch_dependents();
 
   // this CTA's cost range and the requests it touches
   const int64_t Tot = p.tc_total, P = p.n_cta_head;

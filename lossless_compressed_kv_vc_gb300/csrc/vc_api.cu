@@ -69,9 +69,11 @@ static_assert(VC_DRAFT_COUNTER_BYTES % 256 == 0, "partials start 256-byte aligne
 static size_t draft_counter_bytes() { return VC_DRAFT_COUNTER_BYTES; }
 
 // Last library operation launched on each stream. A draft step may start streaming before the
-// kernel ahead of it in the stream finishes unless that kernel writes KV_comp (a compress or an
-// append after accept: the only writers of kept rows, indices and quantised blocks among the
-// library's kernels, all of which trigger their dependents early).
+// kernel ahead of it in the stream finishes unless a kernel since the last draft step writes KV_comp
+// (a compress, an append after accept, or a call on a live cache: the writers of kept rows, indices
+// and quantised blocks among the library's kernels, which trigger their dependents early). Kernels
+// between them (verify, accept) trigger theirs before they wait, so they do not end the hazard: it
+// lasts until a draft step, which then waits before it triggers its own dependents.
 enum { kOpNone = 0, kOpCompress = 1, kOpDraft = 2, kOpVerify = 3, kOpAccept = 4 };
 static std::mutex g_op_mu;
 static std::unordered_map<cudaStream_t, int> g_last_op;
@@ -84,7 +86,8 @@ static int last_op(cudaStream_t s) {
 
 static void set_last_op(cudaStream_t s, int op) {
   std::lock_guard<std::mutex> lock(g_op_mu);
-  g_last_op[s] = op;
+  int& last = g_last_op[s];
+  if (last != kOpCompress || op == kOpDraft) last = op;
 }
 
 namespace vc {

@@ -673,3 +673,44 @@ def test_prefix_uncommon_head_counts(vc, Hq, Hkv, d):
 @pytest.mark.parametrize("Hq,Hkv,d", [(64, 64, 64), (48, 1, 128), (96, 2, 64), (256, 1, 64)])
 def test_scored_uncommon_head_counts(vc, Hq, Hkv, d):
     _attn_case(vc, Hq, Hkv, d, [70, 200, 1], [1, 256 // (Hq // Hkv) if Hq // Hkv > 1 else 7, 1], scored=True)
+
+
+def test_draft_after_eviction_and_accept(vc):
+    """A draft's compact rows shrunk in place by vc_evict_kv, then vc_accept, then two draft steps, none waited
+    for on the host: accept lets its followers start before it ends, and the drafts must not read rows that are
+    still being moved. Equal to the same drafts on settled rows."""
+    Hq, Hkv, d, n, keep, L = 32, 8, 128, 40000, 20000, 2
+    g = gen(30)
+    k0, v0 = randn(g, Hkv, n, d), randn(g, Hkv, n, d)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda").expand(Hkv, n).contiguous()
+    kw, vw = (torch.zeros((Hkv, 4, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q, kn, vn = randn(g, L, Hq, d), randn(g, Hkv, d), randn(g, Hkv, d)
+    shape = vc.vc_shape(1, Hq, Hkv, d)
+    ws = torch.zeros(vc.vc_workspace_size(vc.VC_CALL_DRAFT, shape, 0), dtype=torch.uint8, device="cuda")
+    ws_e = torch.empty(vc.vc_evict_workspace_size(shape, n), dtype=torch.uint8, device="cuda")
+    logits = torch.randn((1, 2, 512), generator=g, device="cuda")
+    tok = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    lens, out_tok = torch.ones(1, dtype=torch.int32, device="cuda"), torch.empty((1, 2), dtype=torch.int32, device="cuda")
+    n_acc = torch.empty(1, dtype=torch.int32, device="cuda")
+    for _ in range(10):
+        k, v, p = k0.clone(), v0.clone(), pos.clone()
+        score = torch.rand((Hkv, n), generator=g, device="cuda")
+        comp = vc.vc_kv_comp(mode=vc.VC_TOKEN_DROP, keep=keep, compact=1, k_rows=k.data_ptr(), v_rows=v.data_ptr(),
+                             rows_cap=n, k_win=kw.data_ptr(), v_win=vw.data_ptr(), win_cap=4)
+
+        def drafts():
+            o = torch.empty((L, Hq, d), dtype=torch.bfloat16, device="cuda")
+            for step in range(L):
+                comp.n_win = step
+                req = (vc.vc_draft_req * 1)(vc.vc_draft_req(q=q[step].data_ptr(), k_new=kn.data_ptr(),
+                                                            v_new=vn.data_ptr(), o=o[step].data_ptr(), comp=comp))
+                vc.vc_draft_attn(shape, req, ws)
+            return o
+
+        evict = (vc.vc_evict_req * 1)(vc.vc_evict_req(vc.live_kv(k, v, n, score, p), keep, 4, n - 10))
+        torch.cuda.synchronize()
+        vc.vc_evict_kv(shape, evict, ws_e)
+        vc.vc_accept(1, 1, 512, logits, tok, lens, out_tok, n_acc)
+        got = drafts()
+        torch.cuda.synchronize()
+        assert torch.equal(got, drafts())
