@@ -402,7 +402,7 @@ size_t vc_importance_workspace_size(const vc_shape* shape, int32_t window, int32
  * Rows 0..n-1 of every KV head are valid, in any order of positions: attention without a mask does
  * not depend on the order, and vc_evict_kv fills the rows it frees from the back. The caller moves
  * n: up by n_rows after vc_rope_append, to min(n, keep) after vc_evict_kv. Rows n..cap-1 are never
- * read, whatever they hold. The requests of one call that write (vc_rope_append, vc_scored_attn,
+ * read, whatever they hold. Hkv <= 65535 (VC_ERR_UNSUPPORTED). The requests of one call that write (vc_rope_append, vc_scored_attn,
  * vc_evict_kv) have caches of their own; vc_prefix_attn only reads them, so requests may share one. */
 typedef struct vc_live_kv {
   void* k;           /* bf16 [Hkv][cap][d] */
@@ -426,7 +426,7 @@ typedef struct vc_live_kv {
  * layout: VC_ROPE_HALF pairs channels (j, j + rot_dim / 2), VC_ROPE_INTERLEAVED (2 j, 2 j + 1).
  * Channels rot_dim..d-1 pass through. The caller may change or fill in freq itself.
  * Errors: VC_ERR_INVALID (null, unknown kind or layout, base or factor not finite and positive, amp
- * not finite; BANDS: orig_ctx < 1, low < 0 or high <= low); VC_ERR_UNSUPPORTED (rot_dim not a
+ * not finite in fp32; BANDS: orig_ctx < 1, low < 0 or high <= low); VC_ERR_UNSUPPORTED (rot_dim not a
  * multiple of 16 in 16..2 * VC_ROPE_MAX_PAIRS). Host only. */
 #define VC_ROPE_MAX_PAIRS 64
 #define VC_ROPE_NONE 0
@@ -458,7 +458,8 @@ vc_status vc_rope_init(const vc_rope_config* config, vc_rope* out);
  * accuracy: cos and sin are within 2^-21 for every |position * theta| < 2^30).
  * q_out may be q itself when q is packed; otherwise outputs do not overlap inputs. q may be NULL
  * (with q_out) for keys alone. Requests with n_rows == 0 are skipped; pos0 + n_rows must stay
- * within int32. rot_dim <= d. Rotation in fp32, rounded once to bf16. */
+ * within int32. rot_dim <= d. Rotation in fp32, rounded once to bf16.
+ * Errors before anything is launched: VC_ERR_INVALID; VC_ERR_UNSUPPORTED (d, rot_dim, more than 2^30 tokens). */
 typedef struct vc_rope_req {
   const void* q;       /* bf16, token t's [Hq][d] at q + t * q_stride */
   const void* k;       /* bf16, token t's [Hkv][d] at k + t * k_stride */
@@ -488,7 +489,9 @@ vc_status vc_rope_append(const vc_shape* shape, const vc_rope* rope, const vc_ro
  * the product with V, output rounded to bf16.
  * ws: vc_prefix_workspace_size(shape, max_rows) bytes for calls of up to max_rows rows a request; no
  * initialisation. Calls that overlap on the GPU must not share a workspace.
- * Errors before anything is launched: VC_ERR_INVALID, VC_ERR_WORKSPACE. */
+ * Errors before anything is launched: VC_ERR_INVALID; VC_ERR_WORKSPACE; VC_ERR_UNSUPPORTED (caches of more
+ * than 2^30 rows, calls whose query rows or tiles reach 2^29). dev_status receives VC_DEV_TIMEOUT if a bounded
+ * wait gives up, VC_DEV_INTERNAL if the launch is not laid out as the kernel needs; outputs are then invalid. */
 typedef struct vc_live_req {
   const void* q;     /* bf16 [n_rows][Hq][d] */
   void* o;           /* bf16 [n_rows][Hq][d] */
@@ -506,7 +509,8 @@ size_t vc_prefix_workspace_size(const vc_shape* shape, int32_t max_rows);
  * the same bits). n_rows * Hq/Hkv <= VC_SCORED_MAX_ROWS (VC_ERR_UNSUPPORTED beyond: split a longer
  * chunk over calls, each after its own vc_rope_append); every kv needs score.
  * ws: vc_scored_workspace_size(shape, max_rows, max_n) bytes for calls of up to max_rows rows a
- * request over caches of up to max_n rows; no initialisation. */
+ * request over caches of up to max_n rows; no initialisation; errors, overlapping calls and dev_status as
+ * above. */
 #define VC_SCORED_MAX_ROWS 256
 
 vc_status vc_scored_attn(const vc_shape* shape, const vc_live_req* req, void* ws, size_t ws_bytes,
@@ -523,7 +527,9 @@ size_t vc_scored_workspace_size(const vc_shape* shape, int32_t max_rows, int32_t
  * K, V, score and position. Rows keep..n-1 are left as they were; the caller sets n to min(n, keep).
  * Every kv needs score and pos. keep >= 1. Requests with n <= keep are left alone.
  * ws: vc_evict_workspace_size(shape, max_n) bytes for caches of up to max_n rows; no initialisation.
- * dev_status receives VC_DEV_INTERNAL if a plan does not add up (nothing is moved for that head). */
+ * Calls that overlap on the GPU must not share a workspace.
+ * Errors before anything is launched: VC_ERR_INVALID; VC_ERR_WORKSPACE; VC_ERR_UNSUPPORTED (more than 2^30 rows).
+ * dev_status receives VC_DEV_INTERNAL if a plan does not add up (what does not is not moved). */
 typedef struct vc_evict_req {
   vc_live_kv kv;
   int32_t keep;

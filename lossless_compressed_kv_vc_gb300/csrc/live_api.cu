@@ -14,6 +14,7 @@ bool a4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
 
 vc_status check_shape(const vc_shape* s) {
   if (!s || s->B < 1 || s->B > VC_MAX_BATCH || s->Hkv < 1 || s->Hq < s->Hkv || s->Hq % s->Hkv != 0) return VC_ERR_INVALID;
+  if (s->Hkv > 65535) return VC_ERR_UNSUPPORTED;  // a grid's second dimension
   return s->d == 64 || s->d == 128 ? VC_OK : VC_ERR_UNSUPPORTED;
 }
 
@@ -80,7 +81,7 @@ vc_status vc_rope_init(const vc_rope_config* c, vc_rope* out) {
   if (!c || !out) return VC_ERR_INVALID;
   if (c->kind < VC_ROPE_NONE || c->kind > VC_ROPE_BANDS) return VC_ERR_INVALID;
   if (c->layout != VC_ROPE_HALF && c->layout != VC_ROPE_INTERLEAVED) return VC_ERR_INVALID;
-  if (!(c->base > 0) || !isfinite(c->base) || !isfinite(c->amp)) return VC_ERR_INVALID;
+  if (!(c->base > 0) || !isfinite(c->base) || !isfinite((float)c->amp)) return VC_ERR_INVALID;
   if (c->kind != VC_ROPE_NONE && (!(c->factor > 0) || !isfinite(c->factor))) return VC_ERR_INVALID;
   if (c->kind == VC_ROPE_BANDS && (c->orig_ctx < 1 || !(c->low >= 0) || !(c->high > c->low) || !isfinite(c->high)))
     return VC_ERR_INVALID;
@@ -109,7 +110,7 @@ vc_status vc_rope_append(const vc_shape* shape, const vc_rope* rope, const vc_ro
   if (st != VC_OK) return st;
   if (!rope || !req || (rope->layout != VC_ROPE_HALF && rope->layout != VC_ROPE_INTERLEAVED)) return VC_ERR_INVALID;
   if (rope->rot_dim < 16 || rope->rot_dim > shape->d || rope->rot_dim % 16 != 0) return VC_ERR_UNSUPPORTED;
-  if (!isfinite(rope->amp)) return VC_ERR_INVALID;
+  if (!isfinite((float)rope->amp)) return VC_ERR_INVALID;
   RopeParams p;
   memset(&p, 0, sizeof(p));
   p.Hq = shape->Hq;

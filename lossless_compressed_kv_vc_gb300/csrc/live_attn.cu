@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
         for (int i = 0; i < 32 / RW; ++i) {
           const int r = i * RW + lane / PR, c = lane % PR, rr = (warp & 3) * 32 + r;
           const bf16* from = reinterpret_cast<const bf16*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), r));
-          const uint4 v = from ? __ldg(reinterpret_cast<const uint4*>(from) + c) : make_uint4(0, 0, 0, 0);
+          const uint4 v = from ? __ldcg(reinterpret_cast<const uint4*>(from) + c) : make_uint4(0, 0, 0, 0);
           *reinterpret_cast<uint4*>(sQ + (c >> 3) * (LM * 128) + rr * 128 + (((c ^ rr) & 7) << 4)) = v;
         }
         fence_proxy_async_smem();
@@ -770,9 +770,9 @@ __global__ void __launch_bounds__(256, SCORED ? 3 : 4) live_finish_kernel(const 
             const int k = k0 + c0 + c;
             const float* src = (k < a.count ? p.ws_o[0] + a.at(k) * D : p.ws_o[1] + o.at(k - a.count) * D) + lane * E;
             if constexpr (E == 4)
-              *reinterpret_cast<float4*>(v[c]) = __ldg(reinterpret_cast<const float4*>(src));
+              *reinterpret_cast<float4*>(v[c]) = __ldcg(reinterpret_cast<const float4*>(src));
             else
-              *reinterpret_cast<float2*>(v[c]) = __ldg(reinterpret_cast<const float2*>(src));
+              *reinterpret_cast<float2*>(v[c]) = __ldcg(reinterpret_cast<const float2*>(src));
           }
         }
 #pragma unroll
@@ -825,7 +825,7 @@ __global__ void __launch_bounds__(256, SCORED ? 3 : 4) live_finish_kernel(const 
       for (int c = 0; c < SP; ++c)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          if (r0 + 4 * e < rows && 64 * c < quads) v[c][e] = __ldg(s + (size_t)(64 * c) * rows + r0 + 4 * e);
+          if (r0 + 4 * e < rows && 64 * c < quads) v[c][e] = __ldcg(s + (size_t)(64 * c) * rows + r0 + 4 * e);
     };
     load2(gl);  // in flight while the rows' lse are merged
     float w[SP];

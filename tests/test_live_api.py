@@ -252,3 +252,18 @@ def test_live_kv_refuses_strided_tensors(vc):
     assert vc.live_kv(k, k, 3).cap == 8
     with pytest.raises(ValueError):
         vc.live_kv(k[:, ::2], k, 3)
+
+
+def test_sizes_beyond_the_kernels_counts_are_refused(vc):
+    uns = vc.VC_ERR_UNSUPPORTED
+    big = vc.vc_shape(1, 65536, 65536, 64)
+    for scored in (False, True):
+        assert _attn(vc, scored, shape=big) == uns
+        assert _attn(vc, scored, shape=vc.vc_shape(1, 256, 256, 64), n=2 ** 30, cap=2 ** 30) == uns  # 2^31 tiles
+    assert _rope(vc, shape=big) == uns
+    assert vc.vc_evict_workspace_size(big, 10) == vc.vc_prefix_workspace_size(big, 1) == 0
+    t = vc.vc_rope_init(0, 64)
+    t.amp = 1e300                                                    # finite, but not in fp32
+    assert _rope(vc, rope=t) == vc.VC_ERR_INVALID
+    with pytest.raises(vc.VCError):
+        vc.vc_rope_init(0, 64, amp=1e300)
