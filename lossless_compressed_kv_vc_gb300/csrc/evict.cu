@@ -19,7 +19,6 @@ constexpr int kEvThreads = 1024;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvHeld = 40 * 1024;  // ranks a CTA holds at most (160 KB)
 constexpr int kEvBins = 2048;
-constexpr int kEvCopies = 2;
 constexpr int kEvCoarse = kEvBins / 32;  // sums of 32 consecutive bins
 
 __device__ __forceinline__ uint32_t evict_rank(float s, int pos, int sink, int recent_from) {
@@ -51,18 +50,16 @@ __device__ __forceinline__ uint32_t ev_ld_cluster(const void* p, uint32_t rank) 
 // CL CTAs (a cluster) per (KV head, request), each with a consecutive slice of the rows, each warp with a
 // consecutive segment of the slice. HELD: the slice's ranks stay in shared memory; otherwise (more than
 // kEvHeld rows a CTA) they are taken from memory again in every pass.
-// The histograms' counters exist kEvCopies times, a lane using one of them, so that lanes with the same
-// digit wait for each other less: scores share few exponents (16384 rows: 18.7 -> 7 thousand clocks).
 template <int CL, bool HELD>
 __global__ void __launch_bounds__(kEvThreads, 2) evict_select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ uint32_t held[];  // [seg * kEvWarps] ranks
-  __shared__ uint32_t count[kEvBins * kEvCopies];
+  __shared__ uint32_t count[kEvBins];
   __shared__ uint32_t fine[2][kEvBins], coarse[2][kEvCoarse];  // by pass: the cluster may still read the last one's
   __shared__ uint32_t s_prefix, s_rem;
   __shared__ int s_cnt[2][kEvWarps];
   __shared__ int s_cta[2];  // this CTA's rows above T and equal to T
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < kEvBins * kEvCopies; i += kEvThreads) count[i] = 0;
+  for (int i = tid; i < kEvBins; i += kEvThreads) count[i] = 0;
   if (tid == 0) s_prefix = 0;
   pdl_wait();
   pdl_launch_dependents();
@@ -78,19 +75,13 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_select_kernel(const __gri
   const int seg = ((s1 - s0 + 31) / 32 + kEvWarps - 1) / kEvWarps * 32;  // rows of a warp
   const int w0 = min(s1, s0 + warp * seg), w1 = min(s1, w0 + seg);
   uint32_t* mine = held + warp * seg;
-  auto load = [&](int i) { return i < w1 ? evict_rank(__ldg(score + i), __ldg(pos + i), sink, recent_from) : 0u; };
+  auto load = [&](int i) { return i < w1 ? evict_rank(__ldcg(score + i), __ldcg(pos + i), sink, recent_from) : 0u; };
   auto rank_of = [&](int i) { return HELD ? mine[i - w0] : load(i); };
-  // one more row of digit dg in lanes with `in`: the lanes of the warp's commonest case, one digit for most
-  // of them (guarded rows, rows without any weight), are added up before they reach the counters
+  // A shared atomic a row, whatever the digits: on 131072 rows of 32 heads this pass's calls took 36.6 us with
+  // one digit for all rows and 35.6 with evenly spread scores; adding equal digits of a warp up first 39 to 49,
+  // of a thread's rows in a row 38 to 43.
   auto tally = [&](bool in, uint32_t dg) {
-    const unsigned act = __ballot_sync(0xffffffffu, in);
-    if (!act) return;
-    const int lead = __ffs(act) - 1;
-    const uint32_t lead_dg = __shfl_sync(0xffffffffu, dg, lead);
-    const unsigned same = __ballot_sync(0xffffffffu, in && dg == lead_dg);
-    const bool joined = (same >> lane) & 1u;  // one atomic instruction for all
-    if (lane == lead || (in && !joined))
-      atomicAdd(&count[dg * kEvCopies + lane % kEvCopies], joined ? (uint32_t)__popc(same) : 1u);
+    if (in) atomicAdd(&count[dg], 1u);
   };
   if (tid == 0) s_rem = (uint32_t)keep;
   __syncthreads();
@@ -124,16 +115,12 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_select_kernel(const __gri
       }
     }
     __syncthreads();
-    // the copies' sums and those of 32 bins each: only the latter, and then the 32 bins of one of them, are
+    // the sums of 32 bins each: only these, and then the 32 bins of one of them, are
     // added up over the cluster (reading all bins of all CTAs kept the cluster's network busy for longer
     // than everything else)
     for (int c = warp; c < kEvCoarse; c += kEvWarps) {
-      uint32_t v = 0;
-#pragma unroll
-      for (int k = 0; k < kEvCopies; ++k) {
-        v += count[(32 * c + lane) * kEvCopies + k];
-        count[(32 * c + lane) * kEvCopies + k] = 0;  // for the next pass
-      }
+      uint32_t v = count[32 * c + lane];
+      count[32 * c + lane] = 0;  // for the next pass
       fine[pass & 1][32 * c + lane] = v;
       v = __reduce_add_sync(0xffffffffu, v);
       if (lane == 0) coarse[pass & 1][c] = v;
@@ -319,12 +306,16 @@ cudaError_t launch_evict(const EvictParams& p, int d, cudaStream_t s) {
     n = p.req[b].n > n ? p.req[b].n : n;
     room = p.req[b].room > room ? p.req[b].room : room;
   }
-  // CTAs per head: enough to hold the ranks; as many as one wave holds (two CTAs an SM) with at least 1024 rows
-  // each (below that the passes' fixed part, about 8 us, is all that is left); and in several waves still with
-  // 4096 rows each, which even out over the SMs
+  // CTAs per head: enough to hold the ranks; one an SM where the heads leave SMs free and there are 8192 rows to
+  // cut (8 heads: 1 and 8 CTAs a head take 20.6 and 12.8 us at 16384 rows, 10.6 and 11.5 at 4096: the passes'
+  // fixed part, and the cluster's); two an SM from 16384 rows on (128 heads: 29.1 -> 22.7 us); and more of up to
+  // 16384 rows, which even out over the SMs and of which an SM holds two (192 heads, 65536 rows: 156 us with 2,
+  // 116 with 4, 143 with 8).
   const int64_t all = (int64_t)p.Hkv * p.B;
   int cl = 1;
-  while (cl < 8 && (n > cl * kEvHeld || (all * cl * 2 <= 304 && n >= cl * 2 * 1024) || n >= cl * 2 * 4096)) cl *= 2;
+  while (cl < 8 && (n > cl * kEvHeld || (n >= 8192 && all * cl * 2 <= 152) || (n >= 16384 && cl == 1 && all <= 152) ||
+                    (n > cl * 16384 && cl < 4)))
+    cl *= 2;
   cudaError_t e = n > 8 * kEvHeld ? launch_select<8, false>(p, n, s)
                   : cl == 8       ? launch_select<8, true>(p, n, s)
                   : cl == 4       ? launch_select<4, true>(p, n, s)
