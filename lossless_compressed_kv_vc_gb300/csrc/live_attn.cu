@@ -21,6 +21,14 @@
 // tensor cores work for the other. A unit of more than 128 rows gives each chain 128 rows and every tile
 // (a tile serves 256 rows and costs 2); one of up to 128 rows gives both chains the same rows and a half of
 // every tile (which costs 1), and each leaves its own partial. So both chains walk through every tile.
+//
+// What bounds it. One token a request: K and V from DRAM (8 caches of 8200 rows, 8 heads of 128: 49 us with the
+// merge, 236 MB, 0.71 of the copy rate; 4 of 131072: 385 us, 0.83), the rest start-up and, where scores are
+// kept, the second kernel's pass over them. Drafts over a prefix (1000 rows of a KV head, 65536 keys): 394 us,
+// 1.22 PFLOP/s, 0.64 of the bf16 peak: shared memory's bandwidth, since a pair of chains moves 320 KB a tile (Q
+// twice 64, as S steps of 64 keys read it twice, K and V twice 32 each, and 64 in from L2), 2560 clocks at 128
+// bytes each of about 3000; leaving out all exponentials changes nothing. Many short caches (a few tiles a
+// piece): the pieces' fixed part, about 6 us each, of which instruction fetch is the largest.
 #include "tc05.cuh"
 
 #include <cudaTypedefs.h>
@@ -531,9 +539,14 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
           tc05::wait_ld();
           const int last = last_key - k0;
           if (last < LS - 1) {
+            // as bits, several of which become predicates at a time: half the instructions of 64 comparisons
+            const uint32_t lo = last >= 31 ? 0xffffffffu : last < 0 ? 0u : (2u << last) - 1u;  // keys that are seen
+            const uint32_t hi = last < 32 ? 0u : (2u << (last - 32)) - 1u;
 #pragma unroll
-            for (int e = 0; e < LS; ++e)
-              if (e > last) x[e] = -INFINITY;
+            for (int e = 0; e < 32; ++e) {
+              if (!((lo >> e) & 1u)) x[e] = -INFINITY;
+              if (!((hi >> e) & 1u)) x[32 + e] = -INFINITY;
+            }
           }
           if constexpr (SCORED) {
             if (row_ok) {  // four keys of neighbouring rows in neighbouring lanes: whole lines
@@ -904,8 +917,10 @@ static int live_sms() {
 static int64_t units_of(int64_t rows) { return (rows + LU - 1) / LU; }
 static int slot_rows_of(int64_t rows) { return rows <= LM ? (int)(2 * rows) : LU; }
 // CTAs for the prefix's and the own caches' costs: at most one per SM, none with a range below `least`, the
-// cost of the kind's dearest tile (so that none holds less than a tile). With several units of prefix rows their number is a multiple of the units' (a last unit of
-// up to LM rows counting half), where that leaves the longest range within a tenth of the shortest possible.
+// cost of the kind's dearest tile (so that none holds less than a tile). With several units of prefix rows
+// their number is a multiple of the units' (a last unit of up to LM rows counting half), where that leaves the
+// longest range within a tenth of the shortest possible (1000 rows over 65536 keys: ranges cut at the same
+// tiles read 526 MB from DRAM, others 2100 MB; 427 and 593 us when that was measured).
 static void share_ctas(const int64_t (&cost)[2], const int (&least)[2], int prefix_rows, int32_t (&n)[2]) {
   int most[2];
   for (int k = 0; k < 2; ++k) {
