@@ -47,8 +47,9 @@ constexpr int LTHREADS = 512;
 // Registers a thread: launched with 128 (65536 / 512), then 144 in the softmax warpgroups and 80 in the others
 constexpr int LREG_SOFTMAX = 144, LREG_ISSUE = 80;
 static_assert(256 * (LREG_SOFTMAX + LREG_ISSUE) <= 65536, "no more than the block was launched with");
-constexpr int SCORE_KEYS = 1024;  // keys of a score block: 256 a pass
+constexpr int SCORE_KEYS = 1024;  // keys of a score block at most: 256 a pass
 static_assert(SCORE_KEYS % 256 == 0 && LN % 4 == 0, "whole vectors of scores");
+static_assert(VC_SCORED_MAX_ROWS <= LU, "a head's scored rows are one unit");
 
 struct LiveGroup {
   int32_t n;          // keys
@@ -73,7 +74,7 @@ struct LiveParams {
   // what is searched lies together: a scan over the groups' own fields took the constant cache 8 us to
   // bring in at 33 groups
   int32_t cost_begin[VC_MAX_BATCH + 2];   // first cost of each group in its kind's sequence [units][Hkv][tiles]
-  int32_t chunk_begin[VC_MAX_BATCH + 2];  // scored: first score block of each group, [Hkv][ceil(n / SCORE_KEYS)]
+  int32_t chunk_begin[VC_MAX_BATCH + 2];  // scored: first score block of each group, [Hkv][ceil(n / 2^score_shift)]
   int32_t tok_begin[VC_MAX_BATCH + 1];    // first query token of each request
   int32_t own_of[VC_MAX_BATCH];           // group of the request's own cache, -1: empty
   LiveGroup grp[VC_MAX_BATCH + 1];        // the prefix first where there is one
@@ -85,7 +86,7 @@ struct LiveParams {
   int32_t n_cta[2], cta_cost[2], cta_more[2];
   int32_t keep_ws;                      // tiles read once leave L2 (evict first) to the workspace
   int32_t merge_blocks, merge_warps;    // blocks of the merge, warps a row (1, 2, 4 or 8)
-  int32_t score_blocks;
+  int32_t score_blocks, score_shift;    // blocks of 2^score_shift keys: 256, 512 or 1024
   int32_t slot_rows[2];                 // partial rows of a slot: prefix, own
   float* ws_o[2];                       // [slots][slot_rows][d]; slot = CTA of the kind + (unit, head)
   float* ws_lse[2];                     // [slots][slot_rows], log2 domain, -inf: saw nothing
@@ -200,6 +201,19 @@ __device__ __forceinline__ bool lwait(uint64_t* bar, uint32_t parity, int32_t* s
     if ((it & 31u) == 31u && *abort) return false;
   }
   set_status(st, VC_DEV_TIMEOUT);
+  *abort = 1;
+  return false;
+}
+
+// The same by a whole warp, which goes on or gives up together: its collective instructions need every lane.
+__device__ __forceinline__ bool lwait_warp(uint64_t* bar, uint32_t parity, int32_t* st, volatile int* abort) {
+  bool done = false;
+  for (uint32_t it = 0; it < kSpinLimit && !done; ++it) {
+    done = mbar_try_wait(bar, parity);
+    if ((it & 31u) == 31u && *abort) break;
+  }
+  if (__all_sync(0xffffffffu, done)) return true;
+  if (!*abort) set_status(st, VC_DEV_TIMEOUT);
   *abort = 1;
   return false;
 }
@@ -426,7 +440,7 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
     uint32_t g = 0, t = 0, looked = 0, seen = 0;
     // P V of step s done (and with it those before): asked for steps whose S has been read, so the phase
     // before on that buffer is over
-    auto pv_done = [&](uint32_t s) { return lwait(&ofull[2 * w + (s & 1)], (s >> 1) & 1, p.dev_status, s_abort); };
+    auto pv_done = [&](uint32_t s) { return lwait_warp(&ofull[2 * w + (s & 1)], (s >> 1) & 1, p.dev_status, s_abort); };
     bool ok = true;
     auto slot_of = [&](const LiveGroup& R) {
       return (size_t)(blockIdx.x - (kind ? p.n_cta[0] : 0)) + R.unit_begin + q.u * p.Hkv + q.hk;
@@ -523,7 +537,7 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
         for (int h = q.h0(w); h < h1; ++h, ++t, fresh = false) {
           const int k0 = j * LN + h * LS;  // the step's first key
           const uint32_t tP = tS + (t & 1) * LS;
-          if (!lwait(&sfull[2 * w + (t & 1)], (t >> 1) & 1, p.dev_status, s_abort)) {
+          if (!lwait_warp(&sfull[2 * w + (t & 1)], (t >> 1) & 1, p.dev_status, s_abort)) {
             ok = false;
             break;
           }
@@ -614,7 +628,7 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
           // NaN value row to the latter, so if V holds any, the threads add up the seen keys themselves.
           if (blind < min(n, k0 + LS)) {
             const uint32_t iv = 2 * g + 1;
-            if (!landed(iv, seen)) {
+            if (!__all_sync(0xffffffffu, landed(iv, seen))) {
               ok = false;
               break;
             }
@@ -630,7 +644,7 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
             if (bad) s_odd[w] = t + 1;
             __syncwarp();
             if (lane == 0) mbar_arrive(&vbar[w]);
-            if (!lwait(&vbar[w], looked & 1, p.dev_status, s_abort)) {
+            if (!lwait_warp(&vbar[w], looked & 1, p.dev_status, s_abort)) {
               ok = false;
               break;
             }
@@ -719,8 +733,8 @@ __device__ __forceinline__ LParts live_parts(const LiveParams& p, int kind, int 
 
 // Merge: one to eight warps per (token, query head), o = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M) over the
 // partials of the prefix and of the own cache: a lane per partial takes the weights, then the warp adds
-// up the partials' channels, four loads in flight. Scores: a block per 1024 keys of a (request, KV head)
-// merges the head's rows' lse, a warp a row, then sums 2^(s scale - lse) over the rows for each key.
+// up the partials' channels, four loads in flight. Scores: a block per 256 to 1024 keys of a (request, KV head)
+// merges the head's rows' lse, four rows a warp at a time, then sums 2^(s scale - lse) over the rows for each key.
 template <int D, bool SCORED>
 __global__ void __launch_bounds__(256, SCORED ? 3 : 4) live_finish_kernel(const __grid_constant__ LiveParams p) {
   constexpr int E = D / 32;  // channels a lane
@@ -822,14 +836,15 @@ __global__ void __launch_bounds__(256, SCORED ? 3 : 4) live_finish_kernel(const 
     const int id = blockIdx.x;
     const int g = last_begin(p.chunk_begin, p.n_grp, id);
     const LiveGroup& R = p.grp[g];
-    const int chunks = (R.n + SCORE_KEYS - 1) / SCORE_KEYS;
-    const int hk = (id - p.chunk_begin[g]) / chunks, k0 = (id - p.chunk_begin[g] - hk * chunks) * SCORE_KEYS;
+    const int chunks = (R.n + (1 << p.score_shift) - 1) >> p.score_shift;
+    const int hk = (id - p.chunk_begin[g]) / chunks, k0 = (id - p.chunk_begin[g] - hk * chunks) << p.score_shift;
     const int rows = R.rows, gl = threadIdx.x & 3;  // four lanes share a group of four keys, rows gl, gl + 4, ...
     const float4* s = reinterpret_cast<const float4*>(R.s) + ((size_t)hk * R.tiles * (LN / 4) + k0 / 4 + threadIdx.x / 4) * rows;
     float* score = R.score + (size_t)hk * R.cap + k0 + threadIdx.x;  // its key in a pass of 256
-    const int left = R.n - k0 - (int)threadIdx.x, quads = (R.n - k0 + 3) / 4 - (int)threadIdx.x / 4;
-    LParts part{0, 0, 0, 0};
-    if (warp < rows) part = live_parts(p, 1, g, hk, warp);
+    const int keys = min(R.n - k0, 1 << p.score_shift);  // of this block
+    const int left = keys - (int)threadIdx.x, quads = (keys + 3) / 4 - (int)threadIdx.x / 4;
+    LParts part{0, 0, 0, 0};  // of row 0; row r's are r further on
+    if (warp < rows) part = live_parts(p, 1, g, hk, 0);
     pdl_wait();
     pdl_launch_dependents();
     float4 v[SP][2];
@@ -844,14 +859,32 @@ __global__ void __launch_bounds__(256, SCORED ? 3 : 4) live_finish_kernel(const 
     float w[SP];
 #pragma unroll
     for (int c = 0; c < SP; ++c) w[c] = 256 * c < left ? score[256 * c] : 0.f;
-    for (int r = warp; r < rows; r += 8) {
-      if (r > warp) part = live_parts(p, 1, g, hk, r);
-      float M = -INFINITY, L = 0.f;
-      for (int k = lane; k < part.count; k += 32) M = fmaxf(M, p.ws_lse[1][part.at(k)]);
-      M = warp_max(M);
-      for (int k = lane; k < part.count; k += 32) L += weight(p.ws_lse[1][part.at(k)], M);
-      L = warp_sum(L);
-      if (lane == 0) s_lse[r] = L != 0.f ? M + log2f(L) : INFINITY;  // a row that sees nothing has weights 2^-inf
+    constexpr int LR = 4;  // rows a warp merges at a time
+    for (int r0 = warp; r0 < rows; r0 += 8 * LR) {
+      float M[LR], L[LR];
+#pragma unroll
+      for (int e = 0; e < LR; ++e) M[e] = -INFINITY, L[e] = 0.f;
+      for (int k = lane; k < part.count; k += 32) {
+        const float* l = p.ws_lse[1] + part.at(k) + r0;
+#pragma unroll
+        for (int e = 0; e < LR; ++e)
+          if (r0 + 8 * e < rows) M[e] = fmaxf(M[e], l[8 * e]);
+      }
+#pragma unroll
+      for (int e = 0; e < LR; ++e)
+        if (r0 + 8 * e < rows) M[e] = warp_max(M[e]);
+      for (int k = lane; k < part.count; k += 32) {
+        const float* l = p.ws_lse[1] + part.at(k) + r0;
+#pragma unroll
+        for (int e = 0; e < LR; ++e)
+          if (r0 + 8 * e < rows) L[e] += weight(l[8 * e], M[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < LR; ++e)
+        if (r0 + 8 * e < rows) {
+          const float l = warp_sum(L[e]);
+          if (lane == 0) s_lse[r0 + 8 * e] = l != 0.f ? M[e] + log2f(l) : INFINITY;  // a row that sees nothing has weights 2^-inf
+        }
     }
     __syncthreads();
     float4 sum[SP];
@@ -1001,7 +1034,6 @@ cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_
     R.tiles = (n + LN - 1) / LN;
     R.unit_begin = (int32_t)units[kind];
     p.cost_begin[p.n_grp] = (int32_t)cost[kind];
-    p.chunk_begin[p.n_grp] = (int32_t)chunks;
     if (R.rows > LM) least[kind] = 2;
     const int sr = slot_rows_of(R.rows);
     p.slot_rows[kind] = sr > p.slot_rows[kind] ? sr : p.slot_rows[kind];
@@ -1036,6 +1068,25 @@ cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_
   const int64_t out_rows = (int64_t)a.n_tok * a.Hq;
   if (*st == VC_OK && out_rows + chunks >= INT32_MAX / 2) *st = VC_ERR_UNSUPPORTED;
   if (*st != VC_OK) return cudaSuccess;
+  // Keys of a score block: fewer where 1024 leave SMs without two blocks, unless a block has little to do (us with
+  // 1024 and with 256 keys: 6 heads of 128 rows and 14419 keys 95, 70; 48 of 32 and 957 26.9, 22.5; 16 of 5 and
+  // 7009 22.9, 25.4)
+  if (scored) {
+    int keys = SCORE_KEYS;
+    int most_rows = 0;
+    for (int g = 0; g < p.n_grp; ++g) most_rows = p.grp[g].rows > most_rows ? p.grp[g].rows : most_rows;
+    auto blocks = [&](int keys) {
+      int64_t n = 0;
+      for (int g = 0; g < p.n_grp; ++g) {
+        p.chunk_begin[g] = (int32_t)n;
+        n += (int64_t)a.Hkv * ((p.grp[g].n + keys - 1) / keys);
+      }
+      return n;
+    };
+    chunks = blocks(SCORE_KEYS);
+    while (keys > 256 && chunks < 2 * live_sms() && keys * most_rows >= 16384) chunks = blocks(keys /= 2);
+    p.score_shift = keys == 256 ? 8 : keys == 512 ? 9 : 10;
+  }
   share_ctas(cost, least, p.has_prefix ? p.grp[0].rows : 0, p.n_cta);
   for (int kind = 0; kind < 2; ++kind)
     if (p.n_cta[kind] > 0) {

@@ -714,3 +714,14 @@ def test_draft_after_eviction_and_accept(vc):
         got = drafts()
         torch.cuda.synchronize()
         assert torch.equal(got, drafts())
+
+
+@pytest.mark.parametrize("rows", [1, 3, 8, 64])
+def test_scored_around_the_score_blocks(vc, rows):
+    """Lengths around the blocks of keys that scores are added up in, with few rows and with many."""
+    _attn_case(vc, 8, 2, 64, [255, 256, 257, 511, 513, 1023, 1025, 2049], [rows] * 8, scored=True)
+
+
+def test_scored_many_rows_of_long_caches(vc):
+    """128 query rows a head over keys of many CTAs: more partials a row than a warp's lanes."""
+    _attn_case(vc, 32, 2, 128, [14419, 9000], [8, 8], scored=True)
