@@ -402,7 +402,8 @@ size_t vc_importance_workspace_size(const vc_shape* shape, int32_t window, int32
  * Rows 0..n-1 of every KV head are valid, in any order of positions: attention without a mask does
  * not depend on the order, and vc_evict_kv fills the rows it frees from the back. The caller moves
  * n: up by n_rows after vc_rope_append, to min(n, keep) after vc_evict_kv. Rows n..cap-1 are never
- * read, whatever they hold. Hkv <= 65535 (VC_ERR_UNSUPPORTED). The requests of one call that write (vc_rope_append, vc_scored_attn,
+ * read, whatever they hold. Hkv <= 65535 (VC_ERR_UNSUPPORTED). The device current to the calling thread is
+ * the one that holds the buffers. The requests of one call that write (vc_rope_append, vc_scored_attn,
  * vc_evict_kv) have caches of their own; vc_prefix_attn only reads them, so requests may share one. */
 typedef struct vc_live_kv {
   void* k;           /* bf16 [Hkv][cap][d] */

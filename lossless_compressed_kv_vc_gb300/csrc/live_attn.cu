@@ -24,8 +24,8 @@
 //
 // What bounds it. One token a request: K and V from DRAM (8 caches of 8200 rows, 8 heads of 128: 49 us with the
 // merge, 236 MB, 0.71 of the copy rate; 4 of 131072: 385 us, 0.83), the rest start-up and, where scores are
-// kept, the second kernel's pass over them. Drafts over a prefix (1000 rows of a KV head, 65536 keys): 394 us,
-// 1.22 PFLOP/s, 0.64 of the bf16 peak: shared memory's bandwidth, since a pair of chains moves 320 KB a tile (Q
+// kept, the second kernel's pass over them. Drafts over a prefix (2000 rows of a KV head, 65536 keys): 396 us,
+// 1.21 PFLOP/s, 0.64 of the bf16 peak: shared memory's bandwidth, since a pair of chains moves 320 KB a tile (Q
 // twice 64, as S steps of 64 keys read it twice, K and V twice 32 each, and 64 in from L2), 2560 clocks at 128
 // bytes each of about 3000; leaving out all exponentials changes nothing. Many short caches (a few tiles a
 // piece): the pieces' fixed part, about 6 us each, of which instruction fetch is the largest.
@@ -937,13 +937,12 @@ static bool live_map(CUtensorMap* m, const void* base, int d, int rows, int64_t 
 }
 
 static int live_sms() {
-  static int n = 0;
-  if (n == 0) {
+  static const int n = [] {
     int dev = 0, v = 0;
-    n = cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess
-            ? v
-            : 152;
-  }
+    const bool ok = cudaGetDevice(&dev) == cudaSuccess &&
+                    cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+    return ok ? v : 152;
+  }();
   return n;
 }
 
@@ -952,7 +951,7 @@ static int slot_rows_of(int64_t rows) { return rows <= LM ? (int)(2 * rows) : LU
 // CTAs for the prefix's and the own caches' costs: at most one per SM, none with a range below `least`, the
 // cost of the kind's dearest tile (so that none holds less than a tile). With several units of prefix rows
 // their number is a multiple of the units' (a last unit of up to LM rows counting half), where that leaves the
-// longest range within a tenth of the shortest possible (1000 rows over 65536 keys: ranges cut at the same
+// longest range within a tenth of the shortest possible (2000 rows over 65536 keys: ranges cut at the same
 // tiles read 526 MB from DRAM, others 2100 MB; 427 and 593 us when that was measured).
 static void share_ctas(const int64_t (&cost)[2], const int (&least)[2], int prefix_rows, int32_t (&n)[2]) {
   int most[2];

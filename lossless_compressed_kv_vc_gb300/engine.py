@@ -751,8 +751,10 @@ class LiveBatch:
             pk, pv, ctx = prefix
             for t in (pk, pv):
                 if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape != pk.shape or t.shape[0] != Hkv or \
-                        t.shape[2] != d or not t.is_contiguous() or not 0 <= ctx <= t.shape[1]:
-                    raise ValueError("a prefix is (k, v, rows): contiguous bf16 [Hkv][cap][d], 0 <= rows <= cap")
+                        t.shape[2] != d or not t.is_contiguous() or t.device.type != self.device.type or \
+                        not 0 <= ctx <= t.shape[1]:
+                    raise ValueError("a prefix is (k, v, rows): contiguous bf16 [Hkv][cap][d] on the batch's device, "
+                                     "0 <= rows <= cap")
             self._prefix = vc_kv_full(pk.data_ptr(), pv.data_ptr(), ctx, pk.shape[1])
             size = vc_prefix_workspace_size(self.shape, max_rows)
         else:
@@ -787,8 +789,8 @@ class LiveBatch:
             raise ValueError("rows: one count per request, 0 .. min(max_rows, the tokens given)")
         for t, heads in ((q, self.Hq), (k, self.Hkv), (v, self.Hkv)):
             if t.dtype != torch.bfloat16 or tuple(t.shape) != (self.B, q.shape[1], heads, self.d) or \
-                    t.stride(3) != 1 or (heads > 1 and t.stride(2) != self.d):
-                raise ValueError("q, k and v are bf16 [B][R][heads][d] with each token's heads contiguous")
+                    t.stride(3) != 1 or (heads > 1 and t.stride(2) != self.d) or t.device.type != self.device.type:
+                raise ValueError("q, k and v are bf16 [B][R][heads][d] on the batch's device, each token's heads contiguous")
         for b in range(self.B):
             e = self._rope_req[b]
             e.q, e.k, e.v = q[b].data_ptr(), k[b].data_ptr(), v[b].data_ptr()
@@ -806,8 +808,8 @@ class LiveBatch:
         if len(rows) != self.B or any(r < 0 or r > self.max_rows for r in rows):
             raise ValueError("rows: one count per request, 0 .. max_rows")
         if o.dtype != torch.bfloat16 or o.dim() != 4 or o.shape[0] != self.B or o.shape[1] < max(rows) or \
-                tuple(o.shape[2:]) != (self.Hq, self.d) or not o[0].is_contiguous():
-            raise ValueError("o is bf16 [B][R][Hq][d], R >= max(rows), each request's rows contiguous")
+                tuple(o.shape[2:]) != (self.Hq, self.d) or not o[0].is_contiguous() or o.device.type != self.device.type:
+            raise ValueError("o is bf16 [B][R][Hq][d] on the batch's device, R >= max(rows), each request's rows contiguous")
         for b in range(self.B):
             e = self._live_req[b]
             e.q, e.o, e.n_rows, e.kv = self.q_rot[b].data_ptr(), o[b].data_ptr(), rows[b], self._kv(b)

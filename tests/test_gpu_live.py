@@ -725,3 +725,21 @@ def test_scored_around_the_score_blocks(vc, rows):
 def test_scored_many_rows_of_long_caches(vc):
     """128 query rows a head over keys of many CTAs: more partials a row than a warp's lanes."""
     _attn_case(vc, 32, 2, 128, [14419, 9000], [8, 8], scored=True)
+
+
+def test_live_batch_refuses_host_tensors(vc):
+    """A tensor in host memory is turned down before its address reaches a kernel."""
+    from lossless_compressed_kv_vc_gb300 import engine
+    t = _table(vc, 64)
+    z = lambda h, dev: torch.zeros((1, 1, h, 64), dtype=torch.bfloat16, device=dev)
+    lb = engine.LiveBatch(8, 2, 64, 1, 10, t)
+    for args in ((z(8, "cpu"), z(2, "cuda"), z(2, "cuda")), (z(8, "cuda"), z(2, "cpu"), z(2, "cuda")),
+                 (z(8, "cuda"), z(2, "cuda"), z(2, "cpu"))):
+        with pytest.raises(ValueError):
+            lb.append(*args, [1])
+    with pytest.raises(ValueError):
+        lb.attend(z(8, "cpu"), [1])
+    pk = torch.zeros((2, 20, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        engine.LiveBatch(8, 2, 64, 1, 10, t, prefix=(pk, pk, 5))
+    assert lb.n == [0] and lb.next_pos == [0]
