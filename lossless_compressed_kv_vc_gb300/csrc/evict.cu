@@ -12,9 +12,9 @@
 // takes consecutive moves: their plan, scores and positions lane by lane (neighbours in memory), then
 // their K and V rows, several in flight.
 //
-// What bounds it. 32 heads of 131072 rows shrunk to 32768: select 36 us (34 MB; the shared atomics of the first
-// pass, then barriers), move about 150 us (820 MB in rows of 256 bytes, 0.8 of the copy rate). 64 heads, 32 rows
-// over 8192: 14 us, three passes of barriers and cluster reads, and two launches.
+// What bounds it. 32 heads of 131072 rows shrunk to 32768: select 28 us (34 MB; the shared atomics of the first
+// pass, then barriers), move 140 us (820 MB in rows of 256 bytes, 0.86 of the copy rate). 64 heads, 32 rows over
+// 8192: 14 us, three passes over the held ranks with their barriers, and two launches.
 #include "vc_internal.cuh"
 
 namespace vc {
@@ -81,9 +81,9 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_select_kernel(const __gri
   uint32_t* mine = held + warp * seg;
   auto load = [&](int i) { return i < w1 ? evict_rank(__ldcg(score + i), __ldcg(pos + i), sink, recent_from) : 0u; };
   auto rank_of = [&](int i) { return HELD ? mine[i - w0] : load(i); };
-  // A shared atomic a row, whatever the digits: on 131072 rows of 32 heads this pass's calls took 36.6 us with
-  // one digit for all rows and 35.6 with evenly spread scores; adding equal digits of a warp up first 39 to 49,
-  // of a thread's rows in a row 38 to 43.
+  // A shared atomic a row, whatever the digits: 32 heads of 131072 rows take 28.8 us with one digit for all rows
+  // and 27.9 with evenly spread scores; adding up a warp's equal digits first, or a thread's, cost more than it
+  // saved (by 3 to 20 us).
   auto tally = [&](bool in, uint32_t dg) {
     if (in) atomicAdd(&count[dg], 1u);
   };
@@ -97,15 +97,21 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_select_kernel(const __gri
     const uint32_t prefix = s_prefix;
     if (pass == 0) {
 #pragma unroll 1
-      for (int base = w0; base < w1; base += 32 * 4) {  // loads of four groups of 32 rows in flight
-        uint32_t u[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) u[k] = load(base + 32 * k + lane);
+      for (int base = w0; base < w1; base += 32 * 4) {  // four groups of 32 rows: eight loads in flight
+        float sc[4];
+        int ps[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int i = base + 32 * k + lane;
-          if (HELD && i < w1) mine[i - w0] = u[k];
-          tally(i < w1, u[k] >> shift);
+          sc[k] = i < w1 ? __ldcg(score + i) : 0.f;
+          ps[k] = i < w1 ? __ldcg(pos + i) : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = base + 32 * k + lane;
+          const uint32_t u = evict_rank(sc[k], ps[k], sink, recent_from);
+          if (HELD && i < w1) mine[i - w0] = u;
+          tally(i < w1, u >> shift);
         }
       }
     } else {
@@ -310,16 +316,13 @@ cudaError_t launch_evict(const EvictParams& p, int d, cudaStream_t s) {
     n = p.req[b].n > n ? p.req[b].n : n;
     room = p.req[b].room > room ? p.req[b].room : room;
   }
-  // CTAs per head: enough to hold the ranks; one an SM where the heads leave SMs free and there are 8192 rows to
-  // cut (8 heads: 1 and 8 CTAs a head take 20.6 and 12.8 us at 16384 rows, 10.6 and 11.5 at 4096: the passes'
-  // fixed part, and the cluster's); two an SM from 16384 rows on (128 heads: 29.1 -> 22.7 us); and more of up to
-  // 16384 rows, which even out over the SMs and of which an SM holds two (192 heads, 65536 rows: 156 us with 2,
-  // 116 with 4, 143 with 8).
+  // CTAs per head: enough to hold the ranks; one an SM where the heads leave SMs free and there are 16384 rows to
+  // cut (8 heads: 1 and 8 CTAs a head take 15.4 and 12.0 us at 16384 rows, 11.1 and 11.7 at 8192: the passes'
+  // fixed part, and the cluster's); and rather four than two with more heads than that, which even out over the SMs
+  // (96 heads, 65536 rows: 52.2 us with 2, 42.6 with 4, 56.7 with 8; 64 heads: 28.0, 32.3, 40.5).
   const int64_t all = (int64_t)p.Hkv * p.B;
   int cl = 1;
-  while (cl < 8 && (n > cl * kEvHeld || (n >= 8192 && all * cl * 2 <= 152) || (n >= 16384 && cl == 1 && all <= 152) ||
-                    (n > cl * 16384 && cl < 4)))
-    cl *= 2;
+  while (cl < 8 && (n > cl * kEvHeld || (n >= 16384 && all * cl * 2 <= 152) || (cl == 2 && all > 76))) cl *= 2;
   cudaError_t e = n > 8 * kEvHeld ? launch_select<8, false>(p, n, s)
                   : cl == 8       ? launch_select<8, true>(p, n, s)
                   : cl == 4       ? launch_select<4, true>(p, n, s)
