@@ -261,6 +261,7 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__
       if (dst < 0 || dst >= r.keep || src < r.keep || src >= r.n) {
         set_status(p.dev_status, VC_DEV_INTERNAL);
         dst = -1;
+        src = 0;
       } else {
         r.score[head + dst] = r.score[head + src];
         r.pos[head + dst] = r.pos[head + src];
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__
         to[e] = __shfl_sync(0xffffffffu, dst, c & 31);
         const int from = __shfl_sync(0xffffffffu, src, c & 31);
         if (c >= cnt) to[e] = -1;
-        if (to[e] >= 0) v[e] = rows[(size_t)from * (LANES / 2)];
+        v[e] = rows[(size_t)from * (LANES / 2)];  // some row where there is none to move: no branch between the loads
       }
 #pragma unroll
       for (int e = 0; e < U; ++e)
