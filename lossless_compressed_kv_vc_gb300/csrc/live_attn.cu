@@ -953,7 +953,12 @@ static int slot_rows_of(int64_t rows) { return rows <= LM ? (int)(2 * rows) : LU
 // their number is a multiple of the units' (a last unit of up to LM rows counting half), where that leaves the
 // longest range within a tenth of the shortest possible (2000 rows over 65536 keys: ranges cut at the same
 // tiles read 526 MB from DRAM, others 2100 MB; 427 and 593 us when that was measured).
-static void share_ctas(const int64_t (&cost)[2], const int (&least)[2], int prefix_rows, int32_t (&n)[2]) {
+// They are shared by `weighed`, in which a unit of a head costs at least kLeastUnit: a piece of one tile takes as
+// long as four of a longer one (224 rows over 54472 keys beside 28 own caches of up to 112: 58 us by the tiles
+// alone, 44 with 4, 45.5 with 8; with 8 a batch of 4 over 3389 and up to 788 keys goes from 16.4 to 18.3).
+constexpr int kLeastUnit = 4;
+static void share_ctas(const int64_t (&cost)[2], const int64_t (&weighed)[2], const int (&least)[2], int prefix_rows,
+                       int32_t (&n)[2]) {
   int most[2];
   for (int k = 0; k < 2; ++k) {
     const int64_t m = cost[k] / least[k];
@@ -965,15 +970,21 @@ static void share_ctas(const int64_t (&cost)[2], const int (&least)[2], int pref
   const int step = units < 2 ? 1 : 2 * units - half;  // in half units; twice as many CTAs without a half one
   if (most[0] == 0 || (most[0] + most[1] <= live_sms() && step == 1)) return;
   const int room = live_sms();
-  int64_t best = -1, best_aligned = -1;
-  int at = 0, at_aligned = 0;
+  // the shortest longest range; among equals the shortest ranges together
+  struct Best {
+    int64_t longest = INT64_MAX, sum = INT64_MAX;
+    int at = 0;
+    void take(int64_t l, int64_t s, int c) {
+      if (l < longest || (l == longest && s < sum)) longest = l, sum = s, at = c;
+    }
+  } any, aligned;
   for (int c = 1; c <= most[0] && (most[1] == 0 || c < room); ++c) {
     const int o = most[1] < room - c ? most[1] : room - c;
-    const int64_t p0 = (cost[0] + c - 1) / c, p1 = o > 0 ? (cost[1] + o - 1) / o : 0, longest = p0 > p1 ? p0 : p1;
-    if (best < 0 || longest < best) best = longest, at = c;
-    if ((half ? c : 2 * c) % step == 0 && (best_aligned < 0 || longest < best_aligned)) best_aligned = longest, at_aligned = c;
+    const int64_t p0 = (weighed[0] + c - 1) / c, p1 = o > 0 ? (weighed[1] + o - 1) / o : 0, longest = p0 > p1 ? p0 : p1;
+    any.take(longest, p0 + p1, c);
+    if ((half ? c : 2 * c) % step == 0) aligned.take(longest, p0 + p1, c);
   }
-  if (at_aligned && best_aligned * 10 <= best * 11) at = at_aligned;
+  const int at = aligned.at && aligned.longest * 10 <= any.longest * 11 ? aligned.at : any.at;
   n[0] = at;
   n[1] = most[1] < room - at ? most[1] : room - at;
 }
@@ -1017,7 +1028,7 @@ cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_
   p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)a.d));
   p.dev_status = a.dev_status;
   p.slot_rows[0] = p.slot_rows[1] = 1;
-  int64_t cost[2] = {0, 0}, units[2] = {0, 0}, chunks = 0;
+  int64_t cost[2] = {0, 0}, weighed[2] = {0, 0}, units[2] = {0, 0}, chunks = 0;
   int least[2] = {1, 1};
   size_t s_floats = 0;
   // adds the group of a key sequence; `b`: the request whose own cache it is, -1: the prefix
@@ -1038,7 +1049,10 @@ cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_
     p.slot_rows[kind] = sr > p.slot_rows[kind] ? sr : p.slot_rows[kind];
     units[kind] += (int64_t)a.Hkv * R.units;
     // every unit but the last has LU rows
-    cost[kind] += (int64_t)a.Hkv * R.tiles * (2 * R.units - (R.rows - (R.units - 1) * LU <= LM ? 1 : 0));
+    const int64_t all = (int64_t)a.Hkv * R.tiles * (2 * R.units - (R.rows - (R.units - 1) * LU <= LM ? 1 : 0));
+    const int64_t few = (int64_t)a.Hkv * R.units * kLeastUnit;
+    cost[kind] += all;
+    weighed[kind] += all > few ? all : few;
     if (scored) {
       chunks += (int64_t)a.Hkv * ((n + SCORE_KEYS - 1) / SCORE_KEYS);
       s_floats += (size_t)a.Hkv * R.rows * R.tiles * LN;
@@ -1086,7 +1100,7 @@ cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_
     while (keys > 256 && chunks < 2 * live_sms() && keys * most_rows >= 16384) chunks = blocks(keys /= 2);
     p.score_shift = keys == 256 ? 8 : keys == 512 ? 9 : 10;
   }
-  share_ctas(cost, least, p.has_prefix ? p.grp[0].rows : 0, p.n_cta);
+  share_ctas(cost, weighed, least, p.has_prefix ? p.grp[0].rows : 0, p.n_cta);
   for (int kind = 0; kind < 2; ++kind)
     if (p.n_cta[kind] > 0) {
       p.cta_cost[kind] = (int32_t)(cost[kind] / p.n_cta[kind]);
