@@ -12,9 +12,9 @@
 // takes consecutive moves: their plan, scores and positions lane by lane (neighbours in memory), then
 // their K and V rows, several in flight.
 //
-// What bounds it. 32 heads of 131072 rows shrunk to 32768: select 28 us (34 MB; the shared atomics of the first
-// pass, then barriers), move 140 us (820 MB in rows of 256 bytes, 0.86 of the copy rate). 64 heads, 32 rows over
-// 8192: 14 us, three passes over the held ranks with their barriers, and two launches.
+// What bounds it. 32 heads of 131072 rows shrunk to 32768: select 30 us (34 MB; the shared atomics of the first
+// pass, then barriers), move 131 us (804 MB in rows of 256 bytes, 0.91 of the copy rate). 64 heads, 32 rows over
+// 8192: 12 us, three passes over the held ranks with their barriers, and two launches.
 #include "vc_internal.cuh"
 
 namespace vc {
