@@ -85,7 +85,7 @@ struct LiveParams {
   // by kind: its CTAs, the cost of each one's range and how many (the first) have one more
   int32_t n_cta[2], cta_cost[2], cta_more[2];
   int32_t keep_ws;                      // tiles read once leave L2 (evict first) to the workspace
-  int32_t merge_blocks, merge_warps;    // blocks of the merge, warps a row (1, 2, 4 or 8)
+  int32_t merge_blocks, merge_warps;    // blocks of the merge, warps a row (1, 2, 4 or 8; 0: several rows a warp)
   int32_t score_blocks, score_shift;    // blocks of 2^score_shift keys: 256, 512 or 1024
   int32_t slot_rows[2];                 // partial rows of a slot: prefix, own
   float* ws_o[2];                       // [slots][slot_rows][d]; slot = CTA of the kind + (unit, head)
@@ -731,6 +731,9 @@ __device__ __forceinline__ LParts live_parts(const LiveParams& p, int kind, int 
   return q;
 }
 
+// Weight of a partial beside the largest lse M: 0 where it saw nothing; M stays -inf only beside a NaN.
+__device__ __forceinline__ float merge_weight(float l, float M) { return l == -INFINITY ? 0.f : M == -INFINITY ? NAN : exp2f(l - M); }
+
 // Merge: one to eight warps per (token, query head), o = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M) over the
 // partials of the prefix and of the own cache: a lane per partial takes the weights, then the warp adds
 // up the partials' channels, four loads in flight. Scores: a block per 256 to 1024 keys of a (request, KV head)
@@ -753,8 +756,6 @@ __global__ void __launch_bounds__(256, SCORED ? 3 : 4) live_finish_kernel(const 
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     return v;
   };
-  // weight of a partial beside the largest lse M: 0 where it saw nothing; M stays -inf only beside a NaN
-  auto weight = [](float l, float M) { return l == -INFINITY ? 0.f : M == -INFINITY ? NAN : exp2f(l - M); };
   if (!SCORED || (int)blockIdx.x >= p.score_blocks) {  // the longer score blocks go first
     const int wpr = p.merge_warps, part = warp % wpr;  // warps of a row, this one among them
     const int64_t id = (int64_t)(blockIdx.x - p.score_blocks) * (8 / wpr) + warp / wpr;
@@ -782,7 +783,7 @@ __global__ void __launch_bounds__(256, SCORED ? 3 : 4) live_finish_kernel(const 
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
     const int beg = total * part / wpr, end = total * (part + 1) / wpr;
     for (int k0 = beg; k0 < end; k0 += 32) {
-      const float l = lse_of(k0 + lane, end), f = weight(l, M);
+      const float l = lse_of(k0 + lane, end), f = merge_weight(l, M);
       const unsigned wrote = __ballot_sync(0xffffffffu, l != -INFINITY);
       L += f;
       const int cnt = min(32, end - k0);
@@ -877,7 +878,7 @@ __global__ void __launch_bounds__(256, SCORED ? 3 : 4) live_finish_kernel(const 
         const float* l = p.ws_lse[1] + part.at(k) + r0;
 #pragma unroll
         for (int e = 0; e < LR; ++e)
-          if (r0 + 8 * e < rows) L[e] += weight(l[8 * e], M[e]);
+          if (r0 + 8 * e < rows) L[e] += merge_weight(l[8 * e], M[e]);
       }
 #pragma unroll
       for (int e = 0; e < LR; ++e)
@@ -919,6 +920,71 @@ __global__ void __launch_bounds__(256, SCORED ? 3 : 4) live_finish_kernel(const 
       if (256 * c < left) score[256 * c] = w[c] + mine;
     }
   }
+}
+
+// The merge for many rows of few partials: LIVE_SUB lanes a row, four rows a warp side by side. A row's time is
+// that of its dependent loads, whatever its partials, so a warp a row takes (62496 rows of 2 to 4 partials) 56 us.
+constexpr int LIVE_SUB = 8;
+template <int D>
+__global__ void __launch_bounds__(256, 4) live_merge_kernel(const __grid_constant__ LiveParams p) {
+  constexpr int Q = D / 4 / LIVE_SUB;  // float4 a lane: number sl, sl + LIVE_SUB, ... of the row
+  const int lane = threadIdx.x & 31, sl = lane % LIVE_SUB, first = lane - sl;
+  const int64_t id = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LIVE_SUB;
+  const bool live = id < (int64_t)p.n_tok * p.Hq;
+  LParts a{0, 0, 0, 0}, o{0, 0, 0, 0};  // of the prefix, of the own cache
+  bf16* dst = nullptr;
+  if (live) {
+    const int tok = (int)(id / p.Hq), hq = (int)(id - (int64_t)tok * p.Hq), hk = hq / p.G, gq = hq - hk * p.G;
+    const int b = live_req_of(p, tok), i = tok - p.tok_begin[b], own = p.own_of[b];
+    if (p.has_prefix) a = live_parts(p, 0, 0, hk, tok * p.G + gq);
+    if (own >= 0) o = live_parts(p, 1, own, hk, i * p.G + gq);
+    dst = p.o[b] + ((size_t)i * p.Hq + hq) * D;
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  const int total = a.count + o.count, most = __reduce_max_sync(0xffffffffu, total);
+  auto lse_of = [&](int k) {
+    return k >= total ? -INFINITY : k < a.count ? p.ws_lse[0][a.at(k)] : p.ws_lse[1][o.at(k - a.count)];
+  };
+  const float l0 = lse_of(sl);  // most rows have no more than a lane each
+  float M = l0;
+  for (int k0 = LIVE_SUB; k0 < most; k0 += LIVE_SUB) M = fmaxf(M, lse_of(k0 + sl));
+#pragma unroll
+  for (int off = LIVE_SUB / 2; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float L = 0.f;
+  float4 acc[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < most; k0 += LIVE_SUB) {
+    const float l = k0 ? lse_of(k0 + sl) : l0, f = merge_weight(l, M);
+    const unsigned wrote = __ballot_sync(0xffffffffu, l != -INFINITY) >> first;
+    L += f;
+    const int cnt = min(LIVE_SUB, most - k0);
+#pragma unroll 2
+    for (int c = 0; c < cnt; ++c) {
+      const float fc = __shfl_sync(0xffffffffu, f, first + c);
+      if ((wrote >> c) & 1u) {  // a partial that saw nothing was not written
+        const int k = k0 + c;
+        const float4* src = reinterpret_cast<const float4*>(k < a.count ? p.ws_o[0] + a.at(k) * D : p.ws_o[1] + o.at(k - a.count) * D) + sl;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const float4 v = __ldcg(src + q * LIVE_SUB);
+          acc[q].x = fmaf(fc, v.x, acc[q].x);
+          acc[q].y = fmaf(fc, v.y, acc[q].y);
+          acc[q].z = fmaf(fc, v.z, acc[q].z);
+          acc[q].w = fmaf(fc, v.w, acc[q].w);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int off = LIVE_SUB / 2; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+  if (!live) return;
+  const float inv = L != 0.f ? 1.f / L : 0.f;
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+    reinterpret_cast<uint2*>(dst)[sl + q * LIVE_SUB] =
+        make_uint2(pack_bf16x2(acc[q].x * inv, acc[q].y * inv), pack_bf16x2(acc[q].z * inv, acc[q].w * inv));
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -1012,6 +1078,7 @@ static cudaError_t launch_live_t(const LiveParams& p, const LiveMaps& maps, cuda
     e = launch_pdl(live_attn_kernel<D, SCORED>, dim3(p.n_cta[0] + p.n_cta[1]), dim3(LTHREADS), LCfg<D>::SMEM, s, p, maps);
     if (e != cudaSuccess) return e;
   }
+  if (p.merge_warps == 0) return launch_pdl(live_merge_kernel<D>, dim3(p.merge_blocks), dim3(256), 0, s, p);
   return launch_pdl(live_finish_kernel<D, SCORED>, dim3(p.merge_blocks + p.score_blocks), dim3(256), 0, s, p);
 }
 
@@ -1114,8 +1181,10 @@ cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_
     if (units[kind]) parts += 2 * (1 + p.n_cta[kind] / units[kind]);
   int wpr = 1;
   while (wpr < 8 && parts > 4 * wpr && out_rows * wpr * 2 <= (int64_t)live_sms() * 4 * 8) wpr *= 2;
-  p.merge_warps = wpr;
-  p.merge_blocks = (int32_t)((out_rows * wpr + 7) / 8);
+  // Several rows a warp where they are more than the warps of a wave and have few partials
+  const bool side = !scored && parts <= LIVE_SUB && out_rows > (int64_t)live_sms() * 4 * 8;
+  p.merge_warps = side ? 0 : wpr;
+  p.merge_blocks = (int32_t)(side ? (out_rows * LIVE_SUB + 255) / 256 : (out_rows * wpr + 7) / 8);
   p.score_blocks = (int32_t)chunks;
   uint8_t* at = static_cast<uint8_t*>(a.ws);
   size_t need = 0;

@@ -743,3 +743,11 @@ def test_live_batch_refuses_host_tensors(vc):
     with pytest.raises(ValueError):
         engine.LiveBatch(8, 2, 64, 1, 10, t, prefix=(pk, pk, 5))
     assert lb.n == [0] and lb.next_pos == [0]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("P", [None, 70, 1000])
+def test_prefix_many_rows_of_few_keys(vc, d, P):
+    """More rows than a wave of warps, each with a few partials: rows that see nothing, empty own caches, several
+    units a head."""
+    _attn_case(vc, 32, 2, d, [66, 300, 20, 0, 41], [40, 41, 39, 40, 1], P=P)
