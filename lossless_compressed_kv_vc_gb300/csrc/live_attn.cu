@@ -24,8 +24,8 @@
 //
 // What bounds it. One token a request: K and V from DRAM (8 caches of 8200 rows, 8 heads of 128: 49 us with the
 // merge, 236 MB, 0.71 of the copy rate; 4 of 131072: 385 us, 0.83), the rest start-up and, where scores are
-// kept, the second kernel's pass over them. Drafts over a prefix (2000 rows of a KV head, 65536 keys): 396 us,
-// 1.21 PFLOP/s, 0.64 of the bf16 peak: shared memory's bandwidth, since a pair of chains moves 320 KB a tile (Q
+// kept, the second kernel's pass over them. Drafts over a prefix (2000 rows of a KV head, 65536 keys): 387 us,
+// 1.24 PFLOP/s, 0.66 of the bf16 peak: shared memory's bandwidth, since a pair of chains moves 320 KB a tile (Q
 // twice 64, as S steps of 64 keys read it twice, K and V twice 32 each, and 64 in from L2), 2560 clocks at 128
 // bytes each of about 3000; leaving out all exponentials changes nothing. Many short caches (a few tiles a
 // piece): the pieces' fixed part, about 6 us each, of which instruction fetch is the largest.
@@ -923,7 +923,8 @@ __global__ void __launch_bounds__(256, SCORED ? 3 : 4) live_finish_kernel(const 
 }
 
 // The merge for many rows of few partials: LIVE_SUB lanes a row, four rows a warp side by side. A row's time is
-// that of its dependent loads, whatever its partials, so a warp a row takes (62496 rows of 2 to 4 partials) 56 us.
+// that of its dependent loads, whatever its partials (62496 rows of 2 to 4: the call 105 us with a warp a row, 68
+// so; 16000 of about 6: 396, 387).
 constexpr int LIVE_SUB = 8;
 template <int D>
 __global__ void __launch_bounds__(256, 4) live_merge_kernel(const __grid_constant__ LiveParams p) {
@@ -1181,7 +1182,8 @@ cudaError_t launch_live_attn(const LiveArgs& a, bool scored, cudaStream_t s, vc_
     if (units[kind]) parts += 2 * (1 + p.n_cta[kind] / units[kind]);
   int wpr = 1;
   while (wpr < 8 && parts > 4 * wpr && out_rows * wpr * 2 <= (int64_t)live_sms() * 4 * 8) wpr *= 2;
-  // Several rows a warp where they are more than the warps of a wave and have few partials
+  // Several rows a warp where they are more than the warps of a wave and have few partials (with fewer rows both
+  // take the same)
   const bool side = !scored && parts <= LIVE_SUB && out_rows > (int64_t)live_sms() * 4 * 8;
   p.merge_warps = side ? 0 : wpr;
   p.merge_blocks = (int32_t)(side ? (out_rows * LIVE_SUB + 255) / 256 : (out_rows * wpr + 7) / 8);
