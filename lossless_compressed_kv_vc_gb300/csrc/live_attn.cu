@@ -161,7 +161,7 @@ struct LCfg {
   static constexpr int OFF_BAR = OFF_T + NST * T_BYTES;
   static constexpr int SMEM = OFF_BAR + 448;
   static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
-  static_assert((2 * NST + 20) * 8 + 24 + sizeof(LPiece) <= 448, "barriers fit");
+  static_assert((2 * NST + 20) * 8 + 32 + sizeof(LPiece) <= 448, "barriers fit");
   static constexpr int OCOL = 4 * LS;          // TMEM: S (and P) of chain w at (2 w + step % 2) LS, O at OCOL + w D
   static constexpr uint32_t TCOLS = 512;
   static_assert(OCOL + 2 * D <= (int)TCOLS, "TMEM");
@@ -253,9 +253,12 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
   uint64_t* xbar = vbar + 2;      // [4] drain of an issuer's MMAs
   uint32_t* tslot = reinterpret_cast<uint32_t*>(xbar + 4);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
-  volatile uint32_t* s_odd = tslot + 2;  // [2] 1 + the chain's last step whose P V the softmax warps took
-  volatile uint32_t* s_issued = tslot + 4;  // loads issued so far
-  LPiece* s_first = reinterpret_cast<LPiece*>(tslot + 6);  // the CTA's first piece
+  // [2][2] by S buffer, as the barriers are: 1 + the chain's last step in it whose P V the softmax warps took. A
+  // warp may be a step ahead of the others, and so ahead of the P V issuer, which reads a step's word once all
+  // four have left the step; the word's next step needs the issuer's commit behind that.
+  volatile uint32_t* s_odd = tslot + 2;
+  volatile uint32_t* s_issued = tslot + 6;  // loads issued so far
+  LPiece* s_first = reinterpret_cast<LPiece*>(tslot + 8);  // the CTA's first piece
 
   if (warp == 12) tc05::alloc(tslot, C::TCOLS);
   if (tid == 13 * 32) *s_first = live_first(p);  // once: its code and parameters are cold in every cache
@@ -269,12 +272,12 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
         mbar_init(&sfull[i], 1);
         mbar_init(&pfull[i], 4);
         mbar_init(&ofull[i], 1);
+        s_odd[i] = 0;
       }
       mbar_init(&qfull[w], 4);
       mbar_init(&vbar[w], 4);
       mbar_init(&xbar[w], 1);
       mbar_init(&xbar[2 + w], 1);
-      s_odd[w] = 0;
     }
     fence_mbar_init();
     *s_abort = 0;
@@ -370,7 +373,7 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
                 break;
               }
               tc05::fence_after();
-              if (s_odd[w] != t + 1) {
+              if (s_odd[2 * w + (t & 1)] != t + 1) {
                 const uint32_t tP = tS + (t & 1) * LS, va = vaddr + h * (LS / 16) * 2048;
 #pragma unroll
                 for (int kk = 0; kk < LS / 16; ++kk)
@@ -641,7 +644,7 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
               const uint4 v = *reinterpret_cast<const uint4*>(sV + (c >> 3) * (LN * 128) + kv * 128 + (((c ^ kv) & 7) << 4));
               bad |= nonfinite_bf16x2(v.x) || nonfinite_bf16x2(v.y) || nonfinite_bf16x2(v.z) || nonfinite_bf16x2(v.w);
             }
-            if (bad) s_odd[w] = t + 1;
+            if (bad) s_odd[2 * w + (t & 1)] = t + 1;
             __syncwarp();
             if (lane == 0) mbar_arrive(&vbar[w]);
             if (!lwait_warp(&vbar[w], looked & 1, p.dev_status, s_abort)) {
@@ -649,7 +652,7 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
               break;
             }
             ++looked;
-            if (s_odd[w] == t + 1) {
+            if (s_odd[2 * w + (t & 1)] == t + 1) {
               if (!fresh && !pv_done(t - 1)) {
                 ok = false;
                 break;

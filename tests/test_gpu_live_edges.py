@@ -1,0 +1,85 @@
+"""GPU tests of the live-cache calls at the places where a masked or broken value could leak: value rows that are
+broken in several steps of a chain. Tolerances and helpers are those of test_gpu_live.py.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from tests.test_gpu_live import NAN, bits, cache, f64, gen, randn
+from tests.util import assert_attn_close
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def vc():
+    import __graft_entry__ as g
+    g.build()
+    import lossless_compressed_kv_vc_gb300 as m
+    return m
+
+
+def _attend(vc, Hq, Hkv, d, reqs, scored, prefix=None):
+    """reqs: (q, k, v, n, score) each; the outputs and the call's device status."""
+    B = len(reqs)
+    outs = [torch.zeros_like(r[0]) for r in reqs]
+    arr = (vc.vc_live_req * B)(*[vc.vc_live_req(q.data_ptr(), o.data_ptr(), q.shape[0], vc.live_kv(k, v, n, s))
+                                 for (q, k, v, n, s), o in zip(reqs, outs)])
+    shape, R = vc.vc_shape(B, Hq, Hkv, d), max(r[0].shape[0] for r in reqs)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    if scored:
+        ws = torch.empty(vc.vc_scored_workspace_size(shape, R, max(r[3] for r in reqs)), dtype=torch.uint8, device="cuda")
+        vc.vc_scored_attn(shape, arr, ws, status)
+    else:
+        ws = torch.empty(vc.vc_prefix_workspace_size(shape, R), dtype=torch.uint8, device="cuda")
+        vc.vc_prefix_attn(shape, prefix, arr, ws, status)
+    torch.cuda.synchronize()
+    return outs, int(status.item())
+
+
+# Hq, Hkv, d, n, query rows, broken own rows: new keys that lie in two or three 64-key steps of a chain, the steps
+# one behind the other, with a broken value row in each.
+STEPS = [(8, 2, 64, 160, 64, (120, 159)),             # chains of 128 rows each: keys 96..159 in two steps
+         (8, 2, 64, 159, 64, tuple(range(118, 159))),  # every row from one on
+         (16, 4, 128, 290, 64, (250, 260, 289)),
+         (4, 4, 128, 300, 128, (190, 290)),            # both chains the same rows, a half of every tile each
+         (4, 4, 128, 340, 128, (240, 330)),
+         (32, 4, 128, 460, 40, (432, 450, 459)),       # a unit of 256 rows and one of 64
+         (4, 4, 64, 520, 128, (400, 450, 500, 519))]
+
+
+@pytest.mark.parametrize("scored", [False, True])
+@pytest.mark.parametrize("case", STEPS)
+@pytest.mark.parametrize("bad", [NAN, float("inf")])
+def test_broken_values_in_consecutive_steps(vc, case, bad, scored):
+    """Rows before the first broken token come out as the oracle's over the keys they see, rows from it on are not
+    finite, whichever warp of a chain is ahead; weights do not depend on V."""
+    Hq, Hkv, d, n, r, broken = case
+    if scored and r * (Hq // Hkv) > 256:
+        r = 256 // (Hq // Hkv)
+    g = gen(41)
+    reqs, first = [], broken[0] - (n - r)  # the first row that sees a broken one
+    assert 0 < first < r
+    for _ in range(4):
+        q, (k, v, score, _) = randn(g, r, Hq, d), cache(g, Hkv, d, n, n + 3)
+        v[:, list(broken)] = bad
+        reqs.append((q, k, v, n, score))
+    refs = [O.live_attn(f64(q), f64(k[:, :n]), np.where(np.isfinite(f64(v[:, :n])), f64(v[:, :n]), 0.0))
+            for q, k, v, _, _ in reqs]
+    old = [s.clone() for *_, s in reqs]
+    for _ in range(10):
+        for (*_, s), o in zip(reqs, old):
+            s.copy_(o)
+        outs, status = _attend(vc, Hq, Hkv, d, reqs, scored)
+        assert status == 0
+        for o, (_, _, _, _, s), was, (ref, w) in zip(outs, reqs, old, refs):
+            assert_attn_close(o[:first], ref[:first])
+            assert not torch.isfinite(o[first:]).any()
+            if scored:
+                # a factor within 1 +- (2 d 2^-23 max sum|q k| / sqrt(d) + 2^-20), and the sum's two roundings; with
+                # unit normal q and k, sum|q k| / sqrt(d) stays below 16 at these sizes
+                lim = w * (2 * d * 2.0 ** -23 * 16 + 2.0 ** -20) + 2.0 ** -23 * (f64(was[:, :n]) + w)
+                assert np.all(np.abs(f64(s[:, :n]) - f64(was[:, :n]) - w) <= lim)
+            else:
+                assert np.array_equal(bits(s), bits(was))
