@@ -783,14 +783,16 @@ class LiveBatch:
 
     def append(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rows: List[int], stream=None):
         """The next rows[b] tokens of every request: q bf16 [B][R][Hq][d], k and v bf16 [B][R][Hkv][d],
-        R >= max(rows), any stride between tokens (slices of a fused projection). Rotated queries land in
-        q_rot; caches, n and next_pos move on."""
+        R >= max(rows), any stride between tokens that keeps them apart (slices of a fused projection).
+        Rotated queries land in q_rot; caches, n and next_pos move on."""
         if len(rows) != self.B or any(r < 0 or r > min(self.max_rows, q.shape[1]) for r in rows):
             raise ValueError("rows: one count per request, 0 .. min(max_rows, the tokens given)")
         for t, heads in ((q, self.Hq), (k, self.Hkv), (v, self.Hkv)):
             if t.dtype != torch.bfloat16 or tuple(t.shape) != (self.B, q.shape[1], heads, self.d) or \
                     t.stride(3) != 1 or (heads > 1 and t.stride(2) != self.d) or t.device.type != self.device.type:
                 raise ValueError("q, k and v are bf16 [B][R][heads][d] on the batch's device, each token's heads contiguous")
+            if max(rows) > 1 and t.stride(1) < heads * self.d:  # an expanded tensor's 0 would mean packed tokens
+                raise ValueError("the tokens of q, k and v do not overlap: a stride of heads * d or more between them")
         for b in range(self.B):
             e = self._rope_req[b]
             e.q, e.k, e.v = q[b].data_ptr(), k[b].data_ptr(), v[b].data_ptr()

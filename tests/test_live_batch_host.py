@@ -1,0 +1,82 @@
+"""engine.LiveBatch's host side on the CPU: what it hands to the library, and what it turns down before. The library
+call is replaced by a recorder, so nothing is launched and no address is read."""
+import contextlib
+
+import pytest
+import torch
+
+Hq, Hkv, D = 8, 2, 64
+
+
+class _Event:
+    def record(self, *_):
+        pass
+
+
+class _Calls(list):
+    """The descriptors of each call, by name: (name, shape, [descriptor ...])."""
+
+    def recorder(self, name, at):
+        def call(shape, *args, **kw):
+            arr = args[at]
+            self.append((name, shape, [type(e).from_buffer_copy(e) for e in arr]))
+            return 0
+        return call
+
+
+@pytest.fixture(scope="module")
+def vc():
+    import __graft_entry__ as g
+    g.build()
+    import lossless_compressed_kv_vc_gb300 as m
+    return m
+
+
+@pytest.fixture
+def calls(vc, monkeypatch):
+    from lossless_compressed_kv_vc_gb300 import engine
+    made = _Calls()
+    monkeypatch.setattr(torch.cuda, "Event", _Event)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)  # no streams to put in order
+    for name, at in (("vc_rope_append", 1), ("vc_prefix_attn", 1), ("vc_scored_attn", 0), ("vc_evict_kv", 0)):
+        monkeypatch.setattr(engine, name, made.recorder(name, at))
+    return made
+
+
+def live(vc, B=2, cap=64, **kw):
+    from lossless_compressed_kv_vc_gb300 import engine
+    return engine.LiveBatch(Hq, Hkv, D, B, cap, vc.vc_rope_init(vc.VC_ROPE_NONE, D), device="cpu", **kw)
+
+
+def new(heads, B=2, R=1):
+    return torch.zeros((B, R, heads, D), dtype=torch.bfloat16)
+
+
+def test_strides_of_a_fused_projection_are_passed_on(vc, calls):
+    lb = live(vc, max_rows=4)
+    x = torch.zeros((2, 4, (Hq + 2 * Hkv) * D), dtype=torch.bfloat16)
+    q, k, v = (t.unflatten(2, (-1, D)) for t in x.split([Hq * D, Hkv * D, Hkv * D], 2))
+    lb.append(q, k, v, [4, 2])
+    name, _, arr = calls[0]
+    assert name == "vc_rope_append" and [e.n_rows for e in arr] == [4, 2]
+    for b, e in enumerate(arr):
+        assert (e.q_stride, e.k_stride, e.v_stride) == ((Hq + 2 * Hkv) * D,) * 3
+        assert (e.q, e.k, e.v) == (q[b].data_ptr(), k[b].data_ptr(), v[b].data_ptr())
+    assert lb.n == [4, 2] and lb.next_pos == [4, 2]
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_tokens_that_overlap_are_refused(vc, calls, which):
+    """A tensor expanded over its tokens has stride 0 between them, which the library takes as packed tokens: it
+    would read the memory behind the only one. Nothing is called and nothing moves on."""
+    lb = live(vc, max_rows=4)
+    for make in (lambda h: new(h).expand(2, 4, h, D), lambda h: new(h, R=4).as_strided((2, 4, h, D), (h * D, D, D, 1))):
+        qkv = [new(Hq, R=4), new(Hkv, R=4), new(Hkv, R=4)]
+        qkv[which] = make((Hq, Hkv, Hkv)[which])
+        with pytest.raises(ValueError):
+            lb.append(*qkv, [4, 1])
+        assert not calls and lb.n == [0, 0] and lb.next_pos == [0, 0]
+    qkv[which] = new((Hq, Hkv, Hkv)[which]).expand(2, 4, -1, D)
+    lb.append(*qkv, [1, 1])  # no second token is read
+    assert len(calls) == 1 and lb.n == [1, 1]
