@@ -793,10 +793,12 @@ class LiveBatch:
                 raise ValueError("q, k and v are bf16 [B][R][heads][d] on the batch's device, each token's heads contiguous")
             if max(rows) > 1 and t.stride(1) < heads * self.d:  # an expanded tensor's 0 would mean packed tokens
                 raise ValueError("the tokens of q, k and v do not overlap: a stride of heads * d or more between them")
+        # between the tokens; a single one has none, whatever its tensor's dimension of size one says
+        strides = (q.stride(1), k.stride(1), v.stride(1)) if max(rows) > 1 else (0, 0, 0)
         for b in range(self.B):
             e = self._rope_req[b]
             e.q, e.k, e.v = q[b].data_ptr(), k[b].data_ptr(), v[b].data_ptr()
-            e.q_stride, e.k_stride, e.v_stride = q.stride(1), k.stride(1), v.stride(1)
+            e.q_stride, e.k_stride, e.v_stride = strides
             e.pos, e.pos0, e.n_rows, e.q_out, e.kv = None, self.next_pos[b], rows[b], self.q_rot[b].data_ptr(), self._kv(b)
         with torch.cuda.device(self.device):
             self._order(stream)

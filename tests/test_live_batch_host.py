@@ -80,3 +80,18 @@ def test_tokens_that_overlap_are_refused(vc, calls, which):
     qkv[which] = new((Hq, Hkv, Hkv)[which]).expand(2, 4, -1, D)
     lb.append(*qkv, [1, 1])  # no second token is read
     assert len(calls) == 1 and lb.n == [1, 1]
+
+
+def test_a_single_token_has_no_stride(vc, calls):
+    """[B][heads][1][d] transposed to [B][1][heads][d], the layout of a projection split by heads: the stride of its
+    dimension of size one is d, less than a token, and says nothing."""
+    lb = live(vc)
+    q, k, v = (torch.zeros((2, h, 1, D), dtype=torch.bfloat16).transpose(1, 2) for h in (Hq, Hkv, Hkv))
+    assert q.stride(1) == D
+    lb.append(q, k, v, [1, 1])
+    for b, e in enumerate(calls[0][2]):
+        assert (e.q_stride, e.k_stride, e.v_stride) == (0, 0, 0)
+        assert (e.q, e.k, e.v) == (q[b].data_ptr(), k[b].data_ptr(), v[b].data_ptr())
+    x = torch.zeros((2, 3, Hq + 2 * Hkv, D), dtype=torch.bfloat16)  # the last of three tokens: strides of a longer tensor
+    lb.append(x[:, 2:, :Hq], x[:, 2:, Hq : Hq + Hkv], x[:, 2:, Hq + Hkv :], [1, 0])
+    assert [e.q for e in calls[1][2]] == [x[b, 2].data_ptr() for b in range(2)]
