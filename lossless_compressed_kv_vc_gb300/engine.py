@@ -722,7 +722,7 @@ class LiveBatch:
     all requests and read once for them (vc_prefix_attn); without one, gathering every cached row's
     attention weight (vc_scored_attn), and a cache that has outgrown `budget` rows by more than
     `slack` is cut back to its rows of largest weight (vc_evict_kv), the first `sink` tokens and the
-    newest `recent` ones always among them. budget 0 keeps everything.
+    newest `recent` ones always among them (sink + recent <= budget). budget 0 keeps everything.
 
     k, v: bf16 [B][Hkv][cap][d]; n[b]: rows request b holds; next_pos[b]: its next token's position
     (a prefix takes the first ones). All of a step's calls run on `stream` (the current one by
@@ -735,6 +735,8 @@ class LiveBatch:
             raise ValueError("a batch over a shared prefix keeps its own caches whole: budget needs prefix=None")
         if budget > 0 and (cap < budget + slack + max_rows or min(slack, sink, recent) < 0):
             raise ValueError("cap must hold budget + slack + max_rows rows; slack, sink and recent are not negative")
+        if budget > 0 and sink + recent > budget:  # of too many guarded rows the lower ones stay: the newest would go
+            raise ValueError("the budget must hold the sink and recent rows, which always stay")
         self.Hq, self.Hkv, self.d, self.B, self.cap, self.rope, self.max_rows = Hq, Hkv, d, B, cap, rope, max_rows
         self.prefix, self.budget, self.slack, self.sink, self.recent = prefix, budget, slack, sink, recent
         self.device = torch.device(device)

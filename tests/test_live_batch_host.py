@@ -95,3 +95,17 @@ def test_a_single_token_has_no_stride(vc, calls):
     x = torch.zeros((2, 3, Hq + 2 * Hkv, D), dtype=torch.bfloat16)  # the last of three tokens: strides of a longer tensor
     lb.append(x[:, 2:, :Hq], x[:, 2:, Hq : Hq + Hkv], x[:, 2:, Hq + Hkv :], [1, 0])
     assert [e.q for e in calls[1][2]] == [x[b, 2].data_ptr() for b in range(2)]
+
+
+def test_a_budget_holds_the_rows_that_always_stay(vc, calls):
+    """With more sink and recent rows than the budget, eviction would keep the lower of them and drop the newest."""
+    for kw in (dict(sink=4, recent=128), dict(sink=129, recent=0), dict(sink=0, recent=129)):
+        with pytest.raises(ValueError):
+            live(vc, cap=200, budget=128, **kw)
+    live(vc, cap=200, sink=4, recent=10 ** 6)  # no budget: nothing goes
+    lb = live(vc, B=1, cap=200, budget=128, sink=4, recent=124)
+    lb.n, lb.next_pos = [140], [140]
+    lb.evict()
+    name, shape, (e,) = calls[0]
+    assert (name, shape.B, e.kv.n, e.keep, e.sink, e.recent_from) == ("vc_evict_kv", 1, 140, 128, 4, 16)
+    assert lb.n == [128]
