@@ -743,6 +743,7 @@ class LiveBatch:
         self.shape = vc_shape(B, Hq, Hkv, d)
         new = lambda shape, dt: torch.zeros(shape, dtype=dt, device=self.device)
         self.k, self.v = (new((B, Hkv, cap, d), torch.bfloat16) for _ in range(2))
+        self.device = self.k.device  # with its index: the current device may be another one at the next call
         self.score = new((B, Hkv, cap), torch.float32) if prefix is None else None
         self.pos = new((B, Hkv, cap), torch.int32) if prefix is None else None
         self.q_rot = new((B, max_rows, Hq, d), torch.bfloat16)
@@ -753,7 +754,7 @@ class LiveBatch:
             pk, pv, ctx = prefix
             for t in (pk, pv):
                 if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape != pk.shape or t.shape[0] != Hkv or \
-                        t.shape[2] != d or not t.is_contiguous() or t.device.type != self.device.type or \
+                        t.shape[2] != d or not t.is_contiguous() or t.device != self.device or \
                         not 0 <= ctx <= t.shape[1]:
                     raise ValueError("a prefix is (k, v, rows): contiguous bf16 [Hkv][cap][d] on the batch's device, "
                                      "0 <= rows <= cap")
@@ -791,7 +792,7 @@ class LiveBatch:
             raise ValueError("rows: one count per request, 0 .. min(max_rows, the tokens given)")
         for t, heads in ((q, self.Hq), (k, self.Hkv), (v, self.Hkv)):
             if t.dtype != torch.bfloat16 or tuple(t.shape) != (self.B, q.shape[1], heads, self.d) or \
-                    t.stride(3) != 1 or (heads > 1 and t.stride(2) != self.d) or t.device.type != self.device.type:
+                    t.stride(3) != 1 or (heads > 1 and t.stride(2) != self.d) or t.device != self.device:
                 raise ValueError("q, k and v are bf16 [B][R][heads][d] on the batch's device, each token's heads contiguous")
             if max(rows) > 1 and t.stride(1) < heads * self.d:  # an expanded tensor's 0 would mean packed tokens
                 raise ValueError("the tokens of q, k and v do not overlap: a stride of heads * d or more between them")
@@ -814,7 +815,7 @@ class LiveBatch:
         if len(rows) != self.B or any(r < 0 or r > self.max_rows for r in rows):
             raise ValueError("rows: one count per request, 0 .. max_rows")
         if o.dtype != torch.bfloat16 or o.dim() != 4 or o.shape[0] != self.B or o.shape[1] < max(rows) or \
-                tuple(o.shape[2:]) != (self.Hq, self.d) or not o[0].is_contiguous() or o.device.type != self.device.type:
+                tuple(o.shape[2:]) != (self.Hq, self.d) or not o[0].is_contiguous() or o.device != self.device:
             raise ValueError("o is bf16 [B][R][Hq][d] on the batch's device, R >= max(rows), each request's rows contiguous")
         for b in range(self.B):
             e = self._live_req[b]

@@ -109,3 +109,41 @@ def test_a_budget_holds_the_rows_that_always_stay(vc, calls):
     name, shape, (e,) = calls[0]
     assert (name, shape.B, e.kv.n, e.keep, e.sink, e.recent_from) == ("vc_evict_kv", 1, 140, 128, 4, 16)
     assert lb.n == [128]
+
+
+class _On0(torch.Tensor):
+    """A host tensor that says it is on the first GPU."""
+    device = torch.device("cuda", 0)
+
+
+class _On1(torch.Tensor):
+    device = torch.device("cuda", 1)
+
+
+def test_tensors_of_another_gpu_are_refused(vc, calls, monkeypatch):
+    """The batch lives on the device that was current when it was made; a tensor of another one of the same kind is
+    turned down before its address is passed on."""
+    for name in ("zeros", "empty"):
+        real = getattr(torch, name)
+        monkeypatch.setattr(torch, name, lambda *a, device, real=real, **kw: real(*a, **kw).as_subclass(_On0))
+    from lossless_compressed_kv_vc_gb300 import engine
+    table = vc.vc_rope_init(vc.VC_ROPE_NONE, D)
+    lb = engine.LiveBatch(Hq, Hkv, D, 2, 64, table, device="cuda")
+    assert lb.device == torch.device("cuda", 0)
+    make = lambda h, on: torch.ones((2, 1, h, D), dtype=torch.bfloat16).as_subclass(on)
+    for which in range(3):
+        on = [_On0] * 3
+        on[which] = _On1
+        with pytest.raises(ValueError):
+            lb.append(make(Hq, on[0]), make(Hkv, on[1]), make(Hkv, on[2]), [1, 1])
+    with pytest.raises(ValueError):
+        lb.attend(make(Hq, _On1), [1, 1])
+    pk, pv = (torch.ones((Hkv, 20, D), dtype=torch.bfloat16).as_subclass(c) for c in (_On0, _On1))
+    for prefix in ((pk, pv, 5), (pv, pk, 5)):
+        with pytest.raises(ValueError):
+            engine.LiveBatch(Hq, Hkv, D, 2, 64, table, prefix=prefix, device="cuda")
+    assert not calls and lb.n == [0, 0]
+    lb.append(make(Hq, _On0), make(Hkv, _On0), make(Hkv, _On0), [1, 1])
+    lb.attend(make(Hq, _On0), [1, 1])
+    engine.LiveBatch(Hq, Hkv, D, 2, 64, table, prefix=(pk, pk, 5), device="cuda")
+    assert [c[0] for c in calls] == ["vc_rope_append", "vc_scored_attn"]
