@@ -817,6 +817,8 @@ class LiveBatch:
         if o.dtype != torch.bfloat16 or o.dim() != 4 or o.shape[0] != self.B or o.shape[1] < max(rows) or \
                 tuple(o.shape[2:]) != (self.Hq, self.d) or not o[0].is_contiguous() or o.device != self.device:
             raise ValueError("o is bf16 [B][R][Hq][d] on the batch's device, R >= max(rows), each request's rows contiguous")
+        if sum(r > 0 for r in rows) > 1 and o.stride(0) < max(rows) * self.Hq * self.d:
+            raise ValueError("each request's rows of o are its own")
         for b in range(self.B):
             e = self._live_req[b]
             e.q, e.o, e.n_rows, e.kv = self.q_rot[b].data_ptr(), o[b].data_ptr(), rows[b], self._kv(b)

@@ -147,3 +147,17 @@ def test_tensors_of_another_gpu_are_refused(vc, calls, monkeypatch):
     lb.attend(make(Hq, _On0), [1, 1])
     engine.LiveBatch(Hq, Hkv, D, 2, 64, table, prefix=(pk, pk, 5), device="cuda")
     assert [c[0] for c in calls] == ["vc_rope_append", "vc_scored_attn"]
+
+
+def test_outputs_that_overlap_are_refused(vc, calls):
+    """An output expanded over the batch would take every request's rows in one place."""
+    lb = live(vc, max_rows=3)
+    one = new(Hq, B=1, R=3)
+    for o in (one.expand(2, 3, Hq, D), new(Hq, R=3).as_strided((2, 3, Hq, D), (2 * Hq * D, Hq * D, D, 1))):
+        with pytest.raises(ValueError):
+            lb.attend(o, [3, 1])
+    assert not calls
+    lb.attend(one.expand(2, 3, Hq, D), [0, 3])
+    o = torch.zeros((2, 5, Hq, D), dtype=torch.bfloat16)[:, :3]
+    lb.attend(o, [3, 2])
+    assert [e.o for e in calls[1][2]] == [o[b].data_ptr() for b in range(2)]
