@@ -460,7 +460,8 @@ vc_status vc_rope_init(const vc_rope_config* config, vc_rope* out);
  * q_out may be q itself when q is packed; otherwise outputs do not overlap inputs. q may be NULL
  * (with q_out) for keys alone. Requests with n_rows == 0 are skipped; pos0 + n_rows must stay
  * within int32. rot_dim <= d. Rotation in fp32, rounded once to bf16.
- * Errors before anything is launched: VC_ERR_INVALID; VC_ERR_UNSUPPORTED (d, rot_dim, more than 2^30 tokens). */
+ * Errors before anything is launched: VC_ERR_INVALID; VC_ERR_UNSUPPORTED (d, rot_dim, more than 2^30 tokens,
+ * tokens of more than 2^33 channels). */
 typedef struct vc_rope_req {
   const void* q;       /* bf16, token t's [Hq][d] at q + t * q_stride */
   const void* k;       /* bf16, token t's [Hkv][d] at k + t * k_stride */

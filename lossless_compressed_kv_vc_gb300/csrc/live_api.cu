@@ -111,6 +111,8 @@ vc_status vc_rope_append(const vc_shape* shape, const vc_rope* rope, const vc_ro
   if (!rope || !req || (rope->layout != VC_ROPE_HALF && rope->layout != VC_ROPE_INTERLEAVED)) return VC_ERR_INVALID;
   if (rope->rot_dim < 16 || rope->rot_dim > shape->d || rope->rot_dim % 16 != 0) return VC_ERR_UNSUPPORTED;
   if (!isfinite((float)rope->amp)) return VC_ERR_INVALID;
+  // a token's 16-byte pieces are numbered in 32 bits, with room for a step beyond the last one
+  if (((int64_t)shape->Hq + 2 * (int64_t)shape->Hkv) * (shape->d / 8) > (int64_t(1) << 30)) return VC_ERR_UNSUPPORTED;
   RopeParams p;
   memset(&p, 0, sizeof(p));
   p.Hq = shape->Hq;
