@@ -901,6 +901,17 @@ __global__ void __launch_bounds__(256, SCORED ? 3 : 4) live_finish_kernel(const 
       for (int e = 0; e < 2; ++e)
         if (r0 + 4 * e < rows) {
           const float lse = s_lse[r0 + 4 * e];
+          if (lse != lse) {  // the row's weights are NaN: those of the keys it sees, not of the ones behind them
+            const int seen = R.n - R.n_rows + (r0 + 4 * e) / p.G - (k0 + (threadIdx.x & ~3));  // last one, from the group's first
+#pragma unroll
+            for (int c = 0; c < SP; ++c) {
+              if (256 * c <= seen) sum[c].x = lse;
+              if (256 * c + 1 <= seen) sum[c].y = lse;
+              if (256 * c + 2 <= seen) sum[c].z = lse;
+              if (256 * c + 3 <= seen) sum[c].w = lse;
+            }
+            continue;
+          }
 #pragma unroll
           for (int c = 0; c < SP; ++c) {
             sum[c].x += ex2_approx(fmaf(v[c][e].x, p.scale_log2, -lse));

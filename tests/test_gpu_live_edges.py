@@ -83,3 +83,34 @@ def test_broken_values_in_consecutive_steps(vc, case, bad, scored):
                 assert np.all(np.abs(f64(s[:, :n]) - f64(was[:, :n]) - w) <= lim)
             else:
                 assert np.array_equal(bits(s), bits(was))
+
+
+@pytest.mark.parametrize("what", ["query", "key"])
+@pytest.mark.parametrize("Hq,Hkv,d,n,r,at", [(8, 2, 64, 300, 5, 0), (8, 2, 64, 257, 5, 2), (32, 2, 128, 1030, 8, 5),
+                                             (4, 4, 64, 1100, 120, 40), (4, 4, 128, 64, 64, 1)])
+def test_a_broken_row_leaves_the_weights_of_keys_it_does_not_see(vc, Hq, Hkv, d, n, r, at, what):
+    """One head of row `at` has a NaN query, or its key an infinite channel that gives it a product of +inf, and so NaN
+    weights, and the other rows that see it -inf, a weight of 0: the scores of keys that only other rows see stay
+    finite."""
+    g = gen(43)
+    q, (k, v, score, _) = randn(g, r, Hq, d), cache(g, Hkv, d, n, n + 3)
+    if what == "query":
+        q[at, 0] = NAN
+    else:
+        k[:, n - r + at, 3] = float("inf")
+        q[..., 3] = -q[..., 3].abs() - 0.125
+        q[at, 0, 3] *= -1
+    with np.errstate(invalid="ignore"):
+        ref, w = O.live_attn(f64(q), f64(k[:, :n]), f64(v[:, :n]))
+    was = f64(score[:, :n])
+    (o,), status = _attend(vc, Hq, Hkv, d, [(q, k, v, n, score)], True)
+    got = f64(score[:, :n])
+    assert status == 0
+    assert np.array_equal(np.isnan(got), np.isnan(w)) and np.isnan(w).any() and np.isfinite(w).any()
+    fine = np.isfinite(w)
+    # as above, with the largest |q k| of finite keys below 16
+    lim = w * (2 * d * 2.0 ** -23 * 16 + 2.0 ** -20) + 2.0 ** -23 * (was + w)
+    assert np.all(np.abs(got - was - w)[fine] <= lim[fine])
+    rows = np.isfinite(ref).all(-1)
+    assert np.array_equal(torch.isfinite(o).all(-1).cpu().numpy(), rows)
+    assert_attn_close(o[torch.tensor(rows)][:, None], ref[rows][:, None])
