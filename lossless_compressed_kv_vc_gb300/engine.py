@@ -812,13 +812,7 @@ class LiveBatch:
 
     def attend(self, o: torch.Tensor, rows: List[int], stream=None):
         """Attention of the rows just appended, into o bf16 [B][R][Hq][d], R >= max(rows)."""
-        if len(rows) != self.B or any(r < 0 or r > self.max_rows for r in rows):
-            raise ValueError("rows: one count per request, 0 .. max_rows")
-        if o.dtype != torch.bfloat16 or o.dim() != 4 or o.shape[0] != self.B or o.shape[1] < max(rows) or \
-                tuple(o.shape[2:]) != (self.Hq, self.d) or not o[0].is_contiguous() or o.device != self.device:
-            raise ValueError("o is bf16 [B][R][Hq][d] on the batch's device, R >= max(rows), each request's rows contiguous")
-        if sum(r > 0 for r in rows) > 1 and o.stride(0) < max(rows) * self.Hq * self.d:
-            raise ValueError("each request's rows of o are its own")
+        self._check_out(o, rows)
         for b in range(self.B):
             e = self._live_req[b]
             e.q, e.o, e.n_rows, e.kv = self.q_rot[b].data_ptr(), o[b].data_ptr(), rows[b], self._kv(b)
@@ -828,6 +822,17 @@ class LiveBatch:
                 vc_prefix_attn(self.shape, self._prefix, self._live_req, self.ws, self.dev_status, stream)
             else:
                 vc_scored_attn(self.shape, self._live_req, self.ws, self.dev_status, stream)
+
+    def _check_out(self, o: torch.Tensor, rows: List[int]):
+        if len(rows) != self.B or any(r < 0 or r > self.max_rows for r in rows):
+            raise ValueError("rows: one count per request, 0 .. max_rows")
+        if o.dtype != torch.bfloat16 or o.dim() != 4 or o.shape[0] != self.B or o.shape[1] < max(rows) or \
+                tuple(o.shape[2:]) != (self.Hq, self.d) or not o[0].is_contiguous() or o.device != self.device:
+            raise ValueError("o is bf16 [B][R][Hq][d] on the batch's device, R >= max(rows), each request's rows contiguous")
+        if sum(r > 0 for r in rows) > 1 and o.stride(0) < max(rows) * self.Hq * self.d:
+            raise ValueError("each request's rows of o are its own")
+        if any(r > 0 and (o.data_ptr() + 2 * b * o.stride(0)) % 16 for b, r in enumerate(rows)):
+            raise ValueError("each request's rows of o start on a 16-byte boundary")
 
     def evict(self, stream=None):
         """Cut caches that hold more than budget + slack rows back to budget."""
@@ -848,6 +853,7 @@ class LiveBatch:
              stream=None):
         """append, attend and evict for the next rows (one token per request by default)."""
         rows = [1] * self.B if rows is None else rows
+        self._check_out(o, rows)  # before the caches move on
         self.append(q, k, v, rows, stream)
         self.attend(o, rows, stream)
         self.evict(stream)

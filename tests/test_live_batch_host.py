@@ -161,3 +161,16 @@ def test_outputs_that_overlap_are_refused(vc, calls):
     o = torch.zeros((2, 5, Hq, D), dtype=torch.bfloat16)[:, :3]
     lb.attend(o, [3, 2])
     assert [e.o for e in calls[1][2]] == [o[b].data_ptr() for b in range(2)]
+
+
+def test_a_step_with_a_bad_output_moves_nothing(vc, calls):
+    """step looks at its output before it appends: the caller can give the same tokens again."""
+    lb = live(vc)
+    q, k, v = new(Hq), new(Hkv), new(Hkv)
+    odd = torch.zeros(2 * Hq * D + 4, dtype=torch.bfloat16)[4:].view(2, 1, Hq, D)
+    for o in (new(Hq).float(), new(Hkv), new(Hq, B=1), new(Hq, B=1).expand(2, 1, Hq, D), odd):
+        with pytest.raises(ValueError):
+            lb.step(q, k, v, o)
+        assert not calls and lb.n == [0, 0] and lb.next_pos == [0, 0]
+    lb.step(q, k, v, new(Hq))
+    assert [c[0] for c in calls] == ["vc_rope_append", "vc_scored_attn"] and lb.n == [1, 1]
