@@ -790,6 +790,8 @@ class LiveBatch:
         Rotated queries land in q_rot; caches, n and next_pos move on."""
         if len(rows) != self.B or any(r < 0 or r > min(self.max_rows, q.shape[1]) for r in rows):
             raise ValueError("rows: one count per request, 0 .. min(max_rows, the tokens given)")
+        if any(p + r >= 2 ** 31 for p, r in zip(self.next_pos, rows)):
+            raise ValueError("positions are int32")
         for t, heads in ((q, self.Hq), (k, self.Hkv), (v, self.Hkv)):
             if t.dtype != torch.bfloat16 or tuple(t.shape) != (self.B, q.shape[1], heads, self.d) or \
                     t.stride(3) != 1 or (heads > 1 and t.stride(2) != self.d) or t.device != self.device:

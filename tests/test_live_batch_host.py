@@ -174,3 +174,16 @@ def test_a_step_with_a_bad_output_moves_nothing(vc, calls):
         assert not calls and lb.n == [0, 0] and lb.next_pos == [0, 0]
     lb.step(q, k, v, new(Hq))
     assert [c[0] for c in calls] == ["vc_rope_append", "vc_scored_attn"] and lb.n == [1, 1]
+
+
+def test_positions_stay_within_int32(vc, calls):
+    """A descriptor's int32 would take 2^31 as a position before the first."""
+    lb = live(vc, cap=200, budget=128)
+    lb.next_pos = [2 ** 31 - 2, 7]
+    x = [new(h) for h in (Hq, Hkv, Hkv)]
+    lb.append(*x, [1, 1])
+    assert [e.pos0 for e in calls[0][2]] == [2 ** 31 - 2, 7]
+    with pytest.raises(ValueError):
+        lb.append(*x, [1, 1])
+    assert len(calls) == 1 and lb.n == [1, 1] and lb.next_pos == [2 ** 31 - 1, 8]
+    lb.append(*x, [0, 1])
