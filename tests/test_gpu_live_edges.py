@@ -114,3 +114,82 @@ def test_a_broken_row_leaves_the_weights_of_keys_it_does_not_see(vc, Hq, Hkv, d,
     rows = np.isfinite(ref).all(-1)
     assert np.array_equal(torch.isfinite(o).all(-1).cpu().numpy(), rows)
     assert_attn_close(o[torch.tensor(rows)][:, None], ref[rows][:, None])
+
+
+def _smallest(call, enough, wrong):
+    """The smallest workspace, in bytes, that call(bytes) does not turn down with the status `wrong`."""
+    lo, hi = 0, enough  # lo is refused
+    assert call(0) == wrong and call(enough) == 0
+    while hi - lo > 1:
+        mid = (lo + hi) // 2
+        st = call(mid)
+        assert st in (0, wrong)
+        lo, hi = (mid, hi) if st == wrong else (lo, mid)
+    return hi
+
+
+@pytest.mark.parametrize("kind", ["prefix", "scored", "evict"])
+def test_the_least_workspace_and_a_byte_less(vc, kind):
+    """A call needs no more than the size that the library names. With the least that it takes the words behind stay
+    as they were and its results are those with all of it; a byte less is refused and nothing is written."""
+    Hq, Hkv, d = 8, 2, 64
+    ns, rows, B = [500, 70, 300], [9, 9, 2], 3
+    g = gen(47)
+    shape = vc.vc_shape(B, Hq, Hkv, d)
+    state = [cache(g, Hkv, d, n, n + 2) for n in ns]
+    for (_, _, _, p), n in zip(state, ns):
+        p[:, :n] = torch.arange(n, device="cuda", dtype=torch.int32)
+    qs = [randn(g, r, Hq, d) for r in rows]
+    outs = [torch.full_like(q, 7.0) for q in qs]
+    old = [[t.clone() for t in s] for s in state] + [[o.clone() for o in outs]]
+    pk, pv, _, _ = cache(g, Hkv, d, 300, 300)
+    prefix = vc.vc_kv_full(pk.data_ptr(), pv.data_ptr(), 300, 300)
+    size = {"prefix": vc.vc_prefix_workspace_size(shape, max(rows)), "evict": vc.vc_evict_workspace_size(shape, max(ns)),
+            "scored": vc.vc_scored_workspace_size(shape, max(rows), max(ns))}[kind]
+    buf = torch.empty(size + 4096, dtype=torch.uint8, device="cuda")
+
+    def restore():
+        for now, was in zip(state + [outs], old):
+            for a, b in zip(now, was):
+                a.copy_(b)
+
+    def call(n):
+        restore()
+        buf.fill_(0x5A)
+        kvs = [vc.live_kv(k, v, m, s, p) for (k, v, s, p), m in zip(state, ns)]
+        ws = buf[:n] if n else None
+        if kind == "evict":
+            arr = (vc.vc_evict_req * B)(*[vc.vc_evict_req(kv, m // 2, 4, m - 9) for kv, m in zip(kvs, ns)])
+            st = vc.vc_evict_kv(shape, arr, ws, raise_on_error=False)
+        else:
+            arr = (vc.vc_live_req * B)(*[vc.vc_live_req(q.data_ptr(), o.data_ptr(), q.shape[0], kv)
+                                         for q, o, kv in zip(qs, outs, kvs)])
+            st = vc.vc_scored_attn(shape, arr, ws, raise_on_error=False) if kind == "scored" else \
+                vc.vc_prefix_attn(shape, prefix, arr, ws, raise_on_error=False)
+        torch.cuda.synchronize()
+        assert bool((buf[n:] == 0x5A).all())
+        if st != vc.VC_OK:
+            assert bool((buf == 0x5A).all())
+            for now, was in zip(state + [outs], old):
+                for a, b in zip(now, was):
+                    assert np.array_equal(bits(a), bits(b))
+        return st
+
+    assert call(size) == vc.VC_OK
+    want = [[t.clone() for t in s] for s in state + [outs]]
+    least = _smallest(call, size, vc.VC_ERR_WORKSPACE)
+    assert call(least - 1) == vc.VC_ERR_WORKSPACE
+    assert call(least) == vc.VC_OK
+    for now, was in zip(state + [outs], want):
+        for a, b in zip(now, was):
+            assert np.array_equal(bits(a), bits(b))
+
+
+def test_a_batch_keeps_the_index_of_its_device(vc):
+    from lossless_compressed_kv_vc_gb300 import engine
+    lb = engine.LiveBatch(8, 2, 64, 2, 10, vc.vc_rope_init(vc.VC_ROPE_NONE, 64), device="cuda")
+    assert lb.device == torch.device("cuda", torch.cuda.current_device())
+    q, k = (torch.zeros((2, h, 1, 64), dtype=torch.bfloat16, device="cuda").transpose(1, 2) for h in (8, 2))
+    lb.step(q, k, k, torch.zeros((2, 1, 8, 64), dtype=torch.bfloat16, device="cuda"))  # single tokens, split by heads
+    torch.cuda.synchronize()
+    assert lb.n == [1, 1] and int(lb.dev_status.item()) == 0
