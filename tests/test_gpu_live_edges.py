@@ -193,3 +193,36 @@ def test_a_batch_keeps_the_index_of_its_device(vc):
     lb.step(q, k, k, torch.zeros((2, 1, 8, 64), dtype=torch.bfloat16, device="cuda"))  # single tokens, split by heads
     torch.cuda.synchronize()
     assert lb.n == [1, 1] and int(lb.dev_status.item()) == 0
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_with_a_table_filled_by_hand(vc, inter):
+    """Frequencies of the caller's own: a ramp over the pairs' index between plain and squeezed ones, and a factor on
+    every rotated channel (0.1 ln 8 + 1)."""
+    Hq, Hkv, d, rot, R, n, pos0 = 8, 2, 128, 96, 9, 4, 70001
+    freqs = O.rope_freqs("none", rot, 1e6)
+    keep = np.clip((30 - np.arange(rot // 2)) / 20, 0, 1)
+    freqs = keep * freqs + (1 - keep) * freqs / 8
+    amp = 0.1 * np.log(8) + 1
+    table = vc.vc_rope_init(vc.VC_ROPE_NONE, rot, vc.VC_ROPE_INTERLEAVED if inter else vc.VC_ROPE_HALF)
+    table.amp = amp
+    for j, f in enumerate(freqs):
+        table.freq[j] = f
+    g = gen(53)
+    k, v, score, pos = cache(g, Hkv, d, n, n + R)
+    q, kn, vn = randn(g, R, Hq, d), randn(g, R, Hkv, d), randn(g, R, Hkv, d)
+    out = torch.empty_like(q)
+    e = vc.vc_rope_req(q=q.data_ptr(), k=kn.data_ptr(), v=vn.data_ptr(), pos0=pos0, n_rows=R, q_out=out.data_ptr(),
+                       kv=vc.live_kv(k, v, n, score, pos))
+    vc.vc_rope_append(vc.vc_shape(1, Hq, Hkv, d), table, (vc.vc_rope_req * 1)(e))
+    torch.cuda.synchronize()
+    at = pos0 + np.arange(R)
+    for got, x in ((out, q), (k[:, n:].transpose(0, 1), kn)):
+        ref, mag = O.rope(f64(x), at, freqs, inter, amp), np.abs(f64(x))
+        a, b = (slice(0, rot, 2), slice(1, rot, 2)) if inter else (slice(0, rot // 2), slice(rot // 2, rot))
+        lim = 2.0 ** -8 * np.abs(ref)  # as at the top of test_gpu_live.py
+        both = 2.0 ** -20 * amp * (mag[..., a] + mag[..., b])
+        lim[..., a] += both
+        lim[..., b] += both
+        lim[..., rot:] = 0
+        assert np.all(np.abs(f64(got) - ref) <= lim)
