@@ -484,8 +484,9 @@ vc_status vc_rope_append(const vc_shape* shape, const vc_rope* rope, const vc_ro
  * t <= n - n_rows + i of its own cache: its n_rows tokens are the cache's last rows (appended by
  * vc_rope_append, n moved), and row i sees those up to its own. n_rows = 1 is a decode step; more
  * are drafts to verify or a prompt chunk. Scale 1/sqrt(d), GQA as in the other calls. A row that
- * sees no key gets zeros. K or V rows that a query row may not see do not reach it, whatever they
- * hold. Requests with n_rows == 0 are skipped; an own cache may be empty (n == 0).
+ * sees no key, or whose products with all the keys it sees are -infinity, gets zeros. K or V rows that
+ * a query row may not see do not reach it, whatever they hold. Requests with n_rows == 0 are skipped; an
+ * own cache may be empty (n == 0).
  * prefix: ctx >= 0 rows (ctx == 0 or a NULL prefix: none); own caches' score and pos are not read.
  * bf16 products accumulated in fp32 on the tensor cores, softmax in fp32, weights rounded to bf16 for
  * the product with V, output rounded to bf16.
@@ -508,8 +509,9 @@ size_t vc_prefix_workspace_size(const vc_shape* shape, int32_t max_rows);
 /* vc_scored_attn — the same attention over the own caches alone, which also adds to score[h][t] the
  * softmax weight that cached row t got from this call's rows: the sum over the request's n_rows rows
  * and the Hq/Hkv query heads of KV head h, in fp32 from fp32 scores (fixed order: the same call gives
- * the same bits). n_rows * Hq/Hkv <= VC_SCORED_MAX_ROWS (VC_ERR_UNSUPPORTED beyond: split a longer
- * chunk over calls, each after its own vc_rope_append); every kv needs score.
+ * the same bits). A row whose softmax is NaN makes the scores of the keys that it sees NaN, and no others.
+ * n_rows * Hq/Hkv <= VC_SCORED_MAX_ROWS (VC_ERR_UNSUPPORTED beyond: split a longer chunk over calls, each
+ * after its own vc_rope_append); every kv needs score.
  * ws: vc_scored_workspace_size(shape, max_rows, max_n) bytes for calls of up to max_rows rows a
  * request over caches of up to max_n rows; no initialisation; errors, overlapping calls and dev_status as
  * above. */

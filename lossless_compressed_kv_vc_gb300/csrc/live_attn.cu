@@ -24,8 +24,9 @@
 //
 // What bounds it. One token a request: K and V from DRAM (8 caches of 8200 rows, 8 heads of 128: 49 us with the
 // merge, 236 MB, 0.71 of the copy rate; 4 of 131072: 385 us, 0.83), the rest start-up and, where scores are
-// kept, the second kernel's pass over them. Drafts over a prefix (2000 rows of a KV head, 65536 keys): 387 us,
-// 1.24 PFLOP/s, 0.66 of the bf16 peak: shared memory's bandwidth, since a pair of chains moves 320 KB a tile (Q
+// kept, the second kernel's pass over them. Drafts over a prefix (2000 rows of a KV head, 65536 keys): 394 us back
+// to back on two sets of inputs, 414 to 418 with others in each call, 1.15 to 1.22 PFLOP/s, 0.61 to 0.64 of the bf16
+// peak: shared memory's bandwidth, since a pair of chains moves 320 KB a tile (Q
 // twice 64, as S steps of 64 keys read it twice, K and V twice 32 each, and 64 in from L2), 2560 clocks at 128
 // bytes each of about 3000; leaving out all exponentials changes nothing. Many short caches (a few tiles a
 // piece): the pieces' fixed part, about 6 us each, of which instruction fetch is the largest.
@@ -572,10 +573,14 @@ __global__ void __launch_bounds__(LTHREADS, 1) live_attn_kernel(const __grid_con
               for (int e = 0; e < LS / 4; ++e, d += s_rows) *d = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
             }
           }
-          // P = 2^(x scale - m), bf16, over S, with the running maximum as it is: the row's new one is found
-          // alongside, and only when it is larger by more than 2^8 (or this is the piece's first step) is m
-          // moved, O rescaled after the P V before, and P computed again. TMEM loads and stores are
-          // warp-collective: the warp does it together.
+          // P = 2^(x scale - m), bf16, over S: the MMA wants both operands in one 16-bit type, and V is bf16 (its range
+          // is not fp16's). A weight is off by 2^-8 of itself at most; with the output's own rounding the outputs are
+          // 0.0020 to 0.0023 from 64 bits (relative L2), where fp32 weights leave 0.0017. A second product with what
+          // P lacks would double P V's share of the tensor cores and of shared memory. Sums and lse take the weights
+          // unrounded.
+          // The running maximum is taken as it is: the row's new one is found alongside, and only when it is larger by
+          // more than 2^8 (or this is the piece's first step) is m moved, O rescaled after the P V before, and P
+          // computed again. TMEM loads and stores are warp-collective: the warp does it together.
           uint32_t r[LS / 2];
           float u0, u1, mx = -INFINITY, my = -INFINITY, mz = -INFINITY, mw = -INFINITY;
 #pragma unroll 1
@@ -937,8 +942,8 @@ __global__ void __launch_bounds__(256, SCORED ? 3 : 4) live_finish_kernel(const 
 }
 
 // The merge for many rows of few partials: LIVE_SUB lanes a row, four rows a warp side by side. A row's time is
-// that of its dependent loads, whatever its partials (62496 rows of 2 to 4: the call 105 us with a warp a row, 68
-// so; 16000 of about 6: 396, 387).
+// that of its dependent loads, whatever its partials (62496 rows of 2 to 4: the call 107 us with a warp a row, 71
+// so; 16384 over 8192 + 500 keys: 132, 123; 16000 of about 6: 405, 394).
 constexpr int LIVE_SUB = 8;
 template <int D>
 __global__ void __launch_bounds__(256, 4) live_merge_kernel(const __grid_constant__ LiveParams p) {
