@@ -17,7 +17,10 @@
  * staging (vc_stage_full_kv) and the post-accept cache update (vc_append_kv); and, for caches that
  * grow, are shared and shrink while requests decode, rotary append (vc_rope_append), attention over
  * a shared prefix (vc_prefix_attn), attention that gathers each row's weight (vc_scored_attn) and
- * eviction by it (vc_evict_kv). Every compute step runs in this library's CUDA kernels.
+ * eviction by it (vc_evict_kv); and, for drafted trees over a cache of pages, the pages themselves
+ * (vc_pages_init, _reserve, _fork, _trim, _compact), rotary append with several axes (vc_rope_pages),
+ * attention of trees (vc_tree_mask, vc_tree_attn) and their acceptance (vc_tree_accept,
+ * vc_tree_commit). Every compute step runs in this library's CUDA kernels.
  *
  * Conventions for every call
  *   - The caller owns every buffer. The library never allocates device or host memory and never
@@ -75,6 +78,7 @@ typedef enum vc_status {
 #define VC_DEV_TIMEOUT 2       /* a bounded wait on a copy gave up; outputs of that block are invalid */
 #define VC_DEV_RANGE 3         /* a quantisation scale or zero is not finite in fp16 */
 #define VC_DEV_INTERNAL 4      /* a kernel precondition failed (shared-memory alignment); outputs invalid */
+#define VC_DEV_PAGES 5         /* a sequence lacks pages, or its pages' state is broken; what needed them was skipped */
 
 typedef enum vc_mode { VC_TOKEN_DROP = 0, VC_QUANT = 1 } vc_mode;
 typedef enum vc_call { VC_CALL_DRAFT = 0, VC_CALL_VERIFY = 1 } vc_call;
@@ -544,6 +548,200 @@ typedef struct vc_evict_req {
 vc_status vc_evict_kv(const vc_shape* shape, const vc_evict_req* req, void* ws, size_t ws_bytes,
                       int32_t* dev_status, cudaStream_t stream);
 size_t vc_evict_workspace_size(const vc_shape* shape, int32_t max_n);
+
+/* ------------------------------------------------------------------------------------------ */
+/* Drafted trees over a cache of pages.
+ *
+ * A pool of pages holds the caches of many sequences. All that moves while they decode lies in device
+ * memory, so that a whole turn can be replayed as one CUDA graph: the calls below read lengths, tables
+ * and accepted paths on the device and move them on there.
+ *
+ * A sequence holds the pages table[seq][0 .. held[seq]-1]; its row t is row t % page of page
+ * table[seq][t / page]. Rows 0 .. len[seq]-1 are its context. The rows of a turn's tokens lie behind
+ * them until vc_tree_commit: vc_rope_pages writes them, vc_tree_attn attends over them, vc_tree_commit
+ * makes those of the accepted path context and moves len. next[seq] is the next token's position (it
+ * differs from len where image tokens share positions). A page may belong to several sequences
+ * (vc_pages_fork); refs counts them. Rows are only written into a page that one sequence holds:
+ * vc_pages_reserve, before a turn, sees to it.
+ *
+ * free_pages[0 .. n_free-1] is a stack: free_pages[n_free-1] is taken next. Its other words and the
+ * table's behind held are left as they are. vc_pages_init, or the caller, lays the state down.
+ *
+ * Requests of one call name different sequences (VC_ERR_INVALID otherwise), but for vc_tree_attn and a
+ * fork's sources, which are only read. Calls on one pool are ordered by their stream or by events.
+ * State that does not add up (a table entry outside the pool, a length beyond the pages held, rows to
+ * be written where the sequence has no page or shares it) is never followed out of bounds: the rows
+ * or pages it touches are skipped and dev_status receives VC_DEV_PAGES.
+ * Limits: page is 16, 32, 64 or 128; (n_pages + 1) * Hkv < 2^31 and max_pages * page <= 2^30
+ * (VC_ERR_UNSUPPORTED). k and v 16-byte aligned, the others 4-byte. The device current to the calling
+ * thread is the one that holds the buffers. */
+typedef struct vc_paged_kv {
+  void* k;              /* bf16 [n_pages][Hkv][page][d] */
+  void* v;
+  int32_t* refs;        /* int32 [n_pages]: sequences that hold the page, 0: free */
+  int32_t* free_pages;  /* int32 [n_pages]: stack of the free ones */
+  int32_t* n_free;      /* int32 [1] */
+  int32_t* table;       /* int32 [n_seq][max_pages] */
+  int32_t* len;         /* int32 [n_seq]: rows of context */
+  int32_t* held;        /* int32 [n_seq]: pages held, at least the context's */
+  int32_t* next;        /* int32 [n_seq]: position of the next token */
+  int32_t n_pages;
+  int32_t page;         /* rows of a page */
+  int32_t n_seq;
+  int32_t max_pages;    /* pages a sequence can hold */
+} vc_paged_kv;
+
+/* vc_pages_init — all pages free, page 0 taken first, all sequences empty (len, held and next 0). Of
+ * the shape Hkv and d are read (and checked), B and Hq only checked, as in every call of pages. */
+vc_status vc_pages_init(const vc_shape* shape, const vc_paged_kv* kv, cudaStream_t stream);
+
+/* vc_pages_reserve — room for `rows` more rows of each sequence, in pages of its own.
+ * Request by request: if rows > 0 and the page of row len holds rows of the context that another
+ * sequence holds too, the next page from the stack takes its place and those rows (K and V) are copied
+ * into it; then pages from the stack follow until held * page >= len + rows. A request that the stack
+ * or max_pages cannot serve whole is left as it was (VC_DEV_PAGES); those behind it may be served.
+ * ws: vc_pages_workspace_size bytes, no initialisation; calls that overlap must not share one. */
+typedef struct vc_reserve_req {
+  int32_t seq;
+  int32_t rows;    /* >= 0 */
+} vc_reserve_req;
+vc_status vc_pages_reserve(const vc_shape* shape, const vc_paged_kv* kv, const vc_reserve_req* req, void* ws,
+                           size_t ws_bytes, int32_t* dev_status, cudaStream_t stream);
+
+/* vc_pages_fork — sequence dst, which holds no pages (VC_DEV_PAGES otherwise, and nothing is done for
+ * it), becomes a copy of src: the pages of src's context are held by both, len and next are src's. No
+ * row is copied: vc_pages_reserve copies a shared last page once one of them goes on. A sequence that
+ * is some request's dst is no request's src. */
+typedef struct vc_fork_req {
+  int32_t src, dst;
+} vc_fork_req;
+vc_status vc_pages_fork(const vc_shape* shape, const vc_paged_kv* kv, const vc_fork_req* req, int32_t* dev_status,
+                        cudaStream_t stream);
+
+/* vc_pages_trim — each sequence cut to its first `rows` rows (where its context is longer: len = rows and
+ * next = `next`), and the pages behind its context's given back: request by request, the last page
+ * first; a page that no sequence holds any more goes on the stack. rows = 0 frees the sequence,
+ * rows = INT32_MAX gives back what was reserved and not used. */
+typedef struct vc_trim_req {
+  int32_t seq;
+  int32_t rows;    /* >= 0 */
+  int32_t next;
+} vc_trim_req;
+vc_status vc_pages_trim(const vc_shape* shape, const vc_paged_kv* kv, const vc_trim_req* req, int32_t* dev_status,
+                        cudaStream_t stream);
+
+/* vc_pages_compact — the U pages in use moved to pages 0 .. U-1: those behind go into the free ones
+ * among them, both in ascending order, with K, V and their count; the tables of all sequences follow.
+ * The stack is laid down anew: page U is taken next, then U + 1, ... (so the pool's tail can be given
+ * back). Same workspace as vc_pages_reserve. */
+vc_status vc_pages_compact(const vc_shape* shape, const vc_paged_kv* kv, void* ws, size_t ws_bytes, int32_t* dev_status,
+                           cudaStream_t stream);
+
+size_t vc_pages_workspace_size(const vc_shape* shape, const vc_paged_kv* kv);
+
+/* ------------------------------------------------------------------------------------------ */
+/* vc_rope_axes_init — rotary positions with several axes (time, height and width of image and video
+ * tokens): each pair of a vc_rope table turns by the position on one axis. sections[a] pairs, at least
+ * none, belong to axis a; they add up to rot_dim / 2. dealt = 0: axis 0's pairs first, then axis 1's, ...;
+ * dealt = 1: pair by pair round the axes that have pairs left. n_axes is 1 .. VC_ROPE_MAX_AXES. The
+ * caller may change or fill in axis itself. Errors: VC_ERR_INVALID, VC_ERR_UNSUPPORTED. Host only. */
+#define VC_ROPE_MAX_AXES 4
+
+typedef struct vc_rope_axes {
+  vc_rope rope;
+  int32_t n_axes;
+  int32_t axis[VC_ROPE_MAX_PAIRS];  /* axis of each pair */
+} vc_rope_axes;
+
+vc_status vc_rope_axes_init(const vc_rope* rope, int32_t n_axes, const int32_t* sections, int32_t dealt,
+                            vc_rope_axes* out);
+
+/* vc_rope_pages — vc_rope_append for sequences in pages: q and k rotated, k and v written to rows
+ * len .. len+n_rows-1 of each sequence (reserved before; len is left as it is). Token t's position on
+ * axis a is next + off[a * off_stride + t], taken in 64 bits; off_stride 0: the same on every axis;
+ * off NULL: next + t. q, k, v, their strides, q_out and the rotation's accuracy as in vc_rope_append.
+ * Requests with n_rows == 0 are skipped. Tokens whose page the sequence does not hold alone are not
+ * written (VC_DEV_PAGES); their q_out is. Errors as vc_rope_append's. */
+typedef struct vc_rope_page_req {
+  const void* q;       /* bf16, token t's [Hq][d] at q + t * q_stride; NULL (with q_out): keys alone */
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t* off;  /* device int32 [n_axes][off_stride] or [n_rows], or NULL */
+  int64_t off_stride;  /* 0, or >= n_rows */
+  void* q_out;         /* bf16 [n_rows][Hq][d] */
+  int32_t seq;
+  int32_t n_rows;
+} vc_rope_page_req;
+
+vc_status vc_rope_pages(const vc_shape* shape, const vc_rope_axes* axes, const vc_paged_kv* kv,
+                        const vc_rope_page_req* req, int32_t* dev_status, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
+/* Trees of drafts. Node 0 of a request's n_nodes is the last accepted token, whose key and value the
+ * turn itself makes; node i's parent is parent[i], in 0 .. i-1 (anything else: node i is a root of its
+ * own, and is accepted by nothing). Arrays are [B][N_max], a request's first n_nodes entries are read
+ * (n_nodes is held to 0 .. N_max on the device). 1 <= N_max <= VC_TREE_MAX_NODES, any B >= 1.
+ *
+ * vc_tree_mask — for each node the bits of the nodes it sees, itself and its ancestors: bit j % 32 of word
+ * j / 32 of mask[b][i], ceil(N_max / 32) words a node; and its depth (ancestors), which vc_rope_pages
+ * takes as off. Nodes behind n_nodes get no bits and depth 0. depth may be NULL. */
+#define VC_TREE_MAX_NODES 1024
+
+vc_status vc_tree_mask(int32_t B, int32_t N_max, const int32_t* parent, const int32_t* n_nodes, uint32_t* mask,
+                       int32_t* depth, cudaStream_t stream);
+
+/* vc_tree_attn — attention of each request's n_rows tokens, the rows len .. len+n_rows-1 of its sequence
+ * (written by vc_rope_pages, not yet committed). Query row i sees the context's rows and the tokens j
+ * with bit j of mask row i (word j / 32 at mask[i * mask_words]); mask NULL: tokens 0 .. i, so that
+ * n_rows = 1 is a decode step and more are a chain of drafts or a prompt chunk. A mask may be any: a
+ * row that sees no key gets zeros. Rows that a query row may not see do not reach it, whatever they
+ * hold, nor does what the last page holds behind them. Scale 1/sqrt(d), GQA, arithmetic and rounding as
+ * in vc_prefix_attn. Requests with n_rows == 0 are skipped; tokens whose rows lie behind the pages
+ * held are seen by none (VC_DEV_PAGES).
+ * ws: vc_tree_workspace_size(shape, max_rows) bytes for calls of up to max_rows rows a request; no
+ * initialisation; calls that overlap on the GPU must not share one.
+ * Errors before anything is launched: VC_ERR_INVALID; VC_ERR_WORKSPACE; VC_ERR_UNSUPPORTED (calls whose
+ * query rows, or tiles of rows by tiles of pages, reach 2^29). dev_status as for vc_prefix_attn. */
+typedef struct vc_tree_req {
+  const void* q;         /* bf16 [n_rows][Hq][d] */
+  void* o;               /* bf16 [n_rows][Hq][d] */
+  const uint32_t* mask;  /* device [n_rows][mask_words], or NULL */
+  int32_t mask_words;    /* >= ceil(n_rows / 32) with a mask */
+  int32_t seq;
+  int32_t n_rows;
+} vc_tree_req;
+
+vc_status vc_tree_attn(const vc_shape* shape, const vc_paged_kv* kv, const vc_tree_req* req, void* ws, size_t ws_bytes,
+                       int32_t* dev_status, cudaStream_t stream);
+size_t vc_tree_workspace_size(const vc_shape* shape, int32_t max_rows);
+
+/* vc_tree_accept — greedy acceptance along each tree ("Core algorithm", step 3, for trees). logits fp32
+ * [B][N_max][V]: row i is the full pass's prediction after node i; a_i is its argmax (the first of equal
+ * ones; NaN is below everything, a row of NaN alone gives 0). From node 0 on, the path goes to the
+ * child whose token is a_i (the lowest node of several) while there is one. Writes path[b] = the path's
+ * nodes in order, out_tokens[b] = a_i of each (the accepted drafts, and behind them the correction or
+ * bonus token), both then -1 up to N_max entries, and n_acc[b] = the path's length: 1 .. n_nodes, or 0
+ * without nodes. Outputs do not overlap inputs. */
+vc_status vc_tree_accept(int32_t B, int32_t N_max, int32_t V, const float* logits, const int32_t* token,
+                         const int32_t* parent, const int32_t* n_nodes, int32_t* out_tokens, int32_t* path,
+                         int32_t* n_acc, cudaStream_t stream);
+
+/* vc_tree_commit — the accepted path's rows become context: row len + i takes row len + path[i]'s K and V
+ * for i < m, where m = *n_acc held to 0 .. n_rows, then len += m and next += advance (advance < 0: m).
+ * path NULL: the first m rows as they lie; n_acc NULL: m = n_rows (both NULL: a prompt chunk, or a chain
+ * accepted whole). A path entry outside i .. n_rows-1 ends the path there (VC_DEV_PAGES; m = i). Pages are
+ * neither taken nor given back. Requests with n_rows == 0 are skipped. */
+typedef struct vc_commit_req {
+  const int32_t* path;   /* device int32 [n_rows], ascending, or NULL */
+  const int32_t* n_acc;  /* device int32 [1], or NULL */
+  int32_t seq;
+  int32_t n_rows;        /* rows written behind the context */
+  int32_t advance;
+} vc_commit_req;
+
+vc_status vc_tree_commit(const vc_shape* shape, const vc_paged_kv* kv, const vc_commit_req* req, int32_t* dev_status,
+                         cudaStream_t stream);
 
 /* ------------------------------------------------------------------------------------------ */
 /* vc_plan_stagger — choose the two alternating groups of cross-resource staggering ("Cross-resource

@@ -3,8 +3,9 @@
 Argument marshalling only: every step runs in the library's CUDA kernels. The names follow the
 C ABI in include/vc.h (vc_comp_bytes, vc_compress_kv, vc_draft_attn(_noalloc), vc_verify_attn(_heads), vc_accept,
 vc_append_kv, vc_stage_full_kv, vc_snapkv_importance, vc_rope_init, vc_rope_append, vc_prefix_attn,
-vc_scored_attn, vc_evict_kv, vc_plan_stagger(_local), vc_stagger_period and the workspace-size /
-status-string calls). Tensors are torch tensors on the GPU; their data pointers
+vc_scored_attn, vc_evict_kv, vc_pages_init / _reserve / _fork / _trim / _compact, vc_rope_axes_init,
+vc_rope_pages, vc_tree_mask / _attn / _accept / _commit, vc_plan_stagger(_local), vc_stagger_period and
+the workspace-size / status-string calls). Tensors are torch tensors on the GPU; their data pointers
 and the current (or given) CUDA stream are passed through.
 
 Importing this package loads libvc.so and raises ImportError when it has not been built
@@ -23,7 +24,7 @@ if not os.path.exists(LIB_PATH):
 _lib = C.CDLL(LIB_PATH)
 
 VC_OK, VC_ERR_INVALID, VC_ERR_UNSUPPORTED, VC_ERR_CUDA, VC_ERR_NOT_PINNED, VC_ERR_WORKSPACE = range(6)
-VC_DEV_OK, VC_DEV_BOUNDS, VC_DEV_TIMEOUT, VC_DEV_RANGE, VC_DEV_INTERNAL = range(5)
+VC_DEV_OK, VC_DEV_BOUNDS, VC_DEV_TIMEOUT, VC_DEV_RANGE, VC_DEV_INTERNAL, VC_DEV_PAGES = range(6)
 VC_TOKEN_DROP, VC_QUANT = 0, 1
 VC_CALL_DRAFT, VC_CALL_VERIFY = 0, 1
 VC_MAX_BATCH = 32
@@ -38,6 +39,8 @@ VC_ROPE_MAX_PAIRS = 64
 VC_ROPE_NONE, VC_ROPE_LINEAR, VC_ROPE_NTK, VC_ROPE_BANDS = range(4)
 VC_ROPE_HALF, VC_ROPE_INTERLEAVED = 0, 1
 VC_SCORED_MAX_ROWS = 256
+VC_ROPE_MAX_AXES = 4
+VC_TREE_MAX_NODES = 1024
 
 _p = C.c_void_p
 _i32 = C.c_int32
@@ -112,6 +115,41 @@ class vc_evict_req(C.Structure):
     _fields_ = [("kv", vc_live_kv), ("keep", _i32), ("sink", _i32), ("recent_from", _i32)]
 
 
+class vc_paged_kv(C.Structure):
+    _fields_ = [("k", _p), ("v", _p), ("refs", _p), ("free_pages", _p), ("n_free", _p), ("table", _p), ("len", _p),
+                ("held", _p), ("next", _p), ("n_pages", _i32), ("page", _i32), ("n_seq", _i32), ("max_pages", _i32)]
+
+
+class vc_reserve_req(C.Structure):
+    _fields_ = [("seq", _i32), ("rows", _i32)]
+
+
+class vc_fork_req(C.Structure):
+    _fields_ = [("src", _i32), ("dst", _i32)]
+
+
+class vc_trim_req(C.Structure):
+    _fields_ = [("seq", _i32), ("rows", _i32), ("next", _i32)]
+
+
+class vc_rope_axes(C.Structure):
+    _fields_ = [("rope", vc_rope), ("n_axes", _i32), ("axis", _i32 * VC_ROPE_MAX_PAIRS)]
+
+
+class vc_rope_page_req(C.Structure):
+    _fields_ = [("q", _p), ("k", _p), ("v", _p), ("q_stride", C.c_int64), ("k_stride", C.c_int64),
+                ("v_stride", C.c_int64), ("off", _p), ("off_stride", C.c_int64), ("q_out", _p), ("seq", _i32),
+                ("n_rows", _i32)]
+
+
+class vc_tree_req(C.Structure):
+    _fields_ = [("q", _p), ("o", _p), ("mask", _p), ("mask_words", _i32), ("seq", _i32), ("n_rows", _i32)]
+
+
+class vc_commit_req(C.Structure):
+    _fields_ = [("path", _p), ("n_acc", _p), ("seq", _i32), ("n_rows", _i32), ("advance", _i32)]
+
+
 _lib.vc_compress_kv.argtypes = [C.POINTER(vc_shape), C.POINTER(vc_kv_full), C.POINTER(_p), C.POINTER(_i32),
                                 _i32, C.POINTER(vc_kv_comp), _p, _p]
 _lib.vc_draft_attn.argtypes = [C.POINTER(vc_shape), C.POINTER(vc_draft_req), _p, C.c_size_t, _p, _p]
@@ -145,6 +183,23 @@ _lib.vc_scored_workspace_size.restype = C.c_size_t
 _lib.vc_evict_kv.argtypes = [C.POINTER(vc_shape), C.POINTER(vc_evict_req), _p, C.c_size_t, _p, _p]
 _lib.vc_evict_workspace_size.argtypes = [C.POINTER(vc_shape), _i32]
 _lib.vc_evict_workspace_size.restype = C.c_size_t
+_lib.vc_pages_init.argtypes = [C.POINTER(vc_shape), C.POINTER(vc_paged_kv), _p]
+_lib.vc_pages_reserve.argtypes = [C.POINTER(vc_shape), C.POINTER(vc_paged_kv), C.POINTER(vc_reserve_req), _p, C.c_size_t,
+                                  _p, _p]
+_lib.vc_pages_fork.argtypes = [C.POINTER(vc_shape), C.POINTER(vc_paged_kv), C.POINTER(vc_fork_req), _p, _p]
+_lib.vc_pages_trim.argtypes = [C.POINTER(vc_shape), C.POINTER(vc_paged_kv), C.POINTER(vc_trim_req), _p, _p]
+_lib.vc_pages_compact.argtypes = [C.POINTER(vc_shape), C.POINTER(vc_paged_kv), _p, C.c_size_t, _p, _p]
+_lib.vc_pages_workspace_size.argtypes = [C.POINTER(vc_shape), C.POINTER(vc_paged_kv)]
+_lib.vc_pages_workspace_size.restype = C.c_size_t
+_lib.vc_rope_axes_init.argtypes = [C.POINTER(vc_rope), _i32, C.POINTER(_i32), _i32, C.POINTER(vc_rope_axes)]
+_lib.vc_rope_pages.argtypes = [C.POINTER(vc_shape), C.POINTER(vc_rope_axes), C.POINTER(vc_paged_kv),
+                               C.POINTER(vc_rope_page_req), _p, _p]
+_lib.vc_tree_mask.argtypes = [_i32, _i32, _p, _p, _p, _p, _p]
+_lib.vc_tree_attn.argtypes = [C.POINTER(vc_shape), C.POINTER(vc_paged_kv), C.POINTER(vc_tree_req), _p, C.c_size_t, _p, _p]
+_lib.vc_tree_workspace_size.argtypes = [C.POINTER(vc_shape), _i32]
+_lib.vc_tree_workspace_size.restype = C.c_size_t
+_lib.vc_tree_accept.argtypes = [_i32, _i32, _i32, _p, _p, _p, _p, _p, _p, _p, _p]
+_lib.vc_tree_commit.argtypes = [C.POINTER(vc_shape), C.POINTER(vc_paged_kv), C.POINTER(vc_commit_req), _p, _p]
 _lib.vc_workspace_size.argtypes = [_i32, C.POINTER(vc_shape), _i32]
 _lib.vc_workspace_size.restype = C.c_size_t
 _lib.vc_status_string.argtypes = [_i32]
@@ -153,14 +208,19 @@ _lib.vc_version.restype = _i32
 for _f in ("vc_compress_kv", "vc_draft_attn", "vc_draft_attn_noalloc", "vc_verify_attn", "vc_verify_attn_heads",
            "vc_accept", "vc_stage_full_kv", "vc_append_kv", "vc_plan_stagger", "vc_stagger_period",
            "vc_plan_stagger_local", "vc_snapkv_importance", "vc_comp_bytes", "vc_rope_init", "vc_rope_append",
-           "vc_prefix_attn", "vc_scored_attn", "vc_evict_kv"):
+           "vc_prefix_attn", "vc_scored_attn", "vc_evict_kv", "vc_pages_init", "vc_pages_reserve", "vc_pages_fork",
+           "vc_pages_trim", "vc_pages_compact", "vc_rope_axes_init", "vc_rope_pages", "vc_tree_mask", "vc_tree_attn",
+           "vc_tree_accept", "vc_tree_commit"):
     getattr(_lib, _f).restype = _i32
 
 EXPORTS = ["vc_compress_kv", "vc_draft_attn", "vc_draft_attn_noalloc", "vc_verify_attn", "vc_verify_attn_heads",
            "vc_accept", "vc_stage_full_kv", "vc_append_kv", "vc_plan_stagger", "vc_stagger_period",
            "vc_plan_stagger_local", "vc_snapkv_importance", "vc_importance_workspace_size", "vc_workspace_size", "vc_status_string",
            "vc_version", "vc_comp_bytes", "vc_rope_init", "vc_rope_append", "vc_prefix_attn", "vc_prefix_workspace_size",
-           "vc_scored_attn", "vc_scored_workspace_size", "vc_evict_kv", "vc_evict_workspace_size"]
+           "vc_scored_attn", "vc_scored_workspace_size", "vc_evict_kv", "vc_evict_workspace_size",
+           "vc_pages_init", "vc_pages_reserve", "vc_pages_fork", "vc_pages_trim", "vc_pages_compact",
+           "vc_pages_workspace_size", "vc_rope_axes_init", "vc_rope_pages", "vc_tree_mask", "vc_tree_attn",
+           "vc_tree_workspace_size", "vc_tree_accept", "vc_tree_commit"]
 
 
 class VCError(RuntimeError):
@@ -358,6 +418,98 @@ def vc_evict_kv(shape: vc_shape, req, ws=None, dev_status=None, stream=None, rai
     wsb = ws.numel() * ws.element_size() if ws is not None else 0
     st = _lib.vc_evict_kv(C.byref(shape), req, _ptr(ws), wsb, _ptr(dev_status), _stream(stream))
     return _check(st, "vc_evict_kv", raise_on_error)
+
+
+def paged_kv(k, v, refs, free_pages, n_free, table, len, held, next) -> vc_paged_kv:
+    """Descriptor of a pool: k, v bf16 [n_pages][Hkv][page][d]; int32 refs, free_pages [n_pages], n_free [1], table
+    [n_seq][max_pages], len, held, next [n_seq], all contiguous."""
+    n_pages, n_seq = k.shape[0], table.shape[0]
+    for t, n in ((k, v.numel()), (v, k.numel()), (refs, n_pages), (free_pages, n_pages), (n_free, 1), (table, 0), (len, n_seq),
+                 (held, n_seq), (next, n_seq)):
+        if not t.is_contiguous() or t.numel() < n:
+            raise ValueError("a pool's tensors are contiguous, with an entry for each page and sequence")
+    return vc_paged_kv(*(t.data_ptr() for t in (k, v, refs, free_pages, n_free, table, len, held, next)), n_pages,
+                       k.shape[2], n_seq, table.shape[1])
+
+
+def vc_pages_init(shape: vc_shape, kv: vc_paged_kv, stream=None, raise_on_error=True) -> int:
+    return _check(_lib.vc_pages_init(C.byref(shape), C.byref(kv), _stream(stream)), "vc_pages_init", raise_on_error)
+
+
+def vc_pages_workspace_size(shape: vc_shape, kv: vc_paged_kv) -> int:
+    return _lib.vc_pages_workspace_size(C.byref(shape), C.byref(kv))
+
+
+def vc_pages_reserve(shape: vc_shape, kv: vc_paged_kv, req, ws=None, dev_status=None, stream=None,
+                     raise_on_error=True) -> int:
+    """req: vc_reserve_req array [B]."""
+    wsb = ws.numel() * ws.element_size() if ws is not None else 0
+    st = _lib.vc_pages_reserve(C.byref(shape), C.byref(kv), req, _ptr(ws), wsb, _ptr(dev_status), _stream(stream))
+    return _check(st, "vc_pages_reserve", raise_on_error)
+
+
+def vc_pages_fork(shape: vc_shape, kv: vc_paged_kv, req, dev_status=None, stream=None, raise_on_error=True) -> int:
+    """req: vc_fork_req array [B]."""
+    st = _lib.vc_pages_fork(C.byref(shape), C.byref(kv), req, _ptr(dev_status), _stream(stream))
+    return _check(st, "vc_pages_fork", raise_on_error)
+
+
+def vc_pages_trim(shape: vc_shape, kv: vc_paged_kv, req, dev_status=None, stream=None, raise_on_error=True) -> int:
+    """req: vc_trim_req array [B]."""
+    st = _lib.vc_pages_trim(C.byref(shape), C.byref(kv), req, _ptr(dev_status), _stream(stream))
+    return _check(st, "vc_pages_trim", raise_on_error)
+
+
+def vc_pages_compact(shape: vc_shape, kv: vc_paged_kv, ws=None, dev_status=None, stream=None, raise_on_error=True) -> int:
+    wsb = ws.numel() * ws.element_size() if ws is not None else 0
+    st = _lib.vc_pages_compact(C.byref(shape), C.byref(kv), _ptr(ws), wsb, _ptr(dev_status), _stream(stream))
+    return _check(st, "vc_pages_compact", raise_on_error)
+
+
+def vc_rope_axes_init(rope: vc_rope, sections, dealt: bool = False) -> vc_rope_axes:
+    """The rotary table of vc_rope_pages: sections[a] pairs turn by axis a. Raises VCError on bad arguments."""
+    out = vc_rope_axes()
+    n = len(sections)
+    _check(_lib.vc_rope_axes_init(C.byref(rope), n, (_i32 * max(n, 1))(*sections), int(dealt), C.byref(out)),
+           "vc_rope_axes_init", True)
+    return out
+
+
+def vc_rope_pages(shape: vc_shape, axes: vc_rope_axes, kv: vc_paged_kv, req, dev_status=None, stream=None,
+                  raise_on_error=True) -> int:
+    """req: vc_rope_page_req array [B]; the sequences' len stay as they are."""
+    st = _lib.vc_rope_pages(C.byref(shape), C.byref(axes) if axes is not None else None, C.byref(kv), req, _ptr(dev_status),
+                            _stream(stream))
+    return _check(st, "vc_rope_pages", raise_on_error)
+
+
+def vc_tree_mask(B: int, N_max: int, parent, n_nodes, mask, depth=None, stream=None, raise_on_error=True) -> int:
+    st = _lib.vc_tree_mask(B, N_max, _ptr(parent), _ptr(n_nodes), _ptr(mask), _ptr(depth), _stream(stream))
+    return _check(st, "vc_tree_mask", raise_on_error)
+
+
+def vc_tree_workspace_size(shape: vc_shape, max_rows: int) -> int:
+    return _lib.vc_tree_workspace_size(C.byref(shape), max_rows)
+
+
+def vc_tree_attn(shape: vc_shape, kv: vc_paged_kv, req, ws=None, dev_status=None, stream=None, raise_on_error=True) -> int:
+    """req: vc_tree_req array [B]."""
+    wsb = ws.numel() * ws.element_size() if ws is not None else 0
+    st = _lib.vc_tree_attn(C.byref(shape), C.byref(kv), req, _ptr(ws), wsb, _ptr(dev_status), _stream(stream))
+    return _check(st, "vc_tree_attn", raise_on_error)
+
+
+def vc_tree_accept(B: int, N_max: int, V: int, logits, token, parent, n_nodes, out_tokens, path, n_acc, stream=None,
+                   raise_on_error=True) -> int:
+    st = _lib.vc_tree_accept(B, N_max, V, _ptr(logits), _ptr(token), _ptr(parent), _ptr(n_nodes), _ptr(out_tokens),
+                             _ptr(path), _ptr(n_acc), _stream(stream))
+    return _check(st, "vc_tree_accept", raise_on_error)
+
+
+def vc_tree_commit(shape: vc_shape, kv: vc_paged_kv, req, dev_status=None, stream=None, raise_on_error=True) -> int:
+    """req: vc_commit_req array [B]."""
+    st = _lib.vc_tree_commit(C.byref(shape), C.byref(kv), req, _ptr(dev_status), _stream(stream))
+    return _check(st, "vc_tree_commit", raise_on_error)
 
 
 def _costs(costs):

@@ -6,6 +6,8 @@
 // loads and writes it into the request's output slot; then one warp per request finds the first
 // mismatch with a ballot, pads the output with -1 and writes the accepted count. Slots i <= n
 // already hold the right token: a_i == draft_i for i < n, and a_n is the correction or the bonus.
+//
+// Trees of drafts: ancestor masks and depths, and acceptance along the tree, further down.
 #include "vc_internal.cuh"
 
 #include <limits.h>
@@ -25,15 +27,8 @@ __device__ __forceinline__ int clamp_L(int Lb, int L_max) { return Lb < 0 ? 0 : 
 
 constexpr int kAcceptThreads = 512;
 
-__global__ void __launch_bounds__(kAcceptThreads) accept_argmax_kernel(AcceptArgs a) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int row = blockIdx.x;
-  const int rows = a.L_max + 1;
-  const int b = row / rows, i = row % rows;
-  if (i > clamp_L(__ldg(a.L + b), a.L_max)) return;
-  const float* x = a.logits + (size_t)row * a.V;
-  const int V = a.V;
+// The first maximal index of x[0 .. V-1], known to thread 0 of the block (INT_MAX where all are NaN).
+__device__ __forceinline__ int row_argmax(const float* x, int V) {
   float bv = -INFINITY;
   int bi = INT_MAX;
   // scalar head up to 16-byte alignment, vector body, scalar tail
@@ -91,8 +86,19 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_argmax_kernel(AcceptArg
       const int oi = __shfl_xor_sync(0xffffffffu, bi, off);
       better(bv, bi, ov, oi);
     }
-    if (lane == 0) a.out_tokens[(size_t)b * rows + i] = bi;
   }
+  return bi;
+}
+
+__global__ void __launch_bounds__(kAcceptThreads) accept_argmax_kernel(AcceptArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int row = blockIdx.x;
+  const int rows = a.L_max + 1;
+  const int b = row / rows, i = row % rows;
+  if (i > clamp_L(__ldg(a.L + b), a.L_max)) return;
+  const int bi = row_argmax(a.logits + (size_t)row * a.V, a.V);
+  if (threadIdx.x == 0) a.out_tokens[(size_t)b * rows + i] = bi;
 }
 
 __global__ void accept_finalize_kernel(AcceptArgs a) {
@@ -125,6 +131,90 @@ cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t s) {
   cudaError_t e = launch_pdl(accept_argmax_kernel, dim3(a.B * (a.L_max + 1)), dim3(kAcceptThreads), 0, s, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(accept_finalize_kernel, dim3((a.B + 3) / 4), dim3(128), 0, s, a);
+}
+
+// ---- trees of drafts -----------------------------------------------------------------------------------
+// Masks: a thread per node walks to the root in shared memory; ancestors come in descending order, so each
+// word of the node's bits is written once, full. Bound by the walk, about 30 clocks an ancestor.
+__global__ void __launch_bounds__(256) tree_mask_kernel(TreeMaskArgs a) {
+  __shared__ int16_t up[VC_TREE_MAX_NODES];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int b = blockIdx.x, N = a.N_max, words = (N + 31) / 32;
+  const int n = min(max(a.n_nodes[b], 0), N);
+  const int32_t* parent = a.parent + (size_t)b * N;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int p = parent[i];
+    up[i] = (int16_t)(p >= 0 && p < i ? p : -1);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < N; i += blockDim.x) {
+    uint32_t* row = a.mask + ((size_t)b * N + i) * words;
+    int w = words - 1, depth = -1;
+    uint32_t bits = 0;
+    for (int j = i < n ? i : -1; j >= 0; j = up[j], ++depth) {
+      for (; w > (j >> 5); --w, bits = 0) row[w] = bits;
+      bits |= 1u << (j & 31);
+    }
+    for (; w >= 0; --w, bits = 0) row[w] = bits;
+    if (a.depth) a.depth[(size_t)b * N + i] = max(depth, 0);
+  }
+}
+
+// Acceptance: the argmax of each node's row, then a block per request: every node that carries its parent's
+// token offers itself as its parent's next one (the lowest wins), and one thread follows them from node 0.
+__global__ void __launch_bounds__(kAcceptThreads) tree_argmax_kernel(TreeAcceptArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int row = blockIdx.x, b = row / a.N_max;
+  if (row - b * a.N_max >= min(__ldg(a.n_nodes + b), a.N_max)) return;
+  const int bi = row_argmax(a.logits + (size_t)row * a.V, a.V);
+  if (threadIdx.x == 0) a.out_tokens[row] = bi == INT_MAX ? 0 : bi;
+}
+
+__global__ void __launch_bounds__(256) tree_walk_kernel(TreeAcceptArgs a) {
+  __shared__ int32_t pick[VC_TREE_MAX_NODES], next[VC_TREE_MAX_NODES];
+  __shared__ int16_t path[VC_TREE_MAX_NODES];
+  __shared__ int s_len;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int b = blockIdx.x, N = a.N_max;
+  const int n = min(max(a.n_nodes[b], 0), N);
+  const size_t at = (size_t)b * N;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    pick[i] = a.out_tokens[at + i];
+    next[i] = INT_MAX;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int p = a.parent[at + i];
+    if (p >= 0 && p < i && a.token[at + i] == pick[p]) atomicMin(&next[p], i);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int len = 0;
+    for (int cur = n > 0 ? 0 : INT_MAX; cur < n; cur = next[cur]) path[len++] = (int16_t)cur;
+    s_len = len;
+    a.n_acc[b] = len;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < N; i += blockDim.x) {
+    const int node = i < s_len ? path[i] : -1;
+    a.path[at + i] = node;
+    a.out_tokens[at + i] = node >= 0 ? pick[node] : -1;
+  }
+}
+
+cudaError_t launch_tree_mask(const TreeMaskArgs& a, cudaStream_t s) {
+  const int threads = a.N_max >= 256 ? 256 : (a.N_max + 31) / 32 * 32;
+  return launch_pdl(tree_mask_kernel, dim3(a.B), dim3(threads), 0, s, a);
+}
+
+cudaError_t launch_tree_accept(const TreeAcceptArgs& a, cudaStream_t s) {
+  cudaError_t e = launch_pdl(tree_argmax_kernel, dim3(a.B * a.N_max), dim3(kAcceptThreads), 0, s, a);
+  if (e != cudaSuccess) return e;
+  const int threads = a.N_max >= 256 ? 256 : (a.N_max + 31) / 32 * 32;
+  return launch_pdl(tree_walk_kernel, dim3(a.B), dim3(threads), 0, s, a);
 }
 
 }  // namespace vc

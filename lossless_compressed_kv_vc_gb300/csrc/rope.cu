@@ -28,8 +28,10 @@ struct RopeItem {
   int pair, cs;
 };
 
-template <int D>
-__device__ __forceinline__ RopeItem rope_item(const RopeParams& p, const RopeReqDev& r, int t, int i, int per) {
+// Item i of token t; the token's cache rows: head 0's at kt and vt, a head's `head` elements on. P and R: the
+// parameters and request of either kind of cache.
+template <int D, typename P, typename R>
+__device__ __forceinline__ RopeItem rope_item(const P& p, const R& r, bf16* kt, bf16* vt, int64_t head, int t, int i, int per) {
   const int nq = r.q ? p.Hq * per : 0, nk = p.Hkv * per;
   RopeItem e;
   int c;
@@ -42,12 +44,12 @@ __device__ __forceinline__ RopeItem rope_item(const RopeParams& p, const RopeReq
     const int h = (i - nq) / per;
     c = i - nq - h * per;
     e.src = reinterpret_cast<const uint4*>(r.k + t * r.k_stride + (int64_t)h * D);
-    e.dst = reinterpret_cast<uint4*>(r.kc + (h * r.cap + t) * D);
+    e.dst = reinterpret_cast<uint4*>(kt + h * head);
   } else {
     const int h = (i - nq - nk) / (D / 8);
     c = (i - nq - nk) % (D / 8);
     e.src = reinterpret_cast<const uint4*>(r.v + t * r.v_stride + (int64_t)h * D) + c;
-    e.dst = reinterpret_cast<uint4*>(r.vc + (h * r.cap + t) * D) + c;
+    e.dst = reinterpret_cast<uint4*>(vt + h * head) + c;
     e.pair = 0;
     e.cs = -1;
     return e;
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_cons
   RopeItem e{nullptr, nullptr, 0, -1};
   uint4 x, y;
   auto load = [&](int i) {
-    e = rope_item<D>(p, r, t, i, per);
+    e = rope_item<D>(p, r, r.kc + (int64_t)t * D, r.vc + (int64_t)t * D, r.cap * D, t, i, per);
     x = e.src[0];
     if (e.pair) y = e.src[e.pair];
   };
@@ -125,6 +127,73 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_cons
     e.dst[0] = x;
     if (e.pair) e.dst[e.pair] = y;
   }
+}
+
+// The same for sequences in pages, and with several axes: pair j turns by the position on its axis. Where the
+// token's row lies takes three dependent loads (the sequence's length, its table, the page's count); the first
+// pieces' loads and the angles go on meanwhile.
+template <int D>
+__global__ void __launch_bounds__(kRopeThreads, 8) rope_pages_kernel(const __grid_constant__ RopePageParams p) {
+  __shared__ float2 cs[VC_ROPE_MAX_PAIRS];
+  __shared__ int64_t s_row;  // elements to the token's row in head 0, -1: not to be written
+  const PagedDev& kv = p.kv;
+  const int tok = blockIdx.x;
+  int b = 0;
+#pragma unroll 1
+  for (int i = 1; i < p.B; ++i)
+    if (p.req[i].tok_begin <= tok) b = i;
+  const RopePageReqDev& r = p.req[b];
+  const int t = tok - r.tok_begin;
+  const int per = p.inter ? D / 8 : D / 8 - p.rot / 16;  // items of a rotated head
+  const int nq = (r.q ? p.Hq : 0) * per, n = nq + p.Hkv * (per + D / 8);
+  const double turns = (int)threadIdx.x < p.rot / 2 ? p.turns[threadIdx.x] : 0.0;
+  pdl_launch_dependents();
+  pdl_wait();
+  RopeItem e{nullptr, nullptr, 0, -1};
+  uint4 x, y;
+  int64_t row = 0;
+  auto load = [&](int i) {
+    e = rope_item<D>(p, r, kv.k + row, kv.v + row, (int64_t)D << kv.shift, t, i, per);
+    x = e.src[0];
+    if (e.pair) y = e.src[e.pair];
+  };
+  if ((int)threadIdx.x < n) load(threadIdx.x);  // where it goes is found below
+  if ((int)threadIdx.x < p.rot / 2) {
+    const int64_t off = r.off ? r.off[p.axis[threadIdx.x] * r.off_stride + t] : t;
+    double turn = (double)(kv.next[r.seq] + off) * turns;
+    turn -= rint(turn);
+    float sn, cn;
+    sincospif((float)(2.0 * turn), &sn, &cn);
+    cs[threadIdx.x] = make_float2(cn * p.amp, sn * p.amp);
+  }
+  if (threadIdx.x == kRopeThreads - 1) {
+    const int len = kv.len[r.seq];
+    const int64_t at = (int64_t)len + t;
+    int64_t to = -1;
+    if (len >= 0 && at < (int64_t)kv.held_of(r.seq) << kv.shift) {
+      const int page = kv.pages_of(r.seq)[at >> kv.shift];
+      if (kv.has_page(page) && kv.refs[page] == 1) to = (((int64_t)page * p.Hkv << kv.shift) + (at & (kv.rows() - 1))) * D;
+    }
+    if (to < 0) set_status(p.dev_status, VC_DEV_PAGES);
+    s_row = to;
+  }
+  __syncthreads();
+  row = max(s_row, (int64_t)0);
+  const int end = s_row < 0 ? nq : n;  // queries are turned all the same
+  for (int i = threadIdx.x; i < end; i += kRopeThreads) {
+    if (i != (int)threadIdx.x)
+      load(i);
+    else if (i >= nq)  // its source is read already; its place is known now
+      e.dst = rope_item<D>(p, r, kv.k + row, kv.v + row, (int64_t)D << kv.shift, t, i, per).dst;
+    rope_turn(e, x, y, cs);
+    e.dst[0] = x;
+    if (e.pair) e.dst[e.pair] = y;
+  }
+}
+
+cudaError_t launch_rope_pages(const RopePageParams& p, int d, cudaStream_t s) {
+  auto kern = d == 128 ? rope_pages_kernel<128> : rope_pages_kernel<64>;
+  return launch_pdl(kern, dim3(p.n_tok), dim3(kRopeThreads), 0, s, p);
 }
 
 cudaError_t launch_rope(const RopeParams& p, int d, cudaStream_t s) {

@@ -1,0 +1,962 @@
+// Attention of drafted trees, chains and single tokens over sequences in pages, on tcgen05 tensor cores.
+//
+// Token i of a request's n_rows tokens sees the rows of its sequence's context and the tokens its mask names:
+//   s_t = q . k_t / sqrt(d),  o = sum_t 2^(s_t - lse) v_t  (log2 domain).
+//
+// Work decomposition. The rows of one KV head (tokens x G = Hq / Hkv heads) are cut into units of up to 256, the
+// keys (context and tokens) into tiles of 128. Lengths live on the device, so the kernels themselves lay the
+// plan down: one warp, a lane a request, adds up the tiles [request][head][unit][tile], and each CTA (one per SM:
+// 8 softmax warps, 4 MMA issuers, 1 loader) takes an equal range of them by cost. A CTA's part of a unit of a head
+// (a piece) leaves (o, lse) partials; a second kernel merges a row's partials. Where every request has the same
+// number U > 1 of full units, CTA c takes unit c % U in the c / U-th range of [request][head][tile]: the units of
+// a head read a tile at about the same time, and it comes from DRAM once.
+//
+// Within a CTA two chains run side by side, each an issuer thread and a warpgroup of softmax threads (a
+// thread per query row): S = Q K^T into TMEM, softmax in registers, P (bf16) over S in TMEM, O += P V with P
+// read from TMEM. The chains meet only in the ring of K and V tiles. A unit of more than 128 rows gives each
+// chain 128 rows and every tile (a tile costs 2); one of up to 128 rows gives both chains the same rows and a half
+// of every tile (which costs 1), and each leaves its own partial. The loader's lanes fetch a tile page by page,
+// each the pages that it looked up one tile before.
+//
+// What a query row may not see: keys get -infinity by the row's bits of the mask; value rows behind the last
+// token (whatever the page holds there) are zeroed in shared memory, and where a step has a value row that is not
+// finite and not for all, the threads add up the rows they see themselves.
+#include "tc05.cuh"
+
+#include <cudaTypedefs.h>
+#include <math.h>
+#include <string.h>
+
+namespace vc {
+
+namespace {
+
+constexpr int TM = 128;         // query rows of a chain
+constexpr int TN = 128;         // keys per tile
+constexpr int TS = 64;          // keys per step: S and P of half a tile, double-buffered
+constexpr int TU = 2 * TM;      // query rows of a unit
+// warps 0-3, 4-7 softmax of chains 0 and 1; 8, 9 issue their S; 10, 11 their P V; 12 TMA; 13-15 idle (they
+// make a warpgroup with it: registers are handed over by warpgroup)
+constexpr int TTHREADS = 512;
+// Registers a thread: launched with 128 (65536 / 512), then 144 in the softmax warpgroups and 80 in the others
+constexpr int TREG_SOFTMAX = 144, TREG_ISSUE = 80;
+static_assert(256 * (TREG_SOFTMAX + TREG_ISSUE) <= 65536, "no more than the block was launched with");
+
+struct TreeParams {
+  PagedDev kv;
+  TreeReqDev req[VC_MAX_BATCH];
+  int32_t unit_begin[VC_MAX_BATCH];  // first (head, unit) of each request; with lanes: head alone
+  int32_t B, Hq, Hkv, G, n_tok;
+  int32_t lanes;                     // units of every head, each with CTAs of its own (c % lanes); 1: in one sequence
+  int32_t n_cta;                     // CTAs of a lane
+  int32_t least;                     // cost of the dearest tile: no CTA's range is shorter
+  int32_t lane_slots, slot_rows;     // partial slots of a lane, rows of a slot
+  int32_t merge_warps;               // warps a row of the merge
+  float* ws_o;                       // [lanes][lane_slots][slot_rows][d]; slot = CTA of the lane + (head, unit)
+  float* ws_lse;                     // [lanes][lane_slots][slot_rows], log2 domain, -inf: saw nothing
+  float scale_log2;
+  int32_t* dev_status;
+};
+
+struct TreeMaps {
+  CUtensorMap kv[2];  // (d, page, pages * Hkv): box 64 x page x 1
+};
+
+// What follows from the lengths: in shared memory, laid down by one warp of every block.
+struct TreePlan {
+  int32_t cost_begin[VC_MAX_BATCH];  // of each request in the sequence of costs
+  int32_t ctx[VC_MAX_BATCH], n[VC_MAX_BATCH];  // rows of context, and with the tokens' rows
+  int32_t total, ctas, each, more;   // cost; CTAs of a lane with work; a range's cost, and how many have one more
+};
+
+__device__ __forceinline__ int units_of(int rows) { return (rows + TU - 1) / TU; }
+// A tile of all units of a head that stand in one sequence.
+__device__ __forceinline__ int tile_cost(const TreeParams& p, int rows) {
+  const int u = units_of(rows);
+  return p.lanes > 1 ? 2 : 2 * u - (rows - (u - 1) * TU <= TM ? 1 : 0);
+}
+
+__device__ __forceinline__ void tree_plan(const TreeParams& p, TreePlan* s, int lane, bool tell) {
+  int n = 0, ctx = 0, cost = 0;
+  if (lane < p.B) {
+    const TreeReqDev& r = p.req[lane];
+    const int held = p.kv.held_of(r.seq), len = p.kv.len[r.seq], cap = held << p.kv.shift;
+    ctx = min(max(len, 0), cap);
+    n = (int)min((int64_t)cap, (int64_t)ctx + r.n_rows);
+    if (tell && (ctx != len || n - ctx != r.n_rows)) set_status(p.dev_status, VC_DEV_PAGES);
+    cost = p.Hkv * ((n + TN - 1) / TN) * tile_cost(p, r.n_rows * p.G);
+  }
+  int end = cost;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, end, off);
+    if (lane >= off) end += o;
+  }
+  s->cost_begin[lane] = end - cost;
+  s->ctx[lane] = ctx;
+  s->n[lane] = n;
+  if (lane == 31) {
+    s->total = end;
+    const int ctas = min(p.n_cta, max(end / p.least, end > 0));
+    s->ctas = ctas;
+    s->each = ctas ? end / ctas : 0;
+    s->more = ctas ? end - ctas * s->each : 0;
+  }
+}
+
+// CTA c of a lane has the costs from cta_begin(c) on; x lies in those of cta_of(x).
+__device__ __forceinline__ int cta_begin(const TreePlan& s, int c) { return c * s.each + min(c, s.more); }
+__device__ __forceinline__ int cta_of(const TreePlan& s, int x) {
+  const int e = s.more * (s.each + 1);
+  return x < e ? x / (s.each + 1) : s.more + (x - e) / s.each;
+}
+
+// Steps of tile j of n keys: its second half only where it holds keys.
+__device__ __forceinline__ int tree_steps(int n, int j) { return n - j * TN > TS ? 2 : 1; }
+
+// A CTA's part of a unit of a head: tiles [j0, j1). Every role of the CTA walks through the same pieces.
+struct TPiece {
+  int g, hk, u, j0, j1;  // request, KV head, unit of its rows, tiles
+  int rows, tiles;       // the unit's query rows, the request's tiles
+  int at, end;           // cost at which the unit's tiles start, end of the CTA's range
+  bool split;            // both chains hold the same rows, chain w takes half w of every tile
+
+  __device__ __forceinline__ bool valid() const { return at < end; }
+  __device__ __forceinline__ int cost() const { return split ? 1 : 2; }
+  // chain w's steps of tile j of n keys are its halves [h0, h1)
+  __device__ __forceinline__ int h0(int w) const { return split ? w : 0; }
+  __device__ __forceinline__ int h1(int w, int n, int j) const { return min(tree_steps(n, j), split ? w + 1 : 2); }
+  // it has none in the whole piece: chain 1 of a split unit's last, short tile
+  __device__ __forceinline__ bool idle(int w, int n) const { return split && w == 1 && j1 - j0 == 1 && tree_steps(n, j0) == 1; }
+  __device__ __forceinline__ void fit(const TreeParams& p, const TreePlan& s) {
+    rows = min(TU, p.req[g].n_rows * p.G - u * TU);
+    tiles = (s.n[g] + TN - 1) / TN;
+    split = rows <= TM;
+  }
+  __device__ __forceinline__ void cut() { j1 = min(tiles, (end - at + cost() - 1) / cost()); }
+  __device__ __forceinline__ void next(const TreeParams& p, const TreePlan& s) {
+    at += cost() * tiles;
+    if (!valid()) return;
+    if (p.lanes > 1 || ++u == units_of(p.req[g].n_rows * p.G)) {
+      if (p.lanes == 1) u = 0;
+      if (++hk == p.Hkv) {
+        hk = 0;
+        do ++g;
+        while (s.n[g] == 0);  // there is a further one: the range goes on
+      }
+    }
+    fit(p, s);
+    j0 = 0;
+    cut();
+  }
+};
+
+template <int D>
+struct TCfg {
+  static constexpr int KB = D / 64;            // 64-channel (128-byte) blocks
+  static constexpr int T_BYTES = KB * TN * 128;  // a K, V or Q tile
+  static constexpr int NST = D == 128 ? 5 : 10;  // K and V tiles in flight or in use
+  static constexpr int OFF_T = 2 * T_BYTES;    // behind a Q tile per chain
+  static constexpr int OFF_BAR = OFF_T + NST * T_BYTES;
+  static constexpr int BAR_BYTES = (2 * NST + 20) * 8 + 32;
+  static constexpr int SMEM = OFF_BAR + BAR_BYTES + (int)sizeof(TPiece) + (int)sizeof(TreePlan);
+  static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
+  static constexpr int OCOL = 4 * TS;          // TMEM: S (and P) of chain w at (2 w + step % 2) TS, O at OCOL + w D
+  static constexpr uint32_t TCOLS = 512;
+  static_assert(OCOL + 2 * D <= (int)TCOLS, "TMEM");
+};
+
+__device__ __forceinline__ TPiece tree_first(const TreeParams& p, const TreePlan& s) {
+  TPiece q;
+  const int c = blockIdx.x / p.lanes;
+  const int beg = cta_begin(s, c);
+  q.end = cta_begin(s, c + 1);
+  q.g = 0;
+  for (int b = 1; b < p.B; ++b)  // the last request that starts at or before; one without tiles starts where the next does
+    if (s.cost_begin[b] <= beg) q.g = b;
+  const int rows = p.req[q.g].n_rows * p.G, tiles = (s.n[q.g] + TN - 1) / TN, units = units_of(rows);
+  const int head = tiles * tile_cost(p, rows);
+  int rem = beg - s.cost_begin[q.g];
+  q.hk = rem / head;
+  rem -= q.hk * head;
+  q.u = p.lanes > 1 ? blockIdx.x % p.lanes : min(rem / (2 * tiles), units - 1);
+  if (p.lanes == 1) rem -= q.u * 2 * tiles;
+  q.fit(p, s);
+  q.at = beg - rem;
+  q.j0 = (rem + q.cost() - 1) / q.cost();
+  q.cut();
+  if (q.j0 >= q.j1) q.next(p, s);  // the range starts in a unit's last tile, which is the CTA's before
+  return q;
+}
+
+// Bounded mbarrier wait that also gives up when another role of the CTA has aborted.
+__device__ __forceinline__ bool twait(uint64_t* bar, uint32_t parity, int32_t* st, volatile int* abort) {
+  for (uint32_t it = 0; it < kSpinLimit; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 31u) == 31u && *abort) return false;
+  }
+  set_status(st, VC_DEV_TIMEOUT);
+  *abort = 1;
+  return false;
+}
+
+// The same by a whole warp, which goes on or gives up together: its collective instructions need every lane.
+__device__ __forceinline__ bool twait_warp(uint64_t* bar, uint32_t parity, int32_t* st, volatile int* abort) {
+  bool done = false;
+  for (uint32_t it = 0; it < kSpinLimit && !done; ++it) {
+    done = mbar_try_wait(bar, parity);
+    if ((it & 31u) == 31u && *abort) break;
+  }
+  if (__all_sync(0xffffffffu, done)) return true;
+  if (!*abort) set_status(st, VC_DEV_TIMEOUT);
+  *abort = 1;
+  return false;
+}
+
+// Arrives where `on`, without a branch.
+__device__ __forceinline__ void tarrive_if(uint64_t* bar, bool on) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"((uint32_t)on)
+      : "memory");
+}
+
+__device__ __forceinline__ bool broken_bf16x2(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+// Bits of the 64 keys from k0 on that a row sees: its words of the mask, shifted to the step; keys before the
+// first token (node < 0) are context, keys from n on are not there.
+__device__ __forceinline__ void mask_bits(const uint32_t* row, int words, int node, int left, uint32_t& lo, uint32_t& hi) {
+  auto word = [&](int i) { return row && i < words ? __ldg(row + i) : 0u; };
+  uint64_t x;
+  if (node >= 0) {
+    const int w = node >> 5, sh = node & 31;
+    const uint32_t a = word(w), b = word(w + 1), c = sh ? word(w + 2) : 0u;
+    x = (uint64_t)__funnelshift_r(b, c, sh) << 32 | __funnelshift_r(a, b, sh);
+  } else {  // -64 < node
+    x = ((uint64_t)word(1) << 32 | word(0)) << -node | ((1ull << -node) - 1ull);
+  }
+  if (left < 64) x &= (1ull << left) - 1ull;
+  lo = (uint32_t)x;
+  hi = (uint32_t)(x >> 32);
+}
+
+template <int D>
+__global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ TreeMaps maps) {
+  using C = TCfg<D>;
+  constexpr int NST = C::NST;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (smem_u32(smem) & 1023u) {  // the swizzled layouts need 1024-byte aligned tiles
+    pdl_wait();
+    if (tid == 0) set_status(p.dev_status, VC_DEV_INTERNAL);
+    return;
+  }
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [NST] tile landed
+  uint64_t* empty = full + NST;   // [NST] both chains' MMAs are done with it
+  uint64_t* sfull = empty + NST;  // [2][2] S of the chain's step in TMEM buffer step & 1
+  uint64_t* pfull = sfull + 4;    // [2][2] the step's P in the same place (4 warps)
+  uint64_t* ofull = pfull + 4;    // [2][2] its P V done: the buffer may take the S of two steps on
+  uint64_t* qfull = ofull + 4;    // [2] the piece's Q tile in shared memory (4 warps)
+  uint64_t* vbar = qfull + 2;     // [2] the chain's warps have looked through a V tile (4 warps)
+  uint64_t* xbar = vbar + 2;      // [4] drain of an issuer's MMAs
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(xbar + 4);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
+  // [2][2] by S buffer, as the barriers are: 1 + the chain's last step in it whose P V the softmax warps took. A
+  // warp may be a step ahead of the others, and so ahead of the P V issuer, which reads a step's word once all
+  // four have left the step; the word's next step needs the issuer's commit behind that.
+  volatile uint32_t* s_odd = tslot + 2;
+  volatile uint32_t* s_issued = tslot + 6;  // loads issued so far
+  TPiece* s_first = reinterpret_cast<TPiece*>(smem + C::OFF_BAR + C::BAR_BYTES);  // the CTA's first piece
+  TreePlan& plan = *reinterpret_cast<TreePlan*>(s_first + 1);
+
+  if (warp == 12) tc05::alloc(tslot, C::TCOLS);
+  if (warp == 13) {
+    pdl_wait();  // lengths are the kernel's before's
+    tree_plan(p, &plan, lane, blockIdx.x == 0);
+    __syncwarp();
+    if (lane == 0) {
+      if ((int)blockIdx.x / p.lanes < plan.ctas)
+        *s_first = tree_first(p, plan);
+      else
+        s_first->at = s_first->end = 0;
+    }
+  }
+  if (tid == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 2);
+    }
+    for (int w = 0; w < 2; ++w) {
+      for (int i = 2 * w; i < 2 * w + 2; ++i) {
+        mbar_init(&sfull[i], 1);
+        mbar_init(&pfull[i], 4);
+        mbar_init(&ofull[i], 1);
+        s_odd[i] = 0;
+      }
+      mbar_init(&qfull[w], 4);
+      mbar_init(&vbar[w], 4);
+      mbar_init(&xbar[w], 1);
+      mbar_init(&xbar[2 + w], 1);
+    }
+    fence_mbar_init();
+    *s_abort = 0;
+    *s_issued = 0;
+  }
+  tc05::fence_before();
+  __syncthreads();
+  tc05::fence_after();
+  const uint32_t tmem = *tslot;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // Load `it` has landed; `seen` is the caller's count of loads it knows to be issued. A role does not see
+  // every phase of a stage's barrier (the S issuers wait for K tiles only, the P V issuers for V tiles), so the
+  // parity alone could be that of two phases before: once the load is issued, the phase before it is over, and
+  // its own cannot pass until this role releases the stage.
+  // The chains' barriers are kept per S buffer: step s + 2 cannot complete a phase of one before step s's
+  // has been waited for, while with one barrier for both, steps s and s + 1 could both pass unseen.
+  auto landed = [&](uint32_t it, uint32_t& seen) -> bool {
+    for (uint32_t i = 0; seen <= it; ++i) {
+      seen = *s_issued;
+      if (i >= kSpinLimit || ((i & 31u) == 31u && *s_abort)) {
+        if (!*s_abort) set_status(p.dev_status, VC_DEV_TIMEOUT);
+        *s_abort = 1;
+        return false;
+      }
+    }
+    return twait(&full[it % NST], (it / NST) & 1, p.dev_status, s_abort);
+  };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TREG_ISSUE));
+    if (warp == 12) {
+      // ---- TMA: tiles in order, K then V of each, a lane a page and 64-channel block -------------------
+      TPiece q = *s_first;
+      const uint64_t pol = l2_evict_first_policy();
+      const int shift = p.kv.shift, per = TN >> shift;  // pages a tile
+      const int kb = lane / per, pi = lane - kb * per;
+      const bool mine = kb < C::KB;
+      const bool once = p.lanes == 1;  // tiles that one CTA reads once leave L2 first
+      uint32_t it = 0;
+      bool ok = true;
+      for (; q.valid() && ok; q.next(p, plan)) {
+        const int n = plan.n[q.g], pages = (n + p.kv.rows() - 1) >> shift;
+        const int32_t* table = p.kv.pages_of(p.req[q.g].seq);
+        auto look = [&](int j) { return mine && j * per + pi < pages ? __ldg(table + j * per + pi) : 0; };
+        int page = look(q.j0);
+        for (int j = q.j0; j < q.j1 && ok; ++j) {
+          const int ahead = j + 1 < q.j1 ? look(j + 1) : 0;
+          const int cnt = min(per, pages - j * per);  // pages of this tile: at least one
+          const bool load = mine && pi < cnt;
+          if (load && !p.kv.has_page(page)) {
+            set_status(p.dev_status, VC_DEV_PAGES);
+            page = p.kv.n_pages;  // beyond the map: reads as zeros
+          }
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t st = it % NST;
+            if (it >= (uint32_t)NST && !twait_warp(&empty[st], (it / NST - 1) & 1, p.dev_status, s_abort)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(cnt << shift) * 128 * C::KB);
+            __syncwarp();
+            if (load) {
+              uint8_t* dst = smem + C::OFF_T + st * C::T_BYTES + kb * (TN * 128) + ((pi << shift) * 128);
+              if (once)
+                tc05::tma_load_3d_hint(dst, &maps.kv[kv], kb * 64, 0, page * p.Hkv + q.hk, &full[st], pol);
+              else
+                tc05::tma_load_3d(dst, &maps.kv[kv], kb * 64, 0, page * p.Hkv + q.hk, &full[st]);
+            }
+            __syncwarp();
+            ++it;
+            if (lane == 0) {
+              __threadfence_block();
+              *s_issued = it;
+            }
+          }
+          page = ahead;
+        }
+      }
+      if (*s_abort && lane == 0)  // drain (bounded): a ring's worth of loads may still be landing
+        for (uint32_t i = it > (uint32_t)NST ? it - NST : 0; i < it; ++i)
+          mbar_wait_bounded(&full[i % NST], (i / NST) & 1, p.dev_status);
+      __syncwarp();
+    } else if (warp == 10 || warp == 11) {
+      // ---- P V issue of chain w: as soon as a step's P is there ---------------------------------------
+      if (lane == 0) {
+        const int w = warp - 10;
+        constexpr uint32_t IDESC_O = tc05::idesc_bf16(TM, D, true);
+        const uint32_t aT = smem_u32(smem + C::OFF_T), tS = tmem + 2 * w * TS, tO = tmem + C::OCOL + w * D;
+        TPiece q = *s_first;
+        uint32_t g = 0, t = 0, seen = 0;  // tiles of the CTA, steps of the chain
+        bool ok = true;
+        for (; q.valid() && ok; q.next(p, plan)) {
+          const int n = plan.n[q.g];
+          bool acc = false;
+          for (int j = q.j0; j < q.j1 && ok; ++j, ++g) {
+            const uint32_t iv = 2 * g + 1, sv = iv % NST, vaddr = aT + sv * C::T_BYTES;
+            ok = landed(iv, seen);
+            const int h1 = q.h1(w, n, j);
+            for (int h = q.h0(w); h < h1 && ok; ++h, ++t) {
+              if (!twait(&pfull[2 * w + (t & 1)], (t >> 1) & 1, p.dev_status, s_abort)) {
+                ok = false;
+                break;
+              }
+              tc05::fence_after();
+              if (s_odd[2 * w + (t & 1)] != t + 1) {
+                const uint32_t tP = tS + (t & 1) * TS, va = vaddr + h * (TS / 16) * 2048;
+#pragma unroll
+                for (int kk = 0; kk < TS / 16; ++kk)
+                  tc05::mma_ts(tO, tP + kk * 8, tc05::sdesc_sw128(va + kk * 2048, TN * 128, 1024), IDESC_O,
+                               (acc || kk > 0) ? 1u : 0u);
+              }
+              tc05::commit(&ofull[2 * w + (t & 1)]);
+              acc = true;
+            }
+            if (ok) tc05::commit(&empty[sv]);
+          }
+        }
+        // every MMA issued so far has completed before TMEM is released (bounded, even after an abort)
+        tc05::commit(&xbar[2 + w]);
+        mbar_wait_bounded(&xbar[2 + w], 0, p.dev_status);
+      }
+    } else if (warp < 10) {
+      // ---- S issue of chain w: a step ahead of its softmax --------------------------------------------
+      if (lane == 0) {
+        const int w = warp - 8;
+        constexpr uint32_t IDESC_S = tc05::idesc_bf16(TM, TS, false);
+        const uint32_t aQ = smem_u32(smem) + w * C::T_BYTES, aT = smem_u32(smem + C::OFF_T);
+        const uint32_t tS = tmem + 2 * w * TS;
+        TPiece q = *s_first;
+        uint32_t g = 0, t = 0, u = 0, seen = 0;  // tiles of the CTA, steps and pieces of the chain
+        bool ok = true;
+        for (; q.valid() && ok; q.next(p, plan)) {
+          const int n = plan.n[q.g];
+          if (!q.idle(w, n)) {
+            ok = twait(&qfull[w], u & 1, p.dev_status, s_abort);
+            ++u;
+          }
+          for (int j = q.j0; j < q.j1 && ok; ++j, ++g) {
+            const uint32_t ik = 2 * g, sk = ik % NST, kaddr = aT + sk * C::T_BYTES;
+            ok = landed(ik, seen);
+            const int h1 = q.h1(w, n, j);
+            for (int h = q.h0(w); h < h1 && ok; ++h, ++t) {
+              // the P V that read its P from this S buffer is done
+              if (t > 1 && !twait(&ofull[2 * w + (t & 1)], ((t - 2) >> 1) & 1, p.dev_status, s_abort)) {
+                ok = false;
+                break;
+              }
+              tc05::fence_after();
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * (TN * 128) + (kk & 3) * 32;
+                tc05::mma_bf16(tS + (t & 1) * TS, tc05::sdesc_sw128(aQ + off, 16, 1024),
+                               tc05::sdesc_sw128(kaddr + h * TS * 128 + off, 16, 1024), IDESC_S, kk > 0);
+              }
+              tc05::commit(&sfull[2 * w + (t & 1)]);
+            }
+            if (ok) tc05::commit(&empty[sk]);
+          }
+        }
+        tc05::commit(&xbar[w]);
+        mbar_wait_bounded(&xbar[w], 0, p.dev_status);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TREG_SOFTMAX));
+    // ---- softmax of chain w: thread rt owns TMEM lane rt = row rt of the chain ----------------------
+    const int w = warp >> 2, rt = tid & (TM - 1);
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + 2 * w * TS, tO = tmem + lane_off + C::OCOL + w * D;
+    uint8_t* sQ = smem + w * C::T_BYTES;
+    TPiece q = *s_first;
+    uint32_t g = 0, t = 0, looked = 0, seen = 0;
+    // P V of step s done (and with it those before): asked for steps whose S has been read, so the phase
+    // before on that buffer is over
+    auto pv_done = [&](uint32_t s) { return twait_warp(&ofull[2 * w + (s & 1)], (s >> 1) & 1, p.dev_status, s_abort); };
+    bool ok = true;
+    const size_t lane_slot = (size_t)(blockIdx.x % p.lanes) * p.lane_slots + blockIdx.x / p.lanes;
+    auto slot_of = [&]() {
+      return lane_slot + p.unit_begin[q.g] + (p.lanes > 1 ? q.hk : q.hk * units_of(p.req[q.g].n_rows * p.G) + q.u);
+    };
+    // Q of the next piece with steps for this chain, into its Q tile (the chain's S on the last one are all
+    // done: their softmax is); pieces without any leave an empty partial
+    auto fetch = [&]() {
+      for (; q.valid(); g += q.j1 - q.j0, q.next(p, plan)) {
+        const TreeReqDev& R = p.req[q.g];
+        const int ru = q.split ? rt : w * TM + rt, row = q.u * TU + ru;  // row of the unit, of the head
+        const bool row_ok = ru < q.rows;
+        if (q.idle(w, plan.n[q.g])) {
+          if (row_ok) p.ws_lse[slot_of() * p.slot_rows + w * q.rows + ru] = -INFINITY;
+          continue;
+        }
+        const int tok = row / p.G;
+        const bf16* src = row_ok ? R.q + ((size_t)tok * p.Hq + q.hk * p.G + (row - tok * p.G)) * D : nullptr;  // this thread's row
+        // the warp's 32 rows, a row's 16-byte pieces in neighbouring lanes (a lane per row would touch 32 lines a load)
+        constexpr int PR = D / 8, RW = 32 / PR;  // pieces of a row, rows a load
+#pragma unroll
+        for (int i = 0; i < 32 / RW; ++i) {
+          const int r = i * RW + lane / PR, c = lane % PR, rr = (warp & 3) * 32 + r;
+          const bf16* from = reinterpret_cast<const bf16*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), r));
+          const uint4 v = from ? __ldcg(reinterpret_cast<const uint4*>(from) + c) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(sQ + (c >> 3) * (TM * 128) + rr * 128 + (((c ^ rr) & 7) << 4)) = v;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qfull[w]);
+        return;
+      }
+    };
+    // the chain's partial of the piece before: written once the next one's S are under way
+    size_t part = 0;
+    float m_run = 0.f, l_run = 0.f;
+    bool row_ok = false, have = false;
+    while (ok) {
+      fetch();
+      if (have) {
+        // after its last P V
+        if (!pv_done(t - 1)) break;
+        tc05::fence_after();
+        const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
+        // rows in the order of an MMA's accumulator: four lanes hold 8 neighbouring channels (whole 32-byte
+        // sectors), where a lane per row would write 32 lines at a time
+        float* o_row0 = p.ws_o + (part - (rt & 31)) * D + 2 * (lane & 3);  // of the warp's first row
+        const unsigned rows_ok = __ballot_sync(0xffffffffu, row_ok);
+#pragma unroll 1
+        for (int hh = 0; hh < 2; ++hh) {
+          if (!((rows_ok >> (16 * hh)) & 0xffffu)) continue;
+          const int r0 = hh * 16 + (lane >> 2), r1 = r0 + 8;
+          const float i0 = __shfl_sync(0xffffffffu, inv, r0), i1 = __shfl_sync(0xffffffffu, inv, r1);
+          const bool ok0 = (rows_ok >> r0) & 1u, ok1 = (rows_ok >> r1) & 1u;
+#pragma unroll 1
+          for (int cb = 0; cb < D / 32; ++cb) {
+            uint32_t r[16];
+            tc05::ld16x256_x4(tO + ((uint32_t)(hh * 16) << 16) + cb * 32, r);  // warp-collective: every lane loads
+            tc05::wait_ld();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (ok0)
+                *reinterpret_cast<float2*>(o_row0 + (size_t)r0 * D + cb * 32 + 8 * k) =
+                    make_float2(__uint_as_float(r[4 * k]) * i0, __uint_as_float(r[4 * k + 1]) * i0);
+              if (ok1)
+                *reinterpret_cast<float2*>(o_row0 + (size_t)r1 * D + cb * 32 + 8 * k) =
+                    make_float2(__uint_as_float(r[4 * k + 2]) * i1, __uint_as_float(r[4 * k + 3]) * i1);
+            }
+          }
+        }
+        if (row_ok) p.ws_lse[part] = l_run != 0.f ? m_run + log2f(l_run) : -INFINITY;
+        tc05::fence_before();
+      }
+      if (!q.valid()) break;
+      have = true;
+      const TreeReqDev& R = p.req[q.g];
+      const int ru = q.split ? rt : w * TM + rt;
+      row_ok = ru < q.rows;
+      const int row = q.u * TU + ru, tl = row / p.G;
+      part = slot_of() * p.slot_rows + (q.split ? w * q.rows : 0) + ru;
+      const int n = plan.n[q.g], ctx = plan.ctx[q.g];
+      const uint32_t* mrow = R.mask && row_ok ? R.mask + (size_t)tl * R.mask_words : nullptr;
+      // the first key that some row of the chain does not see
+      const int blind = R.mask ? ctx : ctx + (q.u * TU + (q.split ? 0 : w * TM)) / p.G + 1;
+      m_run = -INFINITY, l_run = 0.f;
+      bool fresh = true;  // the piece's first step
+      for (int j = q.j0; j < q.j1 && ok; ++j, ++g) {
+        const int h1 = q.h1(w, n, j);
+        for (int h = q.h0(w); h < h1; ++h, ++t, fresh = false) {
+          const int k0 = j * TN + h * TS;  // the step's first key
+          const uint32_t tP = tS + (t & 1) * TS;
+          uint32_t see_lo = 0xffffffffu, see_hi = 0xffffffffu;  // keys of the step that the row sees
+          if (k0 + TS > min(blind, n)) {
+            if (R.mask && k0 + TS > ctx) {
+              mask_bits(mrow, R.mask_words, k0 - ctx, n - k0, see_lo, see_hi);
+            } else {
+              const int last = min(ctx + tl, n - 1) - k0;
+              see_lo = last >= 31 ? 0xffffffffu : last < 0 ? 0u : (2u << last) - 1u;
+              see_hi = last >= 63 ? 0xffffffffu : last < 32 ? 0u : (2u << (last - 32)) - 1u;
+            }
+          }
+          if (!twait_warp(&sfull[2 * w + (t & 1)], (t >> 1) & 1, p.dev_status, s_abort)) {
+            ok = false;
+            break;
+          }
+          tc05::fence_after();
+          float x[TS];
+#pragma unroll
+          for (int cb = 0; cb < TS / 32; ++cb) {
+            uint32_t r[32];
+            tc05::ld32(tP + cb * 32, r);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[cb * 32 + e] = __uint_as_float(r[e]);
+          }
+          tc05::wait_ld();
+          if ((see_lo & see_hi) != 0xffffffffu) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (!((see_lo >> e) & 1u)) x[e] = -INFINITY;
+              if (!((see_hi >> e) & 1u)) x[32 + e] = -INFINITY;
+            }
+          }
+          // P = 2^(x scale - m), bf16, over S: the MMA wants both operands in one 16-bit type, and V is bf16 (its range
+          // is not fp16's). A weight is off by 2^-8 of itself at most. Sums and lse take the weights unrounded.
+          // The running maximum is taken as it is: the row's new one is found alongside, and only when it is larger by
+          // more than 2^8 (or this is the piece's first step) is m moved, O rescaled after the P V before, and P
+          // computed again. TMEM loads and stores are warp-collective: the warp does it together.
+          uint32_t r[TS / 2];
+          float u0, u1, mx = -INFINITY, my = -INFINITY, mz = -INFINITY, mw = -INFINITY;
+#pragma unroll 1
+          for (int again = 0; again < 2; ++again) {
+            const float mu = m_run == -INFINITY ? 0.f : m_run;
+            const uint64_t sc = f2_pack(p.scale_log2, p.scale_log2), nm = f2_pack(-mu, -mu);
+            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+            for (int e = 0; e < TS / 2; ++e) {
+              float a0, a1;
+              f2_unpack(f2_fma(f2_pack(x[2 * e], x[2 * e + 1]), sc, nm), a0, a1);
+              const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+              acc[e & 3] = f2_add(acc[e & 3], f2_pack(p0, p1));
+              r[e] = pack_bf16x2(p0, p1);
+              float& m = (e & 3) == 0 ? mx : (e & 3) == 1 ? my : (e & 3) == 2 ? mz : mw;
+              m = max3f(m, x[2 * e], x[2 * e + 1]);
+            }
+            f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), u0, u1);
+            if (again) break;
+            const float m_new = fmaxf(m_run, fmaxf(fmaxf(mx, my), fmaxf(mz, mw)) * p.scale_log2);
+            const bool need = m_new > m_run + 8.f;  // from -infinity, any finite score
+            if (!__any_sync(0xffffffffu, need)) break;
+            if (fresh) {
+              m_run = m_new;
+              continue;
+            }
+            if (!pv_done(t - 1)) {
+              ok = false;
+              break;
+            }
+            tc05::fence_after();
+            float f = 1.f;
+            if (need) {
+              f = ex2_approx(m_run - m_new);
+              l_run *= f;
+              m_run = m_new;
+            }
+#pragma unroll 1
+            for (int cb = 0; cb < D / 32; ++cb) {
+              uint32_t o[32];
+              tc05::ld32(tO + cb * 32, o);
+              tc05::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tc05::st32(tO + cb * 32, o);
+            }
+          }
+          if (!ok) break;
+          tc05::st32(tP, r);
+          l_run += u0 + u1;
+          tc05::wait_st();
+          // A step with keys that some rows do not see: a weight of 0 would carry an infinite or NaN value row to
+          // them. Rows from n on, which nobody sees, are zeroed; if others hold such a value, the threads add up the
+          // seen keys themselves.
+          if (k0 + TS > min(blind, n)) {
+            const uint32_t iv = 2 * g + 1;
+            if (!__all_sync(0xffffffffu, landed(iv, seen))) {
+              ok = false;
+              break;
+            }
+            uint8_t* sV = smem + C::OFF_T + (iv % NST) * C::T_BYTES;
+            bool bad = false;
+            const int kv = h * TS + (rt & (TS - 1));  // two threads look through each of the step's rows
+            const bool there = j * TN + kv < n;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              const int c = (rt / TS) * (D / 16) + i;
+              uint4* at = reinterpret_cast<uint4*>(sV + (c >> 3) * (TN * 128) + kv * 128 + (((c ^ kv) & 7) << 4));
+              if (there) {
+                const uint4 v = *at;
+                bad |= broken_bf16x2(v.x) || broken_bf16x2(v.y) || broken_bf16x2(v.z) || broken_bf16x2(v.w);
+              } else {
+                *at = make_uint4(0, 0, 0, 0);  // by both chains where they share the tile
+              }
+            }
+            if (bad) s_odd[2 * w + (t & 1)] = t + 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&vbar[w]);
+            if (!twait_warp(&vbar[w], looked & 1, p.dev_status, s_abort)) {
+              ok = false;
+              break;
+            }
+            ++looked;
+            if (s_odd[2 * w + (t & 1)] == t + 1) {
+              if (!fresh && !pv_done(t - 1)) {
+                ok = false;
+                break;
+              }
+              tc05::fence_after();
+#pragma unroll 1
+              for (int cb = 0; cb < D / 32; ++cb) {
+                uint32_t r[32];
+                if (!fresh) {
+                  tc05::ld32(tO + cb * 32, r);
+                  tc05::wait_ld();
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) r[e] = 0u;
+                }
+#pragma unroll 1
+                for (int kp = 0; kp < TS / 2; ++kp) {  // two keys a column; rare, so kept small
+                  const uint32_t pw = tc05::ld1(tP + kp);
+                  tc05::wait_ld();
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const int k = 2 * kp + e, kt = h * TS + k;
+                    const bool sees = ((k < 32 ? see_lo : see_hi) >> (k & 31)) & 1u;
+                    const float pk = __uint_as_float(e ? pw & 0xffff0000u : pw << 16);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                      const int ch = cb * 4 + c;
+                      const uint4 v = *reinterpret_cast<const uint4*>(sV + (ch >> 3) * (TN * 128) + kt * 128 + (((ch ^ kt) & 7) << 4));
+                      const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                      for (int i = 0; i < 8; ++i) {
+                        const float val = __uint_as_float(i & 1 ? vw[i >> 1] & 0xffff0000u : vw[i >> 1] << 16);
+                        const float a = __uint_as_float(r[c * 8 + i]);
+                        r[c * 8 + i] = __float_as_uint(sees ? fmaf(pk, val, a) : a);
+                      }
+                    }
+                  }
+                }
+                tc05::st32(tO + cb * 32, r);
+              }
+              tc05::wait_st();
+            }
+          }
+          tc05::fence_before();
+          __syncwarp();
+          tarrive_if(&pfull[2 * w + (t & 1)], lane == 0);
+        }
+      }
+      if (!ok) break;
+      q.next(p, plan);
+    }
+  }
+
+  tc05::fence_before();
+  __syncthreads();
+  tc05::fence_after();
+  if (warp == 12) tc05::dealloc(tmem, C::TCOLS);
+}
+
+// Weight of a partial beside the largest lse M: 0 where it saw nothing; M stays -inf only beside a NaN.
+__device__ __forceinline__ float part_weight(float l, float M) { return l == -INFINITY ? 0.f : M == -INFINITY ? NAN : exp2f(l - M); }
+
+// Merge: one to eight warps per (token, query head), o = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M) over its
+// partials: a lane per partial takes the weights, then the warp adds up the partials' channels, four loads in
+// flight.
+template <int D>
+__global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+  constexpr int E = D / 32;  // channels a lane
+  constexpr int PF = 4;      // partials in flight
+  __shared__ TreePlan plan;
+  __shared__ float s_sum[8];
+  __shared__ float s_acc[8][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wpr = p.merge_warps, part = warp % wpr;  // warps of a row, this one among them
+  const int64_t id = (int64_t)blockIdx.x * (8 / wpr) + warp / wpr;
+  const bool live = id < (int64_t)p.n_tok * p.Hq;
+  const int tok = live ? (int)(id / p.Hq) : 0, hq = live ? (int)(id - (int64_t)tok * p.Hq) : 0, hk = hq / p.G;
+  int b = 0;
+  for (int i = 1; i < p.B; ++i)
+    if (p.req[i].tok_begin <= tok) b = i;
+  const TreeReqDev& R = p.req[b];
+  const int i = tok - R.tok_begin, r = i * p.G + hq - hk * p.G;  // token of the request, row of the head
+  pdl_launch_dependents();
+  pdl_wait();
+  if (warp == 0) tree_plan(p, &plan, lane, false);
+  __syncthreads();
+  // where the row's unit left its partials: `count` of them, number k at at(k); a split unit has two a slot
+  const int rows = R.n_rows * p.G, u = r / TU, in_unit = min(TU, rows - u * TU), cost = in_unit <= TM ? 1 : 2;
+  const int tiles = (plan.n[b] + TN - 1) / TN;
+  int count = 0, second = cost == 1 ? in_unit : 0;
+  size_t base = 0;
+  if (live && tiles > 0) {
+    const int at = plan.cost_begin[b] + hk * tiles * tile_cost(p, rows) + (p.lanes > 1 ? 0 : u * 2 * tiles);
+    const int c0 = cta_of(plan, at), c1 = cta_of(plan, at + cost * (tiles - 1));  // of its first and last tile
+    count = (c1 - c0 + 1) * (second ? 2 : 1);
+    const int unit = p.unit_begin[b] + (p.lanes > 1 ? hk : hk * units_of(rows) + u);
+    base = ((size_t)(p.lanes > 1 ? u : 0) * p.lane_slots + c0 + unit) * p.slot_rows + (r - u * TU);
+  }
+  auto index = [&](int k) {
+    return second ? base + (size_t)(k >> 1) * p.slot_rows + (k & 1) * second : base + (size_t)k * p.slot_rows;
+  };
+  auto lse_of = [&](int k, int end) { return k >= end ? -INFINITY : p.ws_lse[index(k)]; };
+  float M = -INFINITY;
+  for (int k0 = 0; k0 < count; k0 += 32) M = fmaxf(M, lse_of(k0 + lane, count));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float L = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  const int beg = count * part / wpr, end = count * (part + 1) / wpr;
+  for (int k0 = beg; k0 < end; k0 += 32) {
+    const float l = lse_of(k0 + lane, end), f = part_weight(l, M);
+    const unsigned wrote = __ballot_sync(0xffffffffu, l != -INFINITY);
+    L += f;
+    const int cnt = min(32, end - k0);
+    for (int c0 = 0; c0 < cnt; c0 += PF) {
+      float v[PF][E], fc[PF];
+#pragma unroll
+      for (int c = 0; c < PF; ++c) {
+        fc[c] = __shfl_sync(0xffffffffu, f, c0 + c);  // c0 + c < 32; nothing was written beyond cnt
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[c][e] = 0.f;
+        if ((wrote >> (c0 + c)) & 1u) {  // a partial that saw nothing was not written
+          const float* src = p.ws_o + index(k0 + c0 + c) * D + lane * E;
+          if constexpr (E == 4)
+            *reinterpret_cast<float4*>(v[c]) = __ldcg(reinterpret_cast<const float4*>(src));
+          else
+            *reinterpret_cast<float2*>(v[c]) = __ldcg(reinterpret_cast<const float2*>(src));
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < PF; ++c)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(fc[c], v[c][e], acc[e]);
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+  if (wpr > 1) {  // the row's warps meet
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+    if (lane == 0) s_sum[warp] = L;
+    __syncthreads();
+    if (part != 0) return;
+    for (int k = 1; k < wpr; ++k) {
+      L += s_sum[warp + k];
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += s_acc[warp + k][lane * E + e];
+    }
+  }
+  if (!live) return;
+  const float inv = L != 0.f ? 1.f / L : 0.f;
+  bf16* dst = R.o + ((size_t)i * p.Hq + hq) * D + lane * E;
+  uint32_t out[E / 2];
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  if constexpr (E == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+  else
+    *reinterpret_cast<uint32_t*>(dst) = out[0];
+}
+
+// ------------------------------------------------------------------------------------------------
+// bf16 pages [n_pages][Hkv][page][d] as a 3-D tensor (d, page, n_pages * Hkv); box 64 x page x 1, 128-byte swizzle.
+bool page_map(CUtensorMap* m, const void* base, int d, int page, int64_t heads) {
+  auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tmap_encoder());
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)heads};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)page * d * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)page, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int tree_sms() {
+  static const int n = [] {
+    int dev = 0, v = 0;
+    const bool ok = cudaGetDevice(&dev) == cudaSuccess &&
+                    cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+    return ok ? v : 152;
+  }();
+  return n;
+}
+
+int64_t host_units(int64_t rows) { return (rows + TU - 1) / TU; }
+int slot_rows_of(int64_t rows) { return rows <= TM ? (int)(2 * rows) : TU; }
+
+template <int D>
+cudaError_t launch_tree_t(const TreeParams& p, const TreeMaps& maps, cudaStream_t s) {
+  static std::atomic<uint64_t> attr{0};
+  cudaError_t e = raise_smem_limit(tree_attn_kernel<D>, TCfg<D>::SMEM, attr);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(tree_attn_kernel<D>, dim3(p.n_cta * p.lanes), dim3(TTHREADS), TCfg<D>::SMEM, s, p, maps);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = (int64_t)p.n_tok * p.Hq;
+  return launch_pdl(tree_merge_kernel<D>, dim3((unsigned)((rows * p.merge_warps + 7) / 8)), dim3(256), 0, s, p);
+}
+
+}  // namespace
+
+// Partials: a slot per CTA and (head, unit), for each lane of CTAs.
+size_t tree_workspace_size(const vc_shape* s, int32_t max_rows) {
+  const int64_t rows = (int64_t)max_rows * (s->Hq / s->Hkv), units = host_units(rows);
+  return (size_t)(tree_sms() + s->B * s->Hkv * units) * slot_rows_of(rows) * (s->d + 1) * sizeof(float) + 256;
+}
+
+cudaError_t launch_tree_attn(const TreeArgs& a, cudaStream_t s, vc_status* st) {
+  TreeParams p;
+  TreeMaps maps;
+  memset(&p, 0, sizeof(p));
+  const int G = a.Hq / a.Hkv;
+  p.kv = a.kv;
+  p.B = a.B;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.G = G;
+  p.n_tok = a.n_tok;
+  p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)a.d));
+  p.dev_status = a.dev_status;
+  const int64_t tiles = ((int64_t)a.kv.max_pages << a.kv.shift) / TN + 1;
+  int64_t cost = 0, units = 0, same = host_units((int64_t)a.req[0].n_rows * G);
+  p.slot_rows = 1;
+  p.least = 1;
+  for (int b = 0; b < a.B; ++b) {
+    p.req[b] = a.req[b];
+    const int64_t rows = (int64_t)a.req[b].n_rows * G, u = host_units(rows);
+    if (u != same || rows - (u - 1) * TU <= TM) same = 1;
+    const int sr = slot_rows_of(rows);
+    p.slot_rows = sr > p.slot_rows ? sr : p.slot_rows;
+    if (rows > TM) p.least = 2;
+    units += u * a.Hkv;
+    cost += 2 * u * a.Hkv * tiles;
+  }
+  // costs are counted in 32 bits
+  if (cost >= INT32_MAX / 2 || units >= INT32_MAX / 2) {
+    *st = VC_ERR_UNSUPPORTED;
+    return cudaSuccess;
+  }
+  const int sms = tree_sms();
+  p.lanes = same > 1 && same <= sms / 2 ? (int)same : 1;
+  p.n_cta = sms / p.lanes;
+  int64_t at = 0;
+  for (int b = 0; b < a.B; ++b) {
+    p.unit_begin[b] = (int32_t)at;
+    at += a.Hkv * (p.lanes > 1 ? 1 : host_units((int64_t)a.req[b].n_rows * G));
+  }
+  p.lane_slots = (int32_t)(p.n_cta + at);
+  const size_t rows = (size_t)p.lanes * p.lane_slots * p.slot_rows;
+  if (!a.ws || (reinterpret_cast<uintptr_t>(a.ws) & 15u) || rows * (a.d + 1) * sizeof(float) > a.ws_bytes) {
+    *st = VC_ERR_WORKSPACE;
+    return cudaSuccess;
+  }
+  p.ws_o = static_cast<float*>(a.ws);
+  p.ws_lse = p.ws_o + rows * a.d;
+  // Warps a row of the merge: a row's partials, about two a CTA that holds part of its unit, by fours (one round
+  // trip each); no more than make a wave of blocks.
+  const int64_t parts = 2 * (1 + p.n_cta / at), out_rows = (int64_t)a.n_tok * a.Hq;
+  p.merge_warps = 1;
+  while (p.merge_warps < 8 && parts > 4 * p.merge_warps && out_rows * p.merge_warps * 2 <= (int64_t)sms * 4 * 8) p.merge_warps *= 2;
+  const int64_t heads = (int64_t)a.kv.n_pages * a.Hkv;
+  if (!page_map(&maps.kv[0], a.kv.k, a.d, 1 << a.kv.shift, heads) || !page_map(&maps.kv[1], a.kv.v, a.d, 1 << a.kv.shift, heads)) {
+    *st = VC_ERR_CUDA;
+    return cudaSuccess;
+  }
+  return a.d == 128 ? launch_tree_t<128>(p, maps, s) : launch_tree_t<64>(p, maps, s);
+}
+
+}  // namespace vc
