@@ -8,6 +8,7 @@ algorithm"). torch is used for memory and streams only.
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass, field
 from typing import List, Optional
 
@@ -18,7 +19,10 @@ from . import (vc_shape, vc_kv_full, vc_kv_comp, vc_draft_req, vc_verify_req, vc
                vc_draft_attn, vc_verify_attn, vc_verify_attn_heads, vc_verify_launches, vc_accept, vc_append_kv, vc_workspace_size,
                vc_rope, vc_rope_req, vc_live_req, vc_evict_req, live_kv, vc_rope_append, vc_prefix_attn,
                vc_prefix_workspace_size, _stream, vc_scored_attn, vc_scored_workspace_size, vc_evict_kv, vc_evict_workspace_size,
-               VC_TOKEN_DROP, VC_QUANT, VC_CALL_DRAFT, VC_CALL_VERIFY)
+               vc_reserve_req, vc_fork_req, vc_trim_req, vc_rope_axes, vc_rope_page_req, vc_tree_req, vc_commit_req, paged_kv,
+               vc_pages_init, vc_pages_reserve, vc_pages_fork, vc_pages_trim, vc_pages_compact, vc_pages_workspace_size,
+               vc_rope_pages, vc_tree_mask, vc_tree_attn, vc_tree_workspace_size, vc_tree_accept, vc_tree_commit,
+               VC_TOKEN_DROP, VC_QUANT, VC_CALL_DRAFT, VC_CALL_VERIFY, VC_MAX_BATCH, VC_TREE_MAX_NODES)
 
 
 @dataclass
@@ -859,3 +863,277 @@ class LiveBatch:
         self.append(q, k, v, rows, stream)
         self.attend(o, rows, stream)
         self.evict(stream)
+
+
+class TreeBatch:
+    """Sequences in one pool of pages that draft trees, chains or single tokens.
+
+    The pool (k, v bf16 [n_pages][Hkv][page][d]) and all that moves while its sequences decode (page
+    tables, lengths, positions, the stack of free pages) live on the device and are read and moved on
+    there, so a turn of fixed sequences and row counts can be captured into a CUDA graph and replayed
+    while the caches grow. `seqs` names the sequences of a call, 0 .. n_seq - 1, at most
+    VC_MAX_BATCH and each once; `rows` the tokens of each, up to max_rows (0: it sits the call out).
+
+    A turn: reserve room, append the tokens' rotated keys and their values behind the context, attend,
+    and commit what was accepted (accept does both ends of that for trees). What the device finds wrong
+    (no pages left, say) lands in dev_status. All calls run on `stream` (the current one by default);
+    like a Batch's, each stream first waits for the construction.
+    """
+
+    def __init__(self, Hq: int, Hkv: int, d: int, n_seq: int, n_pages: int, page: int, axes: vc_rope_axes, max_rows: int = 1,
+                 max_pages: Optional[int] = None, device="cuda"):
+        self.Hq, self.Hkv, self.d, self.n_seq, self.page, self.axes, self.max_rows = Hq, Hkv, d, n_seq, page, axes, max_rows
+        max_pages = n_pages if max_pages is None else max_pages
+        if min(n_seq, n_pages, max_pages, max_rows) < 1 or page not in (16, 32, 64, 128):
+            raise ValueError("n_seq, n_pages, max_pages and max_rows are at least 1, page is 16, 32, 64 or 128")
+        dev = torch.device(device)
+        ints = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=dev)
+        self.k, self.v = (torch.zeros((n_pages, Hkv, page, d), dtype=torch.bfloat16, device=dev) for _ in range(2))
+        self.device = self.k.device  # with its index: the current device may be another one at the next call
+        self.refs, self.free_pages, self.n_free = ints(n_pages), ints(n_pages), ints(1)
+        self.table, self.len, self.held, self.next = ints(n_seq, max_pages), ints(n_seq), ints(n_seq), ints(n_seq)
+        self.dev_status = ints(1)
+        self.kv = paged_kv(self.k, self.v, self.refs, self.free_pages, self.n_free, self.table, self.len, self.held, self.next)
+        most = min(n_seq, VC_MAX_BATCH)
+        shape = self._shape(most)
+        attn, pages = vc_tree_workspace_size(shape, max_rows), vc_pages_workspace_size(shape, self.kv)
+        if attn == 0 or pages == 0:
+            raise ValueError(f"no workspace for Hq {Hq}, Hkv {Hkv}, d {d}, {n_pages} pages of {page} rows, max_rows {max_rows}")
+        self.ws = torch.empty(max(attn, pages), dtype=torch.uint8, device=self.device)
+        self.q_rot = torch.zeros((most, max_rows, Hq, d), dtype=torch.bfloat16, device=self.device)
+        nodes = min(max_rows, VC_TREE_MAX_NODES)
+        self._masks, self._depths = ints(most * nodes * ((nodes + 31) // 32)), ints(most * nodes)
+        with torch.cuda.device(self.device):
+            vc_pages_init(shape, self.kv)
+            self._built = torch.cuda.Event()
+            self._built.record()
+        self._ordered = set()
+
+    def _shape(self, B: int):
+        return vc_shape(B, self.Hq, self.Hkv, self.d)
+
+    _order = LiveBatch._order
+
+    def _check_seqs(self, seqs, rows=None):
+        if not 1 <= len(seqs) <= VC_MAX_BATCH or len(set(seqs)) != len(seqs) or not all(0 <= s < self.n_seq for s in seqs):
+            raise ValueError("seqs: 1 .. VC_MAX_BATCH different sequences of the pool")
+        if rows is not None and (len(rows) != len(seqs) or any(r < 0 or r > self.max_rows for r in rows)):
+            raise ValueError("rows: one count per sequence, 0 .. max_rows")
+
+    def _check_ints(self, t: torch.Tensor, name: str, *shape):
+        if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != self.device:
+            raise ValueError(f"{name} is a contiguous int32 tensor {list(shape)} on the pool's device")
+
+    # ---- pages ----
+    def reserve(self, seqs: List[int], rows: List[int], stream=None):
+        """Room for rows[b] more tokens (any number) of each sequence, in pages that it holds alone."""
+        self._check_seqs(seqs)
+        if len(rows) != len(seqs) or any(not 0 <= r < 2 ** 31 for r in rows):
+            raise ValueError("rows: one count per sequence, not negative")
+        arr = (vc_reserve_req * len(seqs))(*[vc_reserve_req(s, r) for s, r in zip(seqs, rows)])
+        with torch.cuda.device(self.device):
+            self._order(stream)
+            vc_pages_reserve(self._shape(len(seqs)), self.kv, arr, self.ws, self.dev_status, stream)
+
+    def fork(self, pairs, stream=None):
+        """pairs: (source, empty sequence that becomes its copy), at most VC_MAX_BATCH; the pages are shared."""
+        if not 1 <= len(pairs) <= VC_MAX_BATCH or not all(0 <= s < self.n_seq for p in pairs for s in p):
+            raise ValueError("pairs: 1 .. VC_MAX_BATCH of sequences of the pool")
+        if len({b for _, b in pairs}) != len(pairs) or {a for a, _ in pairs} & {b for _, b in pairs}:
+            raise ValueError("each sequence is copied into once, and none that is copied")
+        arr = (vc_fork_req * len(pairs))(*[vc_fork_req(a, b) for a, b in pairs])
+        with torch.cuda.device(self.device):
+            self._order(stream)
+            vc_pages_fork(self._shape(len(pairs)), self.kv, arr, self.dev_status, stream)
+
+    def trim(self, seqs: List[int], rows: Optional[List[int]] = None, next: Optional[List[int]] = None, stream=None):
+        """Cut each sequence to rows[b] tokens (none by default: it is freed), its next token's position then
+        next[b] (rows[b] by default), and give back the pages behind them. INT32_MAX rows: only the pages
+        reserved and not used."""
+        self._check_seqs(seqs)
+        rows = [0] * len(seqs) if rows is None else rows
+        next = rows if next is None else next
+        if len(rows) != len(seqs) or len(next) != len(seqs) or any(not 0 <= r < 2 ** 31 for r in rows) or \
+                any(not -2 ** 31 <= p < 2 ** 31 for p in next):
+            raise ValueError("rows and next: one per sequence, int32, rows not negative")
+        arr = (vc_trim_req * len(seqs))(*[vc_trim_req(*x) for x in zip(seqs, rows, next)])
+        with torch.cuda.device(self.device):
+            self._order(stream)
+            vc_pages_trim(self._shape(len(seqs)), self.kv, arr, self.dev_status, stream)
+
+    def compact(self, stream=None):
+        """The pages in use moved to the front of the pool."""
+        with torch.cuda.device(self.device):
+            self._order(stream)
+            vc_pages_compact(self._shape(1), self.kv, self.ws, self.dev_status, stream)
+
+    # ---- a turn ----
+    def append(self, seqs: List[int], q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rows: List[int],
+               off: Optional[torch.Tensor] = None, stream=None):
+        """The next rows[b] tokens of every sequence: q bf16 [B][R][Hq][d], k and v bf16 [B][R][Hkv][d],
+        R >= max(rows), any stride between tokens that keeps them apart (slices of a fused projection).
+        off int32: positions from the sequence's next one on, [B][R] the same on every axis (the depths of a
+        tree), or [B][n_axes][R]; one after the other by default. Rotated queries land in q_rot[b]."""
+        self._check_seqs(seqs, rows)
+        B, R = len(seqs), q.shape[1] if q.dim() == 4 else -1
+        if max(rows) > R:
+            raise ValueError("rows: no more than the tokens given")
+        for t, heads in ((q, self.Hq), (k, self.Hkv), (v, self.Hkv)):
+            if t.dtype != torch.bfloat16 or tuple(t.shape) != (B, R, heads, self.d) or t.stride(3) != 1 or \
+                    (heads > 1 and t.stride(2) != self.d) or t.device != self.device:
+                raise ValueError("q, k and v are bf16 [B][R][heads][d] on the pool's device, each token's heads contiguous")
+            if max(rows) > 1 and t.stride(1) < heads * self.d:  # an expanded tensor's 0 would mean packed tokens
+                raise ValueError("the tokens of q, k and v do not overlap: a stride of heads * d or more between them")
+        several = off is not None and off.dim() == 3
+        if off is not None:
+            self._check_ints(off, "off", *((B, self.axes.n_axes, R) if several else (B, R)))
+        strides = (q.stride(1), k.stride(1), v.stride(1)) if max(rows) > 1 else (0, 0, 0)
+        arr = (vc_rope_page_req * B)()
+        for b, e in enumerate(arr):
+            e.q, e.k, e.v = q[b].data_ptr(), k[b].data_ptr(), v[b].data_ptr()
+            e.q_stride, e.k_stride, e.v_stride = strides
+            e.off, e.off_stride = (None, 0) if off is None else (off[b].data_ptr(), R if several else 0)
+            e.q_out, e.seq, e.n_rows = self.q_rot[b].data_ptr(), seqs[b], rows[b]
+        with torch.cuda.device(self.device):
+            self._order(stream)
+            vc_rope_pages(self._shape(B), self.axes, self.kv, arr, self.dev_status, stream)
+
+    def attend(self, seqs: List[int], o: torch.Tensor, rows: List[int], mask: Optional[torch.Tensor] = None, stream=None):
+        """Attention of the rows just appended, into o bf16 [B][R][Hq][d], R >= max(rows). mask int32 [B][R'][words],
+        R' >= max(rows): the tokens that each sees (tree_mask's); by default those up to itself."""
+        self._check_out(seqs, o, rows)
+        if mask is not None:
+            self._check_ints(mask, "mask", *mask.shape)
+            if mask.dim() != 3 or mask.shape[0] != len(seqs) or mask.shape[1] < max(rows) or mask.shape[2] * 32 < max(rows):
+                raise ValueError("mask is [B][R][words], a row and a bit for each token")
+        arr = (vc_tree_req * len(seqs))()
+        for b, e in enumerate(arr):
+            e.q, e.o, e.seq, e.n_rows = self.q_rot[b].data_ptr(), o[b].data_ptr(), seqs[b], rows[b]
+            if mask is not None:
+                e.mask, e.mask_words = mask[b].data_ptr(), mask.shape[2]
+        with torch.cuda.device(self.device):
+            self._order(stream)
+            vc_tree_attn(self._shape(len(seqs)), self.kv, arr, self.ws, self.dev_status, stream)
+
+    def _check_out(self, seqs, o, rows):
+        self._check_seqs(seqs, rows)
+        if o.dtype != torch.bfloat16 or o.dim() != 4 or o.shape[0] != len(seqs) or o.shape[1] < max(rows) or \
+                tuple(o.shape[2:]) != (self.Hq, self.d) or not o[0].is_contiguous() or o.device != self.device:
+            raise ValueError("o is bf16 [B][R][Hq][d] on the pool's device, R >= max(rows), each sequence's rows contiguous")
+        if sum(r > 0 for r in rows) > 1 and o.stride(0) < max(rows) * self.Hq * self.d:
+            raise ValueError("each sequence's rows of o are its own")
+        if any(r > 0 and (o.data_ptr() + 2 * b * o.stride(0)) % 16 for b, r in enumerate(rows)):
+            raise ValueError("each sequence's rows of o start on a 16-byte boundary")
+
+    def commit(self, seqs: List[int], rows: List[int], path: Optional[torch.Tensor] = None,
+               n_acc: Optional[torch.Tensor] = None, advance: Optional[List[int]] = None, stream=None):
+        """Of the rows[b] tokens appended, those of path int32 [B][R] (its first n_acc[b], int32 [B]) become context,
+        moved together; all of them as they lie without a path. The next position moves on by as many, or by
+        advance[b] >= 0 (image tokens that share positions)."""
+        self._check_seqs(seqs, rows)
+        if path is not None:
+            self._check_ints(path, "path", len(seqs), *path.shape[1:])
+            if path.dim() != 2 or path.shape[1] < max(rows):
+                raise ValueError("path is [B][R], R >= max(rows)")
+        if n_acc is not None:
+            self._check_ints(n_acc, "n_acc", len(seqs))
+        if advance is not None and (len(advance) != len(seqs) or any(not 0 <= a < 2 ** 31 for a in advance)):
+            raise ValueError("advance: one count per sequence, not negative")
+        arr = (vc_commit_req * len(seqs))()
+        for b, e in enumerate(arr):
+            e.path = None if path is None else path[b].data_ptr()
+            e.n_acc = None if n_acc is None else n_acc[b:].data_ptr()
+            e.seq, e.n_rows, e.advance = seqs[b], rows[b], -1 if advance is None else advance[b]
+        with torch.cuda.device(self.device):
+            self._order(stream)
+            vc_tree_commit(self._shape(len(seqs)), self.kv, arr, self.dev_status, stream)
+
+    def step(self, seqs: List[int], q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+             rows: Optional[List[int]] = None, parent: Optional[torch.Tensor] = None, n_nodes: Optional[torch.Tensor] = None,
+             stream=None):
+        """Reserve, append and attend for the next tokens of each sequence. Without parent: one token each by default, or
+        a chain, committed at once. With parent int32 [B][R] and n_nodes int32 [B] (rows, on the device): trees, whose
+        tokens stay behind the context until accept commits the path that the full pass agrees with."""
+        rows = [1] * len(seqs) if rows is None else rows
+        self._check_out(seqs, o, rows)  # before the caches move on
+        mask = depth = None
+        if parent is not None:
+            B, N = _check_trees(n_nodes, parent)
+            if B != len(seqs) or not max(rows) <= N <= self.max_rows or parent.device != self.device:
+                raise ValueError("parent is [B][R] on the pool's device, max(rows) <= R <= max_rows")
+            W = (N + 31) // 32
+            mask, depth = self._masks[: B * N * W].view(B, N, W), self._depths[: B * N].view(B, N)
+            with torch.cuda.device(self.device):
+                self._order(stream)
+                tree_mask(parent, n_nodes, mask, depth, stream)
+        self.reserve(seqs, rows, stream)
+        self.append(seqs, q, k, v, rows, depth, stream)
+        self.attend(seqs, o, rows, mask, stream)
+        if parent is None:
+            self.commit(seqs, rows, stream=stream)
+
+    def accept(self, seqs: List[int], logits: torch.Tensor, token: torch.Tensor, parent: torch.Tensor, n_nodes: torch.Tensor,
+               rows: List[int], stream=None):
+        """The longest path of each tree that the full pass agrees with (accept_tree) becomes context. Returns
+        (out_tokens, path, n_acc)."""
+        self._check_seqs(seqs, rows)
+        for t, name in ((token, "token"), (parent, "parent")):
+            self._check_ints(t, name, len(seqs), logits.shape[1])
+        if logits.shape[0] != len(seqs) or logits.shape[1] < max(rows):
+            raise ValueError("logits are [B][R][V], R >= max(rows)")
+        with torch.cuda.device(self.device):
+            self._order(stream)
+            out, path, n_acc = accept_tree(logits, token, parent, n_nodes, stream=stream)
+        self.commit(seqs, rows, path, n_acc, stream=stream)
+        return out, path, n_acc
+
+
+def _on(stream, device):
+    """A context that allocates for `stream`: memory given back is then reused in its order, not the current one's."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device))
+
+
+def _check_trees(n_nodes, *trees):
+    if any(t.dim() != 2 for t in trees):
+        raise ValueError("parent and token are [B][N]")
+    B, N = trees[0].shape
+    for t, shape in [(t, (B, N)) for t in trees] + [(n_nodes, (B,))]:
+        if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != trees[0].device:
+            raise ValueError("parent and token are contiguous int32 [B][N], n_nodes int32 [B], on one device")
+    return B, N
+
+
+def tree_mask(parent: torch.Tensor, n_nodes: torch.Tensor, mask=None, depth=None, stream=None):
+    """Ancestor bits int32 [B][N][ceil(N / 32)] and depths int32 [B][N] of the trees parent int32 [B][N]."""
+    B, N = _check_trees(n_nodes, parent)
+    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=parent.device)
+    with torch.cuda.device(parent.device):
+        with _on(stream, parent.device):
+            mask = new(B, N, (N + 31) // 32) if mask is None else mask
+            depth = new(B, N) if depth is None else depth
+        for t, shape in ((mask, (B, N, (N + 31) // 32)), (depth, (B, N))):
+            if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != parent.device:
+                raise ValueError("mask is contiguous int32 [B][N][ceil(N / 32)], depth [B][N], beside the trees")
+        vc_tree_mask(B, N, parent, n_nodes, mask, depth, stream)
+    return mask, depth
+
+
+def accept_tree(logits: torch.Tensor, token: torch.Tensor, parent: torch.Tensor, n_nodes: torch.Tensor, out_tokens=None,
+                path=None, n_acc=None, stream=None):
+    """Greedy acceptance along each tree: logits fp32 [B][N][V], token and parent int32 [B][N]. Returns out_tokens and path
+    int32 [B][N] (-1 behind) and n_acc int32 [B]."""
+    B, N = _check_trees(n_nodes, token, parent)
+    if logits.dtype != torch.float32 or logits.dim() != 3 or tuple(logits.shape[:2]) != (B, N) or not logits.is_contiguous() or \
+            logits.device != token.device:
+        raise ValueError("logits are contiguous fp32 [B][N][V] beside the trees")
+    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=logits.device)
+    with torch.cuda.device(logits.device):
+        with _on(stream, logits.device):
+            out_tokens = new(B, N) if out_tokens is None else out_tokens
+            path = new(B, N) if path is None else path
+            n_acc = new(B) if n_acc is None else n_acc
+        _check_trees(n_acc, token, out_tokens, path)
+        vc_tree_accept(B, N, logits.shape[2], logits, token, parent, n_nodes, out_tokens, path, n_acc, stream)
+    return out_tokens, path, n_acc
