@@ -42,16 +42,22 @@ constexpr int TTHREADS = 512;
 constexpr int TREG_SOFTMAX = 144, TREG_ISSUE = 80;
 static_assert(256 * (TREG_SOFTMAX + TREG_ISSUE) <= 65536, "no more than the block was launched with");
 
+// The kernel for few rows: 4 warps a CTA, 3 CTAs an SM (2 * 4 * 8 KB of shared memory each at 128 channels)
+constexpr int FR = 16;          // query rows at most
+constexpr int FK = 16;          // keys of a chunk
+constexpr int FWARPS = 4, FCTAS = 3;
+
 struct TreeParams {
   PagedDev kv;
   TreeReqDev req[VC_MAX_BATCH];
   int32_t unit_begin[VC_MAX_BATCH];  // first (head, unit) of each request; with lanes: head alone
   int32_t B, Hq, Hkv, G, n_tok;
+  int32_t few;                       // 1: the kernel for few rows, whose tiles are chunks and whose CTAs are warps
   int32_t lanes;                     // units of every head, each with CTAs of its own (c % lanes); 1: in one sequence
   int32_t n_cta;                     // CTAs of a lane
   int32_t least;                     // cost of the dearest tile: no CTA's range is shorter
   int32_t lane_slots, slot_rows;     // partial slots of a lane, rows of a slot
-  int32_t merge_warps;               // warps a row of the merge
+  int32_t merge_warps;               // warps a row of the merge, 0: several rows a warp
   float* ws_o;                       // [lanes][lane_slots][slot_rows][d]; slot = CTA of the lane + (head, unit)
   float* ws_lse;                     // [lanes][lane_slots][slot_rows], log2 domain, -inf: saw nothing
   float scale_log2;
@@ -73,8 +79,9 @@ __device__ __forceinline__ int units_of(int rows) { return (rows + TU - 1) / TU;
 // A tile of all units of a head that stand in one sequence.
 __device__ __forceinline__ int tile_cost(const TreeParams& p, int rows) {
   const int u = units_of(rows);
-  return p.lanes > 1 ? 2 : 2 * u - (rows - (u - 1) * TU <= TM ? 1 : 0);
+  return p.few ? 1 : p.lanes > 1 ? 2 : 2 * u - (rows - (u - 1) * TU <= TM ? 1 : 0);
 }
+__device__ __forceinline__ int tiles_of(const TreeParams& p, int n) { return p.few ? (n + FK - 1) / FK : (n + TN - 1) / TN; }
 
 __device__ __forceinline__ void tree_plan(const TreeParams& p, TreePlan* s, int lane, bool tell) {
   int n = 0, ctx = 0, cost = 0;
@@ -84,7 +91,7 @@ __device__ __forceinline__ void tree_plan(const TreeParams& p, TreePlan* s, int 
     ctx = min(max(len, 0), cap);
     n = (int)min((int64_t)cap, (int64_t)ctx + r.n_rows);
     if (tell && (ctx != len || n - ctx != r.n_rows)) set_status(p.dev_status, VC_DEV_PAGES);
-    cost = p.Hkv * ((n + TN - 1) / TN) * tile_cost(p, r.n_rows * p.G);
+    cost = p.Hkv * tiles_of(p, n) * tile_cost(p, r.n_rows * p.G);
   }
   int end = cost;
 #pragma unroll
@@ -749,12 +756,305 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
   if (warp == 12) tc05::dealloc(tmem, C::TCOLS);
 }
 
+// ---- few rows ---------------------------------------------------------------------------------------
+// Up to 16 query rows of a KV head (single tokens, small trees): bound by reading K and V, so each warp works for
+// itself, without a barrier: it takes an equal range of the chunks [request][head][16 keys], has three half chunks
+// (K or V) on their way with 16-byte asynchronous copies into its own ring, and multiplies with mma.sync: S = Q K^T
+// with Q in registers, P from S's accumulators as they lie, O += P V. The tcgen05 kernel's fixed part (tensor maps,
+// TMEM, barriers, two chains' start and end) is what this one does without, and a page of 16 rows is as good as a
+// larger one, where TMA boxes of 2 KB hold the other at 0.75 of the copy rate.
+template <int D>
+struct FCfg {
+  static constexpr int HALF = FK * D * 2;             // bytes of a chunk's K or V
+  static constexpr int SMEM = FWARPS * 4 * HALF;      // two chunks a warp
+};
+
+// Bits of the 16 keys from k0 on that row i of a request's tokens sees; node = k0 - ctx > -16.
+__device__ __forceinline__ uint32_t few_bits(const uint32_t* row, int words, bool masked, int tok, int node, int left) {
+  uint32_t x;
+  if (!masked) {
+    const int last = tok - node;  // of the chunk's keys
+    x = last >= 15 ? 0xffffu : last < 0 ? 0u : (2u << last) - 1u;
+  } else {
+    auto word = [&](int i) { return row && i < words ? __ldg(row + i) : 0u; };
+    if (node >= 0)
+      x = __funnelshift_r(word(node >> 5), (node & 31) > 16 ? word((node >> 5) + 1) : 0u, node & 31);
+    else
+      x = word(0) << -node | ((1u << -node) - 1u);
+  }
+  return x & (left < 16 ? (1u << left) - 1u : 0xffffu);
+}
+
+template <int D>
+__global__ void __launch_bounds__(FWARPS * 32, FCTAS) tree_few_kernel(const __grid_constant__ TreeParams p) {
+  using C = FCfg<D>;
+  constexpr int PC = D / 8;  // 16-byte pieces of a row
+  extern __shared__ __align__(128) uint8_t few_smem[];
+  __shared__ TreePlan plan;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (warp == 0) tree_plan(p, &plan, lane, blockIdx.x == 0);
+  __syncthreads();
+  const int wid = warp * gridDim.x + blockIdx.x;  // the first ones on different SMs
+  if (wid >= plan.ctas) return;
+  uint8_t* ring = few_smem + warp * 4 * C::HALF;  // K of chunk 0, V of chunk 0, K of chunk 1, V of chunk 1
+  const int beg = cta_begin(plan, wid), end = cta_begin(plan, wid + 1);
+  int g = 0;
+  for (int b = 1; b < p.B; ++b)  // as in tree_first
+    if (plan.cost_begin[b] <= beg) g = b;
+  int rem = beg - plan.cost_begin[g], tiles = tiles_of(p, plan.n[g]);
+  int hk = rem / tiles;
+  rem -= hk * tiles;
+  const int qrow = lane >> 2, qcol = 2 * (lane & 3);
+  // where this lane's pieces of a half chunk lie in it: row lane / PC + i * 32 / PC
+  constexpr int RS = 32 / PC;  // rows a load of the warp
+  const int prow = lane / PC, pcol = lane % PC;
+  for (int at = beg; at < end;) {
+    const TreeReqDev& R = p.req[g];
+    const int n = plan.n[g], ctx = plan.ctx[g], j0 = rem, j1 = min(tiles, rem + end - at), rows = R.n_rows * p.G;
+    const int32_t* table = p.kv.pages_of(R.seq);
+    // pages of the chunks jb .. jb + 31, a lane each; those that are not the pool's count as none
+    auto look = [&](int jb) {
+      int page = -1;
+      if (jb + lane < j1) {
+        page = __ldg(table + (((jb + lane) * FK) >> p.kv.shift));
+        if (!p.kv.has_page(page)) {
+          set_status(p.dev_status, VC_DEV_PAGES);
+          page = -1;
+        }
+      }
+      return page;
+    };
+    int pages = look(j0), more = look(j0 + 32);  // those in use and the next ones
+    // half chunk `v` (0: K, 1: V) of chunk j into its place; one commit whether there is one or not
+    auto load = [&](int j, int v) {
+      const int page = __shfl_sync(0xffffffffu, pages, (j - j0) & 31);
+      if (j < j1) {
+        const int k0 = j * FK;
+        uint8_t* dst = ring + ((j - j0) & 1) * 2 * C::HALF + v * C::HALF;
+        const bf16* src = (v ? p.kv.v : p.kv.k) +
+                          ((((int64_t)max(page, 0) * p.Hkv + hk) << p.kv.shift) + (k0 & (p.kv.rows() - 1))) * D + prow * D + pcol * 8;
+#pragma unroll
+        for (int i = 0; i < FK / RS; ++i) {
+          const int r = prow + i * RS;
+          cp_async16(dst + r * D * 2 + (((pcol & 8) | ((pcol ^ r) & 7)) << 4), src + i * RS * D, page >= 0 && k0 + r < n ? 16 : 0);
+        }
+      }
+      cp_async_commit();
+    };
+    load(j0, 0);
+    load(j0, 1);
+    load(j0 + 1, 0);
+    load(j0 + 1, 1);
+    // Q in A-fragment order: rows qrow and qrow + 8, channels 16 kk + qcol (+ 8)
+    uint32_t qf[D / 16][4];
+    int tok[2];
+    const uint32_t* mrow[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = qrow + 8 * e;
+      tok[e] = r < rows ? r / p.G : 0;
+      mrow[e] = R.mask && r < rows ? R.mask + (size_t)tok[e] * R.mask_words : nullptr;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(R.q + ((size_t)tok[e] * p.Hq + hk * p.G + (r - tok[e] * p.G)) * D + qcol);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qf[kk][e] = r < rows ? __ldcg(src + kk * 8) : 0u;
+        qf[kk][2 + e] = r < rows ? __ldcg(src + kk * 8 + 4) : 0u;
+      }
+    }
+    const int blind = R.mask ? ctx : ctx + 1;  // the first key that some row may not see
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, acc[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+#pragma unroll 1
+    for (int j = j0; j < j1; ++j) {
+      const int k0 = j * FK;
+      uint8_t* sK = ring + ((j - j0) & 1) * 2 * C::HALF;
+      uint8_t* sV = sK + C::HALF;
+      cp_async_wait<3>();  // K of this chunk is there: behind it its V and the next chunk's
+      __syncwarp();
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      {
+        const int key = ((lane >> 4) << 3) + (lane & 7);
+        const uint8_t* row = sK + key * D * 2;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const int c = 2 * kk + ((lane >> 3) & 1);
+          uint32_t b[4];
+          ldsm_x4(b[0], b[1], b[2], b[3], row + (((c & 8) | ((c ^ key) & 7)) << 4));
+          mma_bf16_16816(s[0], qf[kk], b[0], b[1]);
+          mma_bf16_16816(s[1], qf[kk], b[2], b[3]);
+        }
+      }
+      __syncwarp();  // K has been read by all
+      if (((j - j0 + 2) & 31) == 0) pages = more;
+      load(j + 2, 0);
+      uint32_t see[2] = {0xffffu, 0xffffu};
+      const bool tail = k0 + FK > min(blind, n);
+      if (tail) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          see[e] = few_bits(mrow[e], R.mask_words, R.mask != nullptr, tok[e], k0 - ctx, n - k0);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (!((see[e] >> (8 * t + qcol + i)) & 1u)) s[t][2 * e + i] = -INFINITY;
+        }
+      }
+      // the running maximum moves when it is passed by more than 2^8 (or from -infinity), for the warp together
+      float top[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        top[e] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2)) * p.scale_log2;
+      }
+      if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float was = m[e];
+          if (top[e] > was + 8.f) m[e] = top[e];
+          const float f = was == m[e] ? 1.f : ex2_approx(was - m[e]);
+          l[e] *= f;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            acc[i][2 * e] *= f;
+            acc[i][2 * e + 1] *= f;
+          }
+        }
+      }
+      // P = 2^(s scale - m), rounded to bf16 for the product with V (its range is not fp16's); sums take it unrounded
+      uint32_t pf[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float mu = m[e] == -INFINITY ? 0.f : m[e];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float a = ex2_approx(fmaf(s[t][2 * e], p.scale_log2, -mu)), b = ex2_approx(fmaf(s[t][2 * e + 1], p.scale_log2, -mu));
+          l[e] += a + b;
+          pf[2 * t + e] = pack_bf16x2(a, b);
+        }
+      }
+      cp_async_wait<3>();  // V of this chunk
+      __syncwarp();
+      bool odd = false;
+      if (tail) {  // a value row that is not finite, and not for all
+#pragma unroll
+        for (int i = 0; i < FK / RS; ++i) {
+          const uint4 v = *reinterpret_cast<const uint4*>(sV + (i * 32 + lane) * 16);
+          odd |= broken_bf16x2(v.x) || broken_bf16x2(v.y) || broken_bf16x2(v.z) || broken_bf16x2(v.w);
+        }
+        odd = __any_sync(0xffffffffu, odd);
+      }
+      if (!odd) {
+        const int key = (((lane >> 3) & 1) << 3) + (lane & 7);
+        const uint8_t* row = sV + key * D * 2;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const int c = 2 * i + (lane >> 4);
+          uint32_t b[4];
+          ldsm_x4_t(b[0], b[1], b[2], b[3], row + (((c & 8) | ((c ^ key) & 7)) << 4));
+          mma_bf16_16816(acc[2 * i], pf, b[0], b[1]);
+          mma_bf16_16816(acc[2 * i + 1], pf, b[2], b[3]);
+        }
+      } else {  // the keys that a row sees, one by one
+#pragma unroll 1
+        for (int k = 0; k < FK; ++k) {
+          const int from = (lane & ~3) | ((k & 7) >> 1);
+          float w[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t x = __shfl_sync(0xffffffffu, k < 8 ? pf[e] : pf[2 + e], from);
+            w[e] = __uint_as_float(k & 1 ? x & 0xffff0000u : x << 16);
+          }
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(sV + k * D * 2 + (((i & 8) | ((i ^ k) & 7)) << 4) + qcol * 2);
+            const float lo = __uint_as_float(v << 16), hi = __uint_as_float(v & 0xffff0000u);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if ((see[e] >> k) & 1u) {
+                acc[i][2 * e] = fmaf(w[e], lo, acc[i][2 * e]);
+                acc[i][2 * e + 1] = fmaf(w[e], hi, acc[i][2 * e + 1]);
+              }
+          }
+        }
+      }
+      __syncwarp();
+      load(j + 2, 1);
+      if (((j - j0 + 2) & 31) == 0) more = look(j + 2 + 32);
+    }
+    cp_async_wait<0>();
+    // the range's partial of this head: four lanes hold 8 neighbouring channels of a row
+    const size_t part = ((size_t)wid + p.unit_begin[g] + hk) * p.slot_rows;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      const int r = qrow + 8 * e;
+      if (r < rows) {
+        const float inv = l[e] != 0.f ? 1.f / l[e] : 0.f;
+        float* dst = p.ws_o + (part + r) * D + qcol;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          *reinterpret_cast<float2*>(dst + 8 * i) = make_float2(acc[i][2 * e] * inv, acc[i][2 * e + 1] * inv);
+        if ((lane & 3) == 0) p.ws_lse[part + r] = l[e] != 0.f ? m[e] + log2f(l[e]) : -INFINITY;
+      }
+    }
+    __syncwarp();
+    at += j1 - j0;
+    rem = 0;
+    if (++hk == p.Hkv && at < end) {
+      hk = 0;
+      do ++g;
+      while (plan.n[g] == 0);
+      tiles = tiles_of(p, plan.n[g]);
+    }
+  }
+}
+
+// ---- merge ------------------------------------------------------------------------------------------
 // Weight of a partial beside the largest lse M: 0 where it saw nothing; M stays -inf only beside a NaN.
 __device__ __forceinline__ float part_weight(float l, float M) { return l == -INFINITY ? 0.f : M == -INFINITY ? NAN : exp2f(l - M); }
 
-// Merge: one to eight warps per (token, query head), o = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M) over its
-// partials: a lane per partial takes the weights, then the warp adds up the partials' channels, four loads in
-// flight.
+// Where a row's unit left its partials: `count` of them, number i at at(i); a split unit has two a slot.
+struct TParts {
+  size_t base;
+  int count, stride, second;  // stride: a slot's rows; second: rows to the slot's second partial, 0: none
+  __device__ __forceinline__ size_t at(int i) const {
+    return second ? base + (size_t)(i >> 1) * stride + (i & 1) * second : base + (size_t)i * stride;
+  }
+};
+
+// Output row `id` of the call (token, query head): its partials and its place.
+template <int D>
+__device__ __forceinline__ TParts tree_parts(const TreeParams& p, const TreePlan& plan, int64_t id, bf16*& dst) {
+  const int tok = (int)(id / p.Hq), hq = (int)(id - (int64_t)tok * p.Hq), hk = hq / p.G;
+  int b = 0;
+  for (int i = 1; i < p.B; ++i)
+    if (p.req[i].tok_begin <= tok) b = i;
+  const TreeReqDev& R = p.req[b];
+  const int i = tok - R.tok_begin, r = i * p.G + hq - hk * p.G;  // token of the request, row of the head
+  dst = R.o + ((size_t)i * p.Hq + hq) * D;
+  const int rows = R.n_rows * p.G, u = p.few ? 0 : r / TU, in_unit = min(TU, rows - u * TU);
+  const int cost = p.few || in_unit <= TM ? 1 : 2, tiles = tiles_of(p, plan.n[b]);
+  TParts q{0, 0, p.slot_rows, !p.few && cost == 1 ? in_unit : 0};
+  if (tiles == 0) return q;
+  const int at = plan.cost_begin[b] + hk * tiles * tile_cost(p, rows) + (p.lanes > 1 ? 0 : u * 2 * tiles);
+  const int c0 = cta_of(plan, at), c1 = cta_of(plan, at + cost * (tiles - 1));  // of its first and last tile
+  const int unit = p.unit_begin[b] + (p.lanes > 1 || p.few ? hk : hk * units_of(rows) + u);
+  q.count = (c1 - c0 + 1) * (q.second ? 2 : 1);
+  q.base = ((size_t)(p.lanes > 1 ? u : 0) * p.lane_slots + c0 + unit) * p.slot_rows + (r - u * TU);
+  return q;
+}
+
+// Merge, o = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M) over a row's partials. Few rows of many partials: one to
+// eight warps a row, a lane per partial takes the weights, then the warp adds up the partials' channels, four loads
+// in flight.
 template <int D>
 __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constant__ TreeParams p) {
   constexpr int E = D / 32;  // channels a lane
@@ -766,40 +1066,22 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
   const int wpr = p.merge_warps, part = warp % wpr;  // warps of a row, this one among them
   const int64_t id = (int64_t)blockIdx.x * (8 / wpr) + warp / wpr;
   const bool live = id < (int64_t)p.n_tok * p.Hq;
-  const int tok = live ? (int)(id / p.Hq) : 0, hq = live ? (int)(id - (int64_t)tok * p.Hq) : 0, hk = hq / p.G;
-  int b = 0;
-  for (int i = 1; i < p.B; ++i)
-    if (p.req[i].tok_begin <= tok) b = i;
-  const TreeReqDev& R = p.req[b];
-  const int i = tok - R.tok_begin, r = i * p.G + hq - hk * p.G;  // token of the request, row of the head
   pdl_launch_dependents();
   pdl_wait();
   if (warp == 0) tree_plan(p, &plan, lane, false);
   __syncthreads();
-  // where the row's unit left its partials: `count` of them, number k at at(k); a split unit has two a slot
-  const int rows = R.n_rows * p.G, u = r / TU, in_unit = min(TU, rows - u * TU), cost = in_unit <= TM ? 1 : 2;
-  const int tiles = (plan.n[b] + TN - 1) / TN;
-  int count = 0, second = cost == 1 ? in_unit : 0;
-  size_t base = 0;
-  if (live && tiles > 0) {
-    const int at = plan.cost_begin[b] + hk * tiles * tile_cost(p, rows) + (p.lanes > 1 ? 0 : u * 2 * tiles);
-    const int c0 = cta_of(plan, at), c1 = cta_of(plan, at + cost * (tiles - 1));  // of its first and last tile
-    count = (c1 - c0 + 1) * (second ? 2 : 1);
-    const int unit = p.unit_begin[b] + (p.lanes > 1 ? hk : hk * units_of(rows) + u);
-    base = ((size_t)(p.lanes > 1 ? u : 0) * p.lane_slots + c0 + unit) * p.slot_rows + (r - u * TU);
-  }
-  auto index = [&](int k) {
-    return second ? base + (size_t)(k >> 1) * p.slot_rows + (k & 1) * second : base + (size_t)k * p.slot_rows;
-  };
-  auto lse_of = [&](int k, int end) { return k >= end ? -INFINITY : p.ws_lse[index(k)]; };
+  TParts q{0, 0, 0, 0};
+  bf16* dst = nullptr;
+  if (live) q = tree_parts<D>(p, plan, id, dst);
+  auto lse_of = [&](int k, int end) { return k >= end ? -INFINITY : p.ws_lse[q.at(k)]; };
   float M = -INFINITY;
-  for (int k0 = 0; k0 < count; k0 += 32) M = fmaxf(M, lse_of(k0 + lane, count));
+  for (int k0 = 0; k0 < q.count; k0 += 32) M = fmaxf(M, lse_of(k0 + lane, q.count));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   float L = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  const int beg = count * part / wpr, end = count * (part + 1) / wpr;
+  const int beg = q.count * part / wpr, end = q.count * (part + 1) / wpr;
   for (int k0 = beg; k0 < end; k0 += 32) {
     const float l = lse_of(k0 + lane, end), f = part_weight(l, M);
     const unsigned wrote = __ballot_sync(0xffffffffu, l != -INFINITY);
@@ -813,7 +1095,7 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
 #pragma unroll
         for (int e = 0; e < E; ++e) v[c][e] = 0.f;
         if ((wrote >> (c0 + c)) & 1u) {  // a partial that saw nothing was not written
-          const float* src = p.ws_o + index(k0 + c0 + c) * D + lane * E;
+          const float* src = p.ws_o + q.at(k0 + c0 + c) * D + lane * E;
           if constexpr (E == 4)
             *reinterpret_cast<float4*>(v[c]) = __ldcg(reinterpret_cast<const float4*>(src));
           else
@@ -842,7 +1124,7 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
   }
   if (!live) return;
   const float inv = L != 0.f ? 1.f / L : 0.f;
-  bf16* dst = R.o + ((size_t)i * p.Hq + hq) * D + lane * E;
+  dst += lane * E;
   uint32_t out[E / 2];
 #pragma unroll
   for (int e = 0; e < E / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
@@ -850,6 +1132,68 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
     *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
   else
     *reinterpret_cast<uint32_t*>(dst) = out[0];
+}
+
+// Many rows of few partials: TSUB lanes a row, four rows a warp side by side, one wave of blocks that go through the
+// rows (each lays the plan down once).
+constexpr int TSUB = 8;
+template <int D>
+__global__ void __launch_bounds__(256, 4) tree_merge_rows_kernel(const __grid_constant__ TreeParams p) {
+  constexpr int Q = D / 4 / TSUB;  // float4 a lane: number sl, sl + TSUB, ... of the row
+  __shared__ TreePlan plan;
+  const int lane = threadIdx.x & 31, sl = lane % TSUB, first = lane - sl;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (threadIdx.x < 32) tree_plan(p, &plan, lane, false);
+  __syncthreads();
+  const int64_t all = (int64_t)p.n_tok * p.Hq;
+  for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w * (32 / TSUB) < all; w += (int64_t)gridDim.x * 8) {
+    const int64_t id = w * (32 / TSUB) + lane / TSUB;
+    const bool live = id < all;
+    TParts q{0, 0, 0, 0};
+    bf16* dst = nullptr;
+    if (live) q = tree_parts<D>(p, plan, id, dst);
+    const int most = __reduce_max_sync(0xffffffffu, q.count);
+    auto lse_of = [&](int k) { return k >= q.count ? -INFINITY : p.ws_lse[q.at(k)]; };
+    const float l0 = lse_of(sl);  // most rows have no more than a lane each
+    float M = l0;
+    for (int k0 = TSUB; k0 < most; k0 += TSUB) M = fmaxf(M, lse_of(k0 + sl));
+#pragma unroll
+    for (int off = TSUB / 2; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float L = 0.f;
+    float4 acc[Q];
+#pragma unroll
+    for (int i = 0; i < Q; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < most; k0 += TSUB) {
+      const float l = k0 ? lse_of(k0 + sl) : l0, f = part_weight(l, M);
+      const unsigned wrote = __ballot_sync(0xffffffffu, l != -INFINITY) >> first;
+      L += f;
+      const int cnt = min(TSUB, most - k0);
+#pragma unroll 2
+      for (int c = 0; c < cnt; ++c) {
+        const float fc = __shfl_sync(0xffffffffu, f, first + c);
+        if ((wrote >> c) & 1u) {  // a partial that saw nothing was not written
+          const float4* src = reinterpret_cast<const float4*>(p.ws_o + q.at(k0 + c) * D) + sl;
+#pragma unroll
+          for (int i = 0; i < Q; ++i) {
+            const float4 v = __ldcg(src + i * TSUB);
+            acc[i].x = fmaf(fc, v.x, acc[i].x);
+            acc[i].y = fmaf(fc, v.y, acc[i].y);
+            acc[i].z = fmaf(fc, v.z, acc[i].z);
+            acc[i].w = fmaf(fc, v.w, acc[i].w);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int off = TSUB / 2; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    if (!live) continue;
+    const float inv = L != 0.f ? 1.f / L : 0.f;
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+      reinterpret_cast<uint2*>(dst)[sl + i * TSUB] =
+          make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
+  }
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -877,25 +1221,37 @@ int tree_sms() {
 }
 
 int64_t host_units(int64_t rows) { return (rows + TU - 1) / TU; }
+int few_warps() { return tree_sms() * FCTAS * FWARPS; }
 int slot_rows_of(int64_t rows) { return rows <= TM ? (int)(2 * rows) : TU; }
 
 template <int D>
 cudaError_t launch_tree_t(const TreeParams& p, const TreeMaps& maps, cudaStream_t s) {
-  static std::atomic<uint64_t> attr{0};
-  cudaError_t e = raise_smem_limit(tree_attn_kernel<D>, TCfg<D>::SMEM, attr);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(tree_attn_kernel<D>, dim3(p.n_cta * p.lanes), dim3(TTHREADS), TCfg<D>::SMEM, s, p, maps);
+  static std::atomic<uint64_t> attr{0}, few_attr{0};
+  cudaError_t e;
+  if (p.few) {
+    e = raise_smem_limit(tree_few_kernel<D>, FCfg<D>::SMEM, few_attr);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(tree_few_kernel<D>, dim3(p.n_cta / FWARPS), dim3(FWARPS * 32), FCfg<D>::SMEM, s, p);
+  } else {
+    e = raise_smem_limit(tree_attn_kernel<D>, TCfg<D>::SMEM, attr);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(tree_attn_kernel<D>, dim3(p.n_cta * p.lanes), dim3(TTHREADS), TCfg<D>::SMEM, s, p, maps);
+  }
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)p.n_tok * p.Hq;
-  return launch_pdl(tree_merge_kernel<D>, dim3((unsigned)((rows * p.merge_warps + 7) / 8)), dim3(256), 0, s, p);
+  if (p.merge_warps) return launch_pdl(tree_merge_kernel<D>, dim3((unsigned)((rows * p.merge_warps + 7) / 8)), dim3(256), 0, s, p);
+  const int64_t blocks = (rows * TSUB + 255) / 256, wave = 4 * tree_sms();
+  return launch_pdl(tree_merge_rows_kernel<D>, dim3((unsigned)(blocks < wave ? blocks : wave)), dim3(256), 0, s, p);
 }
 
 }  // namespace
 
 // Partials: a slot per CTA and (head, unit), for each lane of CTAs.
+// Calls of few rows have a slot per warp instead, of no more rows.
 size_t tree_workspace_size(const vc_shape* s, int32_t max_rows) {
-  const int64_t rows = (int64_t)max_rows * (s->Hq / s->Hkv), units = host_units(rows);
-  return (size_t)(tree_sms() + s->B * s->Hkv * units) * slot_rows_of(rows) * (s->d + 1) * sizeof(float) + 256;
+  const int64_t rows = (int64_t)max_rows * (s->Hq / s->Hkv), units = host_units(rows), heads = (int64_t)s->B * s->Hkv;
+  const int64_t few = (few_warps() + heads) * (rows < FR ? rows : FR), many = (tree_sms() + heads * units) * slot_rows_of(rows);
+  return (size_t)(rows <= FR || few > many ? few : many) * (s->d + 1) * sizeof(float) + 256;
 }
 
 cudaError_t launch_tree_attn(const TreeArgs& a, cudaStream_t s, vc_status* st) {
@@ -911,7 +1267,10 @@ cudaError_t launch_tree_attn(const TreeArgs& a, cudaStream_t s, vc_status* st) {
   p.n_tok = a.n_tok;
   p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)a.d));
   p.dev_status = a.dev_status;
-  const int64_t tiles = ((int64_t)a.kv.max_pages << a.kv.shift) / TN + 1;
+  int most = 0;
+  for (int b = 0; b < a.B; ++b) most = a.req[b].n_rows > most ? a.req[b].n_rows : most;
+  p.few = (int64_t)most * G <= FR;
+  const int64_t tiles = ((int64_t)a.kv.max_pages << a.kv.shift) / (p.few ? FK : TN) + 1;
   int64_t cost = 0, units = 0, same = host_units((int64_t)a.req[0].n_rows * G);
   p.slot_rows = 1;
   p.least = 1;
@@ -919,11 +1278,11 @@ cudaError_t launch_tree_attn(const TreeArgs& a, cudaStream_t s, vc_status* st) {
     p.req[b] = a.req[b];
     const int64_t rows = (int64_t)a.req[b].n_rows * G, u = host_units(rows);
     if (u != same || rows - (u - 1) * TU <= TM) same = 1;
-    const int sr = slot_rows_of(rows);
+    const int sr = p.few ? (int)rows : slot_rows_of(rows);
     p.slot_rows = sr > p.slot_rows ? sr : p.slot_rows;
     if (rows > TM) p.least = 2;
     units += u * a.Hkv;
-    cost += 2 * u * a.Hkv * tiles;
+    cost += (p.few ? 1 : 2 * u) * a.Hkv * tiles;
   }
   // costs are counted in 32 bits
   if (cost >= INT32_MAX / 2 || units >= INT32_MAX / 2) {
@@ -932,7 +1291,7 @@ cudaError_t launch_tree_attn(const TreeArgs& a, cudaStream_t s, vc_status* st) {
   }
   const int sms = tree_sms();
   p.lanes = same > 1 && same <= sms / 2 ? (int)same : 1;
-  p.n_cta = sms / p.lanes;
+  p.n_cta = p.few ? few_warps() : sms / p.lanes;
   int64_t at = 0;
   for (int b = 0; b < a.B; ++b) {
     p.unit_begin[b] = (int32_t)at;
@@ -946,13 +1305,15 @@ cudaError_t launch_tree_attn(const TreeArgs& a, cudaStream_t s, vc_status* st) {
   }
   p.ws_o = static_cast<float*>(a.ws);
   p.ws_lse = p.ws_o + rows * a.d;
-  // Warps a row of the merge: a row's partials, about two a CTA that holds part of its unit, by fours (one round
-  // trip each); no more than make a wave of blocks.
-  const int64_t parts = 2 * (1 + p.n_cta / at), out_rows = (int64_t)a.n_tok * a.Hq;
+  // Warps a row of the merge: a row's partials, about two a CTA that holds part of its unit (one a warp of the other
+  // kernel), by fours (one round trip each); no more than make a wave of blocks. Several rows a warp where they are
+  // more than the warps of a wave.
+  const int64_t parts = (p.few ? 1 : 2) * (1 + p.n_cta / at), out_rows = (int64_t)a.n_tok * a.Hq, wave = (int64_t)sms * 4 * 8;
   p.merge_warps = 1;
-  while (p.merge_warps < 8 && parts > 4 * p.merge_warps && out_rows * p.merge_warps * 2 <= (int64_t)sms * 4 * 8) p.merge_warps *= 2;
+  while (p.merge_warps < 8 && parts > 4 * p.merge_warps && out_rows * p.merge_warps * 2 <= wave) p.merge_warps *= 2;
+  if (out_rows > wave) p.merge_warps = 0;
   const int64_t heads = (int64_t)a.kv.n_pages * a.Hkv;
-  if (!page_map(&maps.kv[0], a.kv.k, a.d, 1 << a.kv.shift, heads) || !page_map(&maps.kv[1], a.kv.v, a.d, 1 << a.kv.shift, heads)) {
+  if (!p.few && (!page_map(&maps.kv[0], a.kv.k, a.d, 1 << a.kv.shift, heads) || !page_map(&maps.kv[1], a.kv.v, a.d, 1 << a.kv.shift, heads))) {
     *st = VC_ERR_CUDA;
     return cudaSuccess;
   }
