@@ -7,16 +7,20 @@
 // keys (context and tokens) into tiles of 128. Lengths live on the device, so the kernels themselves lay the
 // plan down: one warp, a lane a request, adds up the tiles [request][head][unit][tile], and each CTA (one per SM:
 // 8 softmax warps, 4 MMA issuers, 1 loader) takes an equal range of them by cost. A CTA's part of a unit of a head
-// (a piece) leaves (o, lse) partials; a second kernel merges a row's partials. Where every request has the same
+// (a piece) leaves an (o, lse) partial; a second kernel merges a row's partials. Where every request has the same
 // number U > 1 of full units, CTA c takes unit c % U in the c / U-th range of [request][head][tile]: the units of
 // a head read a tile at about the same time, and it comes from DRAM once.
 //
-// Within a CTA two chains run side by side, each an issuer thread and a warpgroup of softmax threads (a
-// thread per query row): S = Q K^T into TMEM, softmax in registers, P (bf16) over S in TMEM, O += P V with P
-// read from TMEM. The chains meet only in the ring of K and V tiles. A unit of more than 128 rows gives each
-// chain 128 rows and every tile (a tile costs 2); one of up to 128 rows gives both chains the same rows and a half
-// of every tile (which costs 1), and each leaves its own partial. The loader's lanes fetch a tile page by page,
-// each the pages that it looked up one tile before.
+// Within a CTA two chains run side by side, each an issuer of S, one of P V and a warpgroup of softmax threads
+// (a thread per query row): S = Q K^T into TMEM, softmax in registers, P (bf16) over S in TMEM, O += P V with P read
+// from TMEM. The chains meet only in the ring of K and V tiles, so one's softmax runs while the tensor cores work for
+// the other. A unit of more than 128 rows gives each chain 128 rows and every tile (a tile costs 2); one of up to 128
+// rows gives both chains the same rows and a half of every tile (which costs 1), and at the end of a piece the two
+// sums meet in TMEM, where a chain's warps reach the other's rows. A piece that is all of a unit writes the output
+// itself. The loader's lanes fetch a tile page by page, each the pages that it looked up one tile before.
+//
+// S of 128 keys at a time would read Q from shared memory half as often, but leaves TMEM one S a chain: a tile then
+// waits for the P V before it (8 trees of 64 over 32768 keys: 537 us so, 420 with two S of 64 keys a chain).
 //
 // What a query row may not see: keys get -infinity by the row's bits of the mask; value rows behind the last
 // token (whatever the page holds there) are zeroed in shared memory, and where a step has a value row that is not
@@ -35,11 +39,11 @@ constexpr int TM = 128;         // query rows of a chain
 constexpr int TN = 128;         // keys per tile
 constexpr int TS = 64;          // keys per step: S and P of half a tile, double-buffered
 constexpr int TU = 2 * TM;      // query rows of a unit
-// warps 0-3, 4-7 softmax of chains 0 and 1; 8, 9 issue their S; 10, 11 their P V; 12 TMA; 13-15 idle (they
-// make a warpgroup with it: registers are handed over by warpgroup)
+// warps 0-3, 4-7 softmax of chains 0 and 1; 8, 9 issue their S; 10, 11 their P V; 12 TMA; 13 lays the plan down; 14
+// and 15 make a warpgroup with them (registers are handed over by warpgroup)
 constexpr int TTHREADS = 512;
-// Registers a thread: launched with 128 (65536 / 512), then 144 in the softmax warpgroups and 80 in the others
-constexpr int TREG_SOFTMAX = 144, TREG_ISSUE = 80;
+// Registers a thread: launched with 128 (65536 / 512), then 168 in the softmax warpgroups and 88 in the others
+constexpr int TREG_SOFTMAX = 168, TREG_ISSUE = 88;
 static_assert(256 * (TREG_SOFTMAX + TREG_ISSUE) <= 65536, "no more than the block was launched with");
 
 // The kernel for few rows: 4 warps a CTA, 3 CTAs an SM (2 * 4 * 8 KB of shared memory each at 128 channels)
@@ -130,11 +134,12 @@ struct TPiece {
 
   __device__ __forceinline__ bool valid() const { return at < end; }
   __device__ __forceinline__ int cost() const { return split ? 1 : 2; }
-  // chain w's steps of tile j of n keys are its halves [h0, h1)
-  __device__ __forceinline__ int h0(int w) const { return split ? w : 0; }
-  __device__ __forceinline__ int h1(int w, int n, int j) const { return min(tree_steps(n, j), split ? w + 1 : 2); }
-  // it has none in the whole piece: chain 1 of a split unit's last, short tile
-  __device__ __forceinline__ bool idle(int w, int n) const { return split && w == 1 && j1 - j0 == 1 && tree_steps(n, j0) == 1; }
+  // chain 1 has none in the whole piece: a split unit's last, short tile
+  __device__ __forceinline__ bool short_one(int n) const { return split && j1 - j0 == 1 && tree_steps(n, j0) == 1; }
+  __device__ __forceinline__ bool idle(int w, int n) const { return w == 1 && short_one(n); }
+  // both chains have sums of the same rows
+  __device__ __forceinline__ bool paired(int n) const { return split && !short_one(n); }
+  __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == tiles; }
   __device__ __forceinline__ void fit(const TreeParams& p, const TreePlan& s) {
     rows = min(TU, p.req[g].n_rows * p.G - u * TU);
     tiles = (s.n[g] + TN - 1) / TN;
@@ -158,15 +163,36 @@ struct TPiece {
   }
 };
 
+// Chain w's steps in a piece: step i holds the keys from beg + i * stride on, those before `full` are seen whole by
+// every row of the chain.
+struct TSteps {
+  int beg, stride, count, full;
+  int blind;  // the first key that some row of the chain does not see
+
+  __device__ __forceinline__ TSteps(const TreeParams& p, const TreePlan& s, const TPiece& q, int w) {
+    const int n = s.n[q.g], ctx = s.ctx[q.g];
+    beg = q.j0 * TN + (q.split ? w * TS : 0);
+    stride = q.split ? TN : TS;
+    const int end = min(n, q.j1 * TN);
+    count = end > beg ? (end - beg + stride - 1) / stride : 0;
+    blind = p.req[q.g].mask ? ctx : ctx + (q.u * TU + (q.split ? 0 : w * TM)) / p.G + 1;
+    const int clear = min(blind, n) - TS - beg;
+    full = min(count, clear >= 0 ? clear / stride + 1 : 0);
+  }
+};
+
 template <int D>
 struct TCfg {
   static constexpr int KB = D / 64;            // 64-channel (128-byte) blocks
   static constexpr int T_BYTES = KB * TN * 128;  // a K, V or Q tile
-  static constexpr int NST = D == 128 ? 5 : 10;  // K and V tiles in flight or in use
-  static constexpr int OFF_T = 2 * T_BYTES;    // behind a Q tile per chain
-  static constexpr int OFF_BAR = OFF_T + NST * T_BYTES;
-  static constexpr int BAR_BYTES = (2 * NST + 20) * 8 + 32;
-  static constexpr int SMEM = OFF_BAR + BAR_BYTES + (int)sizeof(TPiece) + (int)sizeof(TreePlan);
+  // K and V tiles in flight or in use: a ring each, so that every role sees every phase of its barriers
+  static constexpr int KST = D == 128 ? 3 : 5, VST = D == 128 ? 2 : 5;
+  static constexpr int OFF_K = 2 * T_BYTES;    // behind a Q tile per chain
+  static constexpr int OFF_V = OFF_K + KST * T_BYTES;
+  static constexpr int OFF_BAR = OFF_V + VST * T_BYTES;
+  static constexpr int BAR_BYTES = (2 * (KST + VST) + 22) * 8 + 32;
+  static constexpr int OFF_SUM = OFF_BAR + BAR_BYTES;  // [2][TM] maxima and sums of the chains' rows
+  static constexpr int SMEM = OFF_SUM + 2 * TM * 8 + (int)sizeof(TPiece) + (int)sizeof(TreePlan);
   static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
   static constexpr int OCOL = 4 * TS;          // TMEM: S (and P) of chain w at (2 w + step % 2) TS, O at OCOL + w D
   static constexpr uint32_t TCOLS = 512;
@@ -196,20 +222,11 @@ __device__ __forceinline__ TPiece tree_first(const TreeParams& p, const TreePlan
   return q;
 }
 
-// Bounded mbarrier wait that also gives up when another role of the CTA has aborted.
-__device__ __forceinline__ bool twait(uint64_t* bar, uint32_t parity, int32_t* st, volatile int* abort) {
-  for (uint32_t it = 0; it < kSpinLimit; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 31u) == 31u && *abort) return false;
-  }
-  set_status(st, VC_DEV_TIMEOUT);
-  *abort = 1;
-  return false;
-}
-
-// The same by a whole warp, which goes on or gives up together: its collective instructions need every lane.
+// Bounded mbarrier wait by a whole warp, which goes on or gives up together (its collective instructions need every
+// lane), also when another role of the CTA has aborted.
 __device__ __forceinline__ bool twait_warp(uint64_t* bar, uint32_t parity, int32_t* st, volatile int* abort) {
-  bool done = false;
+  bool done = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, done)) return true;
   for (uint32_t it = 0; it < kSpinLimit && !done; ++it) {
     done = mbar_try_wait(bar, parity);
     if ((it & 31u) == 31u && *abort) break;
@@ -218,6 +235,38 @@ __device__ __forceinline__ bool twait_warp(uint64_t* bar, uint32_t parity, int32
   if (!*abort) set_status(st, VC_DEV_TIMEOUT);
   *abort = 1;
   return false;
+}
+
+// A value that all lanes of a warp share, known to be so.
+template <typename T>
+__device__ __forceinline__ T uniform(T x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// tcgen05.mma (A in shared memory, A in tensor memory) and commit by the lanes with `on`, without a branch.
+__device__ __forceinline__ void mma_if(bool on, uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate), "r"((uint32_t)on)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(bool on, uint32_t tmem_d, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate), "r"((uint32_t)on)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(bool on, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"((uint32_t)on)
+      : "memory");
 }
 
 // Arrives where `on`, without a branch.
@@ -254,7 +303,6 @@ __device__ __forceinline__ void mask_bits(const uint32_t* row, int words, int no
 template <int D>
 __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ TreeMaps maps) {
   using C = TCfg<D>;
-  constexpr int NST = C::NST;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (smem_u32(smem) & 1023u) {  // the swizzled layouts need 1024-byte aligned tiles
@@ -262,22 +310,25 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
     if (tid == 0) set_status(p.dev_status, VC_DEV_INTERNAL);
     return;
   }
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [NST] tile landed
-  uint64_t* empty = full + NST;   // [NST] both chains' MMAs are done with it
-  uint64_t* sfull = empty + NST;  // [2][2] S of the chain's step in TMEM buffer step & 1
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [KST] K tile landed
+  uint64_t* kempty = kfull + C::KST;   // [KST] both chains' MMAs are done with it
+  uint64_t* vfull = kempty + C::KST;   // [VST], the same for V
+  uint64_t* vempty = vfull + C::VST;
+  uint64_t* sfull = vempty + C::VST;  // [2][2] S of the chain's step in TMEM buffer step & 1
   uint64_t* pfull = sfull + 4;    // [2][2] the step's P in the same place (4 warps)
   uint64_t* ofull = pfull + 4;    // [2][2] its P V done: the buffer may take the S of two steps on
   uint64_t* qfull = ofull + 4;    // [2] the piece's Q tile in shared memory (4 warps)
   uint64_t* vbar = qfull + 2;     // [2] the chain's warps have looked through a V tile (4 warps)
   uint64_t* xbar = vbar + 2;      // [4] drain of an issuer's MMAs
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(xbar + 4);
+  uint64_t* both = xbar + 4;      // [2] a paired piece: both chains' sums are there; they have been read (8 warps)
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(both + 2);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
   // [2][2] by S buffer, as the barriers are: 1 + the chain's last step in it whose P V the softmax warps took. A
   // warp may be a step ahead of the others, and so ahead of the P V issuer, which reads a step's word once all
   // four have left the step; the word's next step needs the issuer's commit behind that.
   volatile uint32_t* s_odd = tslot + 2;
-  volatile uint32_t* s_issued = tslot + 6;  // loads issued so far
-  TPiece* s_first = reinterpret_cast<TPiece*>(smem + C::OFF_BAR + C::BAR_BYTES);  // the CTA's first piece
+  float2* s_sum = reinterpret_cast<float2*>(smem + C::OFF_SUM);
+  TPiece* s_first = reinterpret_cast<TPiece*>(s_sum + 2 * TM);  // the CTA's first piece
   TreePlan& plan = *reinterpret_cast<TreePlan*>(s_first + 1);
 
   if (warp == 12) tc05::alloc(tslot, C::TCOLS);
@@ -293,9 +344,13 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
     }
   }
   if (tid == 0) {
-    for (int i = 0; i < NST; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 2);
+    for (int i = 0; i < C::KST; ++i) {
+      mbar_init(&kfull[i], 1);
+      mbar_init(&kempty[i], 2);
+    }
+    for (int i = 0; i < C::VST; ++i) {
+      mbar_init(&vfull[i], 1);
+      mbar_init(&vempty[i], 2);
     }
     for (int w = 0; w < 2; ++w) {
       for (int i = 2 * w; i < 2 * w + 2; ++i) {
@@ -306,12 +361,12 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
       }
       mbar_init(&qfull[w], 4);
       mbar_init(&vbar[w], 4);
+      mbar_init(&both[w], 8);
       mbar_init(&xbar[w], 1);
       mbar_init(&xbar[2 + w], 1);
     }
     fence_mbar_init();
     *s_abort = 0;
-    *s_issued = 0;
   }
   tc05::fence_before();
   __syncthreads();
@@ -320,24 +375,8 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
   pdl_wait();
   pdl_launch_dependents();
 
-  // Load `it` has landed; `seen` is the caller's count of loads it knows to be issued. A role does not see
-  // every phase of a stage's barrier (the S issuers wait for K tiles only, the P V issuers for V tiles), so the
-  // parity alone could be that of two phases before: once the load is issued, the phase before it is over, and
-  // its own cannot pass until this role releases the stage.
   // The chains' barriers are kept per S buffer: step s + 2 cannot complete a phase of one before step s's
   // has been waited for, while with one barrier for both, steps s and s + 1 could both pass unseen.
-  auto landed = [&](uint32_t it, uint32_t& seen) -> bool {
-    for (uint32_t i = 0; seen <= it; ++i) {
-      seen = *s_issued;
-      if (i >= kSpinLimit || ((i & 31u) == 31u && *s_abort)) {
-        if (!*s_abort) set_status(p.dev_status, VC_DEV_TIMEOUT);
-        *s_abort = 1;
-        return false;
-      }
-    }
-    return twait(&full[it % NST], (it / NST) & 1, p.dev_status, s_abort);
-  };
-
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TREG_ISSUE));
     if (warp == 12) {
@@ -348,14 +387,14 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
       const int kb = lane / per, pi = lane - kb * per;
       const bool mine = kb < C::KB;
       const bool once = p.lanes == 1;  // tiles that one CTA reads once leave L2 first
-      uint32_t it = 0;
+      uint32_t it = 0;                 // tiles loaded
       bool ok = true;
       for (; q.valid() && ok; q.next(p, plan)) {
         const int n = plan.n[q.g], pages = (n + p.kv.rows() - 1) >> shift;
         const int32_t* table = p.kv.pages_of(p.req[q.g].seq);
         auto look = [&](int j) { return mine && j * per + pi < pages ? __ldg(table + j * per + pi) : 0; };
         int page = look(q.j0);
-        for (int j = q.j0; j < q.j1 && ok; ++j) {
+        for (int j = q.j0; j < q.j1 && ok; ++j, ++it) {
           const int ahead = j + 1 < q.j1 ? look(j + 1) : 0;
           const int cnt = min(per, pages - j * per);  // pages of this tile: at least one
           const bool load = mine && pi < cnt;
@@ -364,114 +403,107 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
             page = p.kv.n_pages;  // beyond the map: reads as zeros
           }
           for (int kv = 0; kv < 2; ++kv) {
-            const uint32_t st = it % NST;
-            if (it >= (uint32_t)NST && !twait_warp(&empty[st], (it / NST - 1) & 1, p.dev_status, s_abort)) {
+            const uint32_t ring = kv ? C::VST : C::KST, st = it % ring;
+            uint64_t* full = kv ? vfull : kfull;
+            if (it >= ring && !twait_warp(&(kv ? vempty : kempty)[st], (it / ring - 1) & 1, p.dev_status, s_abort)) {
               ok = false;
               break;
             }
             if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(cnt << shift) * 128 * C::KB);
             __syncwarp();
             if (load) {
-              uint8_t* dst = smem + C::OFF_T + st * C::T_BYTES + kb * (TN * 128) + ((pi << shift) * 128);
+              uint8_t* dst = smem + (kv ? C::OFF_V : C::OFF_K) + st * C::T_BYTES + kb * (TN * 128) + ((pi << shift) * 128);
               if (once)
                 tc05::tma_load_3d_hint(dst, &maps.kv[kv], kb * 64, 0, page * p.Hkv + q.hk, &full[st], pol);
               else
                 tc05::tma_load_3d(dst, &maps.kv[kv], kb * 64, 0, page * p.Hkv + q.hk, &full[st]);
             }
             __syncwarp();
-            ++it;
-            if (lane == 0) {
-              __threadfence_block();
-              *s_issued = it;
-            }
           }
           page = ahead;
         }
       }
-      if (*s_abort && lane == 0)  // drain (bounded): a ring's worth of loads may still be landing
-        for (uint32_t i = it > (uint32_t)NST ? it - NST : 0; i < it; ++i)
-          mbar_wait_bounded(&full[i % NST], (i / NST) & 1, p.dev_status);
-      __syncwarp();
-    } else if (warp == 10 || warp == 11) {
-      // ---- P V issue of chain w: as soon as a step's P is there ---------------------------------------
-      if (lane == 0) {
-        const int w = warp - 10;
-        constexpr uint32_t IDESC_O = tc05::idesc_bf16(TM, D, true);
-        const uint32_t aT = smem_u32(smem + C::OFF_T), tS = tmem + 2 * w * TS, tO = tmem + C::OCOL + w * D;
-        TPiece q = *s_first;
-        uint32_t g = 0, t = 0, seen = 0;  // tiles of the CTA, steps of the chain
-        bool ok = true;
-        for (; q.valid() && ok; q.next(p, plan)) {
-          const int n = plan.n[q.g];
-          bool acc = false;
-          for (int j = q.j0; j < q.j1 && ok; ++j, ++g) {
-            const uint32_t iv = 2 * g + 1, sv = iv % NST, vaddr = aT + sv * C::T_BYTES;
-            ok = landed(iv, seen);
-            const int h1 = q.h1(w, n, j);
-            for (int h = q.h0(w); h < h1 && ok; ++h, ++t) {
-              if (!twait(&pfull[2 * w + (t & 1)], (t >> 1) & 1, p.dev_status, s_abort)) {
-                ok = false;
-                break;
-              }
-              tc05::fence_after();
-              if (s_odd[2 * w + (t & 1)] != t + 1) {
-                const uint32_t tP = tS + (t & 1) * TS, va = vaddr + h * (TS / 16) * 2048;
-#pragma unroll
-                for (int kk = 0; kk < TS / 16; ++kk)
-                  tc05::mma_ts(tO, tP + kk * 8, tc05::sdesc_sw128(va + kk * 2048, TN * 128, 1024), IDESC_O,
-                               (acc || kk > 0) ? 1u : 0u);
-              }
-              tc05::commit(&ofull[2 * w + (t & 1)]);
-              acc = true;
-            }
-            if (ok) tc05::commit(&empty[sv]);
-          }
-        }
-        // every MMA issued so far has completed before TMEM is released (bounded, even after an abort)
-        tc05::commit(&xbar[2 + w]);
-        mbar_wait_bounded(&xbar[2 + w], 0, p.dev_status);
+      if (*s_abort && lane == 0) {  // drain (bounded): a ring's worth of loads may still be landing; `it` counts K and V
+                                    // of whole tiles, and one K more where the wait for V's place gave up
+        for (uint32_t i = it > C::KST ? it - C::KST : 0; i < it; ++i) mbar_wait_bounded(&kfull[i % C::KST], (i / C::KST) & 1, p.dev_status);
+        for (uint32_t i = it > C::VST ? it - C::VST : 0; i < it; ++i) mbar_wait_bounded(&vfull[i % C::VST], (i / C::VST) & 1, p.dev_status);
       }
-    } else if (warp < 10) {
-      // ---- S issue of chain w: a step ahead of its softmax --------------------------------------------
-      if (lane == 0) {
-        const int w = warp - 8;
-        constexpr uint32_t IDESC_S = tc05::idesc_bf16(TM, TS, false);
-        const uint32_t aQ = smem_u32(smem) + w * C::T_BYTES, aT = smem_u32(smem + C::OFF_T);
-        const uint32_t tS = tmem + 2 * w * TS;
-        TPiece q = *s_first;
-        uint32_t g = 0, t = 0, u = 0, seen = 0;  // tiles of the CTA, steps and pieces of the chain
-        bool ok = true;
-        for (; q.valid() && ok; q.next(p, plan)) {
-          const int n = plan.n[q.g];
-          if (!q.idle(w, n)) {
-            ok = twait(&qfull[w], u & 1, p.dev_status, s_abort);
-            ++u;
-          }
-          for (int j = q.j0; j < q.j1 && ok; ++j, ++g) {
-            const uint32_t ik = 2 * g, sk = ik % NST, kaddr = aT + sk * C::T_BYTES;
-            ok = landed(ik, seen);
-            const int h1 = q.h1(w, n, j);
-            for (int h = q.h0(w); h < h1 && ok; ++h, ++t) {
+      __syncwarp();
+    } else if (warp < 12) {
+      // ---- MMAs of chain w: S (warps 8, 9) a step ahead of the softmax, P V (10, 11) as soon as a step's P is there.
+      // The whole warp goes through this and one lane issues: what the lanes share stays in uniform registers, where
+      // the MMAs take their operands from.
+      const int w = uniform(warp) & 1;
+      const bool lead = lane == 0, of_s = uniform(warp) < 10;
+      const uint32_t base = uniform(smem_u32(smem)), tm = uniform(tmem);
+      const uint32_t tS = tm + 2 * w * TS, tO = tm + C::OCOL + w * D;
+      constexpr uint32_t IDESC_S = tc05::idesc_bf16(TM, TS, false), IDESC_O = tc05::idesc_bf16(TM, D, true);
+      const uint64_t dQ = tc05::sdesc_sw128(base + w * C::T_BYTES, 16, 1024), dK = tc05::sdesc_sw128(base + C::OFF_K, 16, 1024);
+      const uint64_t dV = tc05::sdesc_sw128(base + C::OFF_V, TN * 128, 1024);
+      uint64_t* full = of_s ? kfull : vfull;
+      uint64_t* empty = of_s ? kempty : vempty;
+      const uint32_t ring = of_s ? C::KST : C::VST;
+      TPiece q = *s_first;
+      uint32_t st = 0, ph = 0;  // stage and phase of the next tile
+      uint32_t t = 0, u = 0;    // steps and pieces of the chain
+      bool ok = true;
+      for (; ok; q.next(p, plan)) {
+        const int at = uniform(q.at), end = uniform(q.end);
+        if (at >= end) break;
+        const int whole = uniform(TSteps(p, plan, q, w).full);
+        const int n = uniform(plan.n[q.g]), j0 = uniform(q.j0), j1 = uniform(q.j1), split = uniform((int)q.split);
+        const int h0 = split ? w : 0, hmax = split ? w + 1 : 2;
+        if (of_s && !(h0 >= tree_steps(n, j0) && j1 - j0 == 1)) {  // not idle
+          ok = twait_warp(&qfull[w], u & 1, p.dev_status, s_abort);
+          ++u;
+        }
+        int i = 0;  // steps of the piece
+        for (int j = j0; j < j1 && ok; ++j) {
+          ok = twait_warp(&full[st], ph, p.dev_status, s_abort);
+          const int h1 = min(tree_steps(n, j), hmax);
+          for (int h = h0; h < h1 && ok; ++h, ++t, ++i) {
+            const uint32_t buf = 2 * w + (t & 1), tX = tS + (t & 1) * TS;
+            if (of_s) {
               // the P V that read its P from this S buffer is done
-              if (t > 1 && !twait(&ofull[2 * w + (t & 1)], ((t - 2) >> 1) & 1, p.dev_status, s_abort)) {
+              if (t > 1 && !twait_warp(&ofull[buf], ((t >> 1) - 1) & 1, p.dev_status, s_abort)) {
                 ok = false;
                 break;
               }
               tc05::fence_after();
+              const uint64_t k = dK + ((st * C::T_BYTES + h * TS * 128) >> 4);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * (TN * 128) + (kk & 3) * 32;
-                tc05::mma_bf16(tS + (t & 1) * TS, tc05::sdesc_sw128(aQ + off, 16, 1024),
-                               tc05::sdesc_sw128(kaddr + h * TS * 128 + off, 16, 1024), IDESC_S, kk > 0);
+                const uint32_t off = ((kk >> 2) * (TN * 128) + (kk & 3) * 32) >> 4;
+                mma_if(lead, tX, dQ + off, k + off, IDESC_S, kk > 0);
               }
-              tc05::commit(&sfull[2 * w + (t & 1)]);
+              commit_if(lead, &sfull[buf]);
+            } else {
+              if (!twait_warp(&pfull[buf], (t >> 1) & 1, p.dev_status, s_abort)) {
+                ok = false;
+                break;
+              }
+              tc05::fence_after();
+              if (i < whole || uniform(s_odd[buf]) != t + 1) {
+                const uint64_t v = dV + ((st * C::T_BYTES + h * (TS / 16) * 2048) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < TS / 16; ++kk) mma_ts_if(lead, tO, tX + kk * 8, v + kk * (2048 >> 4), IDESC_O, i > 0 || kk > 0);
+              }
+              commit_if(lead, &ofull[buf]);
             }
-            if (ok) tc05::commit(&empty[sk]);
           }
+          if (!ok) break;
+          if (h0 < h1)
+            commit_if(lead, &empty[st]);
+          else if (lead)  // nothing in this tile, the unit's last, for the chain
+            mbar_arrive(&empty[st]);
+          __syncwarp();
+          if (++st == ring) st = 0, ph ^= 1;
         }
-        tc05::commit(&xbar[w]);
-        mbar_wait_bounded(&xbar[w], 0, p.dev_status);
       }
+      // every MMA issued so far has completed before TMEM is released (bounded, even after an abort)
+      commit_if(lead, &xbar[warp - 8]);
+      mbar_wait_bounded(&xbar[warp - 8], 0, p.dev_status);
+      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TREG_SOFTMAX));
@@ -481,28 +513,20 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
     const uint32_t tS = tmem + lane_off + 2 * w * TS, tO = tmem + lane_off + C::OCOL + w * D;
     uint8_t* sQ = smem + w * C::T_BYTES;
     TPiece q = *s_first;
-    uint32_t g = 0, t = 0, looked = 0, seen = 0;
+    uint32_t g = 0, t = 0, looked = 0, pairs = 0;
     // P V of step s done (and with it those before): asked for steps whose S has been read, so the phase
     // before on that buffer is over
     auto pv_done = [&](uint32_t s) { return twait_warp(&ofull[2 * w + (s & 1)], (s >> 1) & 1, p.dev_status, s_abort); };
     bool ok = true;
     const size_t lane_slot = (size_t)(blockIdx.x % p.lanes) * p.lane_slots + blockIdx.x / p.lanes;
-    auto slot_of = [&]() {
-      return lane_slot + p.unit_begin[q.g] + (p.lanes > 1 ? q.hk : q.hk * units_of(p.req[q.g].n_rows * p.G) + q.u);
-    };
-    // Q of the next piece with steps for this chain, into its Q tile (the chain's S on the last one are all
-    // done: their softmax is); pieces without any leave an empty partial
+    // Q of the next piece with tiles for this chain, into its Q tile (the chain's S on the last one are all
+    // done: their softmax is)
     auto fetch = [&]() {
       for (; q.valid(); g += q.j1 - q.j0, q.next(p, plan)) {
+        if (q.idle(w, plan.n[q.g])) continue;
         const TreeReqDev& R = p.req[q.g];
-        const int ru = q.split ? rt : w * TM + rt, row = q.u * TU + ru;  // row of the unit, of the head
-        const bool row_ok = ru < q.rows;
-        if (q.idle(w, plan.n[q.g])) {
-          if (row_ok) p.ws_lse[slot_of() * p.slot_rows + w * q.rows + ru] = -INFINITY;
-          continue;
-        }
-        const int tok = row / p.G;
-        const bf16* src = row_ok ? R.q + ((size_t)tok * p.Hq + q.hk * p.G + (row - tok * p.G)) * D : nullptr;  // this thread's row
+        const int ru = q.split ? rt : w * TM + rt, row = q.u * TU + ru, tok = row / p.G;  // row of the unit, of the head
+        const bf16* src = ru < q.rows ? R.q + ((size_t)tok * p.Hq + q.hk * p.G + (row - tok * p.G)) * D : nullptr;  // this thread's row
         // the warp's 32 rows, a row's 16-byte pieces in neighbouring lanes (a lane per row would touch 32 lines a load)
         constexpr int PR = D / 8, RW = 32 / PR;  // pieces of a row, rows a load
 #pragma unroll
@@ -518,89 +542,132 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
         return;
       }
     };
-    // the chain's partial of the piece before: written once the next one's S are under way
-    size_t part = 0;
+    // the piece before: written once the next one's S are under way
+    size_t part = 0;        // this row's partial
+    bf16* out = nullptr;    // or its place in the output
     float m_run = 0.f, l_run = 0.f;
-    bool row_ok = false, have = false;
+    bool row_ok = false, have = false, paired = false;
     while (ok) {
       fetch();
       if (have) {
-        // after its last P V
         if (!pv_done(t - 1)) break;
+        // weight of this chain's sum and of the other's
+        float mine = l_run != 0.f ? 1.f / l_run : 0.f, theirs = 0.f, lse = l_run != 0.f ? m_run + log2f(l_run) : -INFINITY;
+        if (paired) {
+          s_sum[w * TM + rt] = make_float2(m_run, l_run);
+          tc05::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&both[0]);
+          if (!twait_warp(&both[0], pairs & 1, p.dev_status, s_abort)) break;
+          const float2 o = s_sum[(w ^ 1) * TM + rt];
+          const float M = fmaxf(m_run, o.x), mu = M == -INFINITY ? 0.f : M;  // rows that saw nothing: weights 0, or NaN
+          mine = ex2_approx(m_run - mu);
+          theirs = ex2_approx(o.x - mu);
+          const float sum = w ? theirs * o.y + mine * l_run : mine * l_run + theirs * o.y;  // the same in both chains
+          lse = sum != 0.f ? M + log2f(sum) : -INFINITY;
+          const float inv = sum != 0.f ? 1.f / sum : 0.f;
+          mine *= inv;
+          theirs *= inv;
+        }
         tc05::fence_after();
-        const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
         // rows in the order of an MMA's accumulator: four lanes hold 8 neighbouring channels (whole 32-byte
-        // sectors), where a lane per row would write 32 lines at a time
+        // sectors), where a lane per row would write 32 lines at a time; of paired chains each writes half the channels
+        const int cb0 = paired ? w * (D / 64) : 0, cb1 = paired ? cb0 + D / 64 : D / 32;
+        const uint32_t tX = tmem + lane_off + C::OCOL + (w ^ 1) * D;  // the other chain's O
         float* o_row0 = p.ws_o + (part - (rt & 31)) * D + 2 * (lane & 3);  // of the warp's first row
         const unsigned rows_ok = __ballot_sync(0xffffffffu, row_ok);
 #pragma unroll 1
         for (int hh = 0; hh < 2; ++hh) {
           if (!((rows_ok >> (16 * hh)) & 0xffffu)) continue;
-          const int r0 = hh * 16 + (lane >> 2), r1 = r0 + 8;
-          const float i0 = __shfl_sync(0xffffffffu, inv, r0), i1 = __shfl_sync(0xffffffffu, inv, r1);
-          const bool ok0 = (rows_ok >> r0) & 1u, ok1 = (rows_ok >> r1) & 1u;
+          const int r0 = hh * 16 + (lane >> 2);
+          float a[2], b[2];
+          bf16* to[2];
+          bool on[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            a[e] = __shfl_sync(0xffffffffu, mine, r0 + 8 * e);
+            b[e] = __shfl_sync(0xffffffffu, theirs, r0 + 8 * e);
+            to[e] = reinterpret_cast<bf16*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), r0 + 8 * e));
+            on[e] = (rows_ok >> (r0 + 8 * e)) & 1u;
+          }
 #pragma unroll 1
-          for (int cb = 0; cb < D / 32; ++cb) {
+          for (int cb = cb0; cb < cb1; ++cb) {
             uint32_t r[16];
             tc05::ld16x256_x4(tO + ((uint32_t)(hh * 16) << 16) + cb * 32, r);  // warp-collective: every lane loads
             tc05::wait_ld();
+            float v[16];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (ok0)
-                *reinterpret_cast<float2*>(o_row0 + (size_t)r0 * D + cb * 32 + 8 * k) =
-                    make_float2(__uint_as_float(r[4 * k]) * i0, __uint_as_float(r[4 * k + 1]) * i0);
-              if (ok1)
-                *reinterpret_cast<float2*>(o_row0 + (size_t)r1 * D + cb * 32 + 8 * k) =
-                    make_float2(__uint_as_float(r[4 * k + 2]) * i1, __uint_as_float(r[4 * k + 3]) * i1);
+            for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]) * a[(k >> 1) & 1];
+            if (paired) {
+              tc05::ld16x256_x4(tX + ((uint32_t)(hh * 16) << 16) + cb * 32, r);
+              tc05::wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] += __uint_as_float(r[k]) * b[(k >> 1) & 1];
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (on[e]) {
+                  const float x = v[4 * k + 2 * e], y = v[4 * k + 2 * e + 1];
+                  if (to[e])
+                    *reinterpret_cast<uint32_t*>(to[e] + cb * 32 + 8 * k + 2 * (lane & 3)) = pack_bf16x2(x, y);
+                  else
+                    *reinterpret_cast<float2*>(o_row0 + (size_t)(r0 + 8 * e) * D + cb * 32 + 8 * k) = make_float2(x, y);
+                }
           }
         }
-        if (row_ok) p.ws_lse[part] = l_run != 0.f ? m_run + log2f(l_run) : -INFINITY;
+        if (row_ok && !out && !(paired && w)) p.ws_lse[part] = lse;
         tc05::fence_before();
+        if (paired) {  // neither chain's next P V before both have read
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&both[1]);
+          if (!twait_warp(&both[1], pairs & 1, p.dev_status, s_abort)) break;
+          ++pairs;
+        }
       }
       if (!q.valid()) break;
       have = true;
+      paired = q.paired(plan.n[q.g]);
       const TreeReqDev& R = p.req[q.g];
       const int ru = q.split ? rt : w * TM + rt;
       row_ok = ru < q.rows;
+      const bool alive = __any_sync(0xffffffffu, row_ok);  // a warp without rows only keeps step
       const int row = q.u * TU + ru, tl = row / p.G;
-      part = slot_of() * p.slot_rows + (q.split ? w * q.rows : 0) + ru;
+      part = (lane_slot + p.unit_begin[q.g] + (p.lanes > 1 ? q.hk : q.hk * units_of(R.n_rows * p.G) + q.u)) * p.slot_rows + ru;
+      out = q.whole() && row_ok ? R.o + ((size_t)tl * p.Hq + q.hk * p.G + (row - tl * p.G)) * D : nullptr;
       const int n = plan.n[q.g], ctx = plan.ctx[q.g];
       const uint32_t* mrow = R.mask && row_ok ? R.mask + (size_t)tl * R.mask_words : nullptr;
-      // the first key that some row of the chain does not see
-      const int blind = R.mask ? ctx : ctx + (q.u * TU + (q.split ? 0 : w * TM)) / p.G + 1;
+      const TSteps steps(p, plan, q, w);
       m_run = -INFINITY, l_run = 0.f;
-      bool fresh = true;  // the piece's first step
-      for (int j = q.j0; j < q.j1 && ok; ++j, ++g) {
-        const int h1 = q.h1(w, n, j);
-        for (int h = q.h0(w); h < h1; ++h, ++t, fresh = false) {
-          const int k0 = j * TN + h * TS;  // the step's first key
-          const uint32_t tP = tS + (t & 1) * TS;
-          uint32_t see_lo = 0xffffffffu, see_hi = 0xffffffffu;  // keys of the step that the row sees
-          if (k0 + TS > min(blind, n)) {
-            if (R.mask && k0 + TS > ctx) {
+      for (int i = 0; i < steps.count; ++i, ++t) {
+        const uint32_t buf = 2 * w + (t & 1), tP = tS + (t & 1) * TS;
+        const bool tail = i >= steps.full;
+        if (!twait_warp(&sfull[buf], (t >> 1) & 1, p.dev_status, s_abort)) {
+          ok = false;
+          break;
+        }
+        tc05::fence_after();
+        uint32_t see_lo = 0xffffffffu, see_hi = 0xffffffffu;  // keys of the step that the row sees
+        if (alive) {
+          float x[TS];
+#pragma unroll
+          for (int c = 0; c < TS / 32; ++c) {
+            uint32_t r[32];
+            tc05::ld32(tP + c * 32, r);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(r[e]);
+          }
+          tc05::wait_ld();
+          if (tail) {
+            const int k0 = steps.beg + i * steps.stride;
+            if (R.mask) {
               mask_bits(mrow, R.mask_words, k0 - ctx, n - k0, see_lo, see_hi);
             } else {
               const int last = min(ctx + tl, n - 1) - k0;
               see_lo = last >= 31 ? 0xffffffffu : last < 0 ? 0u : (2u << last) - 1u;
               see_hi = last >= 63 ? 0xffffffffu : last < 32 ? 0u : (2u << (last - 32)) - 1u;
             }
-          }
-          if (!twait_warp(&sfull[2 * w + (t & 1)], (t >> 1) & 1, p.dev_status, s_abort)) {
-            ok = false;
-            break;
-          }
-          tc05::fence_after();
-          float x[TS];
-#pragma unroll
-          for (int cb = 0; cb < TS / 32; ++cb) {
-            uint32_t r[32];
-            tc05::ld32(tP + cb * 32, r);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) x[cb * 32 + e] = __uint_as_float(r[e]);
-          }
-          tc05::wait_ld();
-          if ((see_lo & see_hi) != 0xffffffffu) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               if (!((see_lo >> e) & 1u)) x[e] = -INFINITY;
@@ -634,7 +701,7 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
             const float m_new = fmaxf(m_run, fmaxf(fmaxf(mx, my), fmaxf(mz, mw)) * p.scale_log2);
             const bool need = m_new > m_run + 8.f;  // from -infinity, any finite score
             if (!__any_sync(0xffffffffu, need)) break;
-            if (fresh) {
+            if (i == 0) {
               m_run = m_new;
               continue;
             }
@@ -663,88 +730,91 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
           tc05::st32(tP, r);
           l_run += u0 + u1;
           tc05::wait_st();
-          // A step with keys that some rows do not see: a weight of 0 would carry an infinite or NaN value row to
-          // them. Rows from n on, which nobody sees, are zeroed; if others hold such a value, the threads add up the
-          // seen keys themselves.
-          if (k0 + TS > min(blind, n)) {
-            const uint32_t iv = 2 * g + 1;
-            if (!__all_sync(0xffffffffu, landed(iv, seen))) {
+        }
+        // A step with keys that some rows do not see: a weight of 0 would carry an infinite or NaN value row to
+        // them. Rows from n on, which nobody sees, are zeroed; if others hold such a value, the threads add up the
+        // seen keys themselves.
+        if (tail) {
+          const int k0 = steps.beg + i * steps.stride, j = k0 / TN, h = k0 / TS & 1;
+          const uint32_t gv = g + j - q.j0;
+          // V has landed: the phase before is over (its P V are done), and its own cannot pass without this chain
+          if (!twait_warp(&vfull[gv % C::VST], (gv / C::VST) & 1, p.dev_status, s_abort)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sV = smem + C::OFF_V + (gv % C::VST) * C::T_BYTES;
+          bool bad = false;
+          const int kv = h * TS + (rt & (TS - 1));  // two threads look through each of the step's rows
+          const bool there = j * TN + kv < n;
+#pragma unroll
+          for (int cc = 0; cc < D / 16; ++cc) {
+            const int c = (rt / TS) * (D / 16) + cc;
+            uint4* at = reinterpret_cast<uint4*>(sV + (c >> 3) * (TN * 128) + kv * 128 + (((c ^ kv) & 7) << 4));
+            if (there) {
+              const uint4 v = *at;
+              bad |= broken_bf16x2(v.x) || broken_bf16x2(v.y) || broken_bf16x2(v.z) || broken_bf16x2(v.w);
+            } else {
+              *at = make_uint4(0, 0, 0, 0);  // by both chains where they share the tile
+            }
+          }
+          if (bad) s_odd[buf] = t + 1;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&vbar[w]);
+          if (!twait_warp(&vbar[w], looked & 1, p.dev_status, s_abort)) {
+            ok = false;
+            break;
+          }
+          ++looked;
+          if (alive && s_odd[buf] == t + 1) {
+            if (i > 0 && !pv_done(t - 1)) {
               ok = false;
               break;
             }
-            uint8_t* sV = smem + C::OFF_T + (iv % NST) * C::T_BYTES;
-            bool bad = false;
-            const int kv = h * TS + (rt & (TS - 1));  // two threads look through each of the step's rows
-            const bool there = j * TN + kv < n;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              const int c = (rt / TS) * (D / 16) + i;
-              uint4* at = reinterpret_cast<uint4*>(sV + (c >> 3) * (TN * 128) + kv * 128 + (((c ^ kv) & 7) << 4));
-              if (there) {
-                const uint4 v = *at;
-                bad |= broken_bf16x2(v.x) || broken_bf16x2(v.y) || broken_bf16x2(v.z) || broken_bf16x2(v.w);
+            tc05::fence_after();
+#pragma unroll 1
+            for (int cb = 0; cb < D / 32; ++cb) {
+              uint32_t r[32];
+              if (i > 0) {
+                tc05::ld32(tO + cb * 32, r);
+                tc05::wait_ld();
               } else {
-                *at = make_uint4(0, 0, 0, 0);  // by both chains where they share the tile
+#pragma unroll
+                for (int e = 0; e < 32; ++e) r[e] = 0u;
               }
-            }
-            if (bad) s_odd[2 * w + (t & 1)] = t + 1;
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&vbar[w]);
-            if (!twait_warp(&vbar[w], looked & 1, p.dev_status, s_abort)) {
-              ok = false;
-              break;
-            }
-            ++looked;
-            if (s_odd[2 * w + (t & 1)] == t + 1) {
-              if (!fresh && !pv_done(t - 1)) {
-                ok = false;
-                break;
-              }
-              tc05::fence_after();
 #pragma unroll 1
-              for (int cb = 0; cb < D / 32; ++cb) {
-                uint32_t r[32];
-                if (!fresh) {
-                  tc05::ld32(tO + cb * 32, r);
-                  tc05::wait_ld();
-                } else {
+              for (int kp = 0; kp < TS / 2; ++kp) {  // two keys a column; rare, so kept small
+                const uint32_t pw = tc05::ld1(tP + kp);
+                tc05::wait_ld();
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) r[e] = 0u;
-                }
-#pragma unroll 1
-                for (int kp = 0; kp < TS / 2; ++kp) {  // two keys a column; rare, so kept small
-                  const uint32_t pw = tc05::ld1(tP + kp);
-                  tc05::wait_ld();
+                for (int e = 0; e < 2; ++e) {
+                  const int k = 2 * kp + e, kt = h * TS + k;
+                  const bool sees = ((k < 32 ? see_lo : see_hi) >> (k & 31)) & 1u;
+                  const float pk = __uint_as_float(e ? pw & 0xffff0000u : pw << 16);
 #pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    const int k = 2 * kp + e, kt = h * TS + k;
-                    const bool sees = ((k < 32 ? see_lo : see_hi) >> (k & 31)) & 1u;
-                    const float pk = __uint_as_float(e ? pw & 0xffff0000u : pw << 16);
+                  for (int c = 0; c < 4; ++c) {
+                    const int ch = cb * 4 + c;
+                    const uint4 v = *reinterpret_cast<const uint4*>(sV + (ch >> 3) * (TN * 128) + kt * 128 + (((ch ^ kt) & 7) << 4));
+                    const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                      const int ch = cb * 4 + c;
-                      const uint4 v = *reinterpret_cast<const uint4*>(sV + (ch >> 3) * (TN * 128) + kt * 128 + (((ch ^ kt) & 7) << 4));
-                      const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                      for (int i = 0; i < 8; ++i) {
-                        const float val = __uint_as_float(i & 1 ? vw[i >> 1] & 0xffff0000u : vw[i >> 1] << 16);
-                        const float a = __uint_as_float(r[c * 8 + i]);
-                        r[c * 8 + i] = __float_as_uint(sees ? fmaf(pk, val, a) : a);
-                      }
+                    for (int y = 0; y < 8; ++y) {
+                      const float val = __uint_as_float(y & 1 ? vw[y >> 1] & 0xffff0000u : vw[y >> 1] << 16);
+                      const float a = __uint_as_float(r[c * 8 + y]);
+                      r[c * 8 + y] = __float_as_uint(sees ? fmaf(pk, val, a) : a);
                     }
                   }
                 }
-                tc05::st32(tO + cb * 32, r);
               }
-              tc05::wait_st();
+              tc05::st32(tO + cb * 32, r);
             }
+            tc05::wait_st();
           }
-          tc05::fence_before();
-          __syncwarp();
-          tarrive_if(&pfull[2 * w + (t & 1)], lane == 0);
         }
+        tc05::fence_before();
+        __syncwarp();
+        tarrive_if(&pfull[buf], lane == 0);
       }
+      g += q.j1 - q.j0;
       if (!ok) break;
       q.next(p, plan);
     }
@@ -991,6 +1061,7 @@ __global__ void __launch_bounds__(FWARPS * 32, FCTAS) tree_few_kernel(const __gr
     cp_async_wait<0>();
     // the range's partial of this head: four lanes hold 8 neighbouring channels of a row
     const size_t part = ((size_t)wid + p.unit_begin[g] + hk) * p.slot_rows;
+    const bool whole = j0 == 0 && j1 == tiles;  // then it is the output
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
@@ -998,6 +1069,13 @@ __global__ void __launch_bounds__(FWARPS * 32, FCTAS) tree_few_kernel(const __gr
       const int r = qrow + 8 * e;
       if (r < rows) {
         const float inv = l[e] != 0.f ? 1.f / l[e] : 0.f;
+        if (whole) {
+          bf16* dst = R.o + ((size_t)tok[e] * p.Hq + hk * p.G + (r - tok[e] * p.G)) * D + qcol;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+            *reinterpret_cast<uint32_t*>(dst + 8 * i) = pack_bf16x2(acc[i][2 * e] * inv, acc[i][2 * e + 1] * inv);
+          continue;
+        }
         float* dst = p.ws_o + (part + r) * D + qcol;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
@@ -1021,13 +1099,11 @@ __global__ void __launch_bounds__(FWARPS * 32, FCTAS) tree_few_kernel(const __gr
 // Weight of a partial beside the largest lse M: 0 where it saw nothing; M stays -inf only beside a NaN.
 __device__ __forceinline__ float part_weight(float l, float M) { return l == -INFINITY ? 0.f : M == -INFINITY ? NAN : exp2f(l - M); }
 
-// Where a row's unit left its partials: `count` of them, number i at at(i); a split unit has two a slot.
+// Where a row's unit left its partials: `count` of them, number i at index at(i). One alone is the output already.
 struct TParts {
   size_t base;
-  int count, stride, second;  // stride: a slot's rows; second: rows to the slot's second partial, 0: none
-  __device__ __forceinline__ size_t at(int i) const {
-    return second ? base + (size_t)(i >> 1) * stride + (i & 1) * second : base + (size_t)i * stride;
-  }
+  int count, stride;  // stride: a slot's rows
+  __device__ __forceinline__ size_t at(int i) const { return base + (size_t)i * stride; }
 };
 
 // Output row `id` of the call (token, query head): its partials and its place.
@@ -1040,14 +1116,14 @@ __device__ __forceinline__ TParts tree_parts(const TreeParams& p, const TreePlan
   const TreeReqDev& R = p.req[b];
   const int i = tok - R.tok_begin, r = i * p.G + hq - hk * p.G;  // token of the request, row of the head
   dst = R.o + ((size_t)i * p.Hq + hq) * D;
-  const int rows = R.n_rows * p.G, u = p.few ? 0 : r / TU, in_unit = min(TU, rows - u * TU);
-  const int cost = p.few || in_unit <= TM ? 1 : 2, tiles = tiles_of(p, plan.n[b]);
-  TParts q{0, 0, p.slot_rows, !p.few && cost == 1 ? in_unit : 0};
+  const int rows = R.n_rows * p.G, u = p.few ? 0 : r / TU;
+  const int cost = p.few || rows - u * TU <= TM ? 1 : 2, tiles = tiles_of(p, plan.n[b]);
+  TParts q{0, 0, p.slot_rows};
   if (tiles == 0) return q;
   const int at = plan.cost_begin[b] + hk * tiles * tile_cost(p, rows) + (p.lanes > 1 ? 0 : u * 2 * tiles);
   const int c0 = cta_of(plan, at), c1 = cta_of(plan, at + cost * (tiles - 1));  // of its first and last tile
   const int unit = p.unit_begin[b] + (p.lanes > 1 || p.few ? hk : hk * units_of(rows) + u);
-  q.count = (c1 - c0 + 1) * (q.second ? 2 : 1);
+  q.count = c1 - c0 + 1;
   q.base = ((size_t)(p.lanes > 1 ? u : 0) * p.lane_slots + c0 + unit) * p.slot_rows + (r - u * TU);
   return q;
 }
@@ -1065,14 +1141,18 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wpr = p.merge_warps, part = warp % wpr;  // warps of a row, this one among them
   const int64_t id = (int64_t)blockIdx.x * (8 / wpr) + warp / wpr;
-  const bool live = id < (int64_t)p.n_tok * p.Hq;
+  bool live = id < (int64_t)p.n_tok * p.Hq;
   pdl_launch_dependents();
   pdl_wait();
   if (warp == 0) tree_plan(p, &plan, lane, false);
   __syncthreads();
-  TParts q{0, 0, 0, 0};
+  TParts q{0, 0, 0};
   bf16* dst = nullptr;
   if (live) q = tree_parts<D>(p, plan, id, dst);
+  if (q.count == 1) {  // written by the piece itself: nothing to add up, the block's barrier is kept
+    live = false;
+    q.count = 0;
+  }
   auto lse_of = [&](int k, int end) { return k >= end ? -INFINITY : p.ws_lse[q.at(k)]; };
   float M = -INFINITY;
   for (int k0 = 0; k0 < q.count; k0 += 32) M = fmaxf(M, lse_of(k0 + lane, q.count));
@@ -1149,10 +1229,14 @@ __global__ void __launch_bounds__(256, 4) tree_merge_rows_kernel(const __grid_co
   const int64_t all = (int64_t)p.n_tok * p.Hq;
   for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w * (32 / TSUB) < all; w += (int64_t)gridDim.x * 8) {
     const int64_t id = w * (32 / TSUB) + lane / TSUB;
-    const bool live = id < all;
-    TParts q{0, 0, 0, 0};
+    bool live = id < all;
+    TParts q{0, 0, 0};
     bf16* dst = nullptr;
     if (live) q = tree_parts<D>(p, plan, id, dst);
+    if (q.count == 1) {  // written by the piece itself
+      live = false;
+      q.count = 0;
+    }
     const int most = __reduce_max_sync(0xffffffffu, q.count);
     auto lse_of = [&](int k) { return k >= q.count ? -INFINITY : p.ws_lse[q.at(k)]; };
     const float l0 = lse_of(sl);  // most rows have no more than a lane each
@@ -1222,7 +1306,7 @@ int tree_sms() {
 
 int64_t host_units(int64_t rows) { return (rows + TU - 1) / TU; }
 int few_warps() { return tree_sms() * FCTAS * FWARPS; }
-int slot_rows_of(int64_t rows) { return rows <= TM ? (int)(2 * rows) : TU; }
+int slot_rows_of(int64_t rows) { return rows <= TM ? (int)rows : TU; }
 
 template <int D>
 cudaError_t launch_tree_t(const TreeParams& p, const TreeMaps& maps, cudaStream_t s) {
@@ -1305,10 +1389,9 @@ cudaError_t launch_tree_attn(const TreeArgs& a, cudaStream_t s, vc_status* st) {
   }
   p.ws_o = static_cast<float*>(a.ws);
   p.ws_lse = p.ws_o + rows * a.d;
-  // Warps a row of the merge: a row's partials, about two a CTA that holds part of its unit (one a warp of the other
-  // kernel), by fours (one round trip each); no more than make a wave of blocks. Several rows a warp where they are
-  // more than the warps of a wave.
-  const int64_t parts = (p.few ? 1 : 2) * (1 + p.n_cta / at), out_rows = (int64_t)a.n_tok * a.Hq, wave = (int64_t)sms * 4 * 8;
+  // Warps a row of the merge: a row's partials, one a CTA (or warp) that holds part of its unit, by fours (one round
+  // trip each); no more than make a wave of blocks. Several rows a warp where they are more than the warps of a wave.
+  const int64_t parts = 1 + p.n_cta / at, out_rows = (int64_t)a.n_tok * a.Hq, wave = (int64_t)sms * 4 * 8;
   p.merge_warps = 1;
   while (p.merge_warps < 8 && parts > 4 * p.merge_warps && out_rows * p.merge_warps * 2 <= wave) p.merge_warps *= 2;
   if (out_rows > wave) p.merge_warps = 0;
