@@ -204,6 +204,7 @@ vc_status vc_rope_pages(const vc_shape* shape, const vc_rope_axes* axes, const v
     p.axis[j] = (int8_t)axes->axis[j];
   }
   int64_t total = 0;
+  int n = 0;
   for (int b = 0; b < shape->B; ++b) {
     const vc_rope_page_req& r = req[b];
     if (r.n_rows < 0) return VC_ERR_INVALID;
@@ -215,7 +216,7 @@ vc_status vc_rope_pages(const vc_shape* shape, const vc_rope_axes* axes, const v
     if (qs < wq || ks < wk || vs < wk || ((qs | ks | vs) & 7)) return VC_ERR_INVALID;
     if (r.q && r.q_out == r.q && qs != wq) return VC_ERR_INVALID;
     if (r.off && (!a4(r.off) || (r.off_stride != 0 && r.off_stride < r.n_rows))) return VC_ERR_INVALID;
-    RopePageReqDev& e = p.req[p.B];
+    RopePageReqDev& e = p.req[n];
     e.q = static_cast<const bf16*>(r.q);
     e.k = static_cast<const bf16*>(r.k);
     e.v = static_cast<const bf16*>(r.v);
@@ -226,11 +227,11 @@ vc_status vc_rope_pages(const vc_shape* shape, const vc_rope_axes* axes, const v
     e.off_stride = r.off_stride;
     e.q_out = static_cast<bf16*>(r.q_out);
     e.seq = r.seq;
-    e.tok_begin = (int32_t)total;
+    p.tok_begin[n++] = (int32_t)total;
     total += r.n_rows;
     if (total > (int64_t(1) << 30)) return VC_ERR_UNSUPPORTED;
-    ++p.B;
   }
+  while (n < VC_MAX_BATCH) p.tok_begin[n++] = INT32_MAX;
   p.n_tok = (int32_t)total;
   return total == 0 ? VC_OK : done(launch_rope_pages(p, shape->d, stream), stream);
 }

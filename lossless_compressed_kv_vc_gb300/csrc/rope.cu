@@ -139,11 +139,11 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_pages_kernel(const __gri
   const PagedDev& kv = p.kv;
   const int tok = blockIdx.x;
   int b = 0;
-#pragma unroll 1
-  for (int i = 1; i < p.B; ++i)
-    if (p.req[i].tok_begin <= tok) b = i;
+#pragma unroll
+  for (int k = VC_MAX_BATCH / 2; k > 0; k >>= 1)
+    if (p.tok_begin[b + k] <= tok) b += k;
   const RopePageReqDev& r = p.req[b];
-  const int t = tok - r.tok_begin;
+  const int t = tok - p.tok_begin[b];
   const int per = p.inter ? D / 8 : D / 8 - p.rot / 16;  // items of a rotated head
   const int nq = (r.q ? p.Hq : 0) * per, n = nq + p.Hkv * (per + D / 8);
   const double turns = (int)threadIdx.x < p.rot / 2 ? p.turns[threadIdx.x] : 0.0;

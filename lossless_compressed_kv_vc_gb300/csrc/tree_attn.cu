@@ -53,8 +53,15 @@ constexpr int FWARPS = 4, FCTAS = 3;
 
 struct TreeParams {
   PagedDev kv;
-  TreeReqDev req[VC_MAX_BATCH];
+  // what the plan reads lies together: 32 requests' own fields a line apart take the constant cache microseconds to
+  // bring in, in every block of every launch
+  int32_t seq[VC_MAX_BATCH], n_rows[VC_MAX_BATCH];
+  int32_t tok_begin[VC_MAX_BATCH];   // first query token of each request, INT32_MAX behind the last one
   int32_t unit_begin[VC_MAX_BATCH];  // first (head, unit) of each request; with lanes: head alone
+  int32_t mask_words[VC_MAX_BATCH];
+  const bf16* q[VC_MAX_BATCH];
+  bf16* o[VC_MAX_BATCH];
+  const uint32_t* mask[VC_MAX_BATCH];
   int32_t B, Hq, Hkv, G, n_tok;
   int32_t few;                       // 1: the kernel for few rows, whose tiles are chunks and whose CTAs are warps
   int32_t lanes;                     // units of every head, each with CTAs of its own (c % lanes); 1: in one sequence
@@ -76,6 +83,7 @@ struct TreeMaps {
 struct TreePlan {
   int32_t cost_begin[VC_MAX_BATCH];  // of each request in the sequence of costs
   int32_t ctx[VC_MAX_BATCH], n[VC_MAX_BATCH];  // rows of context, and with the tokens' rows
+  int32_t rows[VC_MAX_BATCH];        // query rows of a KV head
   int32_t total, ctas, each, more;   // cost; CTAs of a lane with work; a range's cost, and how many have one more
 };
 
@@ -88,14 +96,15 @@ __device__ __forceinline__ int tile_cost(const TreeParams& p, int rows) {
 __device__ __forceinline__ int tiles_of(const TreeParams& p, int n) { return p.few ? (n + FK - 1) / FK : (n + TN - 1) / TN; }
 
 __device__ __forceinline__ void tree_plan(const TreeParams& p, TreePlan* s, int lane, bool tell) {
-  int n = 0, ctx = 0, cost = 0;
+  int n = 0, ctx = 0, cost = 0, rows = 0;
   if (lane < p.B) {
-    const TreeReqDev& r = p.req[lane];
-    const int held = p.kv.held_of(r.seq), len = p.kv.len[r.seq], cap = held << p.kv.shift;
+    const int seq = p.seq[lane], tokens = p.n_rows[lane];
+    const int held = p.kv.held_of(seq), len = p.kv.len[seq], cap = held << p.kv.shift;
     ctx = min(max(len, 0), cap);
-    n = (int)min((int64_t)cap, (int64_t)ctx + r.n_rows);
-    if (tell && (ctx != len || n - ctx != r.n_rows)) set_status(p.dev_status, VC_DEV_PAGES);
-    cost = p.Hkv * tiles_of(p, n) * tile_cost(p, r.n_rows * p.G);
+    n = (int)min((int64_t)cap, (int64_t)ctx + tokens);
+    if (tell && (ctx != len || n - ctx != tokens)) set_status(p.dev_status, VC_DEV_PAGES);
+    rows = tokens * p.G;
+    cost = p.Hkv * tiles_of(p, n) * tile_cost(p, rows);
   }
   int end = cost;
 #pragma unroll
@@ -106,6 +115,7 @@ __device__ __forceinline__ void tree_plan(const TreeParams& p, TreePlan* s, int 
   s->cost_begin[lane] = end - cost;
   s->ctx[lane] = ctx;
   s->n[lane] = n;
+  s->rows[lane] = rows;
   if (lane == 31) {
     s->total = end;
     const int ctas = min(p.n_cta, max(end / p.least, end > 0));
@@ -141,7 +151,7 @@ struct TPiece {
   __device__ __forceinline__ bool paired(int n) const { return split && !short_one(n); }
   __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == tiles; }
   __device__ __forceinline__ void fit(const TreeParams& p, const TreePlan& s) {
-    rows = min(TU, p.req[g].n_rows * p.G - u * TU);
+    rows = min(TU, s.rows[g] - u * TU);
     tiles = (s.n[g] + TN - 1) / TN;
     split = rows <= TM;
   }
@@ -149,7 +159,7 @@ struct TPiece {
   __device__ __forceinline__ void next(const TreeParams& p, const TreePlan& s) {
     at += cost() * tiles;
     if (!valid()) return;
-    if (p.lanes > 1 || ++u == units_of(p.req[g].n_rows * p.G)) {
+    if (p.lanes > 1 || ++u == units_of(s.rows[g])) {
       if (p.lanes == 1) u = 0;
       if (++hk == p.Hkv) {
         hk = 0;
@@ -175,7 +185,7 @@ struct TSteps {
     stride = q.split ? TN : TS;
     const int end = min(n, q.j1 * TN);
     count = end > beg ? (end - beg + stride - 1) / stride : 0;
-    blind = p.req[q.g].mask ? ctx : ctx + (q.u * TU + (q.split ? 0 : w * TM)) / p.G + 1;
+    blind = p.mask[q.g] ? ctx : ctx + (q.u * TU + (q.split ? 0 : w * TM)) / p.G + 1;
     const int clear = min(blind, n) - TS - beg;
     full = min(count, clear >= 0 ? clear / stride + 1 : 0);
   }
@@ -207,7 +217,7 @@ __device__ __forceinline__ TPiece tree_first(const TreeParams& p, const TreePlan
   q.g = 0;
   for (int b = 1; b < p.B; ++b)  // the last request that starts at or before; one without tiles starts where the next does
     if (s.cost_begin[b] <= beg) q.g = b;
-  const int rows = p.req[q.g].n_rows * p.G, tiles = (s.n[q.g] + TN - 1) / TN, units = units_of(rows);
+  const int rows = s.rows[q.g], tiles = (s.n[q.g] + TN - 1) / TN, units = units_of(rows);
   const int head = tiles * tile_cost(p, rows);
   int rem = beg - s.cost_begin[q.g];
   q.hk = rem / head;
@@ -331,7 +341,10 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
   TPiece* s_first = reinterpret_cast<TPiece*>(s_sum + 2 * TM);  // the CTA's first piece
   TreePlan& plan = *reinterpret_cast<TreePlan*>(s_first + 1);
 
-  if (warp == 12) tc05::alloc(tslot, C::TCOLS);
+  if (warp == 12) {
+    if (lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.kv[lane]) : "memory");
+    tc05::alloc(tslot, C::TCOLS);
+  }
   if (warp == 13) {
     pdl_wait();  // lengths are the kernel's before's
     tree_plan(p, &plan, lane, blockIdx.x == 0);
@@ -391,7 +404,7 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
       bool ok = true;
       for (; q.valid() && ok; q.next(p, plan)) {
         const int n = plan.n[q.g], pages = (n + p.kv.rows() - 1) >> shift;
-        const int32_t* table = p.kv.pages_of(p.req[q.g].seq);
+        const int32_t* table = p.kv.pages_of(p.seq[q.g]);
         auto look = [&](int j) { return mine && j * per + pi < pages ? __ldg(table + j * per + pi) : 0; };
         int page = look(q.j0);
         for (int j = q.j0; j < q.j1 && ok; ++j, ++it) {
@@ -524,9 +537,8 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
     auto fetch = [&]() {
       for (; q.valid(); g += q.j1 - q.j0, q.next(p, plan)) {
         if (q.idle(w, plan.n[q.g])) continue;
-        const TreeReqDev& R = p.req[q.g];
         const int ru = q.split ? rt : w * TM + rt, row = q.u * TU + ru, tok = row / p.G;  // row of the unit, of the head
-        const bf16* src = ru < q.rows ? R.q + ((size_t)tok * p.Hq + q.hk * p.G + (row - tok * p.G)) * D : nullptr;  // this thread's row
+        const bf16* src = ru < q.rows ? p.q[q.g] + ((size_t)tok * p.Hq + q.hk * p.G + (row - tok * p.G)) * D : nullptr;  // this thread's row
         // the warp's 32 rows, a row's 16-byte pieces in neighbouring lanes (a lane per row would touch 32 lines a load)
         constexpr int PR = D / 8, RW = 32 / PR;  // pieces of a row, rows a load
 #pragma unroll
@@ -629,15 +641,16 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
       if (!q.valid()) break;
       have = true;
       paired = q.paired(plan.n[q.g]);
-      const TreeReqDev& R = p.req[q.g];
       const int ru = q.split ? rt : w * TM + rt;
       row_ok = ru < q.rows;
       const bool alive = __any_sync(0xffffffffu, row_ok);  // a warp without rows only keeps step
       const int row = q.u * TU + ru, tl = row / p.G;
-      part = (lane_slot + p.unit_begin[q.g] + (p.lanes > 1 ? q.hk : q.hk * units_of(R.n_rows * p.G) + q.u)) * p.slot_rows + ru;
-      out = q.whole() && row_ok ? R.o + ((size_t)tl * p.Hq + q.hk * p.G + (row - tl * p.G)) * D : nullptr;
+      part = (lane_slot + p.unit_begin[q.g] + (p.lanes > 1 ? q.hk : q.hk * units_of(plan.rows[q.g]) + q.u)) * p.slot_rows + ru;
+      out = q.whole() && row_ok ? p.o[q.g] + ((size_t)tl * p.Hq + q.hk * p.G + (row - tl * p.G)) * D : nullptr;
       const int n = plan.n[q.g], ctx = plan.ctx[q.g];
-      const uint32_t* mrow = R.mask && row_ok ? R.mask + (size_t)tl * R.mask_words : nullptr;
+      const bool masked = p.mask[q.g] != nullptr;
+      const int words = p.mask_words[q.g];
+      const uint32_t* mrow = masked && row_ok ? p.mask[q.g] + (size_t)tl * words : nullptr;
       const TSteps steps(p, plan, q, w);
       m_run = -INFINITY, l_run = 0.f;
       for (int i = 0; i < steps.count; ++i, ++t) {
@@ -661,8 +674,8 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
           tc05::wait_ld();
           if (tail) {
             const int k0 = steps.beg + i * steps.stride;
-            if (R.mask) {
-              mask_bits(mrow, R.mask_words, k0 - ctx, n - k0, see_lo, see_hi);
+            if (masked) {
+              mask_bits(mrow, words, k0 - ctx, n - k0, see_lo, see_hi);
             } else {
               const int last = min(ctx + tl, n - 1) - k0;
               see_lo = last >= 31 ? 0xffffffffu : last < 0 ? 0u : (2u << last) - 1u;
@@ -676,13 +689,42 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
           }
           // P = 2^(x scale - m), bf16, over S: the MMA wants both operands in one 16-bit type, and V is bf16 (its range
           // is not fp16's). A weight is off by 2^-8 of itself at most. Sums and lse take the weights unrounded.
-          // The running maximum is taken as it is: the row's new one is found alongside, and only when it is larger by
-          // more than 2^8 (or this is the piece's first step) is m moved, O rescaled after the P V before, and P
+          // m is the row's maximum when it was last looked for: as long as a step's weights add up to no more than
+          // 2^10 it is kept (no weight is larger then, and a search in every step cost 15 us of 393 over 32768 keys).
+          // Past that, and in the piece's first step, the maximum is found, O rescaled after the P V before, and P
           // computed again. TMEM loads and stores are warp-collective: the warp does it together.
           uint32_t r[TS / 2];
-          float u0, u1, mx = -INFINITY, my = -INFINITY, mz = -INFINITY, mw = -INFINITY;
+          float sum = 0.f;
 #pragma unroll 1
-          for (int again = 0; again < 2; ++again) {
+          for (bool look = i == 0;; look = true) {
+            if (look) {
+              float top = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < TS; e += 2) top = max3f(top, x[e], x[e + 1]);
+              const float m_new = fmaxf(m_run, top * p.scale_log2);
+              float f = 1.f;
+              if (m_new > m_run) {
+                f = ex2_approx(m_run - m_new);
+                l_run *= f;
+                m_run = m_new;
+              }
+              if (i > 0) {
+                if (!pv_done(t - 1)) {
+                  ok = false;
+                  break;
+                }
+                tc05::fence_after();
+#pragma unroll 1
+                for (int cb = 0; cb < D / 32; ++cb) {
+                  uint32_t o[32];
+                  tc05::ld32(tO + cb * 32, o);
+                  tc05::wait_ld();
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tc05::st32(tO + cb * 32, o);
+                }
+              }
+            }
             const float mu = m_run == -INFINITY ? 0.f : m_run;
             const uint64_t sc = f2_pack(p.scale_log2, p.scale_log2), nm = f2_pack(-mu, -mu);
             uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
@@ -693,42 +735,16 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
               const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
               acc[e & 3] = f2_add(acc[e & 3], f2_pack(p0, p1));
               r[e] = pack_bf16x2(p0, p1);
-              float& m = (e & 3) == 0 ? mx : (e & 3) == 1 ? my : (e & 3) == 2 ? mz : mw;
-              m = max3f(m, x[2 * e], x[2 * e + 1]);
             }
+            float u0, u1;
             f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), u0, u1);
-            if (again) break;
-            const float m_new = fmaxf(m_run, fmaxf(fmaxf(mx, my), fmaxf(mz, mw)) * p.scale_log2);
-            const bool need = m_new > m_run + 8.f;  // from -infinity, any finite score
-            if (!__any_sync(0xffffffffu, need)) break;
-            if (i == 0) {
-              m_run = m_new;
-              continue;
-            }
-            if (!pv_done(t - 1)) {
-              ok = false;
-              break;
-            }
-            tc05::fence_after();
-            float f = 1.f;
-            if (need) {
-              f = ex2_approx(m_run - m_new);
-              l_run *= f;
-              m_run = m_new;
-            }
-#pragma unroll 1
-            for (int cb = 0; cb < D / 32; ++cb) {
-              uint32_t o[32];
-              tc05::ld32(tO + cb * 32, o);
-              tc05::wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tc05::st32(tO + cb * 32, o);
-            }
+            sum = u0 + u1;
+            // a row that has seen nothing yet has no m: its weights say nothing of how large its scores are
+            if (look || !__any_sync(0xffffffffu, sum > 1024.f || m_run == -INFINITY)) break;
           }
           if (!ok) break;
           tc05::st32(tP, r);
-          l_run += u0 + u1;
+          l_run += sum;
           tc05::wait_st();
         }
         // A step with keys that some rows do not see: a weight of 0 would carry an infinite or NaN value row to
@@ -881,9 +897,10 @@ __global__ void __launch_bounds__(FWARPS * 32, FCTAS) tree_few_kernel(const __gr
   constexpr int RS = 32 / PC;  // rows a load of the warp
   const int prow = lane / PC, pcol = lane % PC;
   for (int at = beg; at < end;) {
-    const TreeReqDev& R = p.req[g];
-    const int n = plan.n[g], ctx = plan.ctx[g], j0 = rem, j1 = min(tiles, rem + end - at), rows = R.n_rows * p.G;
-    const int32_t* table = p.kv.pages_of(R.seq);
+    const int n = plan.n[g], ctx = plan.ctx[g], j0 = rem, j1 = min(tiles, rem + end - at), rows = plan.rows[g];
+    const int32_t* table = p.kv.pages_of(p.seq[g]);
+    const bool masked = p.mask[g] != nullptr;
+    const int words = p.mask_words[g];
     // pages of the chunks jb .. jb + 31, a lane each; those that are not the pool's count as none
     auto look = [&](int jb) {
       int page = -1;
@@ -925,15 +942,15 @@ __global__ void __launch_bounds__(FWARPS * 32, FCTAS) tree_few_kernel(const __gr
     for (int e = 0; e < 2; ++e) {
       const int r = qrow + 8 * e;
       tok[e] = r < rows ? r / p.G : 0;
-      mrow[e] = R.mask && r < rows ? R.mask + (size_t)tok[e] * R.mask_words : nullptr;
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(R.q + ((size_t)tok[e] * p.Hq + hk * p.G + (r - tok[e] * p.G)) * D + qcol);
+      mrow[e] = masked && r < rows ? p.mask[g] + (size_t)tok[e] * words : nullptr;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q[g] + ((size_t)tok[e] * p.Hq + hk * p.G + (r - tok[e] * p.G)) * D + qcol);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         qf[kk][e] = r < rows ? __ldcg(src + kk * 8) : 0u;
         qf[kk][2 + e] = r < rows ? __ldcg(src + kk * 8 + 4) : 0u;
       }
     }
-    const int blind = R.mask ? ctx : ctx + 1;  // the first key that some row may not see
+    const int blind = masked ? ctx : ctx + 1;  // the first key that some row may not see
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, acc[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
@@ -967,7 +984,7 @@ __global__ void __launch_bounds__(FWARPS * 32, FCTAS) tree_few_kernel(const __gr
       if (tail) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          see[e] = few_bits(mrow[e], R.mask_words, R.mask != nullptr, tok[e], k0 - ctx, n - k0);
+          see[e] = few_bits(mrow[e], words, masked, tok[e], k0 - ctx, n - k0);
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -1070,7 +1087,7 @@ __global__ void __launch_bounds__(FWARPS * 32, FCTAS) tree_few_kernel(const __gr
       if (r < rows) {
         const float inv = l[e] != 0.f ? 1.f / l[e] : 0.f;
         if (whole) {
-          bf16* dst = R.o + ((size_t)tok[e] * p.Hq + hk * p.G + (r - tok[e] * p.G)) * D + qcol;
+          bf16* dst = p.o[g] + ((size_t)tok[e] * p.Hq + hk * p.G + (r - tok[e] * p.G)) * D + qcol;
 #pragma unroll
           for (int i = 0; i < D / 8; ++i)
             *reinterpret_cast<uint32_t*>(dst + 8 * i) = pack_bf16x2(acc[i][2 * e] * inv, acc[i][2 * e + 1] * inv);
@@ -1108,15 +1125,15 @@ struct TParts {
 
 // Output row `id` of the call (token, query head): its partials and its place.
 template <int D>
-__device__ __forceinline__ TParts tree_parts(const TreeParams& p, const TreePlan& plan, int64_t id, bf16*& dst) {
+__device__ __forceinline__ TParts tree_parts(const TreeParams& p, const TreePlan& plan, const int32_t* tok_begin, int64_t id, bf16*& dst) {
   const int tok = (int)(id / p.Hq), hq = (int)(id - (int64_t)tok * p.Hq), hk = hq / p.G;
   int b = 0;
-  for (int i = 1; i < p.B; ++i)
-    if (p.req[i].tok_begin <= tok) b = i;
-  const TreeReqDev& R = p.req[b];
-  const int i = tok - R.tok_begin, r = i * p.G + hq - hk * p.G;  // token of the request, row of the head
-  dst = R.o + ((size_t)i * p.Hq + hq) * D;
-  const int rows = R.n_rows * p.G, u = p.few ? 0 : r / TU;
+#pragma unroll
+  for (int k = VC_MAX_BATCH / 2; k > 0; k >>= 1)
+    if (tok_begin[b + k] <= tok) b += k;
+  const int i = tok - tok_begin[b], r = i * p.G + hq - hk * p.G;  // token of the request, row of the head
+  dst = p.o[b] + ((size_t)i * p.Hq + hq) * D;
+  const int rows = plan.rows[b], u = p.few ? 0 : r / TU;
   const int cost = p.few || rows - u * TU <= TM ? 1 : 2, tiles = tiles_of(p, plan.n[b]);
   TParts q{0, 0, p.slot_rows};
   if (tiles == 0) return q;
@@ -1136,19 +1153,21 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
   constexpr int E = D / 32;  // channels a lane
   constexpr int PF = 4;      // partials in flight
   __shared__ TreePlan plan;
+  __shared__ int32_t tok_begin[VC_MAX_BATCH];
   __shared__ float s_sum[8];
   __shared__ float s_acc[8][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wpr = p.merge_warps, part = warp % wpr;  // warps of a row, this one among them
   const int64_t id = (int64_t)blockIdx.x * (8 / wpr) + warp / wpr;
   bool live = id < (int64_t)p.n_tok * p.Hq;
+  if (threadIdx.x < VC_MAX_BATCH) tok_begin[threadIdx.x] = p.tok_begin[threadIdx.x];
   pdl_launch_dependents();
   pdl_wait();
   if (warp == 0) tree_plan(p, &plan, lane, false);
   __syncthreads();
   TParts q{0, 0, 0};
   bf16* dst = nullptr;
-  if (live) q = tree_parts<D>(p, plan, id, dst);
+  if (live) q = tree_parts<D>(p, plan, tok_begin, id, dst);
   if (q.count == 1) {  // written by the piece itself: nothing to add up, the block's barrier is kept
     live = false;
     q.count = 0;
@@ -1221,7 +1240,9 @@ template <int D>
 __global__ void __launch_bounds__(256, 4) tree_merge_rows_kernel(const __grid_constant__ TreeParams p) {
   constexpr int Q = D / 4 / TSUB;  // float4 a lane: number sl, sl + TSUB, ... of the row
   __shared__ TreePlan plan;
+  __shared__ int32_t tok_begin[VC_MAX_BATCH];
   const int lane = threadIdx.x & 31, sl = lane % TSUB, first = lane - sl;
+  if (threadIdx.x < VC_MAX_BATCH) tok_begin[threadIdx.x] = p.tok_begin[threadIdx.x];
   pdl_launch_dependents();
   pdl_wait();
   if (threadIdx.x < 32) tree_plan(p, &plan, lane, false);
@@ -1232,7 +1253,7 @@ __global__ void __launch_bounds__(256, 4) tree_merge_rows_kernel(const __grid_co
     bool live = id < all;
     TParts q{0, 0, 0};
     bf16* dst = nullptr;
-    if (live) q = tree_parts<D>(p, plan, id, dst);
+    if (live) q = tree_parts<D>(p, plan, tok_begin, id, dst);
     if (q.count == 1) {  // written by the piece itself
       live = false;
       q.count = 0;
@@ -1358,8 +1379,16 @@ cudaError_t launch_tree_attn(const TreeArgs& a, cudaStream_t s, vc_status* st) {
   int64_t cost = 0, units = 0, same = host_units((int64_t)a.req[0].n_rows * G);
   p.slot_rows = 1;
   p.least = 1;
+  for (int b = a.B; b < VC_MAX_BATCH; ++b) p.tok_begin[b] = INT32_MAX;
   for (int b = 0; b < a.B; ++b) {
-    p.req[b] = a.req[b];
+    const TreeReqDev& r = a.req[b];
+    p.seq[b] = r.seq;
+    p.n_rows[b] = r.n_rows;
+    p.tok_begin[b] = r.tok_begin;
+    p.mask_words[b] = r.mask_words;
+    p.q[b] = r.q;
+    p.o[b] = r.o;
+    p.mask[b] = r.mask;
     const int64_t rows = (int64_t)a.req[b].n_rows * G, u = host_units(rows);
     if (u != same || rows - (u - 1) * TU <= TM) same = 1;
     const int sr = p.few ? (int)rows : slot_rows_of(rows);

@@ -542,14 +542,14 @@ struct RopePageReqDev {
   int64_t off_stride;
   bf16* q_out;
   int32_t seq;
-  int32_t tok_begin;  // first token of the request in the call's token sequence
 };
 struct RopePageParams {
   PagedDev kv;
+  int32_t tok_begin[VC_MAX_BATCH];  // first token of each request in the call's token sequence, INT32_MAX behind the last
   RopePageReqDev req[VC_MAX_BATCH];
   double turns[VC_ROPE_MAX_PAIRS];  // turns a position: theta / 2 pi
   int8_t axis[VC_ROPE_MAX_PAIRS];
-  int32_t B, Hq, Hkv, rot, inter, n_tok;
+  int32_t Hq, Hkv, rot, inter, n_tok;
   float amp;
   int32_t* dev_status;
 };
