@@ -422,6 +422,13 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
               ok = false;
               break;
             }
+            // All CTAs' rings together are 24 MB, 4 us of DRAM's time, and the first piece's Q would queue behind them
+            // (16 x 1000 keys: 6.8 us for it): it goes ahead of all but the first tile of K.
+            if (it == 0 && kv == 1 && (!twait_warp(&qfull[0], 0, p.dev_status, s_abort) ||
+                                       (!q.idle(1, n) && !twait_warp(&qfull[1], 0, p.dev_status, s_abort)))) {
+              ok = false;
+              break;
+            }
             if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(cnt << shift) * 128 * C::KB);
             __syncwarp();
             if (load) {
@@ -602,30 +609,32 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
             to[e] = reinterpret_cast<bf16*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), r0 + 8 * e));
             on[e] = (rows_ok >> (r0 + 8 * e)) & 1u;
           }
+          constexpr int NC = D / 64;  // blocks of 32 channels at a time
 #pragma unroll 1
-          for (int cb = cb0; cb < cb1; ++cb) {
-            uint32_t r[16];
-            tc05::ld16x256_x4(tO + ((uint32_t)(hh * 16) << 16) + cb * 32, r);  // warp-collective: every lane loads
-            tc05::wait_ld();
-            float v[16];
+          for (int cb = cb0; cb < cb1; cb += NC) {
+            uint32_t r[NC][16], o[NC][16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]) * a[(k >> 1) & 1];
-            if (paired) {
-              tc05::ld16x256_x4(tX + ((uint32_t)(hh * 16) << 16) + cb * 32, r);
-              tc05::wait_ld();
-#pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] += __uint_as_float(r[k]) * b[(k >> 1) & 1];
+            for (int c = 0; c < NC; ++c) {  // warp-collective: every lane loads
+              tc05::ld16x256_x4(tO + ((uint32_t)(hh * 16) << 16) + (cb + c) * 32, r[c]);
+              if (paired) tc05::ld16x256_x4(tX + ((uint32_t)(hh * 16) << 16) + (cb + c) * 32, o[c]);
             }
+            tc05::wait_ld();
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int c = 0; c < NC; ++c)
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (on[e]) {
-                  const float x = v[4 * k + 2 * e], y = v[4 * k + 2 * e + 1];
-                  if (to[e])
-                    *reinterpret_cast<uint32_t*>(to[e] + cb * 32 + 8 * k + 2 * (lane & 3)) = pack_bf16x2(x, y);
-                  else
-                    *reinterpret_cast<float2*>(o_row0 + (size_t)(r0 + 8 * e) * D + cb * 32 + 8 * k) = make_float2(x, y);
+              for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  float x = __uint_as_float(r[c][4 * k + 2 * e]) * a[e], y = __uint_as_float(r[c][4 * k + 2 * e + 1]) * a[e];
+                  if (paired) {
+                    x += __uint_as_float(o[c][4 * k + 2 * e]) * b[e];
+                    y += __uint_as_float(o[c][4 * k + 2 * e + 1]) * b[e];
+                  }
+                  const int at = (cb + c) * 32 + 8 * k;
+                  if (on[e] && to[e])
+                    *reinterpret_cast<uint32_t*>(to[e] + at + 2 * (lane & 3)) = pack_bf16x2(x, y);
+                  else if (on[e])
+                    *reinterpret_cast<float2*>(o_row0 + (size_t)(r0 + 8 * e) * D + at) = make_float2(x, y);
                 }
           }
         }
@@ -914,6 +923,22 @@ __global__ void __launch_bounds__(FWARPS * 32, FCTAS) tree_few_kernel(const __gr
       return page;
     };
     int pages = look(j0), more = look(j0 + 32);  // those in use and the next ones
+    // Q, asked for ahead of all K and V, in A-fragment order: rows qrow and qrow + 8, channels 16 kk + qcol (+ 8)
+    uint32_t qf[D / 16][4];
+    int tok[2];
+    const uint32_t* mrow[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = qrow + 8 * e;
+      tok[e] = r < rows ? r / p.G : 0;
+      mrow[e] = masked && r < rows ? p.mask[g] + (size_t)tok[e] * words : nullptr;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q[g] + ((size_t)tok[e] * p.Hq + hk * p.G + (r - tok[e] * p.G)) * D + qcol);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qf[kk][e] = r < rows ? __ldcg(src + kk * 8) : 0u;
+        qf[kk][2 + e] = r < rows ? __ldcg(src + kk * 8 + 4) : 0u;
+      }
+    }
     // half chunk `v` (0: K, 1: V) of chunk j into its place; one commit whether there is one or not
     auto load = [&](int j, int v) {
       const int page = __shfl_sync(0xffffffffu, pages, (j - j0) & 31);
@@ -934,22 +959,6 @@ __global__ void __launch_bounds__(FWARPS * 32, FCTAS) tree_few_kernel(const __gr
     load(j0, 1);
     load(j0 + 1, 0);
     load(j0 + 1, 1);
-    // Q in A-fragment order: rows qrow and qrow + 8, channels 16 kk + qcol (+ 8)
-    uint32_t qf[D / 16][4];
-    int tok[2];
-    const uint32_t* mrow[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = qrow + 8 * e;
-      tok[e] = r < rows ? r / p.G : 0;
-      mrow[e] = masked && r < rows ? p.mask[g] + (size_t)tok[e] * words : nullptr;
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q[g] + ((size_t)tok[e] * p.Hq + hk * p.G + (r - tok[e] * p.G)) * D + qcol);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        qf[kk][e] = r < rows ? __ldcg(src + kk * 8) : 0u;
-        qf[kk][2 + e] = r < rows ? __ldcg(src + kk * 8 + 4) : 0u;
-      }
-    }
     const int blind = masked ? ctx : ctx + 1;  // the first key that some row may not see
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, acc[D / 8][4];
 #pragma unroll
@@ -1356,7 +1365,7 @@ cudaError_t launch_tree_t(const TreeParams& p, const TreeMaps& maps, cudaStream_
 size_t tree_workspace_size(const vc_shape* s, int32_t max_rows) {
   const int64_t rows = (int64_t)max_rows * (s->Hq / s->Hkv), units = host_units(rows), heads = (int64_t)s->B * s->Hkv;
   const int64_t few = (few_warps() + heads) * (rows < FR ? rows : FR), many = (tree_sms() + heads * units) * slot_rows_of(rows);
-  return (size_t)(rows <= FR || few > many ? few : many) * (s->d + 1) * sizeof(float) + 256;
+  return (size_t)(few > many ? few : many) * (s->d + 1) * sizeof(float) + 256;
 }
 
 cudaError_t launch_tree_attn(const TreeArgs& a, cudaStream_t s, vc_status* st) {
@@ -1374,7 +1383,10 @@ cudaError_t launch_tree_attn(const TreeArgs& a, cudaStream_t s, vc_status* st) {
   p.dev_status = a.dev_status;
   int most = 0;
   for (int b = 0; b < a.B; ++b) most = a.req[b].n_rows > most ? a.req[b].n_rows : most;
-  p.few = (int64_t)most * G <= FR;
+  // Up to 8 rows, or 16 with the smallest pages, for the kernel without tensor memory (us of it and of the other: 32 x
+  // 1000 keys, 4 rows a head: 43.7, 49.8; 32 x 200: 25.2, 31.4; 32 x 8200 from pages of 16: 186, 195, of 128: 187, 181;
+  // 8 x 32768 keys, 16 rows, from pages of 64: 193, 183, of 16: 191, 192)
+  p.few = (int64_t)most * G <= (a.kv.shift == 4 ? FR : FR / 2);
   const int64_t tiles = ((int64_t)a.kv.max_pages << a.kv.shift) / (p.few ? FK : TN) + 1;
   int64_t cost = 0, units = 0, same = host_units((int64_t)a.req[0].n_rows * G);
   p.slot_rows = 1;
