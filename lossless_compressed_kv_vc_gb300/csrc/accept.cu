@@ -8,7 +8,7 @@
 // already hold the right token: a_i == draft_i for i < n, and a_n is the correction or the bonus.
 //
 // Trees of drafts: ancestor masks and depths, and acceptance along the tree, further down.
-#include "vc_internal.cuh"
+#include "paged.cuh"
 
 #include <limits.h>
 #include <math.h>

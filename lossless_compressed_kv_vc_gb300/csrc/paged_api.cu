@@ -1,6 +1,6 @@
 // C-ABI entry points of drafted trees over a cache of pages (vc_paged_kv): argument validation and launches.
 // Validation failures return a status and launch nothing.
-#include "vc_internal.cuh"
+#include "paged.cuh"
 
 #include <math.h>
 #include <string.h>

@@ -5,7 +5,7 @@
 // dependent loads, 3 to 6 us), and whatever must not depend on the order of threads is settled by position in
 // the call: pages are taken from and put on the stack at places given by a prefix sum. What is copied, K and V,
 // is left to grids that fill the GPU.
-#include "vc_internal.cuh"
+#include "paged.cuh"
 
 #include <limits.h>
 

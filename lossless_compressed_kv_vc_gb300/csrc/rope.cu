@@ -10,7 +10,7 @@
 // bound by DRAM. A thread's first pieces are on their way while the angles are made (prompt chunks, 336 MB: 59.0
 // us without that, 51.6 with it, 0.96 of the copy rate; with two or three items a thread in flight, and fewer
 // CTAs on an SM for their registers, 60 and 58).
-#include "vc_internal.cuh"
+#include "paged.cuh"
 
 namespace vc {
 

@@ -25,6 +25,7 @@
 // What a query row may not see: keys get -infinity by the row's bits of the mask; value rows behind the last
 // token (whatever the page holds there) are zeroed in shared memory, and where a step has a value row that is not
 // finite and not for all, the threads add up the rows they see themselves.
+#include "paged.cuh"
 #include "tc05.cuh"
 
 #include <cudaTypedefs.h>
