@@ -68,7 +68,7 @@ struct RopePageParams {
   int32_t tok_begin[VC_MAX_BATCH];  // first token of each request in the call's token sequence, INT32_MAX behind the last
   RopePageReqDev req[VC_MAX_BATCH];
   double turns[VC_ROPE_MAX_PAIRS];  // turns a position: theta / 2 pi
-  int8_t axis[VC_ROPE_MAX_PAIRS];
+  uint64_t axis[2];                 // two bits a pair: each thread's own byte of the parameters would be read one by one
   int32_t Hq, Hkv, rot, inter, n_tok;
   float amp;
   int32_t* dev_status;

@@ -201,7 +201,8 @@ vc_status vc_rope_pages(const vc_shape* shape, const vc_rope_axes* axes, const v
   for (int j = 0; j < rope.rot_dim / 2; ++j) {
     if (!isfinite(rope.freq[j]) || axes->axis[j] < 0 || axes->axis[j] >= axes->n_axes) return VC_ERR_INVALID;
     p.turns[j] = rope.freq[j] / (2 * M_PI);
-    p.axis[j] = (int8_t)axes->axis[j];
+    p.axis[j / 32] |= (uint64_t)axes->axis[j] << (2 * (j % 32));
+    static_assert(VC_ROPE_MAX_AXES <= 4 && VC_ROPE_MAX_PAIRS == 64, "two bits a pair");
   }
   int64_t total = 0;
   int n = 0;

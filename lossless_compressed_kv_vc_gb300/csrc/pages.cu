@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(kPageThreads) reserve_plan_kernel(const __grid
     const vc_reserve_req q = p.req[here ? r : 0];
     int held = 0, n = 0, old = -1, refs = 0, more = 0;
     bool ok = here, shared = false;
+    const int avail = min(max(*kv.n_free, 0), kv.n_pages);
     if (here) {
       held = kv.held_of(q.seq);
       n = context_rows(kv, q.seq, held, ok);
@@ -79,7 +80,6 @@ __global__ void __launch_bounds__(kPageThreads) reserve_plan_kernel(const __grid
           ok = false;
       }
     }
-    const int avail = min(max(*kv.n_free, 0), kv.n_pages);
     // of the requests that go on in one page, each that takes a copy leaves it to one sequence less
     const unsigned same = __match_any_sync(0xffffffffu, ok && old >= 0 ? old : -1 - r), lt = (1u << r) - 1u;
     shared = ok && old >= 0 && refs - __popc(same & lt) > 1;

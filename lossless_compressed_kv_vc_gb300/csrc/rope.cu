@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_pages_kernel(const __gri
   };
   if ((int)threadIdx.x < n) load(threadIdx.x);  // where it goes is found below
   if ((int)threadIdx.x < p.rot / 2) {
-    const int64_t off = r.off ? r.off[p.axis[threadIdx.x] * r.off_stride + t] : t;
+    const int64_t off = r.off ? r.off[(int)(p.axis[threadIdx.x / 32] >> (2 * (threadIdx.x % 32)) & 3) * r.off_stride + t] : t;
     double turn = (double)(kv.next[r.seq] + off) * turns;
     turn -= rint(turn);
     float sn, cn;
