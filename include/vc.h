@@ -701,8 +701,9 @@ vc_status vc_tree_mask(int32_t B, int32_t N_max, const int32_t* parent, const in
  * held are seen by none (VC_DEV_PAGES).
  * ws: vc_tree_workspace_size(shape, max_rows) bytes for calls of up to max_rows rows a request; no
  * initialisation; calls that overlap on the GPU must not share one.
- * Errors before anything is launched: VC_ERR_INVALID; VC_ERR_WORKSPACE; VC_ERR_UNSUPPORTED (calls whose
- * query rows, or tiles of rows by tiles of pages, reach 2^29). dev_status as for vc_prefix_attn. */
+ * Errors before anything is launched: VC_ERR_INVALID; VC_ERR_WORKSPACE; VC_ERR_UNSUPPORTED (more than 2^29 query
+ * rows, or so large a table that the sum over the requests of Hkv * ceil(n_rows * Hq / Hkv / 256) * max_pages * page
+ * / 16 passes 2^29). dev_status as for vc_prefix_attn. */
 typedef struct vc_tree_req {
   const void* q;         /* bf16 [n_rows][Hq][d] */
   void* o;               /* bf16 [n_rows][Hq][d] */

@@ -290,6 +290,14 @@ __device__ __forceinline__ void tarrive_if(uint64_t* bar, bool on) {
       : "memory");
 }
 
+// The values of TMEM loads are there; nothing made of them moves before this.
+template <int N>
+__device__ __forceinline__ void arrived(uint32_t (&r)[N]) {
+  tc05::wait_ld();
+#pragma unroll
+  for (int e = 0; e < N; ++e) asm volatile("" : "+r"(r[e]));
+}
+
 __device__ __forceinline__ bool broken_bf16x2(uint32_t w) {
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
@@ -400,11 +408,11 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
       const int shift = p.kv.shift, per = TN >> shift;  // pages a tile
       const int kb = lane / per, pi = lane - kb * per;
       const bool mine = kb < C::KB;
-      const bool once = p.lanes == 1;  // tiles that one CTA reads once leave L2 first
-      uint32_t it = 0;                 // tiles loaded
+      uint32_t it = 0, issued[2] = {0, 0};  // tiles; loads of K and of V on their way
       bool ok = true;
       for (; q.valid() && ok; q.next(p, plan)) {
         const int n = plan.n[q.g], pages = (n + p.kv.rows() - 1) >> shift;
+        const bool once = p.lanes == 1 && plan.rows[q.g] <= TU;  // tiles that one CTA reads once leave L2 first
         const int32_t* table = p.kv.pages_of(p.seq[q.g]);
         auto look = [&](int j) { return mine && j * per + pi < pages ? __ldg(table + j * per + pi) : 0; };
         int page = look(q.j0);
@@ -440,15 +448,18 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
                 tc05::tma_load_3d(dst, &maps.kv[kv], kb * 64, 0, page * p.Hkv + q.hk, &full[st]);
             }
             __syncwarp();
+            ++issued[kv];
           }
           page = ahead;
         }
       }
-      if (*s_abort && lane == 0) {  // drain (bounded): a ring's worth of loads may still be landing; `it` counts K and V
-                                    // of whole tiles, and one K more where the wait for V's place gave up
-        for (uint32_t i = it > C::KST ? it - C::KST : 0; i < it; ++i) mbar_wait_bounded(&kfull[i % C::KST], (i / C::KST) & 1, p.dev_status);
-        for (uint32_t i = it > C::VST ? it - C::VST : 0; i < it; ++i) mbar_wait_bounded(&vfull[i % C::VST], (i / C::VST) & 1, p.dev_status);
-      }
+      // what is on its way lands before the CTA leaves, whoever gave up (bounded)
+      if (lane == 0)
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t ring = kv ? C::VST : C::KST, end = issued[kv];
+          for (uint32_t i = end > ring ? end - ring : 0; i < end; ++i)
+            mbar_wait_bounded(&(kv ? vfull : kfull)[i % ring], (i / ring) & 1, p.dev_status);
+        }
       __syncwarp();
     } else if (warp < 12) {
       // ---- MMAs of chain w: S (warps 8, 9) a step ahead of the softmax, P V (10, 11) as soon as a step's P is there.
@@ -619,7 +630,11 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
               tc05::ld16x256_x4(tO + ((uint32_t)(hh * 16) << 16) + (cb + c) * 32, r[c]);
               if (paired) tc05::ld16x256_x4(tX + ((uint32_t)(hh * 16) << 16) + (cb + c) * 32, o[c]);
             }
-            tc05::wait_ld();
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              arrived(r[c]);
+              if (paired) arrived(o[c]);
+            }
 #pragma unroll
             for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -674,14 +689,15 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
         uint32_t see_lo = 0xffffffffu, see_hi = 0xffffffffu;  // keys of the step that the row sees
         if (alive) {
           float x[TS];
+          {
+            uint32_t lo[32], hi[32];
+            tc05::ld32(tP, lo);
+            tc05::ld32(tP + 32, hi);
+            arrived(lo);
+            arrived(hi);
 #pragma unroll
-          for (int c = 0; c < TS / 32; ++c) {
-            uint32_t r[32];
-            tc05::ld32(tP + c * 32, r);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(r[e]);
+            for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(lo[e]), x[32 + e] = __uint_as_float(hi[e]);
           }
-          tc05::wait_ld();
           if (tail) {
             const int k0 = steps.beg + i * steps.stride;
             if (masked) {
@@ -728,7 +744,7 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
                 for (int cb = 0; cb < D / 32; ++cb) {
                   uint32_t o[32];
                   tc05::ld32(tO + cb * 32, o);
-                  tc05::wait_ld();
+                  arrived(o);
 #pragma unroll
                   for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                   tc05::st32(tO + cb * 32, o);
@@ -803,20 +819,20 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
               uint32_t r[32];
               if (i > 0) {
                 tc05::ld32(tO + cb * 32, r);
-                tc05::wait_ld();
+                arrived(r);
               } else {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) r[e] = 0u;
               }
 #pragma unroll 1
               for (int kp = 0; kp < TS / 2; ++kp) {  // two keys a column; rare, so kept small
-                const uint32_t pw = tc05::ld1(tP + kp);
-                tc05::wait_ld();
+                uint32_t pw[1] = {tc05::ld1(tP + kp)};
+                arrived(pw);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   const int k = 2 * kp + e, kt = h * TS + k;
                   const bool sees = ((k < 32 ? see_lo : see_hi) >> (k & 31)) & 1u;
-                  const float pk = __uint_as_float(e ? pw & 0xffff0000u : pw << 16);
+                  const float pk = __uint_as_float(e ? pw[0] & 0xffff0000u : pw[0] << 16);
 #pragma unroll
                   for (int c = 0; c < 4; ++c) {
                     const int ch = cb * 4 + c;

@@ -545,6 +545,54 @@ def test_broken_rows_reach_only_those_that_see_them(vc, case, bad, tree):
     assert int(p.status.item()) == 0
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,page,n,N", [(8, 2, 64, 16, 700, 1), (8, 2, 64, 16, 700, 4), (8, 2, 64, 32, 700, 30),
+                                               (4, 4, 128, 64, 900, 200), (32, 4, 128, 64, 1000, 64)])
+@pytest.mark.parametrize("shape", ["rising", "falling", "steps", "late", "deep"])
+def test_scores_that_outgrow_the_first_ones(vc, Hq, Hkv, d, page, n, N, shape):
+    """Scores that rise or fall by a factor of up to 2^70 of weight along the keys, in opposite directions for different
+    rows: the maximum moves again and again, or not at all; rows that start far below zero; and a part of a chain that
+    sees nothing at first."""
+    g, rng = gen(19), np.random.default_rng(19)
+    p = build(vc, g, Hq, Hkv, d, page, [(n, N), (0, N)])
+    u = torch.nn.functional.normalize(torch.randn(d, generator=g, device="cuda"), dim=0)
+    reqs, see = [], []
+    for s, ctx in ((0, n), (1, 0)):
+        T = ctx + N
+        t = torch.arange(T, device="cuda").float()
+        c = {"rising": 100 * t / T, "falling": 100 - 100 * t / T, "late": torch.where(t >= T - 3, 100.0, 0.0),
+             "deep": torch.where(t < T // 2, -100.0, 0.0) + 20 * t / T,
+             "steps": torch.tensor(rng.uniform(-60, 60, T // 50 + 1), device="cuda").float()[(t // 50).long()]}[shape]
+        at = torch.arange(T, device="cuda")
+        pages = p.state["table"][s].long()[at // page]
+        k = 0.3 * torch.randn((T, Hkv, d), generator=g, device="cuda") + c[:, None, None] * u
+        p.k[pages, :, at % page] = k.bfloat16()
+        sign = torch.where(torch.rand((N, Hq, 1), generator=g, device="cuda") < 0.3, -1.0, 1.0)
+        q = (torch.randn((N, Hq, d), generator=g, device="cuda") * 0.5 + sign * u * np.sqrt(d) * 0.5).bfloat16()
+        w = rng.random((N, N)) < 0.2 if s else O.ancestors(random_tree(rng, N))[0]
+        reqs.append((s, q, torch.tensor(O.pack_mask(w, (N + 31) // 32), device="cuda")))
+        see.append(w)
+    check(vc, p, Hq, reqs, see, attend(vc, p, reqs))
+    assert int(p.status.item()) == 0
+
+
+def test_infinite_scores(vc):
+    """A context key with an infinite channel: rows whose product with it is -inf leave it out, the others are not finite,
+    as in the oracle."""
+    for Hq, Hkv, d, page, n, N in ((8, 2, 64, 16, 300, 1), (8, 2, 64, 32, 300, 20), (4, 2, 128, 64, 200, 130)):
+        g = gen(29)
+        p = build(vc, g, Hq, Hkv, d, page, [(n, N)])
+        p.k[int(p.ref.table[0, 77 // page]), :, 77 % page, 5] = float("inf")
+        q = randn(g, N, Hq, d)
+        o = attend(vc, p, [(0, q, None)])[0]
+        k, v = (f64(x) for x in p.rows(0, 0, n + N))
+        with np.errstate(invalid="ignore"):
+            ref = O.tree_attn(f64(q), k, v, np.tri(N, dtype=bool))
+        fine = np.isfinite(ref).all(-1)
+        assert fine.any() and not fine.all()
+        assert np.array_equal(torch.isfinite(o).all(-1).cpu().numpy(), fine)
+        assert_attn_close(o[torch.tensor(fine)][:, None], ref[fine][:, None])
+
+
 @pytest.mark.parametrize("Hq,Hkv,d,page", [(8, 2, 64, 16), (32, 8, 128, 64), (12, 2, 64, 128)])
 def test_a_batch_of_thirty_two(vc, Hq, Hkv, d, page):
     """All requests of a call, some without tokens, in an order that is not the sequences', two of one sequence."""
