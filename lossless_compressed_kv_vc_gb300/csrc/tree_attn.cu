@@ -20,7 +20,11 @@
 // itself. The loader's lanes fetch a tile page by page, each the pages that it looked up one tile before.
 //
 // S of 128 keys at a time would read Q from shared memory half as often, but leaves TMEM one S a chain: a tile then
-// waits for the P V before it (8 trees of 64 over 32768 keys: 537 us so, 420 with two S of 64 keys a chain).
+// waits for the P V before it (8 trees of 64 over 32768 keys, 64/8 heads of 128: 499 us so, 395 with two S of 64 keys).
+//
+// What bounds it: up to about 130 rows of a KV head DRAM (16 trees of 25 over up to 16300 rows, 40/8 heads of 128:
+// 946 MB in 158 us with the merge, 0.89 of the copy rate); above that each chain's loop S, softmax, P V, the next S
+// (the case above: 380 us, 1.45 PFLOP/s, 0.77 of the bf16 rate; 357 without any softmax).
 //
 // What a query row may not see: keys get -infinity by the row's bits of the mask; value rows behind the last
 // token (whatever the page holds there) are zeroed in shared memory, and where a step has a value row that is not
@@ -874,7 +878,9 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
 // (K or V) on their way with 16-byte asynchronous copies into its own ring, and multiplies with mma.sync: S = Q K^T
 // with Q in registers, P from S's accumulators as they lie, O += P V. The tcgen05 kernel's fixed part (tensor maps,
 // TMEM, barriers, two chains' start and end) is what this one does without, and a page of 16 rows is as good as a
-// larger one, where TMA boxes of 2 KB hold the other at 0.75 of the copy rate.
+// larger one, where TMA boxes of 2 KB hold the other back (32 tokens over 8200 rows, pages of 16: 186 us, the other
+// 195). Measured with 32 ragged requests of up to 8200 rows, 32/8 heads of 128: 939 MB in 144 us, 6.5 TB/s, which
+// is what reading alone reaches, and 21 us of start-up, plan and merge around it.
 template <int D>
 struct FCfg {
   static constexpr int HALF = FK * D * 2;             // bytes of a chunk's K or V
