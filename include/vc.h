@@ -571,7 +571,7 @@ size_t vc_evict_workspace_size(const vc_shape* shape, int32_t max_n);
  * fork's sources, which are only read. Calls on one pool are ordered by their stream or by events.
  * State that does not add up (a table entry outside the pool, a length beyond the pages held, rows to
  * be written where the sequence has no page or shares it) is never followed out of bounds: the rows
- * or pages it touches are skipped and dev_status receives VC_DEV_PAGES.
+ * or pages it touches are skipped (read as zeros by vc_tree_attn) and dev_status receives VC_DEV_PAGES.
  * Limits: page is 16, 32, 64 or 128; (n_pages + 1) * Hkv < 2^31 and max_pages * page <= 2^30
  * (VC_ERR_UNSUPPORTED). k and v 16-byte aligned, the others 4-byte. The device current to the calling
  * thread is the one that holds the buffers. */

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_argmax_kernel(TreeAcceptA
   pdl_launch_dependents();
   pdl_wait();
   const int row = blockIdx.x, b = row / a.N_max;
-  if (row - b * a.N_max >= min(__ldg(a.n_nodes + b), a.N_max)) return;
+  if (row - b * a.N_max >= min(a.n_nodes[b], a.N_max)) return;
   const int bi = row_argmax(a.logits + (size_t)row * a.V, a.V);
   if (threadIdx.x == 0) a.out_tokens[row] = bi == INT_MAX ? 0 : bi;
 }

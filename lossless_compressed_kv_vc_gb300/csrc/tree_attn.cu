@@ -7,9 +7,11 @@
 // keys (context and tokens) into tiles of 128. Lengths live on the device, so the kernels themselves lay the
 // plan down: one warp, a lane a request, adds up the tiles [request][head][unit][tile], and each CTA (one per SM:
 // 8 softmax warps, 4 MMA issuers, 1 loader) takes an equal range of them by cost. A CTA's part of a unit of a head
-// (a piece) leaves an (o, lse) partial; a second kernel merges a row's partials. Where every request has the same
-// number U > 1 of full units, CTA c takes unit c % U in the c / U-th range of [request][head][tile]: the units of
-// a head read a tile at about the same time, and it comes from DRAM once.
+// (a piece) leaves an (o, lse) partial; a second kernel merges a row's partials. Of a chain (no mask) each unit has
+// the tiles up to the last key that it sees, so a prompt's upper half is not computed (32/8 heads of 128, 2048 tokens
+// over no context: 80 us, 172 with all tiles). Where every request has the same number U > 1 of full units, CTA c
+// may take unit c % U in the c / U-th range of [request][head][tile], a lane, instead: the units of a head read a tile
+// at about the same time, and it comes from DRAM once.
 //
 // Within a CTA two chains run side by side, each an issuer of S, one of P V and a warpgroup of softmax threads
 // (a thread per query row): S = Q K^T into TMEM, softmax in registers, P (bf16) over S in TMEM, O += P V with P read
@@ -33,6 +35,7 @@
 #include "tc05.cuh"
 
 #include <cudaTypedefs.h>
+#include <limits.h>
 #include <math.h>
 #include <string.h>
 
@@ -44,6 +47,10 @@ constexpr int TM = 128;         // query rows of a chain
 constexpr int TN = 128;         // keys per tile
 constexpr int TS = 64;          // keys per step: S and P of half a tile, double-buffered
 constexpr int TU = 2 * TM;      // query rows of a unit
+// What a unit costs beside its tiles (Q, the first and last steps, the output), in the cost of 64 keys for 256 rows: about
+// 5 us. The prompt above: 112 us with 0, 97 with 2, 89 with 4, 80 with 6, 76 with 10; 32 chunks of 60 tokens over 300
+// keys 62, 53, 51, 50, 50; 16 trees of 25 over up to 16300 keys 169, 167, 171, 168, 172.
+constexpr int TPIECE = 6;
 // warps 0-3, 4-7 softmax of chains 0 and 1; 8, 9 issue their S; 10, 11 their P V; 12 TMA; 13 lays the plan down; 14
 // and 15 make a warpgroup with them (registers are handed over by warpgroup)
 constexpr int TTHREADS = 512;
@@ -62,20 +69,22 @@ struct TreeParams {
   // bring in, in every block of every launch
   int32_t seq[VC_MAX_BATCH], n_rows[VC_MAX_BATCH];
   int32_t tok_begin[VC_MAX_BATCH];   // first query token of each request, INT32_MAX behind the last one
-  int32_t unit_begin[VC_MAX_BATCH];  // first (head, unit) of each request; with lanes: head alone
   int32_t mask_words[VC_MAX_BATCH];
   const bf16* q[VC_MAX_BATCH];
   bf16* o[VC_MAX_BATCH];
   const uint32_t* mask[VC_MAX_BATCH];
   int32_t B, Hq, Hkv, G, n_tok;
   int32_t few;                       // 1: the kernel for few rows, whose tiles are chunks and whose CTAs are warps
-  int32_t lanes;                     // units of every head, each with CTAs of its own (c % lanes); 1: in one sequence
-  int32_t n_cta;                     // CTAs of a lane
+  int32_t same;                      // full units of every head where all requests have as many, else 1
+  uint32_t chains;                   // requests without a mask, a bit each
+  int32_t n_cta;                     // CTAs
   int32_t least;                     // cost of the dearest tile: no CTA's range is shorter
-  int32_t lane_slots, slot_rows;     // partial slots of a lane, rows of a slot
+  int32_t slot_rows;                 // rows of a partial's slot
   int32_t merge_warps;               // warps a row of the merge, 0: several rows a warp
-  float* ws_o;                       // [lanes][lane_slots][slot_rows][d]; slot = CTA of the lane + (head, unit)
-  float* ws_lse;                     // [lanes][lane_slots][slot_rows], log2 domain, -inf: saw nothing
+  // A CTA's range begins inside one unit and ends inside one: partials of units that it takes up in their middle in
+  // slot c, of those that it begins and does not end in slot n_cta + c
+  float* ws_o;                       // [2 n_cta][slot_rows][d]
+  float* ws_lse;                     // [2 n_cta][slot_rows], log2 domain, -inf: saw nothing
   float scale_log2;
   int32_t* dev_status;
 };
@@ -90,18 +99,28 @@ struct TreePlan {
   int32_t ctx[VC_MAX_BATCH], n[VC_MAX_BATCH];  // rows of context, and with the tokens' rows
   int32_t rows[VC_MAX_BATCH];        // query rows of a KV head
   int32_t total, ctas, each, more;   // cost; CTAs of a lane with work; a range's cost, and how many have one more
+  int32_t lanes;                     // units of every head, each with CTAs of its own (c % lanes); 1: in one sequence
+  uint32_t cut;                      // requests whose units end with the last key that they see, a bit each
 };
 
 __device__ __forceinline__ int units_of(int rows) { return (rows + TU - 1) / TU; }
-// A tile of all units of a head that stand in one sequence.
-__device__ __forceinline__ int tile_cost(const TreeParams& p, int rows) {
-  const int u = units_of(rows);
-  return p.few ? 1 : p.lanes > 1 ? 2 : 2 * u - (rows - (u - 1) * TU <= TM ? 1 : 0);
-}
 __device__ __forceinline__ int tiles_of(const TreeParams& p, int n) { return p.few ? (n + FK - 1) / FK : (n + TN - 1) / TN; }
 
+// A chain's unit u, full, ends with token (256 u + 255) / G, which sees ctx more keys and itself: with
+// b = floor((255 + G (ctx + 128)) / 128) these are floor((2 u + b) / G) tiles.
+__device__ __forceinline__ int chain_b(int G, int ctx) { return (TU - 1 + G * (ctx + TN)) / TN; }
+static_assert(TU == 2 * TN, "two tiles' rows a unit");
+// Tiles of units 0 .. u - 1, the sum of those: it grows by 2 every G units, and within G units the remainder of b
+// makes it one or two more from some unit on.
+__device__ __forceinline__ int chain_tiles_before(int G, int ctx, int u) {
+  const int b = chain_b(G, ctx), bq = b / G, br = b - bq * G, q = u / G, r = u - q * G;
+  auto part = [&](int m) { return m * bq + max(0, m - (G - br + 1) / 2) + max(0, m - (2 * G - br + 1) / 2); };
+  return q * part(G) + G * q * (q - 1) + part(r) + 2 * q * r;
+}
+
 __device__ __forceinline__ void tree_plan(const TreeParams& p, TreePlan* s, int lane, bool tell) {
-  int n = 0, ctx = 0, cost = 0, rows = 0;
+  int n = 0, ctx = 0, cost = 0, cheap = 0, rows = 0, tiles = 0;
+  bool chain = false;
   if (lane < p.B) {
     const int seq = p.seq[lane], tokens = p.n_rows[lane];
     const int held = p.kv.held_of(seq), len = p.kv.len[seq], cap = held << p.kv.shift;
@@ -109,8 +128,21 @@ __device__ __forceinline__ void tree_plan(const TreeParams& p, TreePlan* s, int 
     n = (int)min((int64_t)cap, (int64_t)ctx + tokens);
     if (tell && (ctx != len || n - ctx != tokens)) set_status(p.dev_status, VC_DEV_PAGES);
     rows = tokens * p.G;
-    cost = p.Hkv * tiles_of(p, n) * tile_cost(p, rows);
+    tiles = tiles_of(p, n);
+    const int u = units_of(rows), last = rows - (u - 1) * TU <= TM ? 1 : 2;
+    cost = cheap = p.few ? tiles : tiles ? TPIECE * u + tiles * (2 * (u - 1) + last) : 0;
+    chain = !p.few && u > 1 && ((p.chains >> lane) & 1u) && n - ctx == tokens && (int64_t)p.G * (ctx + TN) < INT_MAX / 2;
+    if (chain) cheap = TPIECE * u + 2 * chain_tiles_before(p.G, ctx, u - 1) + tiles * last;
   }
+  const int all = __reduce_add_sync(0xffffffffu, cost), least = __reduce_add_sync(0xffffffffu, cheap);
+  // Lanes leave some CTAs without work and do not cut chains; they are taken where that costs up to 1/32 (us with lanes
+  // and without, 64/8 heads of 128: trees of 64 over 32768 keys 386, 414; two chains of 256 over 32768 keys, 0.4% more
+  // tiles, 384, 419; 32/8 heads: four of 512 over 16384, 1.2%, 414, 419, over 8192, 2.2%, 246, 236, over 4096, 4.3%,
+  // 161, 147)
+  const int used = p.n_cta / p.same * p.same;  // CTAs that have a lane
+  const int lanes = p.same > 1 && (int64_t)all * p.n_cta * 32 <= (int64_t)least * used * 33 ? p.same : 1;
+  cost = p.Hkv * (lanes > 1 && tiles ? TPIECE + 2 * tiles : cheap);
+  const unsigned cut = __ballot_sync(0xffffffffu, chain && lanes == 1);
   int end = cost;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -123,11 +155,29 @@ __device__ __forceinline__ void tree_plan(const TreeParams& p, TreePlan* s, int 
   s->rows[lane] = rows;
   if (lane == 31) {
     s->total = end;
-    const int ctas = min(p.n_cta, max(end / p.least, end > 0));
+    const int ctas = min(p.n_cta / lanes, max(end / p.least, end > 0));
     s->ctas = ctas;
     s->each = ctas ? end / ctas : 0;
     s->more = ctas ? end - ctas * s->each : 0;
+    s->lanes = lanes;
+    s->cut = cut;
   }
+}
+
+// Keys that unit u of request g's rows reads, and the cost of the units before it in its head's sequence.
+__device__ __forceinline__ int unit_keys(const TreeParams& p, const TreePlan& s, int g, int u) {
+  const bool less = ((s.cut >> g) & 1u) && (u + 1) * TU < s.rows[g];
+  return less ? s.ctx[g] + ((u + 1) * TU - 1) / p.G + 1 : s.n[g];
+}
+__device__ __forceinline__ int cost_before(const TreeParams& p, const TreePlan& s, int g, int u) {
+  if (s.lanes > 1 || p.few) return 0;
+  return TPIECE * u + 2 * ((s.cut >> g) & 1u ? chain_tiles_before(p.G, s.ctx[g], u) : u * ((s.n[g] + TN - 1) / TN));
+}
+// Cost of a head of request g.
+__device__ __forceinline__ int head_cost(const TreeParams& p, const TreePlan& s, int g) {
+  const int tiles = tiles_of(p, s.n[g]), u = units_of(s.rows[g]);
+  if (p.few) return tiles;
+  return TPIECE + (s.lanes > 1 ? 2 * tiles : cost_before(p, s, g, u - 1) + tiles * (s.rows[g] - (u - 1) * TU <= TM ? 1 : 2));
 }
 
 // CTA c of a lane has the costs from cta_begin(c) on; x lies in those of cta_of(x).
@@ -143,29 +193,30 @@ __device__ __forceinline__ int tree_steps(int n, int j) { return n - j * TN > TS
 // A CTA's part of a unit of a head: tiles [j0, j1). Every role of the CTA walks through the same pieces.
 struct TPiece {
   int g, hk, u, j0, j1;  // request, KV head, unit of its rows, tiles
-  int rows, tiles;       // the unit's query rows, the request's tiles
-  int at, end;           // cost at which the unit's tiles start, end of the CTA's range
+  int rows, n, tiles;    // the unit's query rows, keys and tiles
+  int at, end;           // cost at which the unit's tiles start, end of the CTA's range: a tile is the CTA's where it starts
   bool split;            // both chains hold the same rows, chain w takes half w of every tile
 
   __device__ __forceinline__ bool valid() const { return at < end; }
   __device__ __forceinline__ int cost() const { return split ? 1 : 2; }
   // chain 1 has none in the whole piece: a split unit's last, short tile
-  __device__ __forceinline__ bool short_one(int n) const { return split && j1 - j0 == 1 && tree_steps(n, j0) == 1; }
-  __device__ __forceinline__ bool idle(int w, int n) const { return w == 1 && short_one(n); }
+  __device__ __forceinline__ bool short_one() const { return split && j1 - j0 == 1 && tree_steps(n, j0) == 1; }
+  __device__ __forceinline__ bool idle(int w) const { return w == 1 && short_one(); }
   // both chains have sums of the same rows
-  __device__ __forceinline__ bool paired(int n) const { return split && !short_one(n); }
+  __device__ __forceinline__ bool paired() const { return split && !short_one(); }
   __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == tiles; }
   __device__ __forceinline__ void fit(const TreeParams& p, const TreePlan& s) {
     rows = min(TU, s.rows[g] - u * TU);
-    tiles = (s.n[g] + TN - 1) / TN;
+    n = unit_keys(p, s, g, u);
+    tiles = (n + TN - 1) / TN;
     split = rows <= TM;
   }
   __device__ __forceinline__ void cut() { j1 = min(tiles, (end - at + cost() - 1) / cost()); }
   __device__ __forceinline__ void next(const TreeParams& p, const TreePlan& s) {
-    at += cost() * tiles;
+    at += cost() * tiles + TPIECE;
     if (!valid()) return;
-    if (p.lanes > 1 || ++u == units_of(s.rows[g])) {
-      if (p.lanes == 1) u = 0;
+    if (s.lanes > 1 || ++u == units_of(s.rows[g])) {
+      if (s.lanes == 1) u = 0;
       if (++hk == p.Hkv) {
         hk = 0;
         do ++g;
@@ -185,7 +236,7 @@ struct TSteps {
   int blind;  // the first key that some row of the chain does not see
 
   __device__ __forceinline__ TSteps(const TreeParams& p, const TreePlan& s, const TPiece& q, int w) {
-    const int n = s.n[q.g], ctx = s.ctx[q.g];
+    const int n = q.n, ctx = s.ctx[q.g];
     beg = q.j0 * TN + (q.split ? w * TS : 0);
     stride = q.split ? TN : TS;
     const int end = min(n, q.j1 * TN);
@@ -216,24 +267,34 @@ struct TCfg {
 
 __device__ __forceinline__ TPiece tree_first(const TreeParams& p, const TreePlan& s) {
   TPiece q;
-  const int c = blockIdx.x / p.lanes;
+  const int c = blockIdx.x / s.lanes;
   const int beg = cta_begin(s, c);
   q.end = cta_begin(s, c + 1);
   q.g = 0;
   for (int b = 1; b < p.B; ++b)  // the last request that starts at or before; one without tiles starts where the next does
     if (s.cost_begin[b] <= beg) q.g = b;
-  const int rows = s.rows[q.g], tiles = (s.n[q.g] + TN - 1) / TN, units = units_of(rows);
-  const int head = tiles * tile_cost(p, rows);
+  const int head = head_cost(p, s, q.g);
   int rem = beg - s.cost_begin[q.g];
   q.hk = rem / head;
   rem -= q.hk * head;
-  q.u = p.lanes > 1 ? blockIdx.x % p.lanes : min(rem / (2 * tiles), units - 1);
-  if (p.lanes == 1) rem -= q.u * 2 * tiles;
+  q.u = blockIdx.x % s.lanes;
+  if (s.lanes == 1) {  // the last unit that starts at or before
+    int over = units_of(s.rows[q.g]);
+    while (over - q.u > 1) {
+      const int mid = (q.u + over) / 2;
+      if (cost_before(p, s, q.g, mid) <= rem)
+        q.u = mid;
+      else
+        over = mid;
+    }
+    rem -= cost_before(p, s, q.g, q.u);
+  }
   q.fit(p, s);
+  rem -= TPIECE;
   q.at = beg - rem;
-  q.j0 = (rem + q.cost() - 1) / q.cost();
+  q.j0 = rem > 0 ? (rem + q.cost() - 1) / q.cost() : 0;
   q.cut();
-  if (q.j0 >= q.j1) q.next(p, s);  // the range starts in a unit's last tile, which is the CTA's before
+  if (q.valid() && q.j0 >= q.j1) q.next(p, s);  // the range starts in a unit's last tile, which is the CTA's before
   return q;
 }
 
@@ -309,7 +370,7 @@ __device__ __forceinline__ bool broken_bf16x2(uint32_t w) {
 // Bits of the 64 keys from k0 on that a row sees: its words of the mask, shifted to the step; keys before the
 // first token (node < 0) are context, keys from n on are not there.
 __device__ __forceinline__ void mask_bits(const uint32_t* row, int words, int node, int left, uint32_t& lo, uint32_t& hi) {
-  auto word = [&](int i) { return row && i < words ? __ldg(row + i) : 0u; };
+  auto word = [&](int i) { return row && i < words ? row[i] : 0u; };
   uint64_t x;
   if (node >= 0) {
     const int w = node >> 5, sh = node & 31;
@@ -363,7 +424,7 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
     tree_plan(p, &plan, lane, blockIdx.x == 0);
     __syncwarp();
     if (lane == 0) {
-      if ((int)blockIdx.x / p.lanes < plan.ctas)
+      if ((int)blockIdx.x / plan.lanes < plan.ctas)
         *s_first = tree_first(p, plan);
       else
         s_first->at = s_first->end = 0;
@@ -415,10 +476,10 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
       uint32_t it = 0, issued[2] = {0, 0};  // tiles; loads of K and of V on their way
       bool ok = true;
       for (; q.valid() && ok; q.next(p, plan)) {
-        const int n = plan.n[q.g], pages = (n + p.kv.rows() - 1) >> shift;
-        const bool once = p.lanes == 1 && plan.rows[q.g] <= TU;  // tiles that one CTA reads once leave L2 first
+        const int pages = (q.n + p.kv.rows() - 1) >> shift;
+        const bool once = plan.lanes == 1 && plan.rows[q.g] <= TU;  // tiles that one CTA reads once leave L2 first
         const int32_t* table = p.kv.pages_of(p.seq[q.g]);
-        auto look = [&](int j) { return mine && j * per + pi < pages ? __ldg(table + j * per + pi) : 0; };
+        auto look = [&](int j) { return mine && j * per + pi < pages ? table[j * per + pi] : 0; };
         int page = look(q.j0);
         for (int j = q.j0; j < q.j1 && ok; ++j, ++it) {
           const int ahead = j + 1 < q.j1 ? look(j + 1) : 0;
@@ -438,7 +499,7 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
             // All CTAs' rings together are 24 MB, 4 us of DRAM's time, and the first piece's Q would queue behind them
             // (16 x 1000 keys: 6.8 us for it): it goes ahead of all but the first tile of K.
             if (it == 0 && kv == 1 && (!twait_warp(&qfull[0], 0, p.dev_status, s_abort) ||
-                                       (!q.idle(1, n) && !twait_warp(&qfull[1], 0, p.dev_status, s_abort)))) {
+                                       (!q.idle(1) && !twait_warp(&qfull[1], 0, p.dev_status, s_abort)))) {
               ok = false;
               break;
             }
@@ -487,7 +548,7 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
         const int at = uniform(q.at), end = uniform(q.end);
         if (at >= end) break;
         const int whole = uniform(TSteps(p, plan, q, w).full);
-        const int n = uniform(plan.n[q.g]), j0 = uniform(q.j0), j1 = uniform(q.j1), split = uniform((int)q.split);
+        const int n = uniform(q.n), j0 = uniform(q.j0), j1 = uniform(q.j1), split = uniform((int)q.split);
         const int h0 = split ? w : 0, hmax = split ? w + 1 : 2;
         if (of_s && !(h0 >= tree_steps(n, j0) && j1 - j0 == 1)) {  // not idle
           ok = twait_warp(&qfull[w], u & 1, p.dev_status, s_abort);
@@ -554,12 +615,11 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
     // before on that buffer is over
     auto pv_done = [&](uint32_t s) { return twait_warp(&ofull[2 * w + (s & 1)], (s >> 1) & 1, p.dev_status, s_abort); };
     bool ok = true;
-    const size_t lane_slot = (size_t)(blockIdx.x % p.lanes) * p.lane_slots + blockIdx.x / p.lanes;
     // Q of the next piece with tiles for this chain, into its Q tile (the chain's S on the last one are all
     // done: their softmax is)
     auto fetch = [&]() {
       for (; q.valid(); g += q.j1 - q.j0, q.next(p, plan)) {
-        if (q.idle(w, plan.n[q.g])) continue;
+        if (q.idle(w)) continue;
         const int ru = q.split ? rt : w * TM + rt, row = q.u * TU + ru, tok = row / p.G;  // row of the unit, of the head
         const bf16* src = ru < q.rows ? p.q[q.g] + ((size_t)tok * p.Hq + q.hk * p.G + (row - tok * p.G)) * D : nullptr;  // this thread's row
         // the warp's 32 rows, a row's 16-byte pieces in neighbouring lanes (a lane per row would touch 32 lines a load)
@@ -669,14 +729,14 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
       }
       if (!q.valid()) break;
       have = true;
-      paired = q.paired(plan.n[q.g]);
+      paired = q.paired();
       const int ru = q.split ? rt : w * TM + rt;
       row_ok = ru < q.rows;
       const bool alive = __any_sync(0xffffffffu, row_ok);  // a warp without rows only keeps step
       const int row = q.u * TU + ru, tl = row / p.G;
-      part = (lane_slot + p.unit_begin[q.g] + (p.lanes > 1 ? q.hk : q.hk * units_of(plan.rows[q.g]) + q.u)) * p.slot_rows + ru;
+      part = (size_t)(blockIdx.x + (q.j0 > 0 ? 0 : p.n_cta)) * p.slot_rows + ru;
       out = q.whole() && row_ok ? p.o[q.g] + ((size_t)tl * p.Hq + q.hk * p.G + (row - tl * p.G)) * D : nullptr;
-      const int n = plan.n[q.g], ctx = plan.ctx[q.g];
+      const int n = q.n, ctx = plan.ctx[q.g];
       const bool masked = p.mask[q.g] != nullptr;
       const int words = p.mask_words[q.g];
       const uint32_t* mrow = masked && row_ok ? p.mask[q.g] + (size_t)tl * words : nullptr;
@@ -894,7 +954,7 @@ __device__ __forceinline__ uint32_t few_bits(const uint32_t* row, int words, boo
     const int last = tok - node;  // of the chunk's keys
     x = last >= 15 ? 0xffffu : last < 0 ? 0u : (2u << last) - 1u;
   } else {
-    auto word = [&](int i) { return row && i < words ? __ldg(row + i) : 0u; };
+    auto word = [&](int i) { return row && i < words ? row[i] : 0u; };
     if (node >= 0)
       x = __funnelshift_r(word(node >> 5), (node & 31) > 16 ? word((node >> 5) + 1) : 0u, node & 31);
     else
@@ -937,7 +997,7 @@ __global__ void __launch_bounds__(FWARPS * 32, FCTAS) tree_few_kernel(const __gr
     auto look = [&](int jb) {
       int page = -1;
       if (jb + lane < j1) {
-        page = __ldg(table + (((jb + lane) * FK) >> p.kv.shift));
+        page = table[((jb + lane) * FK) >> p.kv.shift];
         if (!p.kv.has_page(page)) {
           set_status(p.dev_status, VC_DEV_PAGES);
           page = -1;
@@ -1109,7 +1169,7 @@ __global__ void __launch_bounds__(FWARPS * 32, FCTAS) tree_few_kernel(const __gr
     }
     cp_async_wait<0>();
     // the range's partial of this head: four lanes hold 8 neighbouring channels of a row
-    const size_t part = ((size_t)wid + p.unit_begin[g] + hk) * p.slot_rows;
+    const size_t part = (size_t)(wid + (j0 > 0 ? 0 : p.n_cta)) * p.slot_rows;
     const bool whole = j0 == 0 && j1 == tiles;  // then it is the output
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -1150,9 +1210,9 @@ __device__ __forceinline__ float part_weight(float l, float M) { return l == -IN
 
 // Where a row's unit left its partials: `count` of them, number i at index at(i). One alone is the output already.
 struct TParts {
-  size_t base;
-  int count, stride;  // stride: a slot's rows
-  __device__ __forceinline__ size_t at(int i) const { return base + (size_t)i * stride; }
+  size_t first, base;
+  int count, stride;  // stride: rows from a CTA's slot to that of the next one with the unit
+  __device__ __forceinline__ size_t at(int i) const { return i ? base + (size_t)i * stride : first; }
 };
 
 // Output row `id` of the call (token, query head): its partials and its place.
@@ -1166,14 +1226,14 @@ __device__ __forceinline__ TParts tree_parts(const TreeParams& p, const TreePlan
   const int i = tok - tok_begin[b], r = i * p.G + hq - hk * p.G;  // token of the request, row of the head
   dst = p.o[b] + ((size_t)i * p.Hq + hq) * D;
   const int rows = plan.rows[b], u = p.few ? 0 : r / TU;
-  const int cost = p.few || rows - u * TU <= TM ? 1 : 2, tiles = tiles_of(p, plan.n[b]);
-  TParts q{0, 0, p.slot_rows};
+  const int cost = p.few || rows - u * TU <= TM ? 1 : 2, tiles = tiles_of(p, p.few ? plan.n[b] : unit_keys(p, plan, b, u));
+  TParts q{0, 0, 0, plan.lanes * p.slot_rows};
   if (tiles == 0) return q;
-  const int at = plan.cost_begin[b] + hk * tiles * tile_cost(p, rows) + (p.lanes > 1 ? 0 : u * 2 * tiles);
+  const int at = plan.cost_begin[b] + hk * head_cost(p, plan, b) + cost_before(p, plan, b, u) + (p.few ? 0 : TPIECE);
   const int c0 = cta_of(plan, at), c1 = cta_of(plan, at + cost * (tiles - 1));  // of its first and last tile
-  const int unit = p.unit_begin[b] + (p.lanes > 1 || p.few ? hk : hk * units_of(rows) + u);
   q.count = c1 - c0 + 1;
-  q.base = ((size_t)(p.lanes > 1 ? u : 0) * p.lane_slots + c0 + unit) * p.slot_rows + (r - u * TU);
+  q.base = (size_t)(c0 * plan.lanes + (plan.lanes > 1 ? u : 0)) * p.slot_rows + (r - u * TU);
+  q.first = q.base + (size_t)p.n_cta * p.slot_rows;
   return q;
 }
 
@@ -1197,7 +1257,7 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
   pdl_wait();
   if (warp == 0) tree_plan(p, &plan, lane, false);
   __syncthreads();
-  TParts q{0, 0, 0};
+  TParts q{0, 0, 0, 0};
   bf16* dst = nullptr;
   if (live) q = tree_parts<D>(p, plan, tok_begin, id, dst);
   if (q.count == 1) {  // written by the piece itself: nothing to add up, the block's barrier is kept
@@ -1283,7 +1343,7 @@ __global__ void __launch_bounds__(256, 4) tree_merge_rows_kernel(const __grid_co
   for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w * (32 / TSUB) < all; w += (int64_t)gridDim.x * 8) {
     const int64_t id = w * (32 / TSUB) + lane / TSUB;
     bool live = id < all;
-    TParts q{0, 0, 0};
+    TParts q{0, 0, 0, 0};
     bf16* dst = nullptr;
     if (live) q = tree_parts<D>(p, plan, tok_begin, id, dst);
     if (q.count == 1) {  // written by the piece itself
@@ -1372,7 +1432,7 @@ cudaError_t launch_tree_t(const TreeParams& p, const TreeMaps& maps, cudaStream_
   } else {
     e = raise_smem_limit(tree_attn_kernel<D>, TCfg<D>::SMEM, attr);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(tree_attn_kernel<D>, dim3(p.n_cta * p.lanes), dim3(TTHREADS), TCfg<D>::SMEM, s, p, maps);
+    e = launch_pdl(tree_attn_kernel<D>, dim3(p.n_cta), dim3(TTHREADS), TCfg<D>::SMEM, s, p, maps);
   }
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)p.n_tok * p.Hq;
@@ -1383,11 +1443,10 @@ cudaError_t launch_tree_t(const TreeParams& p, const TreeMaps& maps, cudaStream_
 
 }  // namespace
 
-// Partials: a slot per CTA and (head, unit), for each lane of CTAs.
-// Calls of few rows have a slot per warp instead, of no more rows.
+// Partials: two slots a CTA, or a warp for few rows; how many rows there are in all does not matter.
 size_t tree_workspace_size(const vc_shape* s, int32_t max_rows) {
-  const int64_t rows = (int64_t)max_rows * (s->Hq / s->Hkv), units = host_units(rows), heads = (int64_t)s->B * s->Hkv;
-  const int64_t few = (few_warps() + heads) * (rows < FR ? rows : FR), many = (tree_sms() + heads * units) * slot_rows_of(rows);
+  const int64_t rows = (int64_t)max_rows * (s->Hq / s->Hkv);
+  const int64_t few = 2 * few_warps() * (rows < FR ? rows : FR), many = 2 * tree_sms() * (int64_t)slot_rows_of(rows);
   return (size_t)(few > many ? few : many) * (s->d + 1) * sizeof(float) + 256;
 }
 
@@ -1426,11 +1485,12 @@ cudaError_t launch_tree_attn(const TreeArgs& a, cudaStream_t s, vc_status* st) {
     p.mask[b] = r.mask;
     const int64_t rows = (int64_t)a.req[b].n_rows * G, u = host_units(rows);
     if (u != same || rows - (u - 1) * TU <= TM) same = 1;
+    if (!r.mask) p.chains |= 1u << b;
     const int sr = p.few ? (int)rows : slot_rows_of(rows);
     p.slot_rows = sr > p.slot_rows ? sr : p.slot_rows;
     if (rows > TM) p.least = 2;
     units += u * a.Hkv;
-    cost += (p.few ? 1 : 2 * u) * a.Hkv * tiles;
+    cost += (p.few ? tiles : u * (2 * tiles + TPIECE)) * a.Hkv;
   }
   // costs are counted in 32 bits
   if (cost >= INT32_MAX / 2 || units >= INT32_MAX / 2) {
@@ -1438,15 +1498,9 @@ cudaError_t launch_tree_attn(const TreeArgs& a, cudaStream_t s, vc_status* st) {
     return cudaSuccess;
   }
   const int sms = tree_sms();
-  p.lanes = same > 1 && same <= sms / 2 ? (int)same : 1;
-  p.n_cta = p.few ? few_warps() : sms / p.lanes;
-  int64_t at = 0;
-  for (int b = 0; b < a.B; ++b) {
-    p.unit_begin[b] = (int32_t)at;
-    at += a.Hkv * (p.lanes > 1 ? 1 : host_units((int64_t)a.req[b].n_rows * G));
-  }
-  p.lane_slots = (int32_t)(p.n_cta + at);
-  const size_t rows = (size_t)p.lanes * p.lane_slots * p.slot_rows;
+  p.same = same > 1 && same <= sms / 2 ? (int)same : 1;
+  p.n_cta = p.few ? few_warps() : sms;
+  const size_t rows = 2 * (size_t)p.n_cta * p.slot_rows;
   if (!a.ws || (reinterpret_cast<uintptr_t>(a.ws) & 15u) || rows * (a.d + 1) * sizeof(float) > a.ws_bytes) {
     *st = VC_ERR_WORKSPACE;
     return cudaSuccess;
@@ -1455,7 +1509,7 @@ cudaError_t launch_tree_attn(const TreeArgs& a, cudaStream_t s, vc_status* st) {
   p.ws_lse = p.ws_o + rows * a.d;
   // Warps a row of the merge: a row's partials, one a CTA (or warp) that holds part of its unit, by fours (one round
   // trip each); no more than make a wave of blocks. Several rows a warp where they are more than the warps of a wave.
-  const int64_t parts = 1 + p.n_cta / at, out_rows = (int64_t)a.n_tok * a.Hq, wave = (int64_t)sms * 4 * 8;
+  const int64_t parts = 1 + p.n_cta / units, out_rows = (int64_t)a.n_tok * a.Hq, wave = (int64_t)sms * 4 * 8;
   p.merge_warps = 1;
   while (p.merge_warps < 8 && parts > 4 * p.merge_warps && out_rows * p.merge_warps * 2 <= wave) p.merge_warps *= 2;
   if (out_rows > wave) p.merge_warps = 0;

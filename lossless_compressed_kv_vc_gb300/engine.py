@@ -877,7 +877,8 @@ class TreeBatch:
     A turn: reserve room, append the tokens' rotated keys and their values behind the context, attend,
     and commit what was accepted (accept does both ends of that for trees). What the device finds wrong
     (no pages left, say) lands in dev_status. All calls run on `stream` (the current one by default);
-    like a Batch's, each stream first waits for the construction.
+    like a Batch's, each stream first waits for the construction. They share q_rot and a workspace, so
+    calls on different streams are ordered by the caller.
     """
 
     def __init__(self, Hq: int, Hkv: int, d: int, n_seq: int, n_pages: int, page: int, axes: vc_rope_axes, max_rows: int = 1,
@@ -1059,8 +1060,8 @@ class TreeBatch:
         mask = depth = None
         if parent is not None:
             B, N = _check_trees(n_nodes, parent)
-            if B != len(seqs) or not max(rows) <= N <= self.max_rows or parent.device != self.device:
-                raise ValueError("parent is [B][R] on the pool's device, max(rows) <= R <= max_rows")
+            if B != len(seqs) or not max(rows) <= N <= min(self.max_rows, VC_TREE_MAX_NODES) or parent.device != self.device:
+                raise ValueError("parent is [B][R] on the pool's device, max(rows) <= R <= max_rows and VC_TREE_MAX_NODES")
             W = (N + 31) // 32
             mask, depth = self._masks[: B * N * W].view(B, N, W), self._depths[: B * N].view(B, N)
             with torch.cuda.device(self.device):
@@ -1077,10 +1078,10 @@ class TreeBatch:
         """The longest path of each tree that the full pass agrees with (accept_tree) becomes context. Returns
         (out_tokens, path, n_acc)."""
         self._check_seqs(seqs, rows)
+        if logits.dim() != 3 or logits.shape[0] != len(seqs) or logits.shape[1] < max(rows):
+            raise ValueError("logits are [B][R][V], R >= max(rows)")
         for t, name in ((token, "token"), (parent, "parent")):
             self._check_ints(t, name, len(seqs), logits.shape[1])
-        if logits.shape[0] != len(seqs) or logits.shape[1] < max(rows):
-            raise ValueError("logits are [B][R][V], R >= max(rows)")
         with torch.cuda.device(self.device):
             self._order(stream)
             out, path, n_acc = accept_tree(logits, token, parent, n_nodes, stream=stream)

@@ -488,6 +488,52 @@ def test_trees(vc, case, kind):
     assert all(torch.equal(a, b) for a, b in zip(outs, again))
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,page,sizes", [
+    (8, 1, 64, 16, [(0, 700), (1, 333), (250, 65)]),           # units of 32 tokens, seven or more of them a head
+    (3, 1, 128, 32, [(0, 515), (130, 300)]),                   # a unit ends within a token's heads
+    (5, 5, 64, 128, [(127, 520), (0, 0), (0, 513)]),
+    (16, 1, 128, 64, [(0, 512)]),                              # 32 full units: most of the square is cut away
+    (16, 1, 128, 64, [(9000, 512)]),                           # the same over a context beside which the cut is little
+    (14, 2, 128, 16, [(40, 400), (3000, 37), (0, 37), (12, 1)]),
+    (24, 1, 64, 16, [(0, 128), (64, 128), (128, 128)])])
+@pytest.mark.parametrize("tree", [False, True])
+def test_prompt_chunks(vc, Hq, Hkv, d, page, sizes, tree):
+    """Chains of several units of query rows, which end at different keys; with `tree` every other request has a mask."""
+    g = gen(25)
+    p = build(vc, g, Hq, Hkv, d, page, sizes)
+    reqs, see = [], []
+    for s, (n, N) in enumerate(sizes):
+        w = np.tri(N, dtype=bool)
+        if tree and s % 2 == 0 and N:
+            w = O.ancestors(random_tree(np.random.default_rng(s), N))[0]
+        words = -(-N // 32)
+        reqs.append((s, randn(g, N, Hq, d), torch.tensor(O.pack_mask(w, words), device="cuda") if tree and s % 2 == 0 and N else None))
+        see.append(w)
+    outs = attend(vc, p, reqs)
+    check(vc, p, Hq, reqs, see, outs)
+    assert int(p.status.item()) == 0
+
+
+def test_a_prompt_chunk_with_too_few_pages(vc):
+    """Tokens whose rows lie behind the pages held are seen by none; those that have pages by whom they would be."""
+    g = gen(26)
+    p = build(vc, g, 8, 1, 64, 16, [(20, 200)])
+    held = int(p.ref.held[0])
+    q = randn(g, 400, 8, 64)
+    N = held * 16 - 20  # tokens whose rows the pages have room for
+    at = torch.arange(220, held * 16, device="cuda")
+    pages = p.state["table"][0].long()[at // 16]
+    p.k[pages, :, at % 16], p.v[pages, :, at % 16] = 0, 0  # rows behind the last token hold NaN: now numbers
+    outs = attend(vc, p, [(0, q, None)])
+    torch.cuda.synchronize()
+    assert int(p.status.item()) == vc.VC_DEV_PAGES
+    k, v = (f64(x) for x in p.rows(0, 0, held * 16))
+    assert_attn_close(outs[0][:N], O.tree_attn(f64(q)[:N], k, v, np.tri(N, dtype=bool)), "rows with pages")
+    tail = min(400 - N, N)
+    assert_attn_close(outs[0][400 - tail :], O.tree_attn(np.concatenate([f64(q)[400 - tail :], f64(q)[: N - tail]]), k, v,
+                                                         np.ones((N, N), bool))[:tail], "rows without")
+
+
 def test_a_mask_that_leaves_nothing(vc):
     """No context and an empty row: zeros, whatever K and V hold; beside rows that see themselves."""
     g = gen(12)

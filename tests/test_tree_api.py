@@ -285,6 +285,13 @@ def test_tree_attn_refusals(vc):
     assert vc.vc_tree_workspace_size(vc.vc_shape(1, 8, 2, 64), 0) == 0
 
 
+def test_tree_workspace_does_not_grow_with_the_call(vc):
+    """Two slots a CTA hold every partial, however many requests, heads and rows there are."""
+    size = lambda B, Hq, Hkv, rows: vc.vc_tree_workspace_size(vc.vc_shape(B, Hq, Hkv, 128), rows)
+    assert 0 < size(1, 8, 1, 1) <= size(1, 8, 1, 2) <= size(1, 8, 1, 40)
+    assert size(1, 8, 1, 40) == size(32, 64, 8, 40) == size(32, 64, 8, 100000) < 64 << 20
+
+
 def test_trees_refused(vc):
     inv, uns, kw = vc.VC_ERR_INVALID, vc.VC_ERR_UNSUPPORTED, dict(stream=0, raise_on_error=False)
     mask = lambda B=1, N=4, a=(A, 2 * A, 3 * A, 4 * A): vc.vc_tree_mask(B, N, *a, **kw)
@@ -417,9 +424,16 @@ def test_engine_steps_make_their_calls_in_order(vc, calls):
 
 
 def test_engine_refusals(vc, calls):
+    tb = trees(vc, max_rows=1100)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)
+    calls.clear()
+    with pytest.raises(ValueError):  # more nodes than a tree has
+        tb.step([0], *(torch.empty((1, 1100, h, D), dtype=torch.bfloat16) for h in (HQ, HKV, HKV, HQ)), [1], i(1, 1100), i(1))
+    with pytest.raises(ValueError):
+        tb.accept([0], torch.zeros(8), i(1, 8), i(1, 8), i(1), [1])
+    assert not calls
     tb = trees(vc)
     calls.clear()
-    i = lambda *s: torch.zeros(s, dtype=torch.int32)
     good = dict(q=new(HQ), k=new(HKV), v=new(HKV))
 
     def refused(f, *a, **kw):
