@@ -481,6 +481,13 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
         const int32_t* table = p.kv.pages_of(p.seq[q.g]);
         auto look = [&](int j) { return mine && j * per + pi < pages ? table[j * per + pi] : 0; };
         int page = look(q.j0);
+        if (it > 0)  // the next piece's queries on their way to L2 before the chains ask for them
+          for (int r = lane; r < q.rows; r += 32) {
+            const int row = q.u * TU + r, tok = row / p.G;
+            const bf16* src = p.q[q.g] + ((size_t)tok * p.Hq + q.hk * p.G + (row - tok * p.G)) * D;
+#pragma unroll
+            for (int c = 0; c < D; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + c));
+          }
         for (int j = q.j0; j < q.j1 && ok; ++j, ++it) {
           const int ahead = j + 1 < q.j1 ? look(j + 1) : 0;
           const int cnt = min(per, pages - j * per);  // pages of this tile: at least one
@@ -624,12 +631,16 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
         const bf16* src = ru < q.rows ? p.q[q.g] + ((size_t)tok * p.Hq + q.hk * p.G + (row - tok * p.G)) * D : nullptr;  // this thread's row
         // the warp's 32 rows, a row's 16-byte pieces in neighbouring lanes (a lane per row would touch 32 lines a load)
         constexpr int PR = D / 8, RW = 32 / PR;  // pieces of a row, rows a load
+        uint4 v[32 / RW];  // all on their way at once
 #pragma unroll
         for (int i = 0; i < 32 / RW; ++i) {
-          const int r = i * RW + lane / PR, c = lane % PR, rr = (warp & 3) * 32 + r;
-          const bf16* from = reinterpret_cast<const bf16*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), r));
-          const uint4 v = from ? __ldcg(reinterpret_cast<const uint4*>(from) + c) : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(sQ + (c >> 3) * (TM * 128) + rr * 128 + (((c ^ rr) & 7) << 4)) = v;
+          const bf16* from = reinterpret_cast<const bf16*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i * RW + lane / PR));
+          v[i] = from ? __ldcg(reinterpret_cast<const uint4*>(from) + lane % PR) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 32 / RW; ++i) {
+          const int c = lane % PR, rr = (warp & 3) * 32 + i * RW + lane / PR;
+          *reinterpret_cast<uint4*>(sQ + (c >> 3) * (TM * 128) + rr * 128 + (((c ^ rr) & 7) << 4)) = v[i];
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -667,55 +678,69 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
         tc05::fence_after();
         // rows in the order of an MMA's accumulator: four lanes hold 8 neighbouring channels (whole 32-byte
         // sectors), where a lane per row would write 32 lines at a time; of paired chains each writes half the channels
-        const int cb0 = paired ? w * (D / 64) : 0, cb1 = paired ? cb0 + D / 64 : D / 32;
+        constexpr int NB = D / 32;  // blocks of 32 channels of a row
+        const int cb0 = paired ? w * (NB / 2) : 0, nb = paired ? NB / 2 : NB;
         const uint32_t tX = tmem + lane_off + C::OCOL + (w ^ 1) * D;  // the other chain's O
-        float* o_row0 = p.ws_o + (part - (rt & 31)) * D + 2 * (lane & 3);  // of the warp's first row
+        float* o_row0 = p.ws_o + (part - (rt & 31)) * D + cb0 * 32 + 2 * (lane & 3);  // of the warp's first row
         const unsigned rows_ok = __ballot_sync(0xffffffffu, row_ok);
+        const bool direct = __any_sync(0xffffffffu, out != nullptr);
 #pragma unroll 1
         for (int hh = 0; hh < 2; ++hh) {
           if (!((rows_ok >> (16 * hh)) & 0xffffu)) continue;
           const int r0 = hh * 16 + (lane >> 2);
+          const uint32_t half = (uint32_t)(hh * 16) << 16;
+          uint32_t r[NB][16];
+#pragma unroll
+          for (int c = 0; c < NB / 2; ++c) {  // warp-collective: every lane loads
+            tc05::ld16x256_x4(tO + half + (cb0 + c) * 32, r[c]);
+            tc05::ld16x256_x4((paired ? tX + cb0 * 32 : tO + (NB / 2) * 32) + half + c * 32, r[NB / 2 + c]);
+          }
           float a[2], b[2];
-          bf16* to[2];
-          bool on[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             a[e] = __shfl_sync(0xffffffffu, mine, r0 + 8 * e);
-            b[e] = __shfl_sync(0xffffffffu, theirs, r0 + 8 * e);
-            to[e] = reinterpret_cast<bf16*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), r0 + 8 * e));
-            on[e] = (rows_ok >> (r0 + 8 * e)) & 1u;
+            b[e] = __shfl_sync(0xffffffffu, paired ? theirs : mine, r0 + 8 * e);
           }
-          constexpr int NC = D / 64;  // blocks of 32 channels at a time
-#pragma unroll 1
-          for (int cb = cb0; cb < cb1; cb += NC) {
-            uint32_t r[NC][16], o[NC][16];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {  // warp-collective: every lane loads
-              tc05::ld16x256_x4(tO + ((uint32_t)(hh * 16) << 16) + (cb + c) * 32, r[c]);
-              if (paired) tc05::ld16x256_x4(tX + ((uint32_t)(hh * 16) << 16) + (cb + c) * 32, o[c]);
+          for (int c = 0; c < NB; ++c) arrived(r[c]);
+#pragma unroll
+          for (int c = 0; c < NB / 2; ++c)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float x = __uint_as_float(r[c][k]) * a[k >> 1 & 1], y = __uint_as_float(r[NB / 2 + c][k]) * b[k >> 1 & 1];
+              r[c][k] = __float_as_uint(paired ? x + y : x);
+              r[NB / 2 + c][k] = __float_as_uint(y);
             }
+          if (direct) {
+            bf16* to[2];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              arrived(r[c]);
-              if (paired) arrived(o[c]);
+            for (int e = 0; e < 2; ++e)
+              to[e] = reinterpret_cast<bf16*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), r0 + 8 * e)) +
+                      cb0 * 32 + 8 * (lane & 1) + 2 * (lane & 2);
+#pragma unroll
+            for (int c = 0; c < NB; ++c) {
+              if (c >= nb) continue;
+#pragma unroll
+              for (int k = 0; k < 4; k += 2)  // of two groups of 8 channels an even lane takes the first, with its neighbour's
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t x = pack_bf16x2(__uint_as_float(r[c][4 * k + 2 * e]), __uint_as_float(r[c][4 * k + 2 * e + 1]));
+                  const uint32_t y = pack_bf16x2(__uint_as_float(r[c][4 * k + 4 + 2 * e]), __uint_as_float(r[c][4 * k + 5 + 2 * e]));
+                  const uint32_t z = __shfl_xor_sync(0xffffffffu, lane & 1 ? x : y, 1);
+                  if ((rows_ok >> (r0 + 8 * e)) & 1u) *reinterpret_cast<uint2*>(to[e] + c * 32 + 8 * k) = lane & 1 ? make_uint2(z, y) : make_uint2(x, z);
+                }
             }
+          } else {
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
+            for (int c = 0; c < NB; ++c) {
+              if (c >= nb) continue;
 #pragma unroll
               for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float x = __uint_as_float(r[c][4 * k + 2 * e]) * a[e], y = __uint_as_float(r[c][4 * k + 2 * e + 1]) * a[e];
-                  if (paired) {
-                    x += __uint_as_float(o[c][4 * k + 2 * e]) * b[e];
-                    y += __uint_as_float(o[c][4 * k + 2 * e + 1]) * b[e];
-                  }
-                  const int at = (cb + c) * 32 + 8 * k;
-                  if (on[e] && to[e])
-                    *reinterpret_cast<uint32_t*>(to[e] + at + 2 * (lane & 3)) = pack_bf16x2(x, y);
-                  else if (on[e])
-                    *reinterpret_cast<float2*>(o_row0 + (size_t)(r0 + 8 * e) * D + at) = make_float2(x, y);
-                }
+                for (int e = 0; e < 2; ++e)
+                  if ((rows_ok >> (r0 + 8 * e)) & 1u)
+                    *reinterpret_cast<uint2*>(o_row0 + (size_t)(r0 + 8 * e) * D + c * 32 + 8 * k) = make_uint2(r[c][4 * k + 2 * e], r[c][4 * k + 2 * e + 1]);
+            }
           }
         }
         if (row_ok && !out && !(paired && w)) p.ws_lse[part] = lse;
