@@ -123,7 +123,7 @@ __device__ __forceinline__ void tree_plan(const TreeParams& p, TreePlan* s, int 
   bool chain = false;
   if (lane < p.B) {
     const int seq = p.seq[lane], tokens = p.n_rows[lane];
-    const int held = p.kv.held_of(seq), len = p.kv.len[seq], cap = held << p.kv.shift;
+    const int held = min(max(__ldcg(p.kv.held + seq), 0), p.kv.max_pages), len = __ldcg(p.kv.len + seq), cap = held << p.kv.shift;
     ctx = min(max(len, 0), cap);
     n = (int)min((int64_t)cap, (int64_t)ctx + tokens);
     if (tell && (ctx != len || n - ctx != tokens)) set_status(p.dev_status, VC_DEV_PAGES);
@@ -964,8 +964,8 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
 // with Q in registers, P from S's accumulators as they lie, O += P V. The tcgen05 kernel's fixed part (tensor maps,
 // TMEM, barriers, two chains' start and end) is what this one does without, and a page of 16 rows is as good as a
 // larger one, where TMA boxes of 2 KB hold the other back (32 tokens over 8200 rows, pages of 16: 186 us, the other
-// 195). Measured with 32 ragged requests of up to 8200 rows, 32/8 heads of 128: 939 MB in 144 us, 6.5 TB/s, which
-// is what reading alone reaches, and 21 us of start-up, plan and merge around it.
+// 195). Measured with 32 ragged requests of up to 8200 rows, 32/8 heads of 128, call after call: 939 MB in 152 us with
+// the merge, 6.2 TB/s. Equal ranges do not end together: SMs in the larger groups get up to 12% less of DRAM.
 template <int D>
 struct FCfg {
   static constexpr int HALF = FK * D * 2;             // bytes of a chunk's K or V
@@ -995,8 +995,8 @@ __global__ void __launch_bounds__(FWARPS * 32, FCTAS) tree_few_kernel(const __gr
   extern __shared__ __align__(128) uint8_t few_smem[];
   __shared__ TreePlan plan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // behind the wait, when all CTAs are there: a merge waiting on an SM would keep one from it
   if (warp == 0) tree_plan(p, &plan, lane, blockIdx.x == 0);
   __syncthreads();
   const int wid = warp * gridDim.x + blockIdx.x;  // the first ones on different SMs
@@ -1264,7 +1264,9 @@ __device__ __forceinline__ TParts tree_parts(const TreeParams& p, const TreePlan
 
 // Merge, o = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M) over a row's partials. Few rows of many partials: one to
 // eight warps a row, a lane per partial takes the weights, then the warp adds up the partials' channels, four loads
-// in flight.
+// in flight, the first four ahead of the weights. Bound by latency: it follows another kernel, so all that does not
+// need that one's results is done before the wait. The plan is such: the attention kernels let this one start after
+// their own wait, when whatever wrote the lengths has ended and is in L2, and they leave them as they are.
 template <int D>
 __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constant__ TreeParams p) {
   constexpr int E = D / 32;  // channels a lane
@@ -1278,8 +1280,6 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
   const int64_t id = (int64_t)blockIdx.x * (8 / wpr) + warp / wpr;
   bool live = id < (int64_t)p.n_tok * p.Hq;
   if (threadIdx.x < VC_MAX_BATCH) tok_begin[threadIdx.x] = p.tok_begin[threadIdx.x];
-  pdl_launch_dependents();
-  pdl_wait();
   if (warp == 0) tree_plan(p, &plan, lane, false);
   __syncthreads();
   TParts q{0, 0, 0, 0};
@@ -1289,6 +1289,20 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
     live = false;
     q.count = 0;
   }
+  const int beg = q.count * part / wpr, end = q.count * (part + 1) / wpr;
+  auto fetch = [&](float (&v)[E], int k) {
+    const float* src = p.ws_o + q.at(k) * D + lane * E;
+    if constexpr (E == 4)
+      *reinterpret_cast<float4*>(v) = __ldcg(reinterpret_cast<const float4*>(src));
+    else
+      *reinterpret_cast<float2*>(v) = __ldcg(reinterpret_cast<const float2*>(src));
+  };
+  pdl_wait();
+  pdl_launch_dependents();
+  float ahead[PF][E];
+#pragma unroll
+  for (int c = 0; c < PF; ++c)
+    if (beg + c < end) fetch(ahead[c], beg + c);
   auto lse_of = [&](int k, int end) { return k >= end ? -INFINITY : p.ws_lse[q.at(k)]; };
   float M = -INFINITY;
   for (int k0 = 0; k0 < q.count; k0 += 32) M = fmaxf(M, lse_of(k0 + lane, q.count));
@@ -1297,7 +1311,6 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
   float L = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  const int beg = q.count * part / wpr, end = q.count * (part + 1) / wpr;
   for (int k0 = beg; k0 < end; k0 += 32) {
     const float l = lse_of(k0 + lane, end), f = part_weight(l, M);
     const unsigned wrote = __ballot_sync(0xffffffffu, l != -INFINITY);
@@ -1308,14 +1321,14 @@ __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constan
 #pragma unroll
       for (int c = 0; c < PF; ++c) {
         fc[c] = __shfl_sync(0xffffffffu, f, c0 + c);  // c0 + c < 32; nothing was written beyond cnt
+        const bool wr = (wrote >> (c0 + c)) & 1u;      // a partial that saw nothing was not written
+        if (k0 + c0 == beg) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[c][e] = 0.f;
-        if ((wrote >> (c0 + c)) & 1u) {  // a partial that saw nothing was not written
-          const float* src = p.ws_o + q.at(k0 + c0 + c) * D + lane * E;
-          if constexpr (E == 4)
-            *reinterpret_cast<float4*>(v[c]) = __ldcg(reinterpret_cast<const float4*>(src));
-          else
-            *reinterpret_cast<float2*>(v[c]) = __ldcg(reinterpret_cast<const float2*>(src));
+          for (int e = 0; e < E; ++e) v[c][e] = wr ? ahead[c][e] : 0.f;
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[c][e] = 0.f;
+          if (wr) fetch(v[c], k0 + c0 + c);
         }
       }
 #pragma unroll
@@ -1360,10 +1373,10 @@ __global__ void __launch_bounds__(256, 4) tree_merge_rows_kernel(const __grid_co
   __shared__ int32_t tok_begin[VC_MAX_BATCH];
   const int lane = threadIdx.x & 31, sl = lane % TSUB, first = lane - sl;
   if (threadIdx.x < VC_MAX_BATCH) tok_begin[threadIdx.x] = p.tok_begin[threadIdx.x];
-  pdl_launch_dependents();
-  pdl_wait();
   if (threadIdx.x < 32) tree_plan(p, &plan, lane, false);
   __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
   const int64_t all = (int64_t)p.n_tok * p.Hq;
   for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w * (32 / TSUB) < all; w += (int64_t)gridDim.x * 8) {
     const int64_t id = w * (32 / TSUB) + lane / TSUB;
