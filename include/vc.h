@@ -680,7 +680,7 @@ vc_status vc_rope_pages(const vc_shape* shape, const vc_rope_axes* axes, const v
 /* ------------------------------------------------------------------------------------------ */
 /* Trees of drafts. Node 0 of a request's n_nodes is the last accepted token, whose key and value the
  * turn itself makes; node i's parent is parent[i], in 0 .. i-1 (anything else: node i is a root of its
- * own, and is accepted by nothing). Arrays are [B][N_max], a request's first n_nodes entries are read
+ * own, and is accepted by nothing). Arrays are [B][N_max], whole; a request's first n_nodes entries count
  * (n_nodes is held to 0 .. N_max on the device). 1 <= N_max <= VC_TREE_MAX_NODES, any B >= 1.
  *
  * vc_tree_mask — for each node the bits of the nodes it sees, itself and its ancestors: bit j % 32 of word

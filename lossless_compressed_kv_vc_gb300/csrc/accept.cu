@@ -142,9 +142,9 @@ __global__ void __launch_bounds__(256) tree_mask_kernel(TreeMaskArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   const int b = blockIdx.x, N = a.N_max, words = (N + 31) / 32;
-  const int n = min(max(a.n_nodes[b], 0), N);
+  const int nodes = a.n_nodes[b], n = min(max(nodes, 0), N);
   const int32_t* parent = a.parent + (size_t)b * N;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+  for (int i = threadIdx.x; i < N; i += blockDim.x) {  // those behind the last node too: not one after the other's load
     const int p = parent[i];
     up[i] = (int16_t)(p >= 0 && p < i ? p : -1);
   }
@@ -183,14 +183,23 @@ __global__ void __launch_bounds__(256) tree_walk_kernel(TreeAcceptArgs a) {
   const int b = blockIdx.x, N = a.N_max;
   const int n = min(max(a.n_nodes[b], 0), N);
   const size_t at = (size_t)b * N;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    pick[i] = a.out_tokens[at + i];
-    next[i] = INT_MAX;
+  // a node a thread, up to four: one round trip for all three arrays (a node behind the last one is read and not used)
+  int up[VC_TREE_MAX_NODES / 256], tok[VC_TREE_MAX_NODES / 256];
+#pragma unroll
+  for (int u = 0; u < VC_TREE_MAX_NODES / 256; ++u) {
+    const int i = threadIdx.x + u * blockDim.x;
+    if (i < N) {
+      up[u] = a.parent[at + i];
+      tok[u] = a.token[at + i];
+      pick[i] = a.out_tokens[at + i];
+      next[i] = INT_MAX;
+    }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int p = a.parent[at + i];
-    if (p >= 0 && p < i && a.token[at + i] == pick[p]) atomicMin(&next[p], i);
+#pragma unroll
+  for (int u = 0; u < VC_TREE_MAX_NODES / 256; ++u) {
+    const int i = threadIdx.x + u * blockDim.x;
+    if (i < n && up[u] >= 0 && up[u] < i && tok[u] == pick[up[u]]) atomicMin(&next[up[u]], i);
   }
   __syncthreads();
   if (threadIdx.x == 0) {

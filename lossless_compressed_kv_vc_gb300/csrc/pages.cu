@@ -360,6 +360,7 @@ __global__ void __launch_bounds__(256) commit_kernel(const __grid_constant__ Com
   const int32_t* pages = kv.pages_of(q.seq);
   bool ok = true;
   const int n = context_rows(kv, q.seq, held, ok);
+  const int early = q.path && (int)threadIdx.x < q.n_rows ? q.path[threadIdx.x] : 0;  // beside the other state, not behind it
   int m = q.n_acc ? min(max(*q.n_acc, 0), q.n_rows) : q.n_rows;
   if (m > (held << kv.shift) - n) {  // rows that were never written
     m = (held << kv.shift) - n;
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(256) commit_kernel(const __grid_constant__ Com
     for (int i0 = 0; i0 < m; i0 += kCommitRows) {
       __syncthreads();
       for (int i = i0 + threadIdx.x; i < min(m, i0 + kCommitRows); i += blockDim.x) {
-        const int from = q.path[i];
+        const int from = i < (int)blockDim.x ? early : q.path[i];
         bool good = from >= i && from < q.n_rows && (int64_t)n + from < (int64_t)held << kv.shift;
         int64_t src = 0, dst = -1;
         if (good && from != i) {
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(256) commit_kernel(const __grid_constant__ Com
       for (int c = threadIdx.x; c < 2 * cols; c += blockDim.x) {
         const int col = c < cols ? c : c - cols;
         uint4* pool = reinterpret_cast<uint4*>(c < cols ? kv.k : kv.v) + (int64_t)(col / (D / 8)) * head + col % (D / 8);
-        constexpr int U = 8;  // rows in flight
+        constexpr int U = 16;  // rows in flight
         for (int i = 0; i < end; i += U) {
           uint4 v[U];
 #pragma unroll
