@@ -136,7 +136,7 @@ cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t s) {
 // ---- trees of drafts -----------------------------------------------------------------------------------
 // Masks: a thread per node walks to the root in shared memory; ancestors come in descending order, so each
 // word of the node's bits is written once, full. Bound by the walk, about 30 clocks an ancestor (16 trees of 32:
-// 4 us, which is a launch and two dependent loads).
+// 4 us, which is a launch and one round trip).
 __global__ void __launch_bounds__(256) tree_mask_kernel(TreeMaskArgs a) {
   __shared__ int16_t up[VC_TREE_MAX_NODES];
   pdl_launch_dependents();

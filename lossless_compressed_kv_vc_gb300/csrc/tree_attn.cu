@@ -963,8 +963,7 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
 // (K or V) on their way with 16-byte asynchronous copies into its own ring, and multiplies with mma.sync: S = Q K^T
 // with Q in registers, P from S's accumulators as they lie, O += P V. The tcgen05 kernel's fixed part (tensor maps,
 // TMEM, barriers, two chains' start and end) is what this one does without, and a page of 16 rows is as good as a
-// larger one, where TMA boxes of 2 KB hold the other back (32 tokens over 8200 rows, pages of 16: 186 us, the other
-// 195). Measured with 32 ragged requests of up to 8200 rows, 32/8 heads of 128, call after call: 939 MB in 152 us with
+// larger one, where TMA boxes of 2 KB hold the other back. Measured with 32 ragged requests of up to 8200 rows, 32/8 heads of 128, call after call: 939 MB in 152 us with
 // the merge, 6.2 TB/s. Equal ranges do not end together: SMs in the larger groups get up to 12% less of DRAM.
 template <int D>
 struct FCfg {
@@ -1503,10 +1502,11 @@ cudaError_t launch_tree_attn(const TreeArgs& a, cudaStream_t s, vc_status* st) {
   p.dev_status = a.dev_status;
   int most = 0;
   for (int b = 0; b < a.B; ++b) most = a.req[b].n_rows > most ? a.req[b].n_rows : most;
-  // Up to 8 rows, or 16 with the smallest pages, for the kernel without tensor memory (us of it and of the other: 32 x
-  // 1000 keys, 4 rows a head: 43.7, 49.8; 32 x 200: 25.2, 31.4; 32 x 8200 from pages of 16: 186, 195, of 128: 187, 181;
-  // 8 x 32768 keys, 16 rows, from pages of 64: 193, 183, of 16: 191, 192)
-  p.few = (int64_t)most * G <= (a.kv.shift == 4 ? FR : FR / 2);
+  // Up to 8 rows, or 16 where the table has room for no more than 4096 keys, for the kernel without tensor memory (us of it
+  // and of the other, call after call: 32 x 1000 keys, 4 rows a head: 31.9, 41.8; 32 x 8200 from pages of 16: 150, 156, of
+  // 128: 153, 148; 8 x 32768, 8 rows, from pages of 16: 170, 173, of 64: 174, 167. With 16 rows: 32 x 200 20.9, 27.1; 32 x
+  // 1000 38.9, 41.9; 32 x 8200 160, 157; 1 x 100000 86, 72: each warp's partial is written and read again)
+  p.few = (int64_t)most * G <= ((int64_t)a.kv.max_pages << a.kv.shift <= 4096 ? FR : FR / 2);
   const int64_t tiles = ((int64_t)a.kv.max_pages << a.kv.shift) / (p.few ? FK : TN) + 1;
   int64_t cost = 0, units = 0, same = host_units((int64_t)a.req[0].n_rows * G);
   p.slot_rows = 1;
