@@ -184,6 +184,22 @@ def test_thirty_two_forks_of_one(vc):
     p.same()
 
 
+@pytest.mark.parametrize("Hkv,d,page,B", [(8, 128, 128, 9), (4, 128, 128, 31), (8, 128, 16, 31), (8, 128, 16, 32), (3, 64, 128, 21),
+                                          (8, 64, 64, 17)])
+def test_copies_of_either_size(vc, Hkv, d, page, B):
+    """Shared last pages of many requests, copied by one launch (up to 2 MB of rows in all) and by two."""
+    g = gen(27)
+    p = Pool(vc, Hkv, Hkv, d, 2 * B + 6, page, B + 1, 4)
+    p.fill(0, 2 * page - 3, 0, g)
+    p.fork(*[(0, i) for i in range(1, B)])
+    p.reserve(*[(i, 1 + i % 5) for i in range(B)])
+    p.same()
+    p.trim(*[(i, page + i if i % 2 else 1, 0) for i in range(1, B)])
+    p.reserve(*[(i, page) for i in range(1, B)])  # some first pages are shared by all
+    p.same()
+    assert p.ref.faults == 0 and int(p.status.item()) == 0
+
+
 def test_trim_of_pages_that_several_requests_hold(vc):
     """A page that several requests of one call give back goes on the stack once, at the place of the last of them."""
     g = gen(4)
