@@ -92,8 +92,8 @@ class Batch:
         for s in streams:
             if s is None:
                 continue
-            if not isinstance(s, torch.cuda.Stream):
-                s = torch.cuda.ExternalStream(int(s))
+            if not isinstance(s, torch.cuda.Stream):  # ExternalStream(0) is a new stream, not the default one
+                s = torch.cuda.ExternalStream(int(s)) if int(s) else torch.cuda.default_stream()
             if s.cuda_stream not in self._ordered:
                 s.wait_event(self._built)
                 self._ordered.add(s.cuda_stream)
@@ -913,7 +913,10 @@ class TreeBatch:
     def _shape(self, B: int):
         return vc_shape(B, self.Hq, self.Hkv, self.d)
 
-    _order = LiveBatch._order
+    def _order(self, stream):
+        """As a LiveBatch's; a stream that has waited costs no more than a look."""
+        if not torch.cuda.is_current_stream_capturing() and _stream(stream) not in self._ordered:
+            Batch._order(self, _stream(stream))
 
     def _check_seqs(self, seqs, rows=None):
         if not 1 <= len(seqs) <= VC_MAX_BATCH or len(set(seqs)) != len(seqs) or not all(0 <= s < self.n_seq for s in seqs):
@@ -931,7 +934,7 @@ class TreeBatch:
         self._check_seqs(seqs)
         if len(rows) != len(seqs) or any(not 0 <= r < 2 ** 31 for r in rows):
             raise ValueError("rows: one count per sequence, not negative")
-        arr = (vc_reserve_req * len(seqs))(*[vc_reserve_req(s, r) for s, r in zip(seqs, rows)])
+        arr = (vc_reserve_req * len(seqs))(*zip(seqs, rows))
         with torch.cuda.device(self.device):
             self._order(stream)
             vc_pages_reserve(self._shape(len(seqs)), self.kv, arr, self.ws, self.dev_status, stream)
@@ -942,7 +945,7 @@ class TreeBatch:
             raise ValueError("pairs: 1 .. VC_MAX_BATCH of sequences of the pool")
         if len({b for _, b in pairs}) != len(pairs) or {a for a, _ in pairs} & {b for _, b in pairs}:
             raise ValueError("each sequence is copied into once, and none that is copied")
-        arr = (vc_fork_req * len(pairs))(*[vc_fork_req(a, b) for a, b in pairs])
+        arr = (vc_fork_req * len(pairs))(*[tuple(x) for x in pairs])
         with torch.cuda.device(self.device):
             self._order(stream)
             vc_pages_fork(self._shape(len(pairs)), self.kv, arr, self.dev_status, stream)
@@ -957,7 +960,7 @@ class TreeBatch:
         if len(rows) != len(seqs) or len(next) != len(seqs) or any(not 0 <= r < 2 ** 31 for r in rows) or \
                 any(not -2 ** 31 <= p < 2 ** 31 for p in next):
             raise ValueError("rows and next: one per sequence, int32, rows not negative")
-        arr = (vc_trim_req * len(seqs))(*[vc_trim_req(*x) for x in zip(seqs, rows, next)])
+        arr = (vc_trim_req * len(seqs))(*zip(seqs, rows, next))
         with torch.cuda.device(self.device):
             self._order(stream)
             vc_pages_trim(self._shape(len(seqs)), self.kv, arr, self.dev_status, stream)
@@ -989,12 +992,9 @@ class TreeBatch:
         if off is not None:
             self._check_ints(off, "off", *((B, self.axes.n_axes, R) if several else (B, R)))
         strides = (q.stride(1), k.stride(1), v.stride(1)) if max(rows) > 1 else (0, 0, 0)
-        arr = (vc_rope_page_req * B)()
-        for b, e in enumerate(arr):
-            e.q, e.k, e.v = q[b].data_ptr(), k[b].data_ptr(), v[b].data_ptr()
-            e.q_stride, e.k_stride, e.v_stride = strides
-            e.off, e.off_stride = (None, 0) if off is None else (off[b].data_ptr(), R if several else 0)
-            e.q_out, e.seq, e.n_rows = self.q_rot[b].data_ptr(), seqs[b], rows[b]
+        at = _rows_at(B, q, k, v, off, self.q_rot)
+        arr = (vc_rope_page_req * B)(*[(qb, kb, vb, *strides, ob, R if several else 0, rb, s, n)
+                                       for qb, kb, vb, ob, rb, s, n in zip(*at, seqs, rows)])
         with torch.cuda.device(self.device):
             self._order(stream)
             vc_rope_pages(self._shape(B), self.axes, self.kv, arr, self.dev_status, stream)
@@ -1007,11 +1007,9 @@ class TreeBatch:
             self._check_ints(mask, "mask", *mask.shape)
             if mask.dim() != 3 or mask.shape[0] != len(seqs) or mask.shape[1] < max(rows) or mask.shape[2] * 32 < max(rows):
                 raise ValueError("mask is [B][R][words], a row and a bit for each token")
-        arr = (vc_tree_req * len(seqs))()
-        for b, e in enumerate(arr):
-            e.q, e.o, e.seq, e.n_rows = self.q_rot[b].data_ptr(), o[b].data_ptr(), seqs[b], rows[b]
-            if mask is not None:
-                e.mask, e.mask_words = mask[b].data_ptr(), mask.shape[2]
+        words = 0 if mask is None else mask.shape[2]
+        arr = (vc_tree_req * len(seqs))(*[(qb, ob, mb, words, s, n) for qb, ob, mb, s, n in
+                                          zip(*_rows_at(len(seqs), self.q_rot, o, mask), seqs, rows)])
         with torch.cuda.device(self.device):
             self._order(stream)
             vc_tree_attn(self._shape(len(seqs)), self.kv, arr, self.ws, self.dev_status, stream)
@@ -1023,7 +1021,7 @@ class TreeBatch:
             raise ValueError("o is bf16 [B][R][Hq][d] on the pool's device, R >= max(rows), each sequence's rows contiguous")
         if sum(r > 0 for r in rows) > 1 and o.stride(0) < max(rows) * self.Hq * self.d:
             raise ValueError("each sequence's rows of o are its own")
-        if any(r > 0 and (o.data_ptr() + 2 * b * o.stride(0)) % 16 for b, r in enumerate(rows)):
+        if any(r > 0 and at % 16 for at, r in zip(*_rows_at(len(rows), o), rows)):
             raise ValueError("each sequence's rows of o start on a 16-byte boundary")
 
     def commit(self, seqs: List[int], rows: List[int], path: Optional[torch.Tensor] = None,
@@ -1040,11 +1038,7 @@ class TreeBatch:
             self._check_ints(n_acc, "n_acc", len(seqs))
         if advance is not None and (len(advance) != len(seqs) or any(not 0 <= a < 2 ** 31 for a in advance)):
             raise ValueError("advance: one count per sequence, not negative")
-        arr = (vc_commit_req * len(seqs))()
-        for b, e in enumerate(arr):
-            e.path = None if path is None else path[b].data_ptr()
-            e.n_acc = None if n_acc is None else n_acc[b:].data_ptr()
-            e.seq, e.n_rows, e.advance = seqs[b], rows[b], -1 if advance is None else advance[b]
+        arr = (vc_commit_req * len(seqs))(*zip(*_rows_at(len(seqs), path, n_acc), seqs, rows, [-1] * len(seqs) if advance is None else advance))
         with torch.cuda.device(self.device):
             self._order(stream)
             vc_tree_commit(self._shape(len(seqs)), self.kv, arr, self.dev_status, stream)
@@ -1089,11 +1083,22 @@ class TreeBatch:
         return out, path, n_acc
 
 
+def _rows_at(B, *tensors):
+    """For each tensor the addresses of its first B rows (None without a tensor): a view of each would cost microseconds."""
+    out = []
+    for t in tensors:
+        at, step = (None, 0) if t is None else (t.data_ptr(), t.stride(0) * t.element_size())
+        out.append(range(at, at + B * step, step) if step else [at] * B)
+    return out
+
+
 def _on(stream, device):
     """A context that allocates for `stream`: memory given back is then reused in its order, not the current one's."""
     if stream is None:
         return contextlib.nullcontext()
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device))
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device) if int(stream) else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def _check_trees(n_nodes, *trees):

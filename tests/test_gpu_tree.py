@@ -1017,6 +1017,27 @@ def test_two_pools_on_two_streams(vc):
         assert torch.equal(tb.len, alone.len) and int(tb.dev_status.item()) == 0
 
 
+@pytest.mark.parametrize("stream", [None, 0])
+def test_a_pool_built_on_a_stream_that_is_behind(vc, stream):
+    """A pool whose construction waits behind other work of its stream, used at once on the default stream."""
+    Hq, Hkv, d, B = 8, 2, 64, 3
+    g = gen(28)
+    make = lambda: _batch(vc, Hq, Hkv, d, n_seq=B, n_pages=40, page=16, max_rows=40)
+    x = [randn(g, B, 40, h, d) for h in (Hq, Hkv, Hkv)]
+    outs = [torch.zeros_like(x[0]) for _ in range(2)]
+    alone = make()
+    torch.cuda.synchronize()
+    alone.step([0, 1, 2], *x, outs[0], [40, 1, 17])
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)  # about 25 ms of device time
+        late = make()
+    late.step([0, 1, 2], *x, outs[1], [40, 1, 17], stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(late.len, alone.len) and torch.equal(late.table[:, 0], alone.table[:, 0])
+    assert int(late.dev_status.item()) == 0 and int(late.n_free.item()) == int(alone.n_free.item())
+
+
 def test_a_pool_that_runs_out(vc):
     """Room is asked for beyond the pool: reported, the sequence's rows are not written anywhere, the others go on."""
     Hq, Hkv, d = 8, 2, 64

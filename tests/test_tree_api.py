@@ -482,3 +482,22 @@ def test_engine_refusals(vc, calls):
     for kw in (dict(page=8), dict(n_seq=0), dict(n_pages=0), dict(max_rows=0), dict(max_pages=0)):
         with pytest.raises(ValueError):
             trees(vc, **kw)
+
+
+def test_the_default_stream_is_waited_on_itself(vc, monkeypatch):
+    """Stream 0 is the default stream, of which ExternalStream would make a new one."""
+    from lossless_compressed_kv_vc_gb300 import engine
+
+    class Default:
+        cuda_stream, waited = 0, []
+
+        def wait_event(self, e):
+            self.waited.append(e)
+
+    class Owner:
+        _ordered, _built = set(), "built"
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda *_: Default())
+    monkeypatch.setattr(torch.cuda, "ExternalStream", None)
+    for _ in range(2):
+        engine.Batch._order(Owner, 0)
+    assert Default.waited == ["built"] and Owner._ordered == {0}
