@@ -9,7 +9,7 @@
 // 8 softmax warps, 4 MMA issuers, 1 loader) takes an equal range of them by cost. A CTA's part of a unit of a head
 // (a piece) leaves an (o, lse) partial; a second kernel merges a row's partials. Of a chain (no mask) each unit has
 // the tiles up to the last key that it sees, so a prompt's upper half is not computed (32/8 heads of 128, 2048 tokens
-// over no context: 80 us, 172 with all tiles). Where every request has the same number U > 1 of full units, CTA c
+// over no context: 112 us, 172 with all tiles; 69 with all that came since). Where every request has the same number U > 1 of full units, CTA c
 // may take unit c % U in the c / U-th range of [request][head][tile], a lane, instead: the units of a head read a tile
 // at about the same time, and it comes from DRAM once.
 //
@@ -25,8 +25,10 @@
 // waits for the P V before it (8 trees of 64 over 32768 keys, 64/8 heads of 128: 499 us so, 395 with two S of 64 keys).
 //
 // What bounds it: up to about 130 rows of a KV head DRAM (16 trees of 25 over up to 16300 rows, 40/8 heads of 128:
-// 946 MB in 158 us with the merge, 0.89 of the copy rate); above that each chain's loop S, softmax, P V, the next S
-// (the case above: 380 us, 1.45 PFLOP/s, 0.77 of the bf16 rate; 357 without any softmax).
+// 946 MB in 154 us with the merge, 0.91 of the copy rate); above that each chain's loop S, softmax, P V, the next S
+// (the case above: 369 us, 1.50 PFLOP/s, 0.79 of the bf16 rate, in a burst; 340 without exponentials and branches). Of a
+// step's 1600 clocks a softmax warp spends 930 on its weights beside the other chain's warp, 135 on S from TMEM, 125 on P
+// back to it, the rest on barriers and waits; the tensor cores need 1260 for both chains' step.
 //
 // What a query row may not see: keys get -infinity by the row's bits of the mask; value rows behind the last
 // token (whatever the page holds there) are zeroed in shared memory, and where a step has a value row that is not
@@ -38,6 +40,7 @@
 #include <limits.h>
 #include <math.h>
 #include <string.h>
+#include <type_traits>
 
 namespace vc {
 
@@ -767,13 +770,17 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
       const uint32_t* mrow = masked && row_ok ? p.mask[q.g] + (size_t)tl * words : nullptr;
       const TSteps steps(p, plan, q, w);
       m_run = -INFINITY, l_run = 0.f;
-      for (int i = 0; i < steps.count; ++i, ++t) {
+      // A step, with `tail` or without what only steps need that some row does not see whole: the others' loop is short,
+      // and its registers go to the weights. The way back to them once a maximum has moved is a copy of its own, as a loop
+      // around them keeps the compiler from overlapping them with what comes next (8 trees of 64 over 32768 keys, 64/8
+      // heads: of 128 channels 378 us with one loop for all, 368 so; of 64 channels 340, 298). With 64 channels P also
+      // goes to TMEM before it is known whether it stands: 275 us. With 128, where the tensor cores set the pace, that
+      // costs more than it gives (382).
+      constexpr bool EAGER = D == 64;
+      auto step = [&](auto kind, int i) -> bool {
+        constexpr bool tail = decltype(kind)::value;
         const uint32_t buf = 2 * w + (t & 1), tP = tS + (t & 1) * TS;
-        const bool tail = i >= steps.full;
-        if (!twait_warp(&sfull[buf], (t >> 1) & 1, p.dev_status, s_abort)) {
-          ok = false;
-          break;
-        }
+        if (!twait_warp(&sfull[buf], (t >> 1) & 1, p.dev_status, s_abort)) return false;
         tc05::fence_after();
         uint32_t see_lo = 0xffffffffu, see_hi = 0xffffffffu;  // keys of the step that the row sees
         if (alive) {
@@ -787,7 +794,7 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(lo[e]), x[32 + e] = __uint_as_float(hi[e]);
           }
-          if (tail) {
+          if constexpr (tail) {
             const int k0 = steps.beg + i * steps.stride;
             if (masked) {
               mask_bits(mrow, words, k0 - ctx, n - k0, see_lo, see_hi);
@@ -810,36 +817,7 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
           // computed again. TMEM loads and stores are warp-collective: the warp does it together.
           uint32_t r[TS / 2];
           float sum = 0.f;
-#pragma unroll 1
-          for (bool look = i == 0;; look = true) {
-            if (look) {
-              float top = -INFINITY;
-#pragma unroll
-              for (int e = 0; e < TS; e += 2) top = max3f(top, x[e], x[e + 1]);
-              const float m_new = fmaxf(m_run, top * p.scale_log2);
-              float f = 1.f;
-              if (m_new > m_run) {
-                f = ex2_approx(m_run - m_new);
-                l_run *= f;
-                m_run = m_new;
-              }
-              if (i > 0) {
-                if (!pv_done(t - 1)) {
-                  ok = false;
-                  break;
-                }
-                tc05::fence_after();
-#pragma unroll 1
-                for (int cb = 0; cb < D / 32; ++cb) {
-                  uint32_t o[32];
-                  tc05::ld32(tO + cb * 32, o);
-                  arrived(o);
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                  tc05::st32(tO + cb * 32, o);
-                }
-              }
-            }
+          auto weights = [&] {
             const float mu = m_run == -INFINITY ? 0.f : m_run;
             const uint64_t sc = f2_pack(p.scale_log2, p.scale_log2), nm = f2_pack(-mu, -mu);
             uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
@@ -854,25 +832,56 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
             float u0, u1;
             f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), u0, u1);
             sum = u0 + u1;
+          };
+          bool look = i == 0;
+          if (!look) {
+            weights();
+            if constexpr (EAGER) tc05::st32(tP, r);  // ahead of the answer, which is rarely yes
             // a row that has seen nothing yet has no m: its weights say nothing of how large its scores are
-            if (look || !__any_sync(0xffffffffu, sum > 1024.f || m_run == -INFINITY)) break;
+            look = __any_sync(0xffffffffu, sum > 1024.f || m_run == -INFINITY);
           }
-          if (!ok) break;
-          tc05::st32(tP, r);
+          if (look) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < TS; e += 2) top = max3f(top, x[e], x[e + 1]);
+            const float m_new = fmaxf(m_run, top * p.scale_log2);
+            float f = 1.f;
+            if (m_new > m_run) {
+              f = ex2_approx(m_run - m_new);
+              l_run *= f;
+              m_run = m_new;
+            }
+            if (i > 0) {
+              if (!pv_done(t - 1)) return false;
+              tc05::fence_after();
+#pragma unroll 1
+              for (int cb = 0; cb < D / 32; ++cb) {
+                uint32_t o[32];
+                tc05::ld32(tO + cb * 32, o);
+                arrived(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tc05::st32(tO + cb * 32, o);
+              }
+            }
+            weights();
+            if constexpr (EAGER) {
+              tc05::wait_st();  // the P of before
+              tc05::st32(tP, r);
+            }
+          }
+          if constexpr (!EAGER) tc05::st32(tP, r);
           l_run += sum;
           tc05::wait_st();
         }
         // A step with keys that some rows do not see: a weight of 0 would carry an infinite or NaN value row to
         // them. Rows from n on, which nobody sees, are zeroed; if others hold such a value, the threads add up the
         // seen keys themselves.
-        if (tail) {
+        if constexpr (tail) {
           const int k0 = steps.beg + i * steps.stride, j = k0 / TN, h = k0 / TS & 1;
           const uint32_t gv = g + j - q.j0;
           // V has landed: the phase before is over (its P V are done), and its own cannot pass without this chain
-          if (!twait_warp(&vfull[gv % C::VST], (gv / C::VST) & 1, p.dev_status, s_abort)) {
-            ok = false;
-            break;
-          }
+          if (!twait_warp(&vfull[gv % C::VST], (gv / C::VST) & 1, p.dev_status, s_abort)) return false;
           uint8_t* sV = smem + C::OFF_V + (gv % C::VST) * C::T_BYTES;
           bool bad = false;
           const int kv = h * TS + (rt & (TS - 1));  // two threads look through each of the step's rows
@@ -892,16 +901,10 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&vbar[w]);
-          if (!twait_warp(&vbar[w], looked & 1, p.dev_status, s_abort)) {
-            ok = false;
-            break;
-          }
+          if (!twait_warp(&vbar[w], looked & 1, p.dev_status, s_abort)) return false;
           ++looked;
           if (alive && s_odd[buf] == t + 1) {
-            if (i > 0 && !pv_done(t - 1)) {
-              ok = false;
-              break;
-            }
+            if (i > 0 && !pv_done(t - 1)) return false;
             tc05::fence_after();
 #pragma unroll 1
             for (int cb = 0; cb < D / 32; ++cb) {
@@ -944,7 +947,13 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
         tc05::fence_before();
         __syncwarp();
         tarrive_if(&pfull[buf], lane == 0);
-      }
+        return true;
+      };
+      int i = 0;
+#pragma unroll 1
+      for (; ok && i < steps.full; ++i, ++t) ok = step(std::false_type(), i);
+#pragma unroll 1
+      for (; ok && i < steps.count; ++i, ++t) ok = step(std::true_type(), i);
       g += q.j1 - q.j0;
       if (!ok) break;
       q.next(p, plan);
