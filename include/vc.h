@@ -572,6 +572,9 @@ size_t vc_evict_workspace_size(const vc_shape* shape, int32_t max_n);
  * State that does not add up (a table entry outside the pool, a length beyond the pages held, rows to
  * be written where the sequence has no page or shares it) is never followed out of bounds: the rows
  * or pages it touches are skipped (read as zeros by vc_tree_attn) and dev_status receives VC_DEV_PAGES.
+ * A sequence that vc_pages_reserve could not serve is in that state for its turn, and keeps its context:
+ * len and next tell afterwards which ones those are. Forks go between turns, not between a source's
+ * vc_rope_pages and vc_tree_commit: its last page is then shared, and the turn's rows in it do not count.
  * Limits: page is 16, 32, 64 or 128; (n_pages + 1) * Hkv < 2^31 and max_pages * page <= 2^30
  * (VC_ERR_UNSUPPORTED). k and v 16-byte aligned, the others 4-byte. The device current to the calling
  * thread is the one that holds the buffers. */
@@ -732,7 +735,9 @@ vc_status vc_tree_accept(int32_t B, int32_t N_max, int32_t V, const float* logit
  * for i < m, where m = *n_acc held to 0 .. n_rows, then len += m and next += advance (advance < 0: m).
  * path NULL: the first m rows as they lie; n_acc NULL: m = n_rows (both NULL: a prompt chunk, or a chain
  * accepted whole). A path entry outside i .. n_rows-1 ends the path there (VC_DEV_PAGES; m = i). Pages are
- * neither taken nor given back. Requests with n_rows == 0 are skipped. */
+ * neither taken nor given back. Requests with n_rows == 0 are skipped. A sequence that does not hold the pages
+ * of all rows len .. len+n_rows-1 alone is left as it was, len and next too (VC_DEV_PAGES): vc_pages_reserve
+ * could not serve it, or a fork came between. The turn can be made again once there is room. */
 typedef struct vc_commit_req {
   const int32_t* path;   /* device int32 [n_rows], ascending, or NULL */
   const int32_t* n_acc;  /* device int32 [1], or NULL */

@@ -386,6 +386,8 @@ __global__ void __launch_bounds__(256) compact_move_kernel(const __grid_constant
 // ---- commit -------------------------------------------------------------------------------------------
 // A block per request, a thread per 16-byte column of the heads' K and V rows, which it moves from the first
 // row to the last: row i takes row path[i] >= i, so that no row is written that a later one still needs.
+// vc_rope_pages has written the turn's rows if all of them lie in pages that the sequence holds alone, which is so
+// where vc_pages_reserve served it. Otherwise nothing becomes context, and the turn can be made again.
 constexpr int kCommitRows = 256;  // rows of the path looked up at a time
 template <int D>
 __global__ void __launch_bounds__(256) commit_kernel(const __grid_constant__ CommitParams p) {
@@ -400,13 +402,21 @@ __global__ void __launch_bounds__(256) commit_kernel(const __grid_constant__ Com
   bool ok = true;
   const int n = context_rows(kv, q.seq, held, ok);
   const int early = q.path && (int)threadIdx.x < q.n_rows ? q.path[threadIdx.x] : 0;  // beside the other state, not behind it
-  int m = q.n_acc ? min(max(*q.n_acc, 0), q.n_rows) : q.n_rows;
-  if (m > (held << kv.shift) - n) {  // rows that were never written
-    m = (held << kv.shift) - n;
+  const int m = q.n_acc ? min(max(*q.n_acc, 0), q.n_rows) : q.n_rows;
+  const int end = (int)(((int64_t)n + q.n_rows + page - 1) >> kv.shift);
+  if (end > held)
     ok = false;
-  }
-  if (!ok && threadIdx.x == 0) set_status(p.dev_status, VC_DEV_PAGES);
+  else
+#pragma unroll 4
+    for (int j = (n >> kv.shift) + threadIdx.x; j < end; j += blockDim.x) {
+      const int own = pages[j];
+      if (!kv.has_page(own) || kv.refs[own] != 1) ok = false;
+    }
   if (threadIdx.x == 0) s_m = m;
+  if (!__syncthreads_and(ok)) {
+    if (threadIdx.x == 0) set_status(p.dev_status, VC_DEV_PAGES);
+    return;
+  }
   const int head = page * (D / 8), cols = p.Hkv * (D / 8);  // pieces of a head's page; 16-byte columns of K
   auto piece = [&](int row) { return ((int64_t)pages[row >> kv.shift] * p.Hkv * page + (row & (page - 1))) * (D / 8); };
   if (q.path)
@@ -414,15 +424,11 @@ __global__ void __launch_bounds__(256) commit_kernel(const __grid_constant__ Com
       __syncthreads();
       for (int i = i0 + threadIdx.x; i < min(m, i0 + kCommitRows); i += blockDim.x) {
         const int from = i < (int)blockDim.x ? early : q.path[i];
-        bool good = from >= i && from < q.n_rows && (int64_t)n + from < (int64_t)held << kv.shift;
+        const bool good = from >= i && from < q.n_rows;
         int64_t src = 0, dst = -1;
-        if (good && from != i) {
-          const int a = pages[(n + from) >> kv.shift], b = pages[(n + i) >> kv.shift];
-          good = kv.has_page(a) && kv.has_page(b) && kv.refs[b] == 1;
-          if (good) {
-            src = piece(n + from);
-            dst = piece(n + i);
-          }
+        if (good && from != i) {  // both among the turn's rows
+          src = piece(n + from);
+          dst = piece(n + i);
         }
         if (!good) {
           atomicMin(&s_m, i);

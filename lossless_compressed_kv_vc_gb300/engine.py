@@ -876,7 +876,9 @@ class TreeBatch:
 
     A turn: reserve room, append the tokens' rotated keys and their values behind the context, attend,
     and commit what was accepted (accept does both ends of that for trees). What the device finds wrong
-    (no pages left, say) lands in dev_status. All calls run on `stream` (the current one by default);
+    (no pages left, say) lands in dev_status. A sequence that the pool had no pages for keeps its context, len and
+    next, whatever its turn's outputs say: they tell which ones those are, and the same turn can be made again
+    once there is room. Forks go between turns. All calls run on `stream` (the current one by default);
     like a Batch's, each stream first waits for the construction. They share q_rot and a workspace, so
     calls on different streams are ordered by the caller.
     """

@@ -89,9 +89,14 @@ class Pages:
         self.free[: self.n_free] = np.arange(len(self.refs) - 1, U - 1, -1)
 
     def commit(self, reqs):
-        """reqs: (seq, rows, path or None, n_acc or None, advance)."""
+        """reqs: (seq, rows, path or None, n_acc or None, advance). A sequence whose rows are not all its own is left."""
         for seq, rows, path, n_acc, advance in reqs:
             n = int(self.len[seq])
+            if rows == 0:
+                continue
+            if not self.own(seq, rows):
+                self.faults += 1
+                continue
             m = rows if n_acc is None else min(max(int(n_acc), 0), rows)
             if path is not None:
                 for i in range(m):
@@ -103,6 +108,11 @@ class Pages:
                     self.put(seq, n + i, k, v)
             self.len[seq] = n + m
             self.next[seq] += m if advance < 0 else advance
+
+    def own(self, seq, rows):
+        """Rows len .. len + rows - 1 all lie in pages that the sequence holds alone."""
+        n, end = int(self.len[seq]) // self.page, -(-(int(self.len[seq]) + rows) // self.page)
+        return end <= self.held[seq] and all(0 <= p < len(self.refs) and self.refs[p] == 1 for p in self.table[seq, n:end])
 
     def rows(self, seq, a, b):
         """K and V [Hkv][b - a][d] of rows a .. b-1."""

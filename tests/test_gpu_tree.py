@@ -281,6 +281,47 @@ def test_commit_along_paths(vc):
     assert int(p.ref.len[s]) == n + 4
 
 
+def test_commit_of_rows_that_were_never_written(vc):
+    """Sequences that reserve could not serve are left as they are, whatever the path says: a last page that another one
+    holds, room for a part of the rows, pages laid down by hand that are nobody's; the others of the call are served."""
+    g = gen(31)
+    p = Pool(vc, 4, 2, 64, 9, 16, 6, 6)
+    p.fill(0, 20, 0, g)
+    p.fill(2, 27, 0, g)
+    p.fill(3, 5, 40, g)
+    p.write(3, 5, 40, g)
+    p.fork((0, 1), (2, 4))
+    p.fill(5, 1, 0, g)
+    p.reserve((1, 3), (2, 9), (4, 1))  # one page left: 1 gets its copy of it, and the others wait
+    p.same()
+    assert p.ref.n_free == 0 and p.ref.faults == 2
+    for s, rows, path, n_acc, advance in ((2, 9, None, None, -1), (2, 5, [0, 1, 2, 3, 4], 5, -1), (4, 1, [0], 1, 4),
+                                          (2, 9, [0, 2, 7, -1, -1, -1, -1, -1, -1], 3, -1), (4, 5, None, 0, 7),
+                                          (5, 17, None, 3, -1), (5, 40, [0] * 40, 1, -1)):
+        p.status.zero_()
+        p.commit((s, rows, path, n_acc, advance), (3, 1, None, None, -1))
+        p.same()
+        assert int(p.status.item()) == vc.VC_DEV_PAGES
+    assert p.ref.len.tolist() == [20, 20, 27, 12, 27, 1]
+    p.status.zero_()
+    p.write(1, 20, 3, g)
+    p.commit((1, 3, [0, 2, -1], 2, -1))
+    p.trim((3, 0, 0))
+    p.reserve((2, 9), (4, 1))
+    p.write(2, 27, 9, g)
+    p.write(4, 27, 1, g)
+    p.commit((2, 9, [0, 4, 7, 8, -1, -1, -1, -1, -1], 4, -1), (4, 1, None, None, -1))
+    p.same()
+    assert int(p.status.item()) == 0 and p.ref.len.tolist() == [20, 22, 31, 0, 28, 1]
+    mine = int(p.ref.table[5, 0])
+    for page, refs in ((9, 1), (-1, 1), (2 ** 30, 1), (mine, 0), (mine, 2)):  # laid down by hand
+        p.state["table"][5, 0], p.state["refs"][mine] = page, refs
+        p.status.zero_()
+        vc.vc_tree_commit(p.shape(), p.kv, p.arr(vc.vc_commit_req, [(None, None, 5, 2, 1)]), p.status)
+        torch.cuda.synchronize()
+        assert int(p.status.item()) == vc.VC_DEV_PAGES and int(p.state["len"][5]) == int(p.state["next"][5]) == 1
+
+
 # ---- rotary append ----------------------------------------------------------------------------------
 def _rope_close(got, x, pos, freqs, axis, inter, amp, heads, d):
     x = f64(x).reshape(-1, heads, d)
@@ -1055,3 +1096,69 @@ def test_a_pool_that_runs_out(vc):
     tb.step([0], *y, o[:1, :1].contiguous())
     torch.cuda.synchronize()
     assert int(tb.dev_status.item()) == 0 and tb.len.tolist() == [41, 0]
+
+
+def _unserved(vc, shared):
+    """A small pool and one that never runs out, as far as the step that the small one cannot serve: sequence 1 has
+    forked from 0 within a page (`shared`), or asks for more rows than its own last page has room for. 2 holds the rest."""
+    Hq, Hkv, d = 8, 2, 64
+    small, large = (_batch(vc, Hq, Hkv, d, n_seq=3, n_pages=n, page=16, max_rows=40, max_pages=9) for n in (7, 40))
+    g = gen(33 + shared)
+    x = [randn(g, 3, 40, h, d) for h in (Hq, Hkv, Hkv)]
+    for tb in (small, large):
+        tb.step([0, 1], *(t[:2] for t in x), torch.zeros_like(x[0][:2]), [27, 0 if shared else 5])
+        if shared:
+            tb.fork([(0, 1)])
+        tb.step([2], *(t[2:].contiguous() for t in x), torch.zeros_like(x[0][2:]), [40])
+        tb.reserve([2], [40 if shared else 24])
+    torch.cuda.synchronize()
+    assert int(small.n_free.item()) == 0 and int(small.dev_status.item()) == 0
+    return small, large, g
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("shared", [False, True])
+def test_a_turn_that_the_pool_cannot_serve_is_made_again(vc, tree, shared):
+    """Lengths and positions stay where they were; with pages given back the same turn equals that of a pool that never
+    ran out, and so do those that follow."""
+    small, large, g = _unserved(vc, shared)
+    Hq, Hkv, d, N, V = 8, 2, 64, 14, 30
+    parent = torch.tensor([random_tree(np.random.default_rng(5), N)], dtype=torch.int32, device="cuda")
+    rows, n_nodes = [N], ints(1, fill=N)
+
+    def turn(tb, q, k, v, logits):
+        o = torch.full((1, N, Hq, d), NAN, dtype=torch.bfloat16, device="cuda")
+        token = logits.argmax(2).gather(1, parent.clamp(min=0).long()).to(torch.int32)
+        tb.step([1], q, k, v, o, rows, *((parent, n_nodes) if tree else ()))
+        if tree:
+            tb.accept([1], logits, token, parent, n_nodes, rows)
+        torch.cuda.synchronize()
+        return o
+
+    before = [t.clone() for t in (small.len, small.next, small.held, small.table, small.refs)]
+    x = [randn(g, 1, N, h, d) for h in (Hq, Hkv, Hkv)] + [torch.randn((1, N, V), generator=g, device="cuda")]
+    turn(small, *x)
+    assert int(small.dev_status.item()) == vc.VC_DEV_PAGES
+    assert all(torch.equal(a, b) for a, b in zip(before, (small.len, small.next, small.held, small.table, small.refs)))
+    small.dev_status.zero_()
+    small.trim([2])
+    large.trim([2])
+    for again in range(3):
+        if again:
+            x = [randn(g, 1, N, h, d) for h in (Hq, Hkv, Hkv)] + [torch.randn((1, N, V), generator=g, device="cuda")]
+        assert torch.equal(turn(small, *x), turn(large, *x))
+        assert int(small.dev_status.item()) == int(large.dev_status.item()) == 0
+        assert torch.equal(small.len, large.len) and torch.equal(small.next, large.next)
+        if again == 0:  # the other one goes on too
+            y = [randn(g, 1, 3, h, d) for h in (Hq, Hkv, Hkv)]
+            outs = [torch.zeros_like(y[0]) for _ in range(2)]
+            for tb, o in zip((small, large), outs):
+                tb.step([0], *y, o, [3])
+            torch.cuda.synchronize()
+            assert torch.equal(*outs)
+    n = int(small.len[1])
+    assert n > before[0][1]
+    for tb in (small, large):
+        at = torch.arange(n, device="cuda")
+        tb.got = [t[tb.table[1].long()[at // 16], :, at % 16] for t in (tb.k, tb.v)]
+    assert all(torch.equal(a, b) for a, b in zip(small.got, large.got))

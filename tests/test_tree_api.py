@@ -131,6 +131,22 @@ def test_pages_of_any_life_stay_counted():
         p.check()
 
 
+def test_a_commit_of_rows_that_are_not_there_leaves_the_sequence():
+    """A page that others hold, or fewer pages than the rows take: nothing becomes context, with a path and without."""
+    p = O.Pages(4, 4, 3, 4, *(np.zeros((4, 1, 4, 2)) for _ in range(2)))
+    p.reserve([(0, 6)])
+    p.commit([(0, 6, None, None, -1)])
+    p.fork([(0, 1)])
+    p.reserve([(2, 8), (1, 1)])  # none is left for 1's copy of the second page
+    p.commit([(1, 1, None, None, 5), (0, 2, [0, 1], 2, -1), (2, 9, None, 1, -1)])
+    assert p.faults == 4 and p.len.tolist() == [6, 6, 0] and p.next.tolist() == [6, 6, 0]
+    p.trim([(2, 0, 0)])
+    p.reserve([(1, 1)])
+    p.commit([(1, 1, None, None, 5), (0, 2, [0, 1], 2, -1), (2, 0, None, None, 9)])
+    assert p.faults == 4 and p.len.tolist() == [8, 7, 0] and p.next.tolist() == [8, 11, 0]
+    p.check()
+
+
 # ---- the table of axes ----------------------------------------------------------------------------
 @pytest.mark.parametrize("sections", [[32], [16, 16], [12, 10, 10], [0, 32, 0], [8, 8, 8, 8], [1, 30, 1]])
 @pytest.mark.parametrize("dealt", [False, True])
