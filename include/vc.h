@@ -701,7 +701,8 @@ vc_status vc_tree_mask(int32_t B, int32_t N_max, const int32_t* parent, const in
  * row that sees no key gets zeros. Rows that a query row may not see do not reach it, whatever they
  * hold, nor does what the last page holds behind them. Scale 1/sqrt(d), GQA, arithmetic and rounding as
  * in vc_prefix_attn. Requests with n_rows == 0 are skipped; tokens whose rows lie behind the pages
- * held are seen by none (VC_DEV_PAGES).
+ * held are seen by none (VC_DEV_PAGES), and no token is where the sequence does not hold the page of row
+ * len alone (VC_DEV_PAGES: the rows were not written; all see the context).
  * ws: vc_tree_workspace_size(shape, max_rows) bytes for calls of up to max_rows rows a request; no
  * initialisation; calls that overlap on the GPU must not share one.
  * Errors before anything is launched: VC_ERR_INVALID; VC_ERR_WORKSPACE; VC_ERR_UNSUPPORTED (more than 2^29 query

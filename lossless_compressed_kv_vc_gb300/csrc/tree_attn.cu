@@ -32,7 +32,8 @@
 //
 // What a query row may not see: keys get -infinity by the row's bits of the mask; value rows behind the last
 // token (whatever the page holds there) are zeroed in shared memory, and where a step has a value row that is not
-// finite and not for all, the threads add up the rows they see themselves.
+// finite and not for all, the threads add up the rows they see themselves. Tokens of a sequence whose last page
+// others hold too have no rows there (vc_rope_pages has skipped them) and count for none.
 #include "paged.cuh"
 #include "tc05.cuh"
 
@@ -106,6 +107,12 @@ struct TreePlan {
   uint32_t cut;                      // requests whose units end with the last key that they see, a bit each
 };
 
+// The page of a sequence's first token, which may hold rows of its context, is the sequence's alone. Those behind it
+// always are, as a fork shares pages of context alone; and if this one is not, vc_pages_reserve had no page for the
+// copy, and vc_rope_pages did not write there.
+__device__ __forceinline__ int token_page(const PagedDev& kv, int seq, int ctx) { return __ldcg(kv.pages_of(seq) + (ctx >> kv.shift)); }
+__device__ __forceinline__ bool holds_alone(const PagedDev& kv, int page) { return kv.has_page(page) && __ldcg(kv.refs + page) == 1; }
+
 __device__ __forceinline__ int units_of(int rows) { return (rows + TU - 1) / TU; }
 __device__ __forceinline__ int tiles_of(const TreeParams& p, int n) { return p.few ? (n + FK - 1) / FK : (n + TN - 1) / TN; }
 
@@ -129,6 +136,9 @@ __device__ __forceinline__ void tree_plan(const TreeParams& p, TreePlan* s, int 
     const int held = min(max(__ldcg(p.kv.held + seq), 0), p.kv.max_pages), len = __ldcg(p.kv.len + seq), cap = held << p.kv.shift;
     ctx = min(max(len, 0), cap);
     n = (int)min((int64_t)cap, (int64_t)ctx + tokens);
+    // two more dependent loads (2048 tokens over no context 68.4 to 69.0 us); the kernel for few rows makes them beside
+    // its first keys, where they cost 0.2 us a call, and 0.7 here
+    if (!p.few && n > ctx && !holds_alone(p.kv, token_page(p.kv, seq, ctx))) n = ctx;
     if (tell && (ctx != len || n - ctx != tokens)) set_status(p.dev_status, VC_DEV_PAGES);
     rows = tokens * p.G;
     tiles = tiles_of(p, n);
@@ -980,7 +990,7 @@ struct FCfg {
   static constexpr int SMEM = FWARPS * 4 * HALF;      // two chunks a warp
 };
 
-// Bits of the 16 keys from k0 on that row i of a request's tokens sees; node = k0 - ctx > -16.
+// Bits of the 16 keys from k0 on that row i of a request's tokens sees; node = k0 - ctx > -16; left: keys from k0 on, if any.
 __device__ __forceinline__ uint32_t few_bits(const uint32_t* row, int words, bool masked, int tok, int node, int left) {
   uint32_t x;
   if (!masked) {
@@ -993,7 +1003,7 @@ __device__ __forceinline__ uint32_t few_bits(const uint32_t* row, int words, boo
     else
       x = word(0) << -node | ((1u << -node) - 1u);
   }
-  return x & (left < 16 ? (1u << left) - 1u : 0xffffu);
+  return x & (left >= 16 ? 0xffffu : left > 0 ? (1u << left) - 1u : 0u);
 }
 
 template <int D>
@@ -1039,6 +1049,8 @@ __global__ void __launch_bounds__(FWARPS * 32, FCTAS) tree_few_kernel(const __gr
       return page;
     };
     int pages = look(j0), more = look(j0 + 32);  // those in use and the next ones
+    const bool tokens = j1 * FK > ctx && n > ctx;
+    const int tpage = tokens ? token_page(p.kv, p.seq[g], ctx) : 0;
     // Q, asked for ahead of all K and V, in A-fragment order: rows qrow and qrow + 8, channels 16 kk + qcol (+ 8)
     uint32_t qf[D / 16][4];
     int tok[2];
@@ -1075,7 +1087,12 @@ __global__ void __launch_bounds__(FWARPS * 32, FCTAS) tree_few_kernel(const __gr
     load(j0, 1);
     load(j0 + 1, 0);
     load(j0 + 1, 1);
-    const int blind = masked ? ctx : ctx + 1;  // the first key that some row may not see
+    int seen = n;  // keys that count
+    if (tokens && !holds_alone(p.kv, tpage)) {
+      seen = ctx;
+      set_status(p.dev_status, VC_DEV_PAGES);
+    }
+    const int blind = min(seen, masked ? ctx : ctx + 1);  // the first key that some row may not see
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, acc[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
@@ -1105,11 +1122,11 @@ __global__ void __launch_bounds__(FWARPS * 32, FCTAS) tree_few_kernel(const __gr
       if (((j - j0 + 2) & 31) == 0) pages = more;
       load(j + 2, 0);
       uint32_t see[2] = {0xffffu, 0xffffu};
-      const bool tail = k0 + FK > min(blind, n);
+      const bool tail = k0 + FK > blind;
       if (tail) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          see[e] = few_bits(mrow[e], words, masked, tok[e], k0 - ctx, n - k0);
+          see[e] = few_bits(mrow[e], words, masked, tok[e], k0 - ctx, seen - k0);
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll

@@ -739,6 +739,41 @@ def test_rows_that_have_no_pages(vc):
     check(vc, p, Hq, reqs[1:], [np.tri(10, dtype=bool), np.tri(4, dtype=bool)], outs[1:])
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,page,n,N", [
+    (8, 2, 64, 16, 200, 1), (8, 2, 64, 16, 9, 2), (32, 8, 128, 16, 3000, 4), (4, 4, 128, 128, 1, 7), (32, 8, 128, 32, 70, 9),
+    (8, 2, 64, 64, 127, 30), (64, 8, 128, 64, 300, 64), (64, 8, 128, 16, 1, 64), (16, 1, 64, 128, 4060, 40), (5, 5, 128, 16, 23, 300)])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("junk", [None, NAN, float("inf")])
+def test_tokens_in_a_page_that_others_hold_are_seen_by_none(vc, Hq, Hkv, d, page, n, N, tree, junk):
+    """Sequences forked within a page and not made ready: their tokens' rows there were never written, whatever the page
+    holds, so all see the context alone, those behind in pages of their own too; reported, and others come out right."""
+    g, rng = gen(32), np.random.default_rng(N + n)
+    p = Pool(vc, Hq, Hkv, d, 5 + 3 * -(-(n + N) // page), page, 3, 1 + -(-(n + N) // page))
+    p.fill(0, n, N, g)
+    p.write(0, n, N, g)
+    p.fill(2, n, N, g)
+    p.write(2, n, N, g)
+    p.fork((0, 1))
+    last = int(p.ref.table[0, n // page])
+    assert p.ref.refs[last] == 2
+    if junk is not None:
+        p.k[last, :, n % page :], p.v[last, :, n % page :] = junk, junk
+    see = O.ancestors(random_tree(rng, N))[0] if tree else np.tri(N, dtype=bool)
+    mask = torch.tensor(O.pack_mask(see, -(-N // 32)), device="cuda") if tree else None
+    none = np.zeros((N, N), bool)
+    for seqs in ([2, 0, 1], [1], [0]):
+        p.status.zero_()
+        reqs = [(s, randn(g, N, Hq, d), mask) for s in seqs]
+        outs = attend(vc, p, reqs)
+        torch.cuda.synchronize()
+        assert int(p.status.item()) == vc.VC_DEV_PAGES
+        check(vc, p, Hq, [r for r in reqs if r[0] == 2], [see], [o for r, o in zip(reqs, outs) if r[0] == 2])
+        k, v = (np.concatenate([f64(x), np.zeros((Hkv, N, d))], 1) for x in p.rows(0, 0, n))
+        for (s, q, _), o in zip(reqs, outs):
+            if s != 2:
+                assert_attn_close(o, O.tree_attn(f64(q), k, v, none), f"sequence {s}")
+
+
 def test_a_sequence_without_pages(vc):
     g = gen(16)
     p = build(vc, g, 8, 2, 64, 16, [(50, 2), (0, 1)])
