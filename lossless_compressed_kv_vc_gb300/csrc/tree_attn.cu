@@ -269,7 +269,7 @@ struct TCfg {
   static constexpr int OFF_K = 2 * T_BYTES;    // behind a Q tile per chain
   static constexpr int OFF_V = OFF_K + KST * T_BYTES;
   static constexpr int OFF_BAR = OFF_V + VST * T_BYTES;
-  static constexpr int BAR_BYTES = (2 * (KST + VST) + 22) * 8 + 32;
+  static constexpr int BAR_BYTES = (2 * (KST + VST) + 24) * 8 + 32;
   static constexpr int OFF_SUM = OFF_BAR + BAR_BYTES;  // [2][TM] maxima and sums of the chains' rows
   static constexpr int SMEM = OFF_SUM + 2 * TM * 8 + (int)sizeof(TPiece) + (int)sizeof(TreePlan);
   static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
@@ -418,7 +418,10 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
   uint64_t* vbar = qfull + 2;     // [2] the chain's warps have looked through a V tile (4 warps)
   uint64_t* xbar = vbar + 2;      // [4] drain of an issuer's MMAs
   uint64_t* both = xbar + 4;      // [2] a paired piece: both chains' sums are there; they have been read (8 warps)
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(both + 2);
+  // [2] the Q tile of the CTA's first piece (4 warps): for the loader, which holds back V for it. Of qfull it could miss
+  // that phase: a chain that sees all of a first piece of one tile asks for its next queries without V.
+  uint64_t* qfirst = both + 2;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(qfirst + 2);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tslot + 1);
   // [2][2] by S buffer, as the barriers are: 1 + the chain's last step in it whose P V the softmax warps took. A
   // warp may be a step ahead of the others, and so ahead of the P V issuer, which reads a step's word once all
@@ -462,6 +465,7 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
       mbar_init(&qfull[w], 4);
       mbar_init(&vbar[w], 4);
       mbar_init(&both[w], 8);
+      mbar_init(&qfirst[w], 4);
       mbar_init(&xbar[w], 1);
       mbar_init(&xbar[2 + w], 1);
     }
@@ -518,8 +522,8 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
             }
             // All CTAs' rings together are 24 MB, 4 us of DRAM's time, and the first piece's Q would queue behind them
             // (16 x 1000 keys: 6.8 us for it): it goes ahead of all but the first tile of K.
-            if (it == 0 && kv == 1 && (!twait_warp(&qfull[0], 0, p.dev_status, s_abort) ||
-                                       (!q.idle(1) && !twait_warp(&qfull[1], 0, p.dev_status, s_abort)))) {
+            if (it == 0 && kv == 1 && (!twait_warp(&qfirst[0], 0, p.dev_status, s_abort) ||
+                                       (!q.idle(1) && !twait_warp(&qfirst[1], 0, p.dev_status, s_abort)))) {
               ok = false;
               break;
             }
@@ -657,7 +661,10 @@ __global__ void __launch_bounds__(TTHREADS, 1) tree_attn_kernel(const __grid_con
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&qfull[w]);
+        if (lane == 0) {
+          mbar_arrive(&qfull[w]);
+          if (g == 0) mbar_arrive(&qfirst[w]);
+        }
         return;
       }
     };

@@ -714,6 +714,22 @@ def test_a_batch_of_thirty_two(vc, Hq, Hkv, d, page):
     assert int(p.status.item()) == 0
 
 
+@pytest.mark.parametrize("G,d,page,n", [(9, 64, 16, 128), (32, 128, 128, 128), (128, 128, 64, 256), (32, 64, 64, 64), (16, 128, 32, 129)])
+def test_pieces_of_one_tile_that_all_see_whole(vc, G, d, page, n):
+    """One token over n - 1 rows: many heads of a tile or two each, in which a chain needs no V before its next queries."""
+    g = gen(36)
+    Hkv, B = 24, 20
+    p = build(vc, g, G * Hkv, Hkv, d, page, [(n - 1, 1)] * B)
+    reqs = [(s, randn(g, 1, G * Hkv, d), None) for s in range(B)]
+    ws = torch.empty(vc.vc_tree_workspace_size(p.shape(B), 1), dtype=torch.uint8, device="cuda")
+    first = attend(vc, p, reqs, ws)
+    check(vc, p, G * Hkv, reqs, [np.ones((1, 1), bool)] * B, first, heads=(0, 11, 23))
+    for _ in range(100):
+        outs = attend(vc, p, reqs, ws)
+    torch.cuda.synchronize()
+    assert int(p.status.item()) == 0 and all(torch.equal(a, b) for a, b in zip(first, outs))
+
+
 def test_rows_that_have_no_pages(vc):
     """Tokens behind the pages held are seen by none; a table entry outside the pool reads as nothing; both are reported
     and the other requests come out right."""
