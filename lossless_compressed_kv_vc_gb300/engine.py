@@ -902,6 +902,7 @@ class TreeBatch:
         attn, pages = vc_tree_workspace_size(shape, max_rows), vc_pages_workspace_size(shape, self.kv)
         if attn == 0 or pages == 0:
             raise ValueError(f"no workspace for Hq {Hq}, Hkv {Hkv}, d {d}, {n_pages} pages of {page} rows, max_rows {max_rows}")
+        vc_rope_pages(self._shape(1), axes, self.kv, (vc_rope_page_req * 1)(), stream=0)  # no tokens: only looks at the table
         self.ws = torch.empty(max(attn, pages), dtype=torch.uint8, device=self.device)
         self.q_rot = torch.zeros((most, max_rows, Hq, d), dtype=torch.bfloat16, device=self.device)
         nodes = min(max_rows, VC_TREE_MAX_NODES)
@@ -980,6 +981,22 @@ class TreeBatch:
         R >= max(rows), any stride between tokens that keeps them apart (slices of a fused projection).
         off int32: positions from the sequence's next one on, [B][R] the same on every axis (the depths of a
         tree), or [B][n_axes][R]; one after the other by default. Rotated queries land in q_rot[b]."""
+        B, R = len(seqs), self._check_tokens(seqs, q, k, v, rows)
+        if off is not None:
+            self._check_ints(off, "off", *((B, self.axes.n_axes, R) if off.dim() == 3 else (B, R)))
+        self._append(seqs, q, k, v, rows, off, stream)
+
+    def _append(self, seqs, q, k, v, rows, off, stream):
+        B, R, several = len(seqs), q.shape[1], off is not None and off.dim() == 3
+        strides = (q.stride(1), k.stride(1), v.stride(1)) if max(rows) > 1 else (0, 0, 0)
+        at = _rows_at(B, q, k, v, off, self.q_rot)
+        arr = (vc_rope_page_req * B)(*[(qb, kb, vb, *strides, ob, R if several else 0, rb, s, n)
+                                       for qb, kb, vb, ob, rb, s, n in zip(*at, seqs, rows)])
+        with torch.cuda.device(self.device):
+            self._order(stream)
+            vc_rope_pages(self._shape(B), self.axes, self.kv, arr, self.dev_status, stream)
+
+    def _check_tokens(self, seqs, q, k, v, rows):
         self._check_seqs(seqs, rows)
         B, R = len(seqs), q.shape[1] if q.dim() == 4 else -1
         if max(rows) > R:
@@ -990,16 +1007,9 @@ class TreeBatch:
                 raise ValueError("q, k and v are bf16 [B][R][heads][d] on the pool's device, each token's heads contiguous")
             if max(rows) > 1 and t.stride(1) < heads * self.d:  # an expanded tensor's 0 would mean packed tokens
                 raise ValueError("the tokens of q, k and v do not overlap: a stride of heads * d or more between them")
-        several = off is not None and off.dim() == 3
-        if off is not None:
-            self._check_ints(off, "off", *((B, self.axes.n_axes, R) if several else (B, R)))
-        strides = (q.stride(1), k.stride(1), v.stride(1)) if max(rows) > 1 else (0, 0, 0)
-        at = _rows_at(B, q, k, v, off, self.q_rot)
-        arr = (vc_rope_page_req * B)(*[(qb, kb, vb, *strides, ob, R if several else 0, rb, s, n)
-                                       for qb, kb, vb, ob, rb, s, n in zip(*at, seqs, rows)])
-        with torch.cuda.device(self.device):
-            self._order(stream)
-            vc_rope_pages(self._shape(B), self.axes, self.kv, arr, self.dev_status, stream)
+            if max(rows) > 1 and t.stride(1) % 8 or any(r > 0 and at % 16 for at, r in zip(*_rows_at(B, t), rows)):
+                raise ValueError("every token of q, k and v starts on a 16-byte boundary")
+        return R
 
     def attend(self, seqs: List[int], o: torch.Tensor, rows: List[int], mask: Optional[torch.Tensor] = None, stream=None):
         """Attention of the rows just appended, into o bf16 [B][R][Hq][d], R >= max(rows). mask int32 [B][R'][words],
@@ -1009,6 +1019,9 @@ class TreeBatch:
             self._check_ints(mask, "mask", *mask.shape)
             if mask.dim() != 3 or mask.shape[0] != len(seqs) or mask.shape[1] < max(rows) or mask.shape[2] * 32 < max(rows):
                 raise ValueError("mask is [B][R][words], a row and a bit for each token")
+        self._attend(seqs, o, rows, mask, stream)
+
+    def _attend(self, seqs, o, rows, mask, stream):
         words = 0 if mask is None else mask.shape[2]
         arr = (vc_tree_req * len(seqs))(*[(qb, ob, mb, words, s, n) for qb, ob, mb, s, n in
                                           zip(*_rows_at(len(seqs), self.q_rot, o, mask), seqs, rows)])
@@ -1052,20 +1065,21 @@ class TreeBatch:
         a chain, committed at once. With parent int32 [B][R] and n_nodes int32 [B] (rows, on the device): trees, whose
         tokens stay behind the context until accept commits the path that the full pass agrees with."""
         rows = [1] * len(seqs) if rows is None else rows
-        self._check_out(seqs, o, rows)  # before the caches move on
+        self._check_out(seqs, o, rows)  # all of it before the pool changes
+        R = self._check_tokens(seqs, q, k, v, rows)
         mask = depth = None
         if parent is not None:
             B, N = _check_trees(n_nodes, parent)
-            if B != len(seqs) or not max(rows) <= N <= min(self.max_rows, VC_TREE_MAX_NODES) or parent.device != self.device:
-                raise ValueError("parent is [B][R] on the pool's device, max(rows) <= R <= max_rows and VC_TREE_MAX_NODES")
+            if (B, N) != (len(seqs), R) or N > min(self.max_rows, VC_TREE_MAX_NODES) or parent.device != self.device:
+                raise ValueError("parent is [B][R] on the pool's device, as q is, R <= max_rows and VC_TREE_MAX_NODES")
             W = (N + 31) // 32
             mask, depth = self._masks[: B * N * W].view(B, N, W), self._depths[: B * N].view(B, N)
             with torch.cuda.device(self.device):
                 self._order(stream)
                 tree_mask(parent, n_nodes, mask, depth, stream)
         self.reserve(seqs, rows, stream)
-        self.append(seqs, q, k, v, rows, depth, stream)
-        self.attend(seqs, o, rows, mask, stream)
+        self._append(seqs, q, k, v, rows, depth, stream)
+        self._attend(seqs, o, rows, mask, stream)
         if parent is None:
             self.commit(seqs, rows, stream=stream)
 

@@ -500,6 +500,51 @@ def test_engine_refusals(vc, calls):
             trees(vc, **kw)
 
 
+def test_engine_steps_look_at_their_tokens_before_the_pool_changes(vc, calls):
+    """Nothing is called for a step whose tokens append would refuse, or whose trees are not as wide as they."""
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)
+    tb = trees(vc)
+    calls.clear()
+    good = dict(q=new(HQ), k=new(HKV), v=new(HKV))
+    for name, heads in (("q", HQ), ("k", HKV), ("v", HKV)):
+        flat = torch.zeros(2 * 8 * heads * D + 64, dtype=torch.bfloat16)
+        wide = torch.zeros((2, 8, heads * D + 4), dtype=torch.bfloat16)
+        for bad in (new(heads).float(), new(heads + 1), new(heads)[:1], new(heads, R=7), new(heads, R=1).expand(2, 8, heads, D),
+                    new(heads).transpose(2, 3).contiguous().transpose(2, 3), new(heads).to("meta"), new(heads)[0],
+                    flat[4 : 4 + 2 * 8 * heads * D].view(2, 8, heads, D), wide[..., : heads * D].unflatten(2, (heads, D)),
+                    flat.as_strided((2, 8, heads, D), (8 * heads * D + 4, heads * D, D, 1))):
+            for tree in ({}, dict(parent=i(2, 8), n_nodes=i(2))):
+                for rows in ([2, 2], [8, 1]):
+                    with pytest.raises(ValueError):
+                        tb.step([0, 1], **{**good, name: bad}, o=new(HQ), rows=rows, **tree)
+                    with pytest.raises(ValueError):
+                        tb.append([0, 1], **{**good, name: bad}, rows=rows)
+                    assert not calls, (name, bad.shape, bad.stride())
+    for R in (2, 7):  # trees narrower than their tokens
+        with pytest.raises(ValueError):
+            tb.step([0, 1], **good, o=new(HQ), rows=[2, 2], parent=i(2, R), n_nodes=i(2))
+        assert not calls
+    with pytest.raises(ValueError):
+        tb.step([0, 1], *(new(h, R=4) for h in (HQ, HKV, HKV)), o=new(HQ), rows=[5, 1])
+    assert not calls
+    tb.step([0, 1], **{**good, "q": torch.zeros(2 * 8 * HQ * D + 4, dtype=torch.bfloat16)[: 2 * 8 * HQ * D].view(2, 8, HQ, D)}, o=new(HQ), rows=[8, 1])
+    one = torch.zeros((2, 1, HQ * D + 4), dtype=torch.bfloat16)[:1, :, : HQ * D].unflatten(2, (HQ, D))
+    tb.step([2], one, new(HKV, 1, 1), new(HKV, 1, 1), new(HQ, 1, 1))  # one token's stride does not matter
+    odd = torch.zeros(8 * HQ * D + 4, dtype=torch.bfloat16).as_strided((2, 8, HQ, D), (4, HQ * D, D, 1))
+    tb.step([0, 1], **{**good, "q": odd}, o=new(HQ), rows=[8, 0])  # nor where a sequence without tokens starts
+
+
+def test_engine_refuses_a_table_of_axes_that_does_not_fit(vc):
+    """At once, not in a step's append behind its reserve."""
+    from lossless_compressed_kv_vc_gb300 import engine
+    wide = vc.vc_rope_axes_init(vc.vc_rope_init(vc.VC_ROPE_NONE, 2 * D), [D])
+    broken = vc.vc_rope_axes_init(vc.vc_rope_init(vc.VC_ROPE_NONE, D), [D // 2])
+    broken.axis[3] = 1
+    for axes in (wide, broken, None):
+        with pytest.raises(vc.VCError):
+            engine.TreeBatch(HQ, HKV, D, n_seq=2, n_pages=4, page=16, axes=axes, device="cpu")
+
+
 def test_the_default_stream_is_waited_on_itself(vc, monkeypatch):
     """Stream 0 is the default stream, of which ExternalStream would make a new one."""
     from lossless_compressed_kv_vc_gb300 import engine
