@@ -706,8 +706,9 @@ vc_status vc_tree_mask(int32_t B, int32_t N_max, const int32_t* parent, const in
  * ws: vc_tree_workspace_size(shape, max_rows) bytes for calls of up to max_rows rows a request; no
  * initialisation; calls that overlap on the GPU must not share one.
  * Errors before anything is launched: VC_ERR_INVALID; VC_ERR_WORKSPACE; VC_ERR_UNSUPPORTED (more than 2^29 query
- * rows, or so large a table that the sum over the requests of Hkv * ceil(n_rows * Hq / Hkv / 256) * max_pages * page
- * / 16 passes 2^29). dev_status as for vc_prefix_attn. */
+ * rows, or so large a table that the work's cost may pass 32 bits: not while the sum over the requests of
+ * Hkv * ceil(n_rows * Hq / Hkv / 256) * max_pages * page / 16 is up to 2^29, and in any case from 2^32 on).
+ * dev_status as for vc_prefix_attn. */
 typedef struct vc_tree_req {
   const void* q;         /* bf16 [n_rows][Hq][d] */
   void* o;               /* bf16 [n_rows][Hq][d] */

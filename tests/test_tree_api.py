@@ -301,6 +301,20 @@ def test_tree_attn_refusals(vc):
     assert vc.vc_tree_workspace_size(vc.vc_shape(1, 8, 2, 64), 0) == 0
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,n_rows", [(1, 8, 8, 1), (1, 8, 2, 256), (1, 4, 4, 300), (32, 2, 2, 9), (4, 64, 8, 40),
+                                             (1, 64, 64, 200)])
+def test_tree_attn_takes_tables_up_to_the_headers_sum(vc, B, Hq, Hkv, n_rows):
+    """Accepted (up to the workspace that is not there) at 2^29 of the header's sum, refused from 2^32 on."""
+    kw = dict(stream=0, raise_on_error=False)
+    arr = (vc.vc_tree_req * B)(*[vc.vc_tree_req(q=A, o=A, seq=b % 10, n_rows=n_rows) for b in range(B)])
+    call = lambda rows: vc.vc_tree_attn(vc.vc_shape(B, Hq, Hkv, 64), _pool(vc, max_pages=rows // 128, page=128), arr, **kw)
+    per = B * Hkv * -(-(n_rows * Hq // Hkv) // 256)  # sixteenths of the sum for each row of the table
+    most = min(2 ** 30, 2 ** 29 * 16 // per // 128 * 128)
+    assert call(most) == vc.VC_ERR_WORKSPACE
+    if 2 ** 32 * 16 // per <= 2 ** 30:
+        assert call(2 ** 32 * 16 // per) == vc.VC_ERR_UNSUPPORTED
+
+
 def test_tree_workspace_does_not_grow_with_the_call(vc):
     """Two slots a CTA hold every partial, however many requests, heads and rows there are."""
     size = lambda B, Hq, Hkv, rows: vc.vc_tree_workspace_size(vc.vc_shape(B, Hq, Hkv, 128), rows)
