@@ -7,8 +7,6 @@
 // is left to grids that fill the GPU.
 #include "paged.cuh"
 
-#include <limits.h>
-
 namespace vc {
 
 constexpr int kPageThreads = 1024;
@@ -68,8 +66,8 @@ __device__ __forceinline__ void reserve_plan(const ReserveParams& p) {
       held = kv.held_of(q.seq);
       n = context_rows(kv, q.seq, held, ok);
       const int64_t want = ((int64_t)n + q.rows + page - 1) >> kv.shift;
-      more = (int)min(max(want - held, (int64_t)0), (int64_t)INT_MAX / 64);
-      if (want > kv.max_pages) ok = false;
+      more = (int)min(max(want - held, (int64_t)0), (int64_t)avail);
+      if (want > kv.max_pages || want - held > avail) ok = false;
       if (ok && q.rows > 0 && (n & (page - 1)) != 0) {  // n <= held * page: the table has this page
         old = kv.pages_of(q.seq)[n >> kv.shift];
         if (kv.has_page(old))
@@ -82,7 +80,9 @@ __device__ __forceinline__ void reserve_plan(const ReserveParams& p) {
     const unsigned same = __match_any_sync(0xffffffffu, ok && old >= 0 ? old : -1 - r), lt = (1u << r) - 1u;
     shared = ok && old >= 0 && refs - __popc(same & lt) > 1;
     int take = ok ? more + shared : 0;
-    if (__reduce_add_sync(0xffffffffu, min(take, INT_MAX / 64)) > avail) {  // one after the other, as long as pages last
+    // 32 requests' sum takes more than 32 bits
+    const int64_t all = ((int64_t)__reduce_add_sync(0xffffffffu, take >> 16) << 16) + __reduce_add_sync(0xffffffffu, take & 0xffff);
+    if (all > avail) {  // one after the other, as long as pages last
       int left = avail;
       unsigned copied = 0;
       for (int i = 0; i < p.B; ++i) {

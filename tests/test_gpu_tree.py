@@ -170,6 +170,27 @@ def test_reserve_when_pages_run_short(vc):
     assert p.ref.faults == 2 and p.ref.n_free == 0
 
 
+def test_reserve_of_more_than_2_to_the_25_pages(vc):
+    """One request for 35 million pages beside one for more than are left: whole, or not at all. Only the state exists:
+    nothing is copied, so that no row of K or V is touched."""
+    n_pages, most, page = 40 * 10 ** 6, 36 * 10 ** 6, 16
+    k = torch.zeros((16,), dtype=torch.bfloat16, device="cuda")
+    st = dict(refs=ints(n_pages), free_pages=ints(n_pages), n_free=ints(1), table=ints(3, most, fill=-77), len=ints(3), held=ints(3),
+              next=ints(3))
+    kv = vc.vc_paged_kv(k.data_ptr(), k.data_ptr(), *(t.data_ptr() for t in st.values()), n_pages, page, 3, most)
+    shape, status = vc.vc_shape(3, 1, 1, 64), ints(1)
+    ws = torch.empty(64, dtype=torch.uint8, device="cuda")
+    vc.vc_pages_init(shape, kv)
+    take = 35 * 10 ** 6
+    reqs = [(0, take * page - 5), (1, 10 ** 7 * page), (2, 17)]
+    vc.vc_pages_reserve(shape, kv, (vc.vc_reserve_req * 3)(*[vc.vc_reserve_req(*r) for r in reqs]), ws, status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == vc.VC_DEV_PAGES and st["held"].tolist() == [take, 0, 2] and int(st["n_free"]) == n_pages - take - 2
+    assert torch.equal(st["table"][0, :take], torch.arange(take, dtype=torch.int32, device="cuda"))
+    assert st["table"][2, :3].tolist() == [take, take + 1, -77] and (st["table"][0, take:] == -77).all() and (st["table"][1] == -77).all()
+    assert (st["refs"][: take + 2] == 1).all() and not st["refs"][take + 2 :].any()
+
+
 def test_thirty_two_forks_of_one(vc):
     """One sequence copied 31 times in one call, room for all in one call: the last one keeps the shared page."""
     g = gen(3)
