@@ -624,7 +624,8 @@ vc_status vc_pages_fork(const vc_shape* shape, const vc_paged_kv* kv, const vc_f
 /* vc_pages_trim — each sequence cut to its first `rows` rows (where its context is longer: len = rows and
  * next = `next`), and the pages behind its context's given back: request by request, the last page
  * first; a page that no sequence holds any more goes on the stack. rows = 0 frees the sequence,
- * rows = INT32_MAX gives back what was reserved and not used. */
+ * rows = INT32_MAX gives back what was reserved and not used. B * max_pages < 2^31 - 1024
+ * (VC_ERR_UNSUPPORTED). */
 typedef struct vc_trim_req {
   int32_t seq;
   int32_t rows;    /* >= 0 */

@@ -125,7 +125,8 @@ vc_status vc_pages_trim(const vc_shape* shape, const vc_paged_kv* kv, const vc_t
   const vc_status st = check_pool(shape, kv, &p.kv);
   if (st != VC_OK) return st;
   if (!req || !seqs_ok(kv, req, shape->B)) return VC_ERR_INVALID;
-  if ((int64_t)shape->B * kv->max_pages > INT32_MAX) return VC_ERR_UNSUPPORTED;  // pages given back, numbered in 32 bits
+  // pages given back are numbered in 32 bits, with room for a step of the block beyond the last one
+  if ((int64_t)shape->B * kv->max_pages > INT32_MAX - 1024) return VC_ERR_UNSUPPORTED;
   for (int b = 0; b < shape->B; ++b) {
     if (req[b].rows < 0) return VC_ERR_INVALID;
     p.req[b] = req[b];

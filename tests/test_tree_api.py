@@ -255,6 +255,15 @@ def test_trim_counts_its_pages_in_32_bits(vc):
     assert vc.vc_pages_trim(vc.vc_shape(32, 8, 2, 64), kv, arr, stream=0, raise_on_error=False) == vc.VC_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("B,max_pages,err", [(32, 2 ** 26 - 1, 2), (32, 2 ** 26 - 32, 2), (32, 2 ** 26 - 33, 1), (31, 2 ** 26, 1)])
+def test_trim_steps_stay_in_32_bits(vc, B, max_pages, err):
+    """The kernel goes through the pages 1024 at a time: the number behind the last step counts too. (Sizes within the
+    limit get as far as the request for fewer than no rows.)"""
+    arr = (vc.vc_trim_req * B)(*[vc.vc_trim_req(i, -1, 0) for i in range(B)])
+    kv = _pool(vc, max_pages=max_pages, n_seq=32)
+    assert vc.vc_pages_trim(vc.vc_shape(B, 8, 2, 64), kv, arr, stream=0, raise_on_error=False) == err
+
+
 def _rope(vc, axes="ok", **kw):
     if axes == "ok":
         axes = vc.vc_rope_axes_init(vc.vc_rope_init(vc.VC_ROPE_NONE, 64), [16, 16])
