@@ -58,7 +58,8 @@ constexpr int TPIECE = 6;
 // warps 0-3, 4-7 softmax of chains 0 and 1; 8, 9 issue their S; 10, 11 their P V; 12 TMA; 13 lays the plan down; 14
 // and 15 make a warpgroup with them (registers are handed over by warpgroup)
 constexpr int TTHREADS = 512;
-// Registers a thread: launched with 128 (65536 / 512), then 176 in the softmax warpgroups and 80 in the others
+// Registers a thread: launched with 128 (65536 / 512), then 176 in the softmax warpgroups and 80 in the others (with 64
+// channels one word is spilled, with 128 none)
 constexpr int TREG_SOFTMAX = 176, TREG_ISSUE = 80;
 static_assert(256 * (TREG_SOFTMAX + TREG_ISSUE) <= 65536, "no more than the block was launched with");
 

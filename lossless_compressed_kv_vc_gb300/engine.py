@@ -878,7 +878,10 @@ class TreeBatch:
     and commit what was accepted (accept does both ends of that for trees). What the device finds wrong
     (no pages left, say) lands in dev_status. A sequence that the pool had no pages for keeps its context, len and
     next, whatever its turn's outputs say: they tell which ones those are, and the same turn can be made again
-    once there is room. Forks go between turns. All calls run on `stream` (the current one by default);
+    once there is room. Forks go between turns. max_pages (n_pages by default) is the most that a sequence can
+    hold: lengths are the device's, so attention of 9 to 16 query rows a KV head takes the kernel for few rows where
+    max_pages * page is no more than 4096; a large pool of short sequences should say so (16 rows over 32 x 200 keys
+    21 us instead of 27). All calls run on `stream` (the current one by default);
     like a Batch's, each stream first waits for the construction. They share q_rot and a workspace, so
     calls on different streams are ordered by the caller.
     """
