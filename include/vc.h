@@ -571,7 +571,10 @@ size_t vc_evict_workspace_size(const vc_shape* shape, int32_t max_n);
  * fork's sources, which are only read. Calls on one pool are ordered by their stream or by events.
  * State that does not add up (a table entry outside the pool, a length beyond the pages held, rows to
  * be written where the sequence has no page or shares it) is never followed out of bounds: the rows
- * or pages it touches are skipped (read as zeros by vc_tree_attn) and dev_status receives VC_DEV_PAGES.
+ * or pages it touches are skipped (vc_tree_attn reads a page outside the pool as zeros, and counts no
+ * tokens that have no page or begin in a shared one) and dev_status receives VC_DEV_PAGES. Pages behind
+ * the one that holds a sequence's last row of context are shared by none of these calls; a caller who
+ * lays the state down keeps to that.
  * A sequence that vc_pages_reserve could not serve is in that state for its turn, and keeps its context:
  * len and next tell afterwards which ones those are. Forks go between turns, not between a source's
  * vc_rope_pages and vc_tree_commit: its last page is then shared, and the turn's rows in it do not count.
